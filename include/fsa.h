@@ -345,10 +345,132 @@ FSA_API fsa_status fsa_cross_attention_fwd_host(const void *q, const void *k, co
 FSA_API fsa_status fsa_mma_rate_probe(int kind, int ctas, int iters, double *flops_per_launch,
                                       void *stream);
 
+/*
+ * The four-bit key/value cache of a language model (an addition of this
+ * library; the pages have no counterpart).
+ *
+ * A cache is one device buffer of num_pages * fsa_kv4_page_bytes() bytes,
+ * 16-byte aligned, owned by the caller: pages of page_size tokens, every page
+ * holding the keys and values of all H_kv heads as MXFP4 (E2M1 codes, one E8M0
+ * scale per 32 elements along D; the scale and rounding rule is
+ * fsa_quantize_mx's).  Slot s is token s % page_size of page s / page_size.
+ * Layout: [page][head][page_size / 32] groups of 32 tokens, 34 D bytes each:
+ *   32 rows of D/2 key code bytes, 32 rows of D/2 value code bytes, 32 rows of
+ *   D/32 key scale bytes, 32 rows of D/32 value scale bytes (X + 127);
+ *   byte t (D/8) + 4 b + j of a key row holds d = 32 b + 8 t + 2 j (low nibble)
+ *   and d + 1; byte g (D/16) + 2 b + j of a value row d = 32 b + 4 g + 2 j and
+ *   d + 1.
+ * D in {64, 128}; page_size a positive multiple of 32, at most 65536;
+ * H_kv in 1 .. 65535; num_pages in 1 .. 2^31 - 1.
+ */
+
+/* Bytes of one page; 0 for invalid arguments. */
+FSA_API uint64_t fsa_kv4_page_bytes(int H_kv, int page_size, int D);
+
+/*
+ * fsa_kv4_append -- quantizes T tokens' keys and values into the cache.
+ *  k, v: bf16 [T][H_kv][D], heads contiguous, tokens k_stride and v_stride
+ *        elements apart (multiples of 8), 16-byte aligned; so parts of one
+ *        projection's output need no copy.  Finite values; a block whose
+ *        largest magnitude is 1.75 * 2^127 or more rounds to 2^128 and is read
+ *        back as infinity.
+ *  slots: device int64 [T], the slot of each token; a token whose slot is
+ *        negative is skipped.  Slots of one call must differ: a slot given
+ *        twice holds a mixture of the two tokens.  A slot beyond the cache is
+ *        skipped and reported by fsa_get_device_error as
+ *        FSA_ERR_INVALID_ARGUMENT.
+ * T in 0 .. 2^31 - 1.  Writes only the given slots' bytes.
+ */
+FSA_API fsa_status fsa_kv4_append(const void *k, const void *v, int64_t k_stride, int64_t v_stride,
+                                  const int64_t *slots, int64_t T, int H_kv, int D, void *cache,
+                                  int64_t num_pages, int page_size, void *stream);
+
+/*
+ * fsa_kv4_read -- the values that the cache holds at T slots, as bf16 (exact)
+ * [T][H_kv][D] with token strides k_stride and v_stride (elements, multiples
+ * of 8, at least H_kv * D), 16-byte aligned.  A negative slot reads as zeros,
+ * one beyond the cache too, reported as by fsa_kv4_append.  A slot may be
+ * given more than once.
+ */
+FSA_API fsa_status fsa_kv4_read(const void *cache, int64_t num_pages, int page_size,
+                                const int64_t *slots, int64_t T, int H_kv, int D, void *k, void *v,
+                                int64_t k_stride, int64_t v_stride, void *stream);
+
+/*
+ * fsa_kv4_attention_fwd -- attention of Sq query tokens per sequence (one when
+ * decoding, a few when checking a draft) over the four-bit cache.
+ *  q: bf16 [B][Sq][Hq][D], heads contiguous, tokens q_stride elements apart (a
+ *     multiple of 8), 16-byte aligned.
+ *  page_table: device int32 [B][max_pages], the pages of each sequence in
+ *     order; entries behind its last page are not read.
+ *  seq_lens: device int32 [B], the number of keys of each sequence, the Sq
+ *     query tokens' own included (append them first).  0 is allowed.
+ *  o: bf16 [B][Sq][Hq][D] contiguous, 16-byte aligned.
+ *  lse: float [B][Sq][Hq] or NULL: natural log of the sum of exp(s).
+ * Query i of sequence b sees the keys j <= seq_lens[b] - Sq + i; query head h
+ * reads key head h / (Hq / Hkv).  s = sm_scale * q . k^ (sm_scale <= 0 selects
+ * 1/sqrt(D)), o = softmax(s) v^ on the cached values as held.  A row that sees
+ * no key gets o = 0 and lse = -infinity.
+ *  - Products in f16 with FP32 accumulation: q is scaled by a power of two per
+ *    row, softmax weights are rounded to f16 (relative to the largest product
+ *    of weight and value scale); sums are FP32.
+ *  - workspace: device buffer of fsa_kv4_attention_workspace_size() bytes,
+ *    256-byte aligned, contents arbitrary; NULL when that size is 0.  Calls
+ *    that may overlap need workspaces of their own.
+ *  - A length outside 0 .. max_pages * page_size is clamped, a page outside the
+ *    cache skipped with all of its keys; both are reported by
+ *    fsa_get_device_error as FSA_ERR_INVALID_ARGUMENT.
+ * Requirements: B, Sq, Hq, Hkv >= 1, Hkv divides Hq, B <= 65535, Hkv <= 65535,
+ * Sq * Hq / Hkv <= 65535, D in {64, 128}, max_pages >= 1, max_pages *
+ * page_size <= 2^30, and a cache as above.
+ */
+FSA_API fsa_status fsa_kv4_attention_fwd(const void *q, int64_t q_stride, const void *cache,
+                                         const int32_t *page_table, const int32_t *seq_lens, void *o,
+                                         float *lse, int B, int Sq, int Hq, int Hkv, int D,
+                                         int64_t num_pages, int page_size, int max_pages,
+                                         float sm_scale, void *workspace, uint64_t workspace_bytes,
+                                         void *stream);
+
+/* Bytes of device workspace that fsa_kv4_attention_fwd needs (0: none, and for
+ * invalid arguments). */
+FSA_API uint64_t fsa_kv4_attention_workspace_size(int B, int Sq, int Hq, int Hkv, int D,
+                                                  int page_size, int max_pages);
+
+/*
+ * fsa_varlen_attention_fwd -- BF16 softmax attention over packed sequences of
+ * different lengths with grouped heads: whole prompts (cu_k = cu_q), or pieces
+ * of prompts that continue a context.
+ *  q: bf16 [Tq][Hq][D]; k, v: bf16 [Tk][Hkv][D]; heads contiguous, tokens
+ *     q_stride / k_stride / v_stride elements apart (multiples of 8, at least
+ *     heads * D), 16-byte aligned.
+ *  cu_q, cu_k: device int32 [B + 1], non-decreasing: sequence b owns query rows
+ *     cu_q[b] .. cu_q[b+1] - 1 and keys cu_k[b] .. cu_k[b+1] - 1.
+ *  causal: query i of a sequence of nq queries and nk keys sees the keys
+ *     j <= nk - nq + i; 0: all keys of its sequence.
+ *  o: bf16 [Tq][Hq][D] contiguous, 16-byte aligned; lse: float [Tq][Hq] or
+ *     NULL.  Rows outside every sequence are left as they were; a row that
+ *     sees no key gets o = 0 and lse = -infinity.
+ * Same arithmetic as fsa_bf16_attention_fwd (FP32 scores and sums, BF16
+ * weights).  The tokens of a sequence must be finite; what stands outside of
+ * it does not reach its outputs.  Bounds that decrease or leave 0 .. Tq or
+ * 0 .. Tk are reported by fsa_get_device_error as FSA_ERR_INVALID_ARGUMENT;
+ * nothing outside the buffers is touched, and the outputs of the sequences
+ * from the first wrong bound on are undefined.
+ * Requirements: B >= 1, Tq, Tk in 0 .. 2^30, Hkv divides Hq, Hkv <= 65535,
+ * Hq / Hkv <= 128, D in {64, 128}.
+ */
+FSA_API fsa_status fsa_varlen_attention_fwd(const void *q, const void *k, const void *v,
+                                            int64_t q_stride, int64_t k_stride, int64_t v_stride,
+                                            const int32_t *cu_q, const int32_t *cu_k, void *o,
+                                            float *lse, int B, int Tq, int Tk, int Hq, int Hkv,
+                                            int D, int causal, float sm_scale, void *stream);
+
 /* Synchronises `stream`, then reads and clears the device error words of the
  * current device (the allocating entry points' word and, once that entry
  * point has run there, fsa_attention_fwd_noalloc's): FSA_OK, FSA_ERR_TIMEOUT,
- * or FSA_ERR_CUDA if the sync itself failed.  Allocates no device memory. */
+ * FSA_ERR_INVALID_ARGUMENT if a kernel met a slot, page or sequence bound
+ * outside its buffer, or FSA_ERR_CUDA if the sync itself failed.  Allocates no
+ * device memory. */
 FSA_API fsa_status fsa_get_device_error(void *stream);
 
 /* Static description of a status code. */

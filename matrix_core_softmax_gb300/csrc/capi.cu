@@ -428,6 +428,174 @@ fsa_status fsa_quantize_mx(const void* x, int64_t batch, int64_t rows, int64_t c
     return e == cudaSuccess ? FSA_OK : FSA_ERR_CUDA;
 }
 
+uint64_t fsa_kv4_page_bytes(int H_kv, int page_size, int D) {
+    if (H_kv < 1 || H_kv > 65535 || page_size < 32 || page_size > 65536 || page_size % 32 != 0 || (D != 64 && D != 128))
+        return 0;
+    return static_cast<uint64_t>(H_kv) * (page_size / 32) * (34 * D);
+}
+
+namespace {
+
+// Shape of a four-bit cache and its address.
+fsa_status check_kv4(const void* cache, int64_t num_pages, int page_size, int H_kv, int D) {
+    if (!cache || !aligned16(cache)) return FSA_ERR_INVALID_ARGUMENT;
+    if (D != 64 && D != 128) return FSA_ERR_UNSUPPORTED;
+    if (num_pages < 1 || num_pages > INT32_MAX || fsa_kv4_page_bytes(H_kv, page_size, D) == 0)
+        return FSA_ERR_INVALID_ARGUMENT;
+    return FSA_OK;
+}
+
+bool token_stride_ok(int64_t stride, int64_t least) { return stride >= least && stride % 8 == 0 && stride < (int64_t{1} << 36); }
+
+fsa_status kv4_rows(const void* k, const void* v, int64_t k_stride, int64_t v_stride, const int64_t* slots, int64_t T,
+                    int H_kv, int D, const void* cache, int64_t num_pages, int page_size, int64_t least, Kv4Rows* a) {
+    fsa_status s = check_kv4(cache, num_pages, page_size, H_kv, D);
+    if (s != FSA_OK) return s;
+    if (T < 0 || T > INT32_MAX) return FSA_ERR_INVALID_ARGUMENT;
+    if (T > 0 && (!k || !v || !slots || !aligned16(k) || !aligned16(v) || (reinterpret_cast<uintptr_t>(slots) & 7) ||
+                  !token_stride_ok(k_stride, least) || !token_stride_ok(v_stride, least)))
+        return FSA_ERR_INVALID_ARGUMENT;
+    *a = Kv4Rows{k, v, k_stride, v_stride, slots, T, num_pages * page_size, H_kv, D, page_size, nullptr};
+    return FSA_OK;
+}
+
+}  // namespace
+
+fsa_status fsa_kv4_append(const void* k, const void* v, int64_t k_stride, int64_t v_stride, const int64_t* slots,
+                          int64_t T, int H_kv, int D, void* cache, int64_t num_pages, int page_size, void* stream) {
+    Kv4Rows a;
+    fsa_status s = kv4_rows(k, v, k_stride, v_stride, slots, T, H_kv, D, cache, num_pages, page_size, 0, &a);
+    if (s != FSA_OK || T == 0) return s;
+    int dev;
+    DeviceState* ds;
+    s = current_device(&dev, &ds);
+    if (s != FSA_OK) return s;
+    a.err_word = ds->err;
+    return launch_kv4_append(a, static_cast<uint8_t*>(cache), static_cast<cudaStream_t>(stream)) == cudaSuccess
+               ? FSA_OK : FSA_ERR_CUDA;
+}
+
+fsa_status fsa_kv4_read(const void* cache, int64_t num_pages, int page_size, const int64_t* slots, int64_t T, int H_kv,
+                        int D, void* k, void* v, int64_t k_stride, int64_t v_stride, void* stream) {
+    Kv4Rows a;
+    fsa_status s = kv4_rows(k, v, k_stride, v_stride, slots, T, H_kv, D, cache, num_pages, page_size,
+                            static_cast<int64_t>(H_kv) * D, &a);
+    if (s != FSA_OK || T == 0) return s;
+    int dev;
+    DeviceState* ds;
+    s = current_device(&dev, &ds);
+    if (s != FSA_OK) return s;
+    a.err_word = ds->err;
+    return launch_kv4_read(a, static_cast<const uint8_t*>(cache), static_cast<cudaStream_t>(stream)) == cudaSuccess
+               ? FSA_OK : FSA_ERR_CUDA;
+}
+
+namespace {
+
+fsa_status check_kv4_attention(int B, int Sq, int Hq, int Hkv, int D, int page_size, int max_pages) {
+    if (D != 64 && D != 128) return FSA_ERR_UNSUPPORTED;
+    if (B < 1 || B > 65535 || Sq < 1 || Hq < 1 || Hkv < 1 || Hkv > 65535 || Hq % Hkv != 0 ||
+        static_cast<int64_t>(Sq) * (Hq / Hkv) > 65535 || max_pages < 1 ||
+        fsa_kv4_page_bytes(Hkv, page_size, D) == 0 || static_cast<int64_t>(max_pages) * page_size > (1 << 30))
+        return FSA_ERR_INVALID_ARGUMENT;
+    return FSA_OK;
+}
+
+}  // namespace
+
+uint64_t fsa_kv4_attention_workspace_size(int B, int Sq, int Hq, int Hkv, int D, int page_size, int max_pages) {
+    if (check_kv4_attention(B, Sq, Hq, Hkv, D, page_size, max_pages) != FSA_OK) return 0;
+    return kv4_attention_workspace_bytes(B, Sq, Hq, Hkv, D, page_size, max_pages);
+}
+
+fsa_status fsa_kv4_attention_fwd(const void* q, int64_t q_stride, const void* cache, const int32_t* page_table,
+                                 const int32_t* seq_lens, void* o, float* lse, int B, int Sq, int Hq, int Hkv, int D,
+                                 int64_t num_pages, int page_size, int max_pages, float sm_scale, void* workspace,
+                                 uint64_t workspace_bytes, void* stream) {
+    fsa_status s = check_kv4_attention(B, Sq, Hq, Hkv, D, page_size, max_pages);
+    if (s != FSA_OK) return s;
+    s = check_kv4(cache, num_pages, page_size, Hkv, D);
+    if (s != FSA_OK) return s;
+    if (!q || !o || !page_table || !seq_lens || !aligned16(q) || !aligned16(o) ||
+        (reinterpret_cast<uintptr_t>(page_table) & 3) || (reinterpret_cast<uintptr_t>(seq_lens) & 3) ||
+        (reinterpret_cast<uintptr_t>(lse) & 3) || !token_stride_ok(q_stride, 0) || !std::isfinite(sm_scale))
+        return FSA_ERR_INVALID_ARGUMENT;
+    const uint64_t need = kv4_attention_workspace_bytes(B, Sq, Hq, Hkv, D, page_size, max_pages);
+    if (need && (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255) || workspace_bytes < need))
+        return FSA_ERR_INVALID_ARGUMENT;
+    int dev;
+    DeviceState* ds;
+    s = current_device(&dev, &ds);
+    if (s != FSA_OK) return s;
+    Kv4AttnLaunch a{};
+    a.q = q;
+    a.q_stride = q_stride;
+    a.cache = static_cast<const uint8_t*>(cache);
+    a.page_table = page_table;
+    a.seq_lens = seq_lens;
+    a.o = o;
+    a.lse = lse;
+    a.workspace = workspace;
+    a.num_pages = num_pages;
+    a.B = B;
+    a.Sq = Sq;
+    a.Hq = Hq;
+    a.Hkv = Hkv;
+    a.D = D;
+    a.page_size = page_size;
+    a.max_pages = max_pages;
+    a.sm_scale = sm_scale > 0.0f ? sm_scale : 1.0f / std::sqrt(static_cast<float>(D));
+    a.timeout_ns = 2000000000ull;
+    a.err_word = ds->err;
+    return launch_kv4_attention(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? FSA_OK : FSA_ERR_CUDA;
+}
+
+fsa_status fsa_varlen_attention_fwd(const void* q, const void* k, const void* v, int64_t q_stride, int64_t k_stride,
+                                    int64_t v_stride, const int32_t* cu_q, const int32_t* cu_k, void* o, float* lse,
+                                    int B, int Tq, int Tk, int Hq, int Hkv, int D, int causal, float sm_scale,
+                                    void* stream) {
+    if (D != 64 && D != 128) return FSA_ERR_UNSUPPORTED;
+    if (B < 1 || Tq < 0 || Tk < 0 || Tq > (1 << 30) || Tk > (1 << 30) || Hq < 1 || Hkv < 1 || Hkv > 65535 ||
+        Hq % Hkv != 0 || Hq / Hkv > 128 || (causal != 0 && causal != 1) || !std::isfinite(sm_scale))
+        return FSA_ERR_INVALID_ARGUMENT;
+    if (!cu_q || !cu_k || (reinterpret_cast<uintptr_t>(cu_q) & 3) || (reinterpret_cast<uintptr_t>(cu_k) & 3) ||
+        (reinterpret_cast<uintptr_t>(lse) & 3))
+        return FSA_ERR_INVALID_ARGUMENT;
+    if (Tq > 0 && (!q || !o || !aligned16(q) || !aligned16(o) || !token_stride_ok(q_stride, static_cast<int64_t>(Hq) * D)))
+        return FSA_ERR_INVALID_ARGUMENT;
+    if (Tk > 0 && (!k || !v || !aligned16(k) || !aligned16(v) ||
+                   !token_stride_ok(k_stride, static_cast<int64_t>(Hkv) * D) ||
+                   !token_stride_ok(v_stride, static_cast<int64_t>(Hkv) * D)))
+        return FSA_ERR_INVALID_ARGUMENT;
+    if (Tq == 0) return FSA_OK;
+    int dev;
+    DeviceState* ds;
+    fsa_status s = current_device(&dev, &ds);
+    if (s != FSA_OK) return s;
+    VarlenLaunch a{};
+    a.q = q;
+    a.k = k;
+    a.v = v;
+    a.q_stride = q_stride;
+    a.k_stride = k_stride;
+    a.v_stride = v_stride;
+    a.o = o;
+    a.lse = lse;
+    a.cu_q = cu_q;
+    a.cu_k = cu_k;
+    a.B = B;
+    a.Tq = Tq;
+    a.Tk = Tk;
+    a.Hq = Hq;
+    a.Hkv = Hkv;
+    a.D = D;
+    a.causal = causal;
+    a.sm_scale = sm_scale > 0.0f ? sm_scale : 1.0f / std::sqrt(static_cast<float>(D));
+    a.timeout_ns = 2000000000ull;
+    a.err_word = ds->err;
+    return launch_varlen_attention(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? FSA_OK : FSA_ERR_CUDA;
+}
+
 uint64_t fsa_attention_workspace_size(int B, int H, int S, int D, int fmt) {
     return fsa_cross_attention_workspace_size(B, H, S, S, D, fmt);
 }
@@ -649,6 +817,7 @@ fsa_status fsa_get_device_error(void* stream) {
         w |= x;
     }
     if (w & kErrTimeout) return FSA_ERR_TIMEOUT;
+    if (w & kErrBadIndex) return FSA_ERR_INVALID_ARGUMENT;
     return w ? FSA_ERR_CUDA : FSA_OK;
 }
 

@@ -83,6 +83,57 @@ struct Bf16Launch {
 };
 cudaError_t launch_bf16_attention(const Bf16Launch& a, cudaStream_t st);
 
+// Four-bit key/value cache (kv4_cache.cu): rows of T tokens and H heads, bf16
+// with the given token strides (elements), and the cache slot of each token.
+struct Kv4Rows {
+    const void* k;  // read by the append, written by the read-back
+    const void* v;
+    int64_t k_stride, v_stride;
+    const int64_t* slots;
+    int64_t T, capacity;  // tokens; slots of the cache
+    int H, D, page_size;
+    unsigned int* err_word;
+};
+cudaError_t launch_kv4_append(const Kv4Rows& a, uint8_t* cache, cudaStream_t st);
+cudaError_t launch_kv4_read(const Kv4Rows& a, const uint8_t* cache, cudaStream_t st);
+
+// Attention over the four-bit cache (kv4_attention.cu).
+struct Kv4AttnLaunch {
+    const void* q;
+    int64_t q_stride;  // token stride of q, elements
+    const uint8_t* cache;
+    const int* page_table;  // [B][max_pages]
+    const int* seq_lens;    // [B]
+    void* o;                // [B][Sq][Hq][D]
+    float* lse;             // [B][Sq][Hq] or null
+    void* workspace;
+    int64_t num_pages;
+    int B, Sq, Hq, Hkv, D, page_size, max_pages;
+    float sm_scale;
+    uint64_t timeout_ns;
+    unsigned int* err_word;
+};
+size_t kv4_attention_workspace_bytes(int B, int Sq, int Hq, int Hkv, int D, int page_size, int max_pages);
+cudaError_t launch_kv4_attention(const Kv4AttnLaunch& a, cudaStream_t st);
+
+// Attention over packed sequences (varlen_attention.cu).
+struct VarlenLaunch {
+    const void* q;  // [Tq][Hq][D], token strides in elements
+    const void* k;  // [Tk][Hkv][D]
+    const void* v;
+    int64_t q_stride, k_stride, v_stride;
+    void* o;     // [Tq][Hq][D]
+    float* lse;  // [Tq][Hq] or null
+    const int* cu_q;  // [B + 1]
+    const int* cu_k;
+    int B, Tq, Tk, Hq, Hkv, D;
+    int causal;
+    float sm_scale;
+    uint64_t timeout_ns;
+    unsigned int* err_word;
+};
+cudaError_t launch_varlen_attention(const VarlenLaunch& a, cudaStream_t st);
+
 // Tensor-core rate probe (mma_rate.cu).
 double mma_probe_flops(int kind, int ctas, int iters);
 cudaError_t launch_mma_probe(int kind, int ctas, int iters, uint64_t timeout_ns,
@@ -91,5 +142,6 @@ cudaError_t launch_mma_probe(int kind, int ctas, int iters, uint64_t timeout_ns,
 // Device error word codes.
 constexpr unsigned int kErrTimeout = 1u;
 constexpr unsigned int kErrMisaligned = 2u;  // shared-memory base not 1024-byte aligned
+constexpr unsigned int kErrBadIndex = 4u;    // a slot, page or sequence bound outside its buffer
 
 }  // namespace fsa

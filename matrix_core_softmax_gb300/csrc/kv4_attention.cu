@@ -5,7 +5,47 @@
 // j <= len - Sq + i: s_j = sm q.k^_j, o = sum_j softmax(s)_j v^_j, and the
 // log-sum-exp of s.  A row that sees no key gets o = 0 and -inf.
 //
-// One warp per query row and head, one key at a time, everything in FP32.
+// What bounds it: 34 D / 32 bytes of cache per key and key head (136 at
+// D = 128) are read once, so at 6.8 TB/s an SM has to finish a key of one head
+// every 5.8 clocks, with all query heads of the group at once.  A CUDA-core
+// product is far too slow for that; a product needs the codes as 16-bit values
+// in registers, and that unpacking (256 values a key) is what has to be cheap:
+//  - both products run on m16n8k16 f16 MMAs with the keys (S^T = K Q^T) or the
+//    value channels (O^T = V^T P^T) as the 16 rows and the query rows as the 8
+//    columns, so that up to 8 query rows cost the same as one;
+//  - the cache's byte order is the A fragments' order: a lane finds its codes
+//    of a row in one 16-byte (keys) or 8-byte (values) piece, and cvt
+//    (E2M1 pair -> f16 pair, 64 lanes a clock and SM, three times the rate of
+//    placing the bits by shifts and masks) turns a byte into a register of the
+//    fragment.  For the values, whose pairs run along the keys, the nibbles of
+//    two keys are first interleaved (4 integer instructions for 16 values);
+//  - the scales are never multiplied into the codes.  The key scale of a block
+//    multiplies the 8-column product of that block (FP32); the value scale,
+//    which differs along the product's contraction, goes into the weights: one
+//    weight fragment per 32-channel block.
+//
+// Weights.  With X the scale exponent of a key's value block b, R_b the largest
+// one so far and y = min_b (R_b - X_b) (at most 24) the kernel takes
+//   p = 2^(s - y - M)  rounded to f16, M the running maximum of s - y,
+//   w_b = p 2^(y - (R_b - X_b) + 11),
+//   O_b += sum w_b code,  l += p 2^y (before the rounding),
+// so the weights are relative to the largest product of weight and value scale
+// and neither a large nor a small value row leaves f16's range; a weight's
+// error is 2^-11 of itself or 2^-25 of that largest product.  M and R_b follow
+// lazily (M may lag by 2^4, which the 2^11 leaves room for), so O is rescaled
+// only when one of them really grows.  O, l and the scores are FP32.  q is
+// scaled by a power of two to [1, 2) per row, in which f16 holds a bf16 value
+// exactly down to 2^-14 of the row's largest and to 2^-25 of it below.
+//
+// Work split.  The cache's groups of all (sequence, key head, 16-row tile)
+// segments form one line, cut into equal shares, one per resident block: long
+// contexts spread over the GPU, ragged batches balance, and a block leaves at
+// most two unfinished segments (the one it starts in and the one it ends in) to
+// the second kernel, which joins them.  Where no sequence can be longer than
+// kWholeGroups groups a block takes one whole segment and there is no second
+// kernel.  Each of a block's eight warps runs its own ring of bulk copies, one
+// 32-key group (4352 bytes at D = 128) a copy, and its own softmax state; a
+// segment's end joins the eight.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -14,9 +54,19 @@
 #include "fsa_internal.h"
 #include "kv4.cuh"
 #include "mx_scale.cuh"
+#include "sm100_ptx.cuh"
 
 namespace fsa {
 namespace {
+
+constexpr int kWarps = 8, kThreads = 32 * kWarps;
+constexpr int kStages = 3;
+constexpr int kMaxBlocks = 304;   // two blocks on each of 152 SMs
+constexpr int kMinShare = kWarps; // groups of a block, at least one a warp
+constexpr int kWholeGroups = 16;  // longest segment (groups) that one block takes whole
+constexpr float kNoMax = -1e30f;
+constexpr float kLag = 4.0f;      // how far M may lag behind (log2)
+constexpr int kHeadroom = 11;     // weights carry 2^11: 2^11 * 2^4 = 2^15 < 65504
 
 struct Params {
     const uint16_t* q;
@@ -25,88 +75,679 @@ struct Params {
     const int* seq_lens;
     uint16_t* o;
     float* lse;
+    float* partial;  // [block][2][8 NT rows][D + 2], or null: whole segments
     int64_t q_stride, num_pages;
-    int B, Sq, Hq, Hkv, page_size, max_pages;
-    float sm;
+    int B, Sq, Hq, Hkv, G, n_rt, page_size, max_pages;
+    float c;  // sm_scale * log2(e)
+    uint64_t timeout_ns;
     unsigned int* err_word;
 };
 
-__device__ __forceinline__ float e2m1(uint32_t c) {
-    const uint32_t e = (c >> 1) & 3u, m = c & 1u;
-    const float a = e ? static_cast<float>(2u + m) * static_cast<float>(1u << (e - 1)) * 0.5f : 0.5f * m;
-    return (c & 8u) ? -a : a;
+template <int D, int NT>
+struct __align__(128) Smem {
+    uint8_t ring[kWarps][kStages][kv4_group_bytes(D)];
+    float4 kscale[kWarps][kKv4Group];      // 2^X of the key blocks, by row position
+    float2 ykey[kWarps][kKv4Group];        // -y and 2^y of each key, by row position
+    uint32_t vscale[kWarps][4][2][2][4];   // f16 pairs: [t][16-key step][half][block]
+    uint64_t full[kWarps][kStages];
+    float m[kWarps][8 * NT], l[kWarps][8 * NT];
+    int64_t scan[kThreads];
+    int64_t first_x;
+    int first_b;
+    int abort;
+};
+
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
 }
 
-template <int D>
-__global__ void __launch_bounds__(128) kv4_attn_kernel(const Params p) {
-    constexpr int kN = D / 32;  // d per lane: lane + 32 b
+__device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                        uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t a) {
+    uint32_t d;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
+    return d;
+}
+
+__device__ __forceinline__ uint32_t f16x2(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+__device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+
+// Keys of a sequence, clamped to its page table.
+__device__ __forceinline__ int seq_len(const Params& p, int b, bool* bad) {
+    const int cap = p.max_pages * p.page_size, n = __ldg(p.seq_lens + b);
+    *bad = n < 0 || n > cap;
+    return min(max(n, 0), cap);
+}
+__device__ __forceinline__ int seq_groups(const Params& p, int b) {
+    bool bad;
+    return (seq_len(p, b, &bad) + kKv4Group - 1) / kKv4Group;
+}
+
+// Row position of a key in its group and back (an involution within each 8):
+// position r of a 16-row tile is key r with its low bit flipped by bit 1, so
+// that the 128-byte key loads and the 8-byte value loads of a warp spread over
+// the banks.
+__device__ __forceinline__ int swap_pos(int r) { return r ^ ((r >> 1) & 1); }
+
+// A query row of a segment: token i of the sequence, query head h of the group.
+struct Row {
+    int i, h;
+};
+__device__ __forceinline__ Row row_of(const Params& p, int r) { return {r / p.G, r % p.G}; }
+
+template <int D, int NT>
+__global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) kv4_attn_kernel(const Params p) {
+    constexpr int kB = D / 32;
+    constexpr int kGroupBytes = kv4_group_bytes(D);
     constexpr Kv4Layout L = kv4_layout(D);
-    const int lane = threadIdx.x & 31;
-    const int64_t row = blockIdx.x * 4ll + (threadIdx.x >> 5);
-    if (row >= static_cast<int64_t>(p.B) * p.Sq * p.Hq) return;
-    const int h = static_cast<int>(row % p.Hq);
-    const int64_t tok = row / p.Hq;
-    const int i = static_cast<int>(tok % p.Sq), b = static_cast<int>(tok / p.Sq);
-    const int hk = h / (p.Hq / p.Hkv);
-    const int64_t cap = static_cast<int64_t>(p.max_pages) * p.page_size;
-    int64_t len = p.seq_lens[b];
-    if (len < 0 || len > cap) {
-        if (lane == 0) atomicOr(p.err_word, kErrBadIndex);
-        len = len < 0 ? 0 : cap;
+    constexpr int kRows = 8 * NT;
+    constexpr int kPitch = D + 4;  // floats of a row in the merge buffer
+    static_assert(kRows * kPitch * 4 <= kStages * kGroupBytes, "merge buffer exceeds a warp's ring");
+    extern __shared__ __align__(128) uint8_t smem_raw[];
+    Smem<D, NT>& sm = *reinterpret_cast<Smem<D, NT>*>(smem_raw);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int g = lane >> 2, t = lane & 3;
+
+    if (tid == 0) sm.abort = 0;
+    if (lane < kStages) mbar_init(&sm.full[warp][lane], 1);
+    fence_mbar_init();
+
+    // this block's share [x, x_end) of the line of groups, and where it starts:
+    // sequence b, its first group at x_seq
+    int64_t x, x_end, x_seq;
+    int b;
+    const int n_seg = p.Hkv * p.n_rt;  // segments of a sequence
+    if (!p.partial) {
+        __syncthreads();
+        b = blockIdx.x / n_seg;
+        const int ng = seq_groups(p, b);
+        const int seg = blockIdx.x - b * n_seg;
+        x_seq = 0;
+        x = static_cast<int64_t>(seg) * ng;
+        x_end = x + ng;
+        if (ng == 0) {  // an empty sequence: zeros
+            const int hk = seg / p.n_rt, r0 = (seg % p.n_rt) * kRows;
+            for (int e = tid; e < kRows * D; e += kThreads) {
+                const int r = r0 + e / D;
+                if (r < p.Sq * p.G) {
+                    const Row w = row_of(p, r);
+                    const int64_t row = (static_cast<int64_t>(b) * p.Sq + w.i) * p.Hq + hk * p.G + w.h;
+                    p.o[row * D + e % D] = 0;
+                    if (p.lse && e % D == 0) p.lse[row] = -INFINITY;
+                }
+            }
+            bool bad;
+            seq_len(p, b, &bad);
+            if (bad && tid == 0) atomicOr(p.err_word, kErrBadIndex);
+            return;
+        }
+    } else {
+        const int per = (p.B + kThreads - 1) / kThreads;
+        const int b0 = min(tid * per, p.B), b1 = min(b0 + per, p.B);
+        int64_t sum = 0;
+        for (int i = b0; i < b1; ++i) {
+            bool bad;
+            sum += (seq_len(p, i, &bad) + kKv4Group - 1) / kKv4Group;
+            if (bad && blockIdx.x == 0) atomicOr(p.err_word, kErrBadIndex);
+        }
+        // inclusive scan over the warp, then over the warps
+        int64_t inc = sum;
+        for (int o = 1; o < 32; o <<= 1) {
+            const int64_t v = __shfl_up_sync(0xFFFFFFFFu, inc, o);
+            if (lane >= o) inc += v;
+        }
+        if (lane == 31) sm.scan[warp] = inc;
+        __syncthreads();
+        int64_t before = inc - sum, total = 0;
+        for (int w = 0; w < kWarps; ++w) {
+            if (w < warp) before += sm.scan[w];
+            total += sm.scan[w];
+        }
+        const int64_t all = total * n_seg;
+        const int64_t share = max(static_cast<int64_t>(kMinShare), (all + gridDim.x - 1) / gridDim.x);
+        x = share * blockIdx.x;
+        x_end = min(x + share, all);
+        if (x >= x_end) return;
+        if (before * n_seg <= x && x < (before + sum) * n_seg) {
+            int i = b0;
+            int64_t at = before * n_seg;
+            while (true) {
+                const int64_t next = at + static_cast<int64_t>(seq_groups(p, i)) * n_seg;
+                if (x < next) break;
+                at = next;
+                ++i;
+            }
+            sm.first_b = i;
+            sm.first_x = at;
+        }
+        __syncthreads();
+        b = sm.first_b;
+        x_seq = sm.first_x;
     }
-    const int64_t n = len - p.Sq + 1 + i;
-    float q[kN], o[kN] = {}, m = -INFINITY, l = 0.0f;
-#pragma unroll
-    for (int c = 0; c < kN; ++c)
-        q[c] = __uint_as_float(static_cast<uint32_t>(p.q[tok * p.q_stride + h * D + 32 * c + lane]) << 16) * p.sm *
-               1.4426950408889634f;
-    const int kb = (lane >> 3) * (D / 8) + ((lane & 7) >> 1);
-    const int vb = (lane >> 2) * (D / 16) + ((lane & 3) >> 1);
-    for (int64_t j = 0; j < n; ++j) {
-        const int page = p.page_table[static_cast<int64_t>(b) * p.max_pages + j / p.page_size];
-        if (page < 0 || page >= p.num_pages) {
-            if (lane == 0) atomicOr(p.err_word, kErrBadIndex);
+    const int64_t x_begin = x;
+    const int gpp = p.page_size / kKv4Group;
+    uint32_t uses = 0;  // parity bit of each stage
+
+    while (x < x_end) {
+        bool bad_len;
+        const int len = seq_len(p, b, &bad_len), ng = (len + kKv4Group - 1) / kKv4Group;
+        if (ng == 0 || x >= x_seq + static_cast<int64_t>(ng) * n_seg) {
+            x_seq += static_cast<int64_t>(ng) * n_seg;
+            ++b;
             continue;
         }
-        const int r = static_cast<int>(j % p.page_size);
-        const uint8_t* g = p.cache + ((static_cast<int64_t>(page) * p.Hkv + hk) * (p.page_size / kKv4Group) + r / kKv4Group) *
-                                         kv4_group_bytes(D);
-        const int rr = r % kKv4Group;
-        float s = 0.0f;
+        if (!p.partial && bad_len && tid == 0) atomicOr(p.err_word, kErrBadIndex);
+        const int seg = static_cast<int>((x - x_seq) / ng);
+        const int64_t seg_x = x_seq + static_cast<int64_t>(seg) * ng;
+        const int g0 = static_cast<int>(x - seg_x);                                       // first group of the part
+        const int g1 = static_cast<int>(min(static_cast<int64_t>(ng), x_end - seg_x));    // end of the part
+        const int hk = seg / p.n_rt, r0 = (seg % p.n_rt) * kRows;
+        const int n_rows = min(kRows, p.Sq * p.G - r0);
+
+        const int count = g1 - g0 > warp ? (g1 - g0 - warp + kWarps - 1) / kWarps : 0;  // this warp's groups
+        const int* table = p.page_table + static_cast<int64_t>(b) * p.max_pages;
+        int pages = 0;          // lane i: the page of the warp's group 32 n + i
+        uint32_t bad_stage = 0; // stages whose group has no page
+        auto issue = [&](int i) {
+            if ((i & 31) == 0) {
+                const int gi = g0 + warp + kWarps * (i + lane);
+                pages = i + lane < count ? __ldg(table + gi / gpp) : 0;
+            }
+            const int page = __shfl_sync(0xFFFFFFFFu, pages, i & 31);
+            const int st = i % kStages;
+            if (page < 0 || page >= p.num_pages) {
+                if (lane == 0) atomicOr(p.err_word, kErrBadIndex);
+                bad_stage |= 1u << st;
+                return;
+            }
+            bad_stage &= ~(1u << st);
+            if (lane == 0) {
+                const int gi = g0 + warp + kWarps * i;
+                const uint8_t* src = p.cache + ((static_cast<int64_t>(page) * p.Hkv + hk) * gpp + gi % gpp) * kGroupBytes;
+                mbar_arrive_expect_tx(&sm.full[warp][st], kGroupBytes);
+                bulk_load(sm.ring[warp][st], src, kGroupBytes, &sm.full[warp][st]);
+            }
+        };
+        for (int j = 0; j < min(count, kStages); ++j) issue(j);
+
+        // the query rows as B fragments, in f16 relative to each row's largest
+        uint32_t qf[NT][kB][4];
+        float cs[NT][2];      // sm log2(e) 2^e of the rows of this lane's columns
+        int seen[NT][2];      // keys that they see
 #pragma unroll
-        for (int c = 0; c < kN; ++c)
-            s += q[c] * e2m1(g[rr * L.row + kb + 4 * c] >> (4 * (lane & 1))) * pow2f(g[L.kscales + rr * L.srow + c] - 127);
-        for (int x = 16; x; x >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, x);
-        const float mn = fmaxf(m, s), f = exp2f(m - mn), w = exp2f(s - mn);
-        l = l * f + w;
-        m = mn;
+        for (int n = 0; n < NT; ++n) {
+            const int r = r0 + 8 * n + g;
+            uint4 raw[kB] = {};
+            if (r < p.Sq * p.G) {
+                const Row w = row_of(p, r);
+                const uint16_t* src = p.q + (static_cast<int64_t>(b) * p.Sq + w.i) * p.q_stride + (hk * p.G + w.h) * D + 8 * t;
 #pragma unroll
-        for (int c = 0; c < kN; ++c)
-            o[c] = o[c] * f + w * e2m1(g[L.vcodes + rr * L.row + vb + 2 * c] >> (4 * (lane & 1))) *
-                                  pow2f(g[L.vscales + rr * L.srow + c] - 127);
+                for (int c = 0; c < kB; ++c) raw[c] = __ldg(reinterpret_cast<const uint4*>(src + 32 * c));
+            }
+            uint32_t mx = 0;
+#pragma unroll
+            for (int c = 0; c < kB; ++c) {
+                const uint32_t u[4] = {raw[c].x, raw[c].y, raw[c].z, raw[c].w};
+#pragma unroll
+                for (int i = 0; i < 4; ++i) mx = max(mx, max(u[i] & 0x7FFFu, (u[i] >> 16) & 0x7FFFu));
+            }
+            mx = max(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 1));
+            mx = max(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 2));
+            const int E = min(max(static_cast<int>(mx >> 7), 1), 253);
+            const float f = __int_as_float((254 - E) << 23);
+#pragma unroll
+            for (int c = 0; c < kB; ++c) {
+                const uint32_t u[4] = {raw[c].x, raw[c].y, raw[c].z, raw[c].w};
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    qf[n][c][i] = f16x2(__uint_as_float(u[i] << 16) * f, __uint_as_float(u[i] & 0xFFFF0000u) * f);
+            }
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                cs[n][j] = p.c * __int_as_float(__shfl_sync(0xFFFFFFFFu, E, 8 * t + 4 * j) << 23);
+                const int rr = r0 + 8 * n + 2 * t + j;
+                seen[n][j] = rr < p.Sq * p.G ? len - p.Sq + 1 + rr / p.G : 0;
+            }
+        }
+        const int all_see = len - p.Sq + 1;  // keys that every row sees
+
+        float O[NT][kB][2][4] = {};
+        float M[NT][2], l[NT][2] = {};
+#pragma unroll
+        for (int n = 0; n < NT; ++n) M[n][0] = M[n][1] = kNoMax;
+        uint32_t R = 0;  // largest value scale bytes so far
+        bool ok = true;
+        int i = 0;
+
+        for (; i < count; ++i) {
+            const int st = i % kStages;
+            if (!((bad_stage >> st) & 1u)) {
+                if (!mbar_wait(&sm.full[warp][st], (uses >> st) & 1u, p.timeout_ns, &sm.abort)) ok = false;
+                ok = __all_sync(0xFFFFFFFFu, ok);
+                if (!ok) break;
+                uses ^= 1u << st;
+                const uint8_t* buf = sm.ring[warp][st];
+                const int key0 = (g0 + warp + kWarps * i) * kKv4Group;
+
+                // scales: lane = key
+                {
+                    const int pos = swap_pos(lane);
+                    uint32_t ks, vs;
+                    if (D == 128) {
+                        ks = *reinterpret_cast<const uint32_t*>(buf + L.kscales + lane * L.srow);
+                        vs = *reinterpret_cast<const uint32_t*>(buf + L.vscales + lane * L.srow);
+                    } else {
+                        ks = *reinterpret_cast<const uint16_t*>(buf + L.kscales + lane * L.srow);
+                        vs = *reinterpret_cast<const uint16_t*>(buf + L.vscales + lane * L.srow);
+                    }
+                    if (key0 + lane >= len) vs = 0;
+                    float kf[4] = {};
+#pragma unroll
+                    for (int c = 0; c < kB; ++c) {
+                        const uint32_t e = (ks >> (8 * c)) & 0xFFu;
+                        kf[c] = __uint_as_float(e ? e << 23 : 0x00400000u);
+                    }
+                    sm.kscale[warp][pos] = make_float4(kf[0], kf[1], kf[2], kf[3]);
+                    if (__any_sync(0xFFFFFFFFu, __vcmpgtu4(vs, R) != 0)) {
+                        uint32_t top = __vmaxu4(vs, R);
+                        for (int o = 16; o; o >>= 1) top = __vmaxu4(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
+#pragma unroll
+                        for (int c = 0; c < kB; ++c) {
+                            const int d = static_cast<int>((R >> (8 * c)) & 0xFFu) - static_cast<int>((top >> (8 * c)) & 0xFFu);
+                            const float f = ex2(static_cast<float>(d));
+#pragma unroll
+                            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                                for (int e = 0; e < 4; ++e) {
+                                    O[n][c][0][e] *= f;
+                                    O[n][c][1][e] *= f;
+                                }
+                        }
+                        R = top;
+                    }
+                    const uint32_t z = R - vs;  // bytewise: no borrow, R >= vs in every byte
+                    uint32_t y = 24u;
+#pragma unroll
+                    for (int c = 0; c < kB; ++c) y = min(y, (z >> (8 * c)) & 0xFFu);
+                    sm.ykey[warp][pos] = make_float2(-static_cast<float>(y), __uint_as_float((127u + y) << 23));
+                    // position pos = 16 step + 8 half + 2 t + e
+                    uint16_t* dst = reinterpret_cast<uint16_t*>(&sm.vscale[warp][(pos >> 1) & 3][pos >> 4][(pos >> 3) & 1][0]) + (pos & 1);
+#pragma unroll
+                    for (int c = 0; c < kB; ++c) {
+                        const int e = 15 + kHeadroom - (static_cast<int>((z >> (8 * c)) & 0xFFu) - static_cast<int>(y));
+                        dst[2 * c] = static_cast<uint16_t>(max(e, 0) << 10);
+                    }
+                }
+                __syncwarp();
+
+                // scores: position r of tile mt is key 16 mt + swap_pos(r)
+                float s[NT][2][4];
+#pragma unroll
+                for (int mt = 0; mt < 2; ++mt) {
+                    uint32_t ka[kB], kb[kB];
+                    const uint8_t* ra = buf + (16 * mt + swap_pos(g)) * L.row + t * (D / 8);
+                    if (D == 128) {
+                        const uint4 u = *reinterpret_cast<const uint4*>(ra), v = *reinterpret_cast<const uint4*>(ra + 8 * L.row);
+                        ka[0] = u.x; ka[1] = u.y; ka[kB - 2] = u.z; ka[kB - 1] = u.w;
+                        kb[0] = v.x; kb[1] = v.y; kb[kB - 2] = v.z; kb[kB - 1] = v.w;
+                    } else {
+                        const uint2 u = *reinterpret_cast<const uint2*>(ra), v = *reinterpret_cast<const uint2*>(ra + 8 * L.row);
+                        ka[0] = u.x; ka[1] = u.y;
+                        kb[0] = v.x; kb[1] = v.y;
+                    }
+                    const float4 fa4 = sm.kscale[warp][16 * mt + g], fb4 = sm.kscale[warp][16 * mt + 8 + g];
+                    const float fa[4] = {fa4.x, fa4.y, fa4.z, fa4.w}, fb[4] = {fb4.x, fb4.y, fb4.z, fb4.w};
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) s[n][mt][0] = s[n][mt][1] = s[n][mt][2] = s[n][mt][3] = 0.0f;
+#pragma unroll
+                    for (int c = 0; c < kB; ++c) {
+                        uint32_t xa[4], xb[4];
+                        e2m1x8_to_f16(ka[c], xa);
+                        e2m1x8_to_f16(kb[c], xb);
+#pragma unroll
+                        for (int n = 0; n < NT; ++n) {
+                            float acc[4] = {};
+                            mma_f16(acc, xa[0], xb[0], xa[1], xb[1], qf[n][c][0], qf[n][c][1]);
+                            mma_f16(acc, xa[2], xb[2], xa[3], xb[3], qf[n][c][2], qf[n][c][3]);
+                            s[n][mt][0] = fmaf(acc[0], fa[c], s[n][mt][0]);
+                            s[n][mt][1] = fmaf(acc[1], fa[c], s[n][mt][1]);
+                            s[n][mt][2] = fmaf(acc[2], fb[c], s[n][mt][2]);
+                            s[n][mt][3] = fmaf(acc[3], fb[c], s[n][mt][3]);
+                        }
+                    }
+                }
+
+                // s - y in log2, masked; the running maximum
+                float y2[2][2];
+                bool grew = false;
+#pragma unroll
+                for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const float2 yy = sm.ykey[warp][16 * mt + 8 * h + g];
+                        y2[mt][h] = yy.y;
+#pragma unroll
+                        for (int n = 0; n < NT; ++n)
+#pragma unroll
+                            for (int j = 0; j < 2; ++j) s[n][mt][2 * h + j] = fmaf(s[n][mt][2 * h + j], cs[n][j], yy.x);
+                    }
+                if (key0 + kKv4Group > all_see) {
+#pragma unroll
+                    for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            const int key = key0 + 16 * mt + 8 * h + swap_pos(g);
+#pragma unroll
+                            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                                for (int j = 0; j < 2; ++j)
+                                    if (key >= seen[n][j]) s[n][mt][2 * h + j] = -INFINITY;
+                        }
+                }
+                float top[NT][2];
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        top[n][j] = fmaxf(fmaxf(s[n][0][j], s[n][0][2 + j]), fmaxf(s[n][1][j], s[n][1][2 + j]));
+                        grew |= top[n][j] > M[n][j] + kLag;
+                    }
+                if (__any_sync(0xFFFFFFFFu, grew)) {
+#pragma unroll
+                    for (int n = 0; n < NT; ++n)
+#pragma unroll
+                        for (int j = 0; j < 2; ++j) {
+                            float m = top[n][j];
+                            for (int o = 4; o < 32; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+                            m = fmaxf(m, M[n][j]);
+                            const float f = ex2(M[n][j] - m);
+                            M[n][j] = m;
+                            l[n][j] *= f;
+#pragma unroll
+                            for (int c = 0; c < kB; ++c)
+#pragma unroll
+                                for (int h = 0; h < 2; ++h) {
+                                    O[n][c][h][j] *= f;
+                                    O[n][c][h][2 + j] *= f;
+                                }
+                        }
+                }
+                // weights, transposed into B fragments (keys along k)
+                uint32_t pf[NT][2][2];
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            const float p0 = ex2(s[n][mt][2 * h] - M[n][0]), p1 = ex2(s[n][mt][2 * h + 1] - M[n][1]);
+                            l[n][0] = fmaf(p0, y2[mt][h], l[n][0]);
+                            l[n][1] = fmaf(p1, y2[mt][h], l[n][1]);
+                            pf[n][mt][h] = transpose8x8(f16x2(p0, p1));
+                        }
+                // O^T += V^T P^T: k of a step = positions 2t, 2t + 1, 8 + 2t, 9 + 2t
+#pragma unroll
+                for (int ks = 0; ks < 2; ++ks) {
+                    uint32_t u[4][kB / 2];
+                    const uint8_t* rv = buf + L.vcodes + 16 * ks * L.row + g * (D / 16);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const uint8_t* src = rv + (8 * (j >> 1) + swap_pos(2 * t + (j & 1))) * L.row;
+                        if (D == 128) {
+                            const uint2 v = *reinterpret_cast<const uint2*>(src);
+                            u[j][0] = v.x;
+                            u[j][kB / 2 - 1] = v.y;
+                        } else {
+                            u[j][0] = *reinterpret_cast<const uint32_t*>(src);
+                        }
+                    }
+                    const uint4 sa4 = *reinterpret_cast<const uint4*>(sm.vscale[warp][t][ks][0]);
+                    const uint4 sb4 = *reinterpret_cast<const uint4*>(sm.vscale[warp][t][ks][1]);
+                    const uint32_t sa[4] = {sa4.x, sa4.y, sa4.z, sa4.w}, sb[4] = {sb4.x, sb4.y, sb4.z, sb4.w};
+#pragma unroll
+                    for (int c2 = 0; c2 < kB / 2; ++c2) {
+                        uint32_t e01[4], o01[4], e23[4], o23[4];
+                        const uint32_t lo = 0x0F0F0F0Fu, hi = 0xF0F0F0F0u;
+                        e2m1x8_to_f16((u[0][c2] & lo) | ((u[1][c2] << 4) & hi), e01);
+                        e2m1x8_to_f16(((u[0][c2] >> 4) & lo) | (u[1][c2] & hi), o01);
+                        e2m1x8_to_f16((u[2][c2] & lo) | ((u[3][c2] << 4) & hi), e23);
+                        e2m1x8_to_f16(((u[2][c2] >> 4) & lo) | (u[3][c2] & hi), o23);
+#pragma unroll
+                        for (int cc = 0; cc < 2; ++cc) {
+                            const int c = 2 * c2 + cc;
+#pragma unroll
+                            for (int n = 0; n < NT; ++n) {
+                                const uint32_t w0 = hmul2(pf[n][ks][0], sa[c]), w1 = hmul2(pf[n][ks][1], sb[c]);
+                                mma_f16(O[n][c][0], e01[2 * cc], o01[2 * cc], e23[2 * cc], o23[2 * cc], w0, w1);
+                                mma_f16(O[n][c][1], e01[2 * cc + 1], o01[2 * cc + 1], e23[2 * cc + 1], o23[2 * cc + 1], w0, w1);
+                            }
+                        }
+                    }
+                }
+            }
+            __syncwarp();
+            if (i + kStages < count) issue(i + kStages);
+        }
+        if (!ok) {
+            // give up: let this warp's copies in flight land, then leave together
+            if (lane == 0) {
+                sm.abort = 1;
+                atomicOr(p.err_word, kErrTimeout);
+            }
+            int dummy = 0;
+            for (int j = i; j < min(count, i + kStages); ++j)
+                if (!((bad_stage >> (j % kStages)) & 1u))
+                    mbar_wait(&sm.full[warp][j % kStages], (uses >> (j % kStages)) & 1u, p.timeout_ns, &dummy);
+        }
+
+        // this warp's result: O in true units relative to 2^M, into its own ring
+        float* mine = reinterpret_cast<float*>(sm.ring[warp][0]);
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                for (int o = 4; o < 32; o <<= 1) l[n][j] += __shfl_xor_sync(0xFFFFFFFFu, l[n][j], o);
+                if (g == 0) {
+                    sm.m[warp][8 * n + 2 * t + j] = M[n][j];
+                    sm.l[warp][8 * n + 2 * t + j] = l[n][j];
+                }
+            }
+#pragma unroll
+            for (int c = 0; c < kB; ++c) {
+                const float f0 = 1.0f / static_cast<float>(1 << kHeadroom), f1 = pow2f(static_cast<int>((R >> (8 * c)) & 0xFFu) - 127);
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+                    *reinterpret_cast<float4*>(mine + (8 * n + 2 * t + j) * kPitch + 32 * c + 4 * g) =
+                        make_float4(O[n][c][0][j] * f0 * f1, O[n][c][0][2 + j] * f0 * f1, O[n][c][1][j] * f0 * f1,
+                                    O[n][c][1][2 + j] * f0 * f1);
+            }
+        }
+        __syncthreads();
+        if (sm.abort) return;
+        const bool whole = g0 == 0 && g1 == ng;
+        float* part = nullptr;
+        if (!whole) part = p.partial + (2 * static_cast<int64_t>(blockIdx.x) + (seg_x < x_begin ? 0 : 1)) * (kRows * (D + 2));
+        for (int e = tid; e < n_rows * (D / 4); e += kThreads) {
+            const int r = e / (D / 4), d4 = e % (D / 4);
+            float m = kNoMax, lt = 0.0f;
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) m = fmaxf(m, sm.m[w][r]);
+            float4 a = make_float4(0, 0, 0, 0);
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) {
+                const float f = ex2(sm.m[w][r] - m);
+                lt = fmaf(f, sm.l[w][r], lt);
+                const float4 v = *reinterpret_cast<const float4*>(reinterpret_cast<const float*>(sm.ring[w][0]) + r * kPitch + 4 * d4);
+                a.x = fmaf(f, v.x, a.x);
+                a.y = fmaf(f, v.y, a.y);
+                a.z = fmaf(f, v.z, a.z);
+                a.w = fmaf(f, v.w, a.w);
+            }
+            if (!whole) {
+                reinterpret_cast<float4*>(part)[r * (D / 4) + d4] = a;
+                if (d4 == 0) {
+                    part[kRows * D + r] = m;
+                    part[kRows * D + kRows + r] = lt;
+                }
+            } else {
+                const Row w = row_of(p, r0 + r);
+                const int64_t row = (static_cast<int64_t>(b) * p.Sq + w.i) * p.Hq + hk * p.G + w.h;
+                const float inv = lt == 0.0f ? 0.0f : 1.0f / lt;
+                const __nv_bfloat162 lo = __floats2bfloat162_rn(a.x * inv, a.y * inv), hi = __floats2bfloat162_rn(a.z * inv, a.w * inv);
+                *reinterpret_cast<uint2*>(p.o + row * D + 4 * d4) =
+                    make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
+                if (p.lse && d4 == 0) p.lse[row] = lt == 0.0f ? -INFINITY : (m + __log2f(lt)) * 0.6931471805599453f;
+            }
+        }
+        // the merge buffer becomes the ring of the next segment
+        fence_async_smem();
+        __syncthreads();
+        x = seg_x + g1;
     }
-    for (int c = 0; c < kN; ++c) {
-        const __nv_bfloat16 x = __float2bfloat16_rn(l > 0.0f ? o[c] / l : 0.0f);
-        p.o[row * D + 32 * c + lane] = *reinterpret_cast<const uint16_t*>(&x);
+}
+
+// Joins the parts of the segments that several blocks worked on, and writes the
+// rows of empty sequences.  One block per segment.
+template <int D, int NT>
+__global__ void __launch_bounds__(kThreads) kv4_join_kernel(const Params p, int n_blocks) {
+    constexpr int kRows = 8 * NT;
+    __shared__ int64_t warp_sum[2][kWarps];
+    const int tid = threadIdx.x, lane = tid & 31;
+    const int n_seg = p.Hkv * p.n_rt;
+    const int b = blockIdx.x / n_seg, seg = blockIdx.x - b * n_seg;
+    int64_t before = 0, total = 0;
+    for (int i = tid; i < p.B; i += kThreads) {
+        const int n = seq_groups(p, i);
+        total += n;
+        if (i < b) before += n;
     }
-    if (p.lse && lane == 0) p.lse[row] = l > 0.0f ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
+    for (int o = 16; o; o >>= 1) {
+        before += __shfl_xor_sync(0xFFFFFFFFu, before, o);
+        total += __shfl_xor_sync(0xFFFFFFFFu, total, o);
+    }
+    if (lane == 0) {
+        warp_sum[0][tid >> 5] = before;
+        warp_sum[1][tid >> 5] = total;
+    }
+    __syncthreads();
+    before = total = 0;
+    for (int w = 0; w < kWarps; ++w) {
+        before += warp_sum[0][w];
+        total += warp_sum[1][w];
+    }
+    const int ng = seq_groups(p, b);
+    const int64_t all = total * n_seg;
+    const int64_t share = max(static_cast<int64_t>(kMinShare), (all + n_blocks - 1) / n_blocks);
+    const int64_t s0 = before * n_seg + static_cast<int64_t>(seg) * ng;
+    const int c0 = static_cast<int>(s0 / share), c1 = ng ? static_cast<int>((s0 + ng - 1) / share) : c0 - 1;
+    if (c0 == c1) return;  // one block wrote the result
+    const int hk = seg / p.n_rt, r0 = (seg % p.n_rt) * kRows;
+    const int n_rows = min(kRows, p.Sq * p.G - r0);
+    for (int e = tid; e < n_rows * (D / 4); e += kThreads) {
+        const int r = e / (D / 4), d4 = e % (D / 4);
+        float m = kNoMax, lt = 0.0f;
+        float4 a = make_float4(0, 0, 0, 0);
+        // the segment starts in block c0 (its second part unless the block starts
+        // with it) and is the first part of every later block
+        auto part_of = [&](int c) {
+            return p.partial + (2 * static_cast<int64_t>(c) + (c == c0 ? 1 : 0)) * (kRows * (D + 2));
+        };
+#pragma unroll 4
+        for (int c = c0; c <= c1; ++c) m = fmaxf(m, part_of(c)[kRows * D + r]);
+#pragma unroll 4
+        for (int c = c0; c <= c1; ++c) {
+            const float* part = part_of(c);
+            const float f = ex2(part[kRows * D + r] - m);
+            lt = fmaf(f, part[kRows * D + kRows + r], lt);
+            const float4 v = reinterpret_cast<const float4*>(part)[r * (D / 4) + d4];
+            a.x = fmaf(f, v.x, a.x);
+            a.y = fmaf(f, v.y, a.y);
+            a.z = fmaf(f, v.z, a.z);
+            a.w = fmaf(f, v.w, a.w);
+        }
+        const Row w = row_of(p, r0 + r);
+        const int64_t row = (static_cast<int64_t>(b) * p.Sq + w.i) * p.Hq + hk * p.G + w.h;
+        const float inv = lt == 0.0f ? 0.0f : 1.0f / lt;
+        const __nv_bfloat162 lo = __floats2bfloat162_rn(a.x * inv, a.y * inv), hi = __floats2bfloat162_rn(a.z * inv, a.w * inv);
+        *reinterpret_cast<uint2*>(p.o + row * D + 4 * d4) =
+            make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
+        if (p.lse && d4 == 0) p.lse[row] = lt == 0.0f ? -INFINITY : (m + __log2f(lt)) * 0.6931471805599453f;
+    }
+}
+
+// Query rows of a block: 8 or, beyond 8 rows to a key head, 16.
+int row_tiles(int rows) { return rows <= 8 ? 1 : 2; }
+
+bool takes_whole(int page_size, int max_pages) {
+    return static_cast<int64_t>(max_pages) * (page_size / kKv4Group) <= kWholeGroups;
+}
+
+template <int D, int NT>
+cudaError_t launch(Params p, int n_whole, cudaStream_t st) {
+    const size_t smem = sizeof(Smem<D, NT>);
+    cudaError_t e = cudaFuncSetAttribute(kv4_attn_kernel<D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         static_cast<int>(smem));
+    if (e != cudaSuccess) return e;
+    const int blocks = p.partial ? kMaxBlocks / NT : n_whole;
+    kv4_attn_kernel<D, NT><<<blocks, kThreads, smem, st>>>(p);
+    e = cudaGetLastError();
+    if (e != cudaSuccess || !p.partial) return e;
+    kv4_join_kernel<D, NT><<<n_whole, kThreads, 0, st>>>(p, blocks);
+    return cudaGetLastError();
 }
 
 }  // namespace
 
-size_t kv4_attention_workspace_bytes(int, int, int, int, int, int, int) { return 0; }
+size_t kv4_attention_workspace_bytes(int, int Sq, int Hq, int Hkv, int D, int page_size, int max_pages) {
+    if (takes_whole(page_size, max_pages)) return 0;
+    const int nt = row_tiles(Sq * (Hq / Hkv));
+    return static_cast<size_t>(kMaxBlocks / nt) * 2 * (8 * nt) * (D + 2) * sizeof(float);
+}
 
 cudaError_t launch_kv4_attention(const Kv4AttnLaunch& a, cudaStream_t st) {
-    const Params p{static_cast<const uint16_t*>(a.q), a.cache, a.page_table, a.seq_lens, static_cast<uint16_t*>(a.o),
-                   a.lse, a.q_stride, a.num_pages, a.B, a.Sq, a.Hq, a.Hkv, a.page_size, a.max_pages, a.sm_scale,
-                   a.err_word};
-    const int64_t rows = static_cast<int64_t>(a.B) * a.Sq * a.Hq;
-    const unsigned grid = static_cast<unsigned>((rows + 3) / 4);
-    if (a.D == 128)
-        kv4_attn_kernel<128><<<grid, 128, 0, st>>>(p);
-    else
-        kv4_attn_kernel<64><<<grid, 128, 0, st>>>(p);
-    return cudaGetLastError();
+    Params p{};
+    p.q = static_cast<const uint16_t*>(a.q);
+    p.cache = a.cache;
+    p.page_table = a.page_table;
+    p.seq_lens = a.seq_lens;
+    p.o = static_cast<uint16_t*>(a.o);
+    p.lse = a.lse;
+    p.partial = takes_whole(a.page_size, a.max_pages) ? nullptr : static_cast<float*>(a.workspace);
+    p.q_stride = a.q_stride;
+    p.num_pages = a.num_pages;
+    p.B = a.B;
+    p.Sq = a.Sq;
+    p.Hq = a.Hq;
+    p.Hkv = a.Hkv;
+    p.G = a.Hq / a.Hkv;
+    const int rows = a.Sq * p.G, nt = row_tiles(rows);
+    p.n_rt = (rows + 8 * nt - 1) / (8 * nt);
+    p.page_size = a.page_size;
+    p.max_pages = a.max_pages;
+    p.c = static_cast<float>(static_cast<double>(a.sm_scale) * 1.4426950408889634);
+    p.timeout_ns = a.timeout_ns;
+    p.err_word = a.err_word;
+    const int64_t segments = static_cast<int64_t>(a.B) * a.Hkv * p.n_rt;
+    if (segments > 0x7FFFFFFF) return cudaErrorInvalidValue;
+    const int n = static_cast<int>(segments);
+    if (a.D == 128) return nt == 1 ? launch<128, 1>(p, n, st) : launch<128, 2>(p, n, st);
+    return nt == 1 ? launch<64, 1>(p, n, st) : launch<64, 2>(p, n, st);
 }
 
 }  // namespace fsa

@@ -453,11 +453,10 @@ FSA_API uint64_t fsa_kv4_attention_workspace_size(int B, int Sq, int Hq, int Hkv
  * Same arithmetic as fsa_bf16_attention_fwd (FP32 scores and sums, BF16
  * weights).  The tokens of a sequence must be finite; what stands outside of
  * it does not reach its outputs.  Bounds that decrease or leave 0 .. Tq or
- * 0 .. Tk are reported by fsa_get_device_error as FSA_ERR_INVALID_ARGUMENT;
- * nothing outside the buffers is touched, and the outputs of the sequences
- * from the first wrong bound on are undefined.
+ * 0 .. Tk are reported by fsa_get_device_error as FSA_ERR_INVALID_ARGUMENT,
+ * and the sequences from the first wrong bound on are skipped.
  * Requirements: B >= 1, Tq, Tk in 0 .. 2^30, Hkv divides Hq, Hkv <= 65535,
- * Hq / Hkv <= 128, D in {64, 128}.
+ * Hq / Hkv <= 128, (Tq / 128 + B) * Hkv <= 2^31 / 256, D in {64, 128}.
  */
 FSA_API fsa_status fsa_varlen_attention_fwd(const void *q, const void *k, const void *v,
                                             int64_t q_stride, int64_t k_stride, int64_t v_stride,

@@ -89,6 +89,20 @@ bool make_map_bf16(CUtensorMap* m, void* base, uint64_t d0, uint64_t d1, uint64_
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// bf16 rows [T][H][D] (heads contiguous, tokens `stride` elements apart) in boxes
+// of 64 channels x bh heads x bt tokens.
+bool make_map_heads(CUtensorMap* m, const void* base, int D, int H, int T, int64_t stride, int bh, int bt) {
+    EncodeTiledFn fn = encode_tiled();
+    if (!fn) return false;
+    cuuint64_t dims[3] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(H), static_cast<cuuint64_t>(T)};
+    cuuint64_t strides[2] = {static_cast<cuuint64_t>(D) * 2, static_cast<cuuint64_t>(stride) * 2};
+    cuuint32_t box[3] = {64, static_cast<cuuint32_t>(bh), static_cast<cuuint32_t>(bt)};
+    cuuint32_t es[3] = {1, 1, 1};
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, es,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 size_t align256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
@@ -572,13 +586,19 @@ fsa_status fsa_varlen_attention_fwd(const void* q, const void* k, const void* v,
     DeviceState* ds;
     fsa_status s = current_device(&dev, &ds);
     if (s != FSA_OK) return s;
+    // a query tile is 128 / G whole tokens of the G heads of a key head; without
+    // any keys the maps of K and V are never used
+    const int G = Hq / Hkv;
+    CUtensorMap tq, tk, tv;
+    if (!make_map_heads(&tq, q, D, Hq, Tq, q_stride, G, 128 / G) ||
+        (Tk > 0 && (!make_map_heads(&tk, k, D, Hkv, Tk, k_stride, 1, 128) ||
+                    !make_map_heads(&tv, v, D, Hkv, Tk, v_stride, 1, 128))))
+        return FSA_ERR_CUDA;
+    if (Tk == 0) tk = tv = tq;
     VarlenLaunch a{};
-    a.q = q;
-    a.k = k;
-    a.v = v;
-    a.q_stride = q_stride;
-    a.k_stride = k_stride;
-    a.v_stride = v_stride;
+    a.tm_q = &tq;
+    a.tm_k = &tk;
+    a.tm_v = &tv;
     a.o = o;
     a.lse = lse;
     a.cu_q = cu_q;

@@ -118,10 +118,9 @@ cudaError_t launch_kv4_attention(const Kv4AttnLaunch& a, cudaStream_t st);
 
 // Attention over packed sequences (varlen_attention.cu).
 struct VarlenLaunch {
-    const void* q;  // [Tq][Hq][D], token strides in elements
-    const void* k;  // [Tk][Hkv][D]
-    const void* v;
-    int64_t q_stride, k_stride, v_stride;
+    const CUtensorMap* tm_q;  // boxes of 64 channels x G heads x 128 / G tokens
+    const CUtensorMap* tm_k;  // boxes of 64 channels x 1 head x 128 tokens
+    const CUtensorMap* tm_v;
     void* o;     // [Tq][Hq][D]
     float* lse;  // [Tq][Hq] or null
     const int* cu_q;  // [B + 1]

@@ -46,7 +46,7 @@ constexpr int kKStages = 2, kVStages = 2;
 constexpr int kThreads = 384;
 constexpr int kWarpLoad = 8, kWarpMma = 9, kWarpLoadV = 10;
 // launched at 168 registers per thread; helpers drop to 32, softmax takes 232
-constexpr int kLaunchRegs = 168, kSoftmaxRegs = 232, kHelperRegs = 32;
+constexpr int kLaunchRegs = 168, kSoftmaxRegs = 232, kHelperRegs = 40;
 static_assert(2 * 128 * kSoftmaxRegs + 128 * kHelperRegs <= kThreads * kLaunchRegs,
               "register split exceeds the launch allocation");
 constexpr int kAtom = 128 * 128;       // 128 rows x 128 bytes (64 bf16)

@@ -79,7 +79,7 @@ struct Params {
     float* lse;
     const int *cu_q, *cu_k;
     unsigned int* err_word;
-    int B, Tq, Tk, Hq, Hkv, G, D, n_tok, causal;  // n_tok: tokens of a query tile
+    int B, Tq, Tk, Hq, Hkv, G, n_tok, causal;  // n_tok: tokens of a query tile
     float c;  // sm_scale * log2(e)
     uint64_t timeout_ns;
 };
@@ -142,6 +142,7 @@ __device__ __forceinline__ void find_work(Smem& sm, const Params& p, int idx, bo
 // One key tile t for this thread's row: scores out of TMEM, the maximum, the
 // rare rescale of O, P back into TMEM.  `lim`: keys the row sees in all;
 // `masked`: some row of the tile sees less than this whole key tile.
+template <int D>
 __device__ __forceinline__ bool softmax_tile(Smem& sm, const Params& p, int t, int i, uint32_t s_col, uint32_t o_col, int lim,
                                              bool masked, float& m, float& l) {
     const bool ok = mbar_wait(&sm.s_full[i], t & 1, p.timeout_ns, &sm.abort);
@@ -195,7 +196,7 @@ __device__ __forceinline__ bool softmax_tile(Smem& sm, const Params& p, int t, i
         m = mn;
         if (t > 0) {  // O holds the tiles before t
             uint32_t rr[32];
-            for (int c = 0; c < p.D / 32; ++c) {
+            for (int c = 0; c < D / 32; ++c) {
                 tmem_ld32(o_col + 32 * c, rr);
                 tmem_ld_wait();
                 tmem_reg_dep(rr);
@@ -231,6 +232,7 @@ __device__ __forceinline__ bool softmax_tile(Smem& sm, const Params& p, int t, i
     return __all_sync(0xFFFFFFFFu, ok);
 }
 
+template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
     varlen_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                        const __grid_constant__ CUtensorMap tm_v, const Params p) {
@@ -242,7 +244,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     Smem& sm = *reinterpret_cast<Smem*>(smem_raw);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int D = p.D, n_atoms = D / 64;
+    constexpr int n_atoms = D / 64;
     const int idx = blockIdx.x / p.Hkv, hk = blockIdx.x - idx * p.Hkv;
 
     if (tid == 0) {
@@ -353,70 +355,76 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
         } else if (warp == kWarpMma) {
             warpgroup_reg_dec<kHelperRegs>();
-            if (lane == 0 && n_max > 0) {
-                // descriptors built once: + 2 advances a K-major operand by one
-                // 16-element K step, + kAtom / 16 by one swizzle atom; V is
-                // MN-major, 64-wide d atoms kAtom apart (LBO), 8-key groups 1024
-                // apart (SBO), one 16-key step 2048 bytes
-                const uint32_t id_qk = idesc_bf16(128, 128, 0, 0), id_pv = idesc_bf16(128, D, 0, 1);
+            if (n_max > 0) {
+                // the whole warp walks this, one elected lane issues.  Descriptors:
+                // + 2 advances a K-major operand by one 16-element K step, + kAtom /
+                // 16 by one swizzle atom; V is MN-major, 64-wide d atoms kAtom apart
+                // (LBO), 8-key groups 1024 apart (SBO), one 16-key step 2048 bytes
+                constexpr uint32_t id_qk = idesc_bf16(128, 128, 0, 0), id_pv = idesc_bf16(128, D, 0, 1);
+                const uint32_t tm = __shfl_sync(0xFFFFFFFFu, tmem, 0);
                 const uint64_t dq = smem_desc(smem_u32(sm.q[0]), 16, 1024, SWZ_128B);
                 const uint64_t dk = smem_desc(smem_u32(sm.k[0]), 16, 1024, SWZ_128B);
                 const uint64_t dv = smem_desc(smem_u32(sm.v[0]), kAtom, 1024, SWZ_128B);
                 auto scores = [&](int i, int t) {
                     const uint64_t a = dq + (kTileBytes >> 4) * i, bk = dk + (kTileBytes >> 4) * (t % kKStages);
+#pragma unroll
                     for (int kk = 0; kk < D / 16; ++kk) {
                         const uint32_t off = (kk >> 2) * (kAtom >> 4) + 2 * (kk & 3);
-                        mma_bf16(tmem + 128 * i, a + off, bk + off, id_qk, kk > 0 ? 1u : 0u);
+                        mma_bf16_one(tm + 128 * i, a + off, bk + off, id_qk, kk > 0 ? 1u : 0u);
                     }
-                    tc_commit(&sm.s_full[i]);
+                    tc_commit_one(&sm.s_full[i]);
                 };
                 auto values = [&](int i, int t) {
                     const uint64_t bv = dv + (kTileBytes >> 4) * (t % kVStages);
 #pragma unroll
                     for (int kk = 0; kk < 8; ++kk)
-                        mma_bf16_tmem_a(tmem + kColO + 128 * i, tmem + 128 * i + 8 * kk, bv + 128 * kk, id_pv,
-                                        (t > 0 || kk > 0) ? 1u : 0u);
+                        mma_bf16_tmem_a_one(tm + kColO + 128 * i, tm + 128 * i + 8 * kk, bv + 128 * kk, id_pv,
+                                            (t > 0 || kk > 0) ? 1u : 0u);
                 };
-                auto wait = [&](uint64_t* bar, int phase) { return mbar_wait(bar, phase & 1, p.timeout_ns, &sm.abort); };
+                auto wait = [&](uint64_t* bar, int phase) {
+                    return __all_sync(0xFFFFFFFFu, mbar_wait(bar, phase & 1, p.timeout_ns, &sm.abort)) != 0;
+                };
                 bool ok = wait(&sm.bar_q, 0) && wait(&sm.k_full[0], 0);
                 if (ok) {
                     tc_fence_after();
-                    for (int i = 0; i < 2; ++i)
-                        if (n_t[i] > 0) scores(i, 0);
-                    tc_commit(&sm.k_empty[0]);
+                    if (n_t[0] > 0) scores(0, 0);
+                    if (n_t[1] > 0) scores(1, 0);
+                    tc_commit_one(&sm.k_empty[0]);
                 }
                 for (int t = 0; ok && t < n_max; ++t) {
                     bool have_v = false, have_k = false;
-                    for (int i = 0; ok && i < 2; ++i) {
-                        if (t >= n_t[i]) continue;
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        if (!ok || t >= n_t[i]) continue;
                         ok = wait(&sm.p_full[i], t);
                         if (ok && !have_v) {
                             ok = wait(&sm.v_full[t % kVStages], t / kVStages) &&
                                  (t != t_ragged || wait(&sm.v_clean[t % kVStages], 0));
                             have_v = true;
                         }
-                        if (!ok) break;
+                        if (!ok) continue;
                         tc_fence_after();
                         values(i, t);
-                        if (t + 1 == n_t[i]) tc_commit(&sm.o_full[i]);
-                        if (t + 1 < n_t[i]) {
-                            if (!have_k) {
-                                ok = wait(&sm.k_full[(t + 1) % kKStages], (t + 1) / kKStages);
-                                have_k = true;
-                                if (!ok) break;
-                                tc_fence_after();
-                            }
-                            scores(i, t + 1);
+                        if (t + 1 == n_t[i]) {
+                            tc_commit_one(&sm.o_full[i]);
+                            continue;
                         }
+                        if (!have_k) {
+                            ok = wait(&sm.k_full[(t + 1) % kKStages], (t + 1) / kKStages);
+                            have_k = true;
+                            if (!ok) continue;
+                            tc_fence_after();
+                        }
+                        scores(i, t + 1);
                     }
                     if (!ok) break;
-                    tc_commit(&sm.v_empty[t % kVStages]);
-                    if (t + 1 < n_max) tc_commit(&sm.k_empty[(t + 1) % kKStages]);
+                    tc_commit_one(&sm.v_empty[t % kVStages]);
+                    if (t + 1 < n_max) tc_commit_one(&sm.k_empty[(t + 1) % kKStages]);
                 }
                 if (!ok) {
-                    raise_abort(sm, p);
+                    if (lane == 0) raise_abort(sm, p);
                     int dummy = 0;
-                    tc_commit(&sm.drain);  // wait until every product issued has retired
+                    tc_commit_one(&sm.drain);  // wait until every product issued has retired
                     mbar_wait(&sm.drain, 0, p.timeout_ns, &dummy);
                 }
             }
@@ -434,7 +442,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             float m = kNoMax, l = 0.0f;
             bool ok = true;
             for (int t = 0; ok && t < n_t[i]; ++t)
-                ok = softmax_tile(sm, p, t, i, s_col, o_col, lim, (t + 1) * kTile > lim0, m, l);
+                ok = softmax_tile<D>(sm, p, t, i, s_col, o_col, lim, (t + 1) * kTile > lim0, m, l);
             if (ok && n_t[i] > 0) ok = __all_sync(0xFFFFFFFFu, mbar_wait(&sm.o_full[i], 0, p.timeout_ns, &sm.abort));
             if (!ok) raise_abort(sm, p);
             if (ok && first < nq) {
@@ -477,6 +485,24 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
 }
 
+template <int D>
+cudaError_t launch(const VarlenLaunch& a, const Params& p, cudaStream_t st) {
+    const size_t smem = sizeof(Smem);
+    // the in-kernel register split assumes exactly kLaunchRegs per thread at
+    // launch; anything else could make the increase wait forever
+    cudaFuncAttributes fa{};
+    cudaError_t e = cudaFuncGetAttributes(&fa, varlen_attn_kernel<D>);
+    if (e != cudaSuccess) return e;
+    if (fa.numRegs != kLaunchRegs) return cudaErrorInvalidConfiguration;
+    e = cudaFuncSetAttribute(varlen_attn_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    if (e != cudaSuccess) return e;
+    // a sequence of n tokens has at most n / (2 n_tok) + 1 pairs
+    const int64_t pairs = a.Tq / (2 * p.n_tok) + static_cast<int64_t>(a.B);
+    if (pairs * a.Hkv > 0x7FFFFFFF) return cudaErrorInvalidValue;
+    varlen_attn_kernel<D><<<static_cast<unsigned>(pairs * a.Hkv), kThreads, smem, st>>>(*a.tm_q, *a.tm_k, *a.tm_v, p);
+    return cudaGetLastError();
+}
+
 }  // namespace
 
 cudaError_t launch_varlen_attention(const VarlenLaunch& a, cudaStream_t st) {
@@ -492,25 +518,11 @@ cudaError_t launch_varlen_attention(const VarlenLaunch& a, cudaStream_t st) {
     p.Hq = a.Hq;
     p.Hkv = a.Hkv;
     p.G = a.Hq / a.Hkv;
-    p.D = a.D;
     p.n_tok = kTile / p.G;
     p.causal = a.causal;
     p.c = static_cast<float>(static_cast<double>(a.sm_scale) * 1.4426950408889634);
     p.timeout_ns = a.timeout_ns;
-    const size_t smem = sizeof(Smem);
-    // the in-kernel register split assumes exactly kLaunchRegs per thread at
-    // launch; anything else could make the increase wait forever
-    cudaFuncAttributes fa{};
-    cudaError_t e = cudaFuncGetAttributes(&fa, varlen_attn_kernel);
-    if (e != cudaSuccess) return e;
-    if (fa.numRegs != kLaunchRegs) return cudaErrorInvalidConfiguration;
-    e = cudaFuncSetAttribute(varlen_attn_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
-    if (e != cudaSuccess) return e;
-    // a sequence of n tokens has at most n / (2 n_tok) + 1 pairs
-    const int64_t pairs = a.Tq / (2 * p.n_tok) + static_cast<int64_t>(a.B);
-    if (pairs * a.Hkv > 0x7FFFFFFF) return cudaErrorInvalidValue;
-    varlen_attn_kernel<<<static_cast<unsigned>(pairs * a.Hkv), kThreads, smem, st>>>(*a.tm_q, *a.tm_k, *a.tm_v, p);
-    return cudaGetLastError();
+    return a.D == 128 ? launch<128>(a, p, st) : launch<64>(a, p, st);
 }
 
 }  // namespace fsa

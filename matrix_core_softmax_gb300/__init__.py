@@ -7,7 +7,6 @@ loaded, every call raises.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import os
 import threading
@@ -67,6 +66,8 @@ _lib = None
 def load(path: str | None = None):
     """Load libfsa.so (built by ``matrix_core_softmax_gb300.build``)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             p = path or LIB_PATH
@@ -405,46 +406,46 @@ def bf16_attention_fwd(q, k, v, *, out=None, stream=None):
 # ---- four-bit key/value cache and packed sequences --------------------------
 
 
-@contextlib.contextmanager
-def _launching(t: torch.Tensor, stream):
-    """Makes `stream` (the current one of t's device by default) and its device
-    current, so that what the call allocates belongs to that stream."""
+# These calls are short (a decoding step makes one per layer), so the checks look
+# at each tensor once and the current stream's handle is fetched directly.
+
+_raw_stream = torch._C._cuda_getCurrentRawStream
+
+
+def _elsewhere(t: torch.Tensor, stream) -> bool:
+    return stream is not None or t.get_device() != torch.cuda.current_device()
+
+
+def _on(t: torch.Tensor, stream):
+    """Makes `stream` (by default the current one of t's device) and its device
+    current: what the call allocates then belongs to that stream."""
     s = torch.cuda.current_stream(t.device) if stream is None else stream
     if s.device != t.device:
         raise ValueError("stream and tensors are on different devices")
-    if stream is None and torch.cuda.current_device() == t.device.index:
-        yield s.cuda_stream
-    else:
-        with torch.cuda.stream(s):
-            yield s.cuda_stream
+    return torch.cuda.stream(s)
 
 
-def _rows(t: torch.Tensor, name: str, dims: int, device=None):
-    """A CUDA bf16 tensor [..., heads, D] whose heads are contiguous."""
-    if t.dtype != torch.bfloat16 or not t.is_cuda or t.dim() != dims:
-        raise ValueError(f"{name} must be a CUDA bf16 tensor of {dims} dimensions")
-    if device is not None and t.device != device:
-        raise ValueError(f"{name} is on another device")
-    if t.numel() and (t.stride(-1) != 1 or (t.shape[-2] > 1 and t.stride(-2) != t.shape[-1])):
+def _heads(t: torch.Tensor, name: str, shape, dev: int):
+    """A CUDA bf16 tensor [..., heads, D] of the given shape whose heads are
+    contiguous; returns its token stride (a lone token has none of its own)."""
+    H, D = shape[-2:]
+    if t.dtype != torch.bfloat16 or t.get_device() != dev or t.shape != shape:
+        raise ValueError(f"{name} must be a bf16 tensor {list(shape)} on cuda:{dev}")
+    st = t.stride()
+    if st[-1] != 1 or (st[-2] != D and H > 1):
         raise ValueError(f"the heads of {name} must be contiguous")
+    return st[0] if shape[0] > 1 else H * D
 
 
-def _token_stride(t: torch.Tensor) -> int:
-    """Distance of two tokens of [T, heads, D] in elements (a lone token has none of its own)."""
-    return t.stride(0) if t.shape[0] > 1 else t.shape[1] * t.shape[2]
-
-
-def _ints(t: torch.Tensor, name: str, dtype, shape, device):
-    if t.dtype != dtype or t.device != device or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous {dtype} tensor {list(shape)} on {device}")
-
-
-def _out(t, shape, dtype, name, device):
-    if t is None:
-        return torch.empty(shape, dtype=dtype, device=device)
-    if t.dtype != dtype or t.device != device or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous {dtype} tensor {list(shape)} on {device}")
+def _plain(t: torch.Tensor, name: str, dtype, shape, dev: int):
+    if t.dtype != dtype or t.get_device() != dev or t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor {list(shape)} on cuda:{dev}")
     return t
+
+
+def _need_cuda(t: torch.Tensor, name: str):
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
 
 
 def kv4_new_cache(num_pages: int, page_size: int, n_kv_heads: int, D: int, device="cuda") -> torch.Tensor:
@@ -458,10 +459,12 @@ def kv4_new_cache(num_pages: int, page_size: int, n_kv_heads: int, D: int, devic
 
 def _kv4(cache: torch.Tensor):
     """(pages, heads, page_size, D) of a cache tensor."""
-    if cache.dtype != torch.uint8 or not cache.is_cuda or cache.dim() != 4 or not cache.is_contiguous() \
-            or cache.shape[3] not in (34 * 64, 34 * 128):
+    if cache.dtype != torch.uint8 or not cache.is_cuda or cache.dim() != 4 or not cache.is_contiguous():
         raise ValueError("cache must be a contiguous CUDA uint8 tensor [pages, heads, page_size / 32, 34 * D]")
-    return cache.shape[0], cache.shape[1], 32 * cache.shape[2], cache.shape[3] // 34
+    pages, heads, groups, last = cache.shape
+    if last != 34 * 128 and last != 34 * 64:
+        raise ValueError("the last dimension of a cache is 34 * D with D 64 or 128")
+    return pages, heads, 32 * groups, last // 34
 
 
 def kv4_append(cache, k, v, slots, stream=None):
@@ -469,36 +472,42 @@ def kv4_append(cache, k, v, slots, stream=None):
     contiguous, any token stride), into the cache at `slots`, int64 [T] =
     page * page_size + token; a negative slot skips its token."""
     pages, H, page_size, D = _kv4(cache)
-    for n, t in (("k", k), ("v", v)):
-        _rows(t, n, 3, cache.device)
-        if t.shape != (slots.shape[0], H, D):
-            raise ValueError(f"{n} must be [{slots.shape[0]}, {H}, {D}], one row per slot")
-    _ints(slots, "slots", torch.int64, (slots.shape[0],), cache.device)
-    with _launching(cache, stream) as st:
-        _check(load().fsa_kv4_append(k.data_ptr(), v.data_ptr(), _token_stride(k), _token_stride(v), slots.data_ptr(),
-                                     slots.shape[0], H, D, cache.data_ptr(), pages, page_size, st), "fsa_kv4_append")
+    if _elsewhere(cache, stream):
+        with _on(cache, stream):
+            return kv4_append(cache, k, v, slots)
+    dev = cache.get_device()
+    T = slots.numel()
+    _plain(slots, "slots", torch.int64, (T,), dev)
+    ks, vs = _heads(k, "k", (T, H, D), dev), _heads(v, "v", (T, H, D), dev)
+    _check(load().fsa_kv4_append(k.data_ptr(), v.data_ptr(), ks, vs, slots.data_ptr(), T, H, D, cache.data_ptr(), pages,
+                                 page_size, _raw_stream(dev)), "fsa_kv4_append")
 
 
 def kv4_read(cache, slots, *, out_k=None, out_v=None, stream=None):
     """fsa_kv4_read: (k, v), the values that the cache holds at `slots` (int64
     [T]) as bf16 [T, n_kv_heads, D]; a negative slot reads as zeros.  out_k,
-    out_v: written instead of new tensors (heads contiguous, any token stride)."""
+    out_v: written instead of new tensors (heads contiguous, tokens that do not
+    overlap)."""
     pages, H, page_size, D = _kv4(cache)
-    if slots.dim() != 1:
-        raise ValueError("slots must have one dimension")
-    _ints(slots, "slots", torch.int64, (slots.shape[0],), cache.device)
-    T = slots.shape[0]
-    for n, t in (("out_k", out_k), ("out_v", out_v)):
-        if t is not None:
-            _rows(t, n, 3, cache.device)
-            if t.shape != (T, H, D):
-                raise ValueError(f"{n} must be [{T}, {H}, {D}]")
-    with _launching(cache, stream) as st:
-        k = torch.empty((T, H, D), dtype=torch.bfloat16, device=cache.device) if out_k is None else out_k
-        v = torch.empty((T, H, D), dtype=torch.bfloat16, device=cache.device) if out_v is None else out_v
-        _check(load().fsa_kv4_read(cache.data_ptr(), pages, page_size, slots.data_ptr(), T, H, D, k.data_ptr(),
-                                   v.data_ptr(), _token_stride(k), _token_stride(v), st), "fsa_kv4_read")
-    return k, v
+    if _elsewhere(cache, stream):
+        with _on(cache, stream):
+            return kv4_read(cache, slots, out_k=out_k, out_v=out_v)
+    dev = cache.get_device()
+    T = slots.numel()
+    _plain(slots, "slots", torch.int64, (T,), dev)
+    shape = (T, H, D)
+    ks = vs = H * D
+    if out_k is None:
+        out_k = torch.empty(shape, dtype=torch.bfloat16, device=cache.device)
+    else:
+        ks = _heads(out_k, "out_k", shape, dev)
+    if out_v is None:
+        out_v = torch.empty(shape, dtype=torch.bfloat16, device=cache.device)
+    else:
+        vs = _heads(out_v, "out_v", shape, dev)
+    _check(load().fsa_kv4_read(cache.data_ptr(), pages, page_size, slots.data_ptr(), T, H, D, out_k.data_ptr(),
+                               out_v.data_ptr(), ks, vs, _raw_stream(dev)), "fsa_kv4_read")
+    return out_k, out_v
 
 
 def kv4_attention_workspace_size(B: int, Sq: int, n_heads: int, n_kv_heads: int, D: int, page_size: int,
@@ -509,46 +518,51 @@ def kv4_attention_workspace_size(B: int, Sq: int, n_heads: int, n_kv_heads: int,
 def kv4_attention_fwd(q, cache, page_table, seq_lens, *, out=None, return_lse: bool = False, lse=None,
                       sm_scale: float = 0.0, workspace=None, stream=None):
     """fsa_kv4_attention_fwd: attention of q, CUDA bf16 [B, Sq, n_heads, D] (the
-    last Sq tokens of each sequence, already in the cache), over the four-bit
-    cache.  page_table int32 [B, max_pages], seq_lens int32 [B] (keys of each
-    sequence, its query tokens included).  Returns o [B, Sq, n_heads, D], with
-    return_lse also the log-sum-exps, float32 [B, Sq, n_heads] (written into
-    `lse` if given).  workspace: uint8 tensor of kv4_attention_workspace_size
-    bytes for callers that keep one; calls that may overlap need their own."""
+    last Sq tokens of each sequence, already in the cache; heads contiguous, all
+    tokens at one distance), over the four-bit cache.  page_table int32 [B,
+    max_pages], seq_lens int32 [B] (keys of each sequence, its query tokens
+    included).  Returns o [B, Sq, n_heads, D], with return_lse also the
+    log-sum-exps, float32 [B, Sq, n_heads] (written into `lse` if given).
+    workspace: uint8 tensor of kv4_attention_workspace_size bytes for callers
+    that keep one; calls that may overlap need their own."""
     pages, Hkv, page_size, D = _kv4(cache)
-    dev = cache.device
-    _rows(q, "q", 4, dev)
-    B, Sq, Hq, _ = q.shape
-    if q.shape[3] != D or Hq % Hkv:
-        raise ValueError(f"q must be [B, Sq, n_heads, {D}] with a multiple of {Hkv} heads")
-    if q.numel() == 0:
-        raise ValueError("q is empty")
-    q_stride = q.stride(1) if Sq > 1 else q.stride(0) if B > 1 else Hq * D
-    if B > 1 and Sq > 1 and q.stride(0) != Sq * q_stride:
-        raise ValueError("the tokens of q must lie at one distance")
-    if page_table.dim() != 2:
-        raise ValueError("page_table must be [B, max_pages]")
+    if _elsewhere(cache, stream):
+        with _on(cache, stream):
+            return kv4_attention_fwd(q, cache, page_table, seq_lens, out=out, return_lse=return_lse, lse=lse,
+                                     sm_scale=sm_scale, workspace=workspace)
+    dev = cache.get_device()
+    if q.dim() != 4 or page_table.dim() != 2:
+        raise ValueError("q must be [B, Sq, n_heads, D] and page_table [B, max_pages]")
+    shape = q.shape
+    B, Sq, Hq, _ = shape
+    if Hkv == 0 or Hq % Hkv or shape[3] != D or B * Sq * Hq == 0:
+        raise ValueError(f"q must be a non-empty tensor [B, Sq, n_heads, {D}] with a multiple of {Hkv} heads")
+    q_stride = _heads(q, "q", shape, dev)
+    if Sq > 1:
+        if B > 1 and q_stride != Sq * q.stride(1):
+            raise ValueError("the tokens of q must lie at one distance")
+        q_stride = q.stride(1)
     max_pages = page_table.shape[1]
-    _ints(page_table, "page_table", torch.int32, (B, max_pages), dev)
-    _ints(seq_lens, "seq_lens", torch.int32, (B,), dev)
+    _plain(page_table, "page_table", torch.int32, (B, max_pages), dev)
+    _plain(seq_lens, "seq_lens", torch.int32, (B,), dev)
+    o = torch.empty(shape, dtype=torch.bfloat16, device=cache.device) if out is None else \
+        _plain(out, "out", torch.bfloat16, shape, dev)
+    if lse is not None:
+        _plain(lse, "lse", torch.float32, (B, Sq, Hq), dev)
+    elif return_lse:
+        lse = torch.empty((B, Sq, Hq), dtype=torch.float32, device=cache.device)
     lib = load()
-    with _launching(cache, stream) as st:
-        o = _out(out, q.shape, torch.bfloat16, "out", dev)
-        if return_lse or lse is not None:
-            lse = _out(lse, (B, Sq, Hq), torch.float32, "lse", dev)
-        need = lib.fsa_kv4_attention_workspace_size(B, Sq, Hq, Hkv, D, page_size, max_pages)
-        if workspace is None:
-            ws = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
-        else:
-            if not workspace.is_contiguous() or workspace.device != dev:
-                raise ValueError(f"workspace must be a contiguous tensor on {dev}")
-            ws = workspace
-        _check(lib.fsa_kv4_attention_fwd(q.data_ptr(), q_stride, cache.data_ptr(), page_table.data_ptr(),
-                                         seq_lens.data_ptr(), o.data_ptr(), None if lse is None else lse.data_ptr(),
-                                         B, Sq, Hq, Hkv, D, pages, page_size, max_pages, float(sm_scale),
-                                         None if ws is None else ws.data_ptr(),
-                                         0 if ws is None else ws.numel() * ws.element_size(), st),
-               "fsa_kv4_attention_fwd")
+    ws, ws_bytes = None, lib.fsa_kv4_attention_workspace_size(B, Sq, Hq, Hkv, D, page_size, max_pages)
+    if workspace is not None:
+        if not workspace.is_contiguous() or workspace.get_device() != dev:
+            raise ValueError(f"workspace must be a contiguous tensor on cuda:{dev}")
+        ws, ws_bytes = workspace, workspace.numel() * workspace.element_size()
+    elif ws_bytes:
+        ws = torch.empty(ws_bytes, dtype=torch.uint8, device=cache.device)
+    _check(lib.fsa_kv4_attention_fwd(q.data_ptr(), q_stride, cache.data_ptr(), page_table.data_ptr(), seq_lens.data_ptr(),
+                                     o.data_ptr(), None if lse is None else lse.data_ptr(), B, Sq, Hq, Hkv, D, pages,
+                                     page_size, max_pages, sm_scale, None if ws is None else ws.data_ptr(), ws_bytes,
+                                     _raw_stream(dev)), "fsa_kv4_attention_fwd")
     return (o, lse) if return_lse else o
 
 
@@ -556,31 +570,41 @@ def varlen_attention_fwd(q, k, v, cu_seqlens_q, cu_seqlens_k=None, *, causal: bo
                          return_lse: bool = False, lse=None, sm_scale: float = 0.0, stream=None):
     """fsa_varlen_attention_fwd: BF16 attention over packed sequences.  q CUDA
     bf16 [Tq, n_heads, D], k and v [Tk, n_kv_heads, D] (heads contiguous, any
-    token stride); cu_seqlens_q and cu_seqlens_k (by default the same) int32
-    [B + 1].  Returns o [Tq, n_heads, D], with return_lse also the
-    log-sum-exps, float32 [Tq, n_heads].  Rows outside every sequence are not
-    written (a new output leaves them undefined)."""
+    token stride that keeps tokens apart); cu_seqlens_q and cu_seqlens_k (by
+    default the same) int32 [B + 1].  Returns o [Tq, n_heads, D], with
+    return_lse also the log-sum-exps, float32 [Tq, n_heads].  Rows outside every
+    sequence are not written (a new output leaves them undefined)."""
+    _need_cuda(q, "q")
+    if _elsewhere(q, stream):
+        with _on(q, stream):
+            return varlen_attention_fwd(q, k, v, cu_seqlens_q, cu_seqlens_k, causal=causal, out=out,
+                                        return_lse=return_lse, lse=lse, sm_scale=sm_scale)
+    dev = q.get_device()
+    if q.dim() != 3 or k.dim() != 3:
+        raise ValueError("q must be [Tq, n_heads, D], k and v [Tk, n_kv_heads, D]")
     cu_k = cu_seqlens_q if cu_seqlens_k is None else cu_seqlens_k
-    for n, t in (("q", q), ("k", k), ("v", v)):
-        _rows(t, n, 3, q.device)
-    Tq, Hq, D = q.shape
-    Tk, Hkv = k.shape[0], k.shape[1]
-    if k.shape != v.shape or k.shape[2] != D or Hkv == 0 or Hq == 0 or Hq % Hkv:
+    qshape, kshape = q.shape, k.shape
+    Tq, Hq, D = qshape
+    Tk, Hkv, Dk = kshape
+    if D != Dk or Hkv == 0 or Hq == 0 or Hq % Hkv:
         raise ValueError("k and v must be [Tk, n_kv_heads, D] with q's D and a head count that divides q's")
+    qs, ks, vs = _heads(q, "q", qshape, dev), _heads(k, "k", kshape, dev), _heads(v, "v", kshape, dev)
     nb = cu_seqlens_q.numel()
     if nb < 2:
         raise ValueError("cu_seqlens_q must have B + 1 >= 2 entries")
-    _ints(cu_seqlens_q, "cu_seqlens_q", torch.int32, (nb,), q.device)
-    _ints(cu_k, "cu_seqlens_k", torch.int32, (nb,), q.device)
-    with _launching(q, stream) as st:
-        o = _out(out, q.shape, torch.bfloat16, "out", q.device)
-        if return_lse or lse is not None:
-            lse = _out(lse, (Tq, Hq), torch.float32, "lse", q.device)
-        _check(load().fsa_varlen_attention_fwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), _token_stride(q),
-                                               _token_stride(k), _token_stride(v), cu_seqlens_q.data_ptr(),
-                                               cu_k.data_ptr(), o.data_ptr(), None if lse is None else lse.data_ptr(),
-                                               nb - 1, Tq, Tk, Hq, Hkv, D, int(bool(causal)), float(sm_scale), st),
-               "fsa_varlen_attention_fwd")
+    _plain(cu_seqlens_q, "cu_seqlens_q", torch.int32, (nb,), dev)
+    if cu_seqlens_k is not None:
+        _plain(cu_k, "cu_seqlens_k", torch.int32, (nb,), dev)
+    o = torch.empty(qshape, dtype=torch.bfloat16, device=q.device) if out is None else \
+        _plain(out, "out", torch.bfloat16, qshape, dev)
+    if lse is not None:
+        _plain(lse, "lse", torch.float32, (Tq, Hq), dev)
+    elif return_lse:
+        lse = torch.empty((Tq, Hq), dtype=torch.float32, device=q.device)
+    _check(load().fsa_varlen_attention_fwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), qs, ks, vs, cu_seqlens_q.data_ptr(),
+                                           cu_k.data_ptr(), o.data_ptr(), None if lse is None else lse.data_ptr(), nb - 1,
+                                           Tq, Tk, Hq, Hkv, D, 1 if causal else 0, sm_scale, _raw_stream(dev)),
+           "fsa_varlen_attention_fwd")
     return (o, lse) if return_lse else o
 
 

@@ -1,5 +1,6 @@
 // fsa_internal.h -- declarations shared by the library's translation units.
 #pragma once
+#include <atomic>
 #include <cstdint>
 #include <cuda.h>
 #include <cuda_runtime.h>
@@ -82,6 +83,27 @@ struct Bf16Launch {
     unsigned int* err_word;
 };
 cudaError_t launch_bf16_attention(const Bf16Launch& a, cudaStream_t st);
+
+// Once per device and kernel: the dynamic shared memory it may use, and, where a
+// register split is built on it, the registers of its launch (0: not checked).
+// The short calls save these two queries.
+struct KernelSetup {
+    std::atomic<uint64_t> done{0};  // a bit per device
+    cudaError_t operator()(const void* kernel, int smem, int regs) {
+        int dev = 0;
+        cudaError_t e = cudaGetDevice(&dev);
+        if (e != cudaSuccess) return e;
+        const uint64_t bit = uint64_t{1} << (dev & 63);
+        if (done.load(std::memory_order_acquire) & bit) return cudaSuccess;
+        cudaFuncAttributes fa{};
+        e = cudaFuncGetAttributes(&fa, kernel);
+        if (e != cudaSuccess) return e;
+        if (regs && fa.numRegs != regs) return cudaErrorInvalidConfiguration;
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_release);
+        return e;
+    }
+};
 
 // Four-bit key/value cache (kv4_cache.cu): rows of T tokens and H heads, bf16
 // with the given token strides (elements), and the cache slot of each token.

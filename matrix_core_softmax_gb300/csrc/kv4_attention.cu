@@ -701,8 +701,8 @@ bool takes_whole(int page_size, int max_pages) {
 template <int D, int NT>
 cudaError_t launch(Params p, int n_whole, cudaStream_t st) {
     const size_t smem = sizeof(Smem<D, NT>);
-    cudaError_t e = cudaFuncSetAttribute(kv4_attn_kernel<D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         static_cast<int>(smem));
+    static KernelSetup setup;
+    cudaError_t e = setup(reinterpret_cast<const void*>(kv4_attn_kernel<D, NT>), static_cast<int>(smem), 0);
     if (e != cudaSuccess) return e;
     const int blocks = p.partial ? kMaxBlocks / NT : n_whole;
     kv4_attn_kernel<D, NT><<<blocks, kThreads, smem, st>>>(p);

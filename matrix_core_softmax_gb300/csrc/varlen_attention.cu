@@ -490,11 +490,8 @@ cudaError_t launch(const VarlenLaunch& a, const Params& p, cudaStream_t st) {
     const size_t smem = sizeof(Smem);
     // the in-kernel register split assumes exactly kLaunchRegs per thread at
     // launch; anything else could make the increase wait forever
-    cudaFuncAttributes fa{};
-    cudaError_t e = cudaFuncGetAttributes(&fa, varlen_attn_kernel<D>);
-    if (e != cudaSuccess) return e;
-    if (fa.numRegs != kLaunchRegs) return cudaErrorInvalidConfiguration;
-    e = cudaFuncSetAttribute(varlen_attn_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    static KernelSetup setup;
+    const cudaError_t e = setup(reinterpret_cast<const void*>(varlen_attn_kernel<D>), static_cast<int>(smem), kLaunchRegs);
     if (e != cudaSuccess) return e;
     // a sequence of n tokens has at most n / (2 n_tok) + 1 pairs
     const int64_t pairs = a.Tq / (2 * p.n_tok) + static_cast<int64_t>(a.B);

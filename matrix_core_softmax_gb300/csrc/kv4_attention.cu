@@ -64,6 +64,7 @@ constexpr int kStages = 3;
 constexpr int kMaxBlocks = 304;   // two blocks on each of 152 SMs
 constexpr int kMinShare = kWarps; // groups of a block, at least one a warp
 constexpr int kWholeGroups = 16;  // longest segment (groups) that one block takes whole
+constexpr uint32_t kNoGroup = 0xFFFFFFFFu;
 constexpr float kNoMax = -1e30f;
 constexpr float kLag = 4.0f;      // how far M may lag behind (log2)
 constexpr int kHeadroom = 11;     // weights carry 2^11: 2^11 * 2^4 = 2^15 < 65504
@@ -108,6 +109,25 @@ __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1,
     asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ void mma_f16_zero(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                             uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+        : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
+}
+
+// Packed unsigned 16-bit minimum and maximum.
+__device__ __forceinline__ uint32_t min16x2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("min.u16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+__device__ __forceinline__ uint32_t max16x2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("max.u16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
 }
 
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t a) {
@@ -242,7 +262,9 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) kv4_attn_kernel(con
     }
     const int64_t x_begin = x;
     const int gpp = p.page_size / kKv4Group;
-    uint32_t uses = 0;  // parity bit of each stage
+    int st = 0;              // stage of the next group, and its phase
+    uint32_t ph = 0;
+    uint32_t bad_stage = 0;  // stages whose group has no page
 
     while (x < x_end) {
         bool bad_len;
@@ -262,27 +284,33 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) kv4_attn_kernel(con
 
         const int count = g1 - g0 > warp ? (g1 - g0 - warp + kWarps - 1) / kWarps : 0;  // this warp's groups
         const int* table = p.page_table + static_cast<int64_t>(b) * p.max_pages;
-        int pages = 0;          // lane i: the page of the warp's group 32 n + i
-        uint32_t bad_stage = 0; // stages whose group has no page
-        auto issue = [&](int i) {
-            if ((i & 31) == 0) {
-                const int gi = g0 + warp + kWarps * (i + lane);
-                pages = i + lane < count ? __ldg(table + gi / gpp) : 0;
+        uint32_t ids = 0;  // lane j: the cache's group number of the warp's group 32 n + j
+        int st_in = st;    // stage of the next copy
+        auto issue = [&](int j) {
+            if ((j & 31) == 0) {
+                const int gi = g0 + warp + kWarps * (j + lane), pi = gi / gpp;
+                ids = kNoGroup;
+                if (j + lane < count) {
+                    const int page = __ldg(table + pi);
+                    if (page >= 0 && page < p.num_pages)  // (a 16 TB cache would have 2^32 groups)
+                        ids = (static_cast<uint32_t>(page) * p.Hkv + hk) * gpp + (gi - pi * gpp);
+                    else
+                        atomicOr(p.err_word, kErrBadIndex);
+                }
             }
-            const int page = __shfl_sync(0xFFFFFFFFu, pages, i & 31);
-            const int st = i % kStages;
-            if (page < 0 || page >= p.num_pages) {
-                if (lane == 0) atomicOr(p.err_word, kErrBadIndex);
-                bad_stage |= 1u << st;
-                return;
-            }
-            bad_stage &= ~(1u << st);
+            const uint32_t id = __shfl_sync(0xFFFFFFFFu, ids, j & 31);
+            bad_stage &= ~(1u << st_in);
+            if (id == kNoGroup) bad_stage |= 1u << st_in;
             if (lane == 0) {
-                const int gi = g0 + warp + kWarps * i;
-                const uint8_t* src = p.cache + ((static_cast<int64_t>(page) * p.Hkv + hk) * gpp + gi % gpp) * kGroupBytes;
-                mbar_arrive_expect_tx(&sm.full[warp][st], kGroupBytes);
-                bulk_load(sm.ring[warp][st], src, kGroupBytes, &sm.full[warp][st]);
+                if (id == kNoGroup) {
+                    mbar_arrive(&sm.full[warp][st_in]);
+                } else {
+                    mbar_arrive_expect_tx(&sm.full[warp][st_in], kGroupBytes);
+                    bulk_load(sm.ring[warp][st_in], p.cache + static_cast<uint64_t>(id) * kGroupBytes, kGroupBytes,
+                              &sm.full[warp][st_in]);
+                }
             }
+            if (++st_in == kStages) st_in = 0;
         };
         for (int j = 0; j < min(count, kStages); ++j) issue(j);
 
@@ -331,21 +359,20 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) kv4_attn_kernel(con
         float M[NT][2], l[NT][2] = {};
 #pragma unroll
         for (int n = 0; n < NT; ++n) M[n][0] = M[n][1] = kNoMax;
-        uint32_t R = 0;  // largest value scale bytes so far
+        uint32_t R02 = 0, R13 = 0;  // largest value scale bytes so far
         bool ok = true;
         int i = 0;
 
         for (; i < count; ++i) {
-            const int st = i % kStages;
+            ok = __all_sync(0xFFFFFFFFu, mbar_wait(&sm.full[warp][st], ph, p.timeout_ns, &sm.abort));
+            if (!ok) break;
             if (!((bad_stage >> st) & 1u)) {
-                if (!mbar_wait(&sm.full[warp][st], (uses >> st) & 1u, p.timeout_ns, &sm.abort)) ok = false;
-                ok = __all_sync(0xFFFFFFFFu, ok);
-                if (!ok) break;
-                uses ^= 1u << st;
                 const uint8_t* buf = sm.ring[warp][st];
                 const int key0 = (g0 + warp + kWarps * i) * kKv4Group;
 
-                // scales: lane = key
+                // scales: lane = key.  A zero scale byte (2^-127, a zero block as a
+                // rule) counts as zero.  Value scale bytes as 16-bit pairs, blocks 0
+                // and 2, 1 and 3.
                 {
                     const int pos = swap_pos(lane);
                     uint32_t ks, vs;
@@ -357,19 +384,28 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) kv4_attn_kernel(con
                         vs = *reinterpret_cast<const uint16_t*>(buf + L.vscales + lane * L.srow);
                     }
                     if (key0 + lane >= len) vs = 0;
-                    float kf[4] = {};
-#pragma unroll
-                    for (int c = 0; c < kB; ++c) {
-                        const uint32_t e = (ks >> (8 * c)) & 0xFFu;
-                        kf[c] = __uint_as_float(e ? e << 23 : 0x00400000u);
-                    }
-                    sm.kscale[warp][pos] = make_float4(kf[0], kf[1], kf[2], kf[3]);
-                    if (__any_sync(0xFFFFFFFFu, __vcmpgtu4(vs, R) != 0)) {
-                        uint32_t top = __vmaxu4(vs, R);
-                        for (int o = 16; o; o >>= 1) top = __vmaxu4(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
+                    float kf[4];
+                    kf[0] = __uint_as_float((ks & 0xFFu) << 23);
+                    kf[1] = __uint_as_float((ks << 15) & 0x7F800000u);
+                    kf[2] = __uint_as_float((ks << 7) & 0x7F800000u);
+                    kf[3] = __uint_as_float((ks >> 1) & 0x7F800000u);
+                    if (D == 128)
+                        sm.kscale[warp][pos] = make_float4(kf[0], kf[1], kf[2], kf[3]);
+                    else
+                        *reinterpret_cast<float2*>(&sm.kscale[warp][pos]) = make_float2(kf[0], kf[1]);
+                    const uint32_t v02 = vs & 0x00FF00FFu, v13 = (vs >> 8) & 0x00FF00FFu;
+                    const uint32_t t02 = max16x2(v02, R02), t13 = max16x2(v13, R13);
+                    if (__any_sync(0xFFFFFFFFu, t02 != R02 || t13 != R13)) {
+                        uint32_t n02 = t02, n13 = t13;
+                        for (int o = 16; o; o >>= 1) {
+                            n02 = max16x2(n02, __shfl_xor_sync(0xFFFFFFFFu, n02, o));
+                            n13 = max16x2(n13, __shfl_xor_sync(0xFFFFFFFFu, n13, o));
+                        }
 #pragma unroll
                         for (int c = 0; c < kB; ++c) {
-                            const int d = static_cast<int>((R >> (8 * c)) & 0xFFu) - static_cast<int>((top >> (8 * c)) & 0xFFu);
+                            const int sh = 16 * (c >> 1);
+                            const int d = static_cast<int>(((c & 1 ? R13 : R02) >> sh) & 0xFFu) -
+                                          static_cast<int>(((c & 1 ? n13 : n02) >> sh) & 0xFFu);
                             const float f = ex2(static_cast<float>(d));
 #pragma unroll
                             for (int n = 0; n < NT; ++n)
@@ -379,19 +415,23 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) kv4_attn_kernel(con
                                     O[n][c][1][e] *= f;
                                 }
                         }
-                        R = top;
+                        R02 = n02;
+                        R13 = n13;
                     }
-                    const uint32_t z = R - vs;  // bytewise: no borrow, R >= vs in every byte
-                    uint32_t y = 24u;
-#pragma unroll
-                    for (int c = 0; c < kB; ++c) y = min(y, (z >> (8 * c)) & 0xFFu);
+                    const uint32_t z02 = R02 - v02, z13 = R13 - v13;  // no borrow: R is the larger in every half
+                    const uint32_t zm = D == 128 ? min16x2(z02, z13) : min(z02, z13);
+                    const uint32_t y = D == 128 ? min(min(zm & 0xFFFFu, zm >> 16), 24u) : min(zm, 24u);
                     sm.ykey[warp][pos] = make_float2(-static_cast<float>(y), __uint_as_float((127u + y) << 23));
+                    // f16 2^(kHeadroom - (z - y)), zero where that has no exponent left
+                    const uint32_t top = (15 + kHeadroom + y) * 0x00010001u;
+                    const uint32_t f02 = (top - min16x2(z02, top)) << 10, f13 = (top - min16x2(z13, top)) << 10;
                     // position pos = 16 step + 8 half + 2 t + e
                     uint16_t* dst = reinterpret_cast<uint16_t*>(&sm.vscale[warp][(pos >> 1) & 3][pos >> 4][(pos >> 3) & 1][0]) + (pos & 1);
-#pragma unroll
-                    for (int c = 0; c < kB; ++c) {
-                        const int e = 15 + kHeadroom - (static_cast<int>((z >> (8 * c)) & 0xFFu) - static_cast<int>(y));
-                        dst[2 * c] = static_cast<uint16_t>(max(e, 0) << 10);
+                    dst[0] = static_cast<uint16_t>(f02);
+                    dst[2] = static_cast<uint16_t>(f13);
+                    if (D == 128) {
+                        dst[4] = static_cast<uint16_t>(f02 >> 16);
+                        dst[6] = static_cast<uint16_t>(f13 >> 16);
                     }
                 }
                 __syncwarp();
@@ -422,8 +462,8 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) kv4_attn_kernel(con
                         e2m1x8_to_f16(kb[c], xb);
 #pragma unroll
                         for (int n = 0; n < NT; ++n) {
-                            float acc[4] = {};
-                            mma_f16(acc, xa[0], xb[0], xa[1], xb[1], qf[n][c][0], qf[n][c][1]);
+                            float acc[4];
+                            mma_f16_zero(acc, xa[0], xb[0], xa[1], xb[1], qf[n][c][0], qf[n][c][1]);
                             mma_f16(acc, xa[2], xb[2], xa[3], xb[3], qf[n][c][2], qf[n][c][3]);
                             s[n][mt][0] = fmaf(acc[0], fa[c], s[n][mt][0]);
                             s[n][mt][1] = fmaf(acc[1], fa[c], s[n][mt][1]);
@@ -543,6 +583,10 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) kv4_attn_kernel(con
             }
             __syncwarp();
             if (i + kStages < count) issue(i + kStages);
+            if (++st == kStages) {
+                st = 0;
+                ph ^= 1u;
+            }
         }
         if (!ok) {
             // give up: let this warp's copies in flight land, then leave together
@@ -551,9 +595,13 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) kv4_attn_kernel(con
                 atomicOr(p.err_word, kErrTimeout);
             }
             int dummy = 0;
-            for (int j = i; j < min(count, i + kStages); ++j)
-                if (!((bad_stage >> (j % kStages)) & 1u))
-                    mbar_wait(&sm.full[warp][j % kStages], (uses >> (j % kStages)) & 1u, p.timeout_ns, &dummy);
+            for (int j = i; j < min(count, i + kStages); ++j) {
+                mbar_wait(&sm.full[warp][st], ph, p.timeout_ns, &dummy);
+                if (++st == kStages) {
+                    st = 0;
+                    ph ^= 1u;
+                }
+            }
         }
 
         // this warp's result: O in true units relative to 2^M, into its own ring
@@ -570,7 +618,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) kv4_attn_kernel(con
             }
 #pragma unroll
             for (int c = 0; c < kB; ++c) {
-                const float f0 = 1.0f / static_cast<float>(1 << kHeadroom), f1 = pow2f(static_cast<int>((R >> (8 * c)) & 0xFFu) - 127);
+                const float f0 = 1.0f / static_cast<float>(1 << kHeadroom), f1 = pow2f(static_cast<int>(((c & 1 ? R13 : R02) >> (16 * (c >> 1))) & 0xFFu) - 127);
 #pragma unroll
                 for (int j = 0; j < 2; ++j)
                     *reinterpret_cast<float4*>(mine + (8 * n + 2 * t + j) * kPitch + 32 * c + 4 * g) =

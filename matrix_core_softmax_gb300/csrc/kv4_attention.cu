@@ -64,6 +64,7 @@ constexpr int kStages = 3;
 constexpr int kMaxBlocks = 304;   // two blocks on each of 152 SMs
 constexpr int kMinShare = kWarps; // groups of a block, at least one a warp
 constexpr int kWholeGroups = 16;  // longest segment (groups) that one block takes whole
+constexpr int kManySegments = 64; // from here on the join takes four rows a block
 constexpr uint32_t kNoGroup = 0xFFFFFFFFu;
 constexpr float kNoMax = -1e30f;
 constexpr float kLag = 4.0f;      // how far M may lag behind (log2)
@@ -171,6 +172,24 @@ struct Row {
 };
 __device__ __forceinline__ Row row_of(const Params& p, int r) { return {r / p.G, r % p.G}; }
 
+// Groups of a block's share of `all` groups.
+__device__ __forceinline__ int64_t share_of(int64_t all, int n_blocks) {
+    return max(static_cast<int64_t>(kMinShare), (all + n_blocks - 1) / n_blocks);
+}
+
+// Four channels of row r of a segment from their weighted sum and the row's
+// maximum and weight sum.
+template <int D>
+__device__ __forceinline__ void write_row(const Params& p, int b, int hk, int r, int d4, float4 a, float m, float l) {
+    const Row w = row_of(p, r);
+    const int64_t row = (static_cast<int64_t>(b) * p.Sq + w.i) * p.Hq + hk * p.G + w.h;
+    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+    const __nv_bfloat162 lo = __floats2bfloat162_rn(a.x * inv, a.y * inv), hi = __floats2bfloat162_rn(a.z * inv, a.w * inv);
+    *reinterpret_cast<uint2*>(p.o + row * D + 4 * d4) =
+        make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
+    if (p.lse && d4 == 0) p.lse[row] = l == 0.0f ? -INFINITY : (m + __log2f(l)) * 0.6931471805599453f;
+}
+
 template <int D, int NT>
 __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) kv4_attn_kernel(const Params p) {
     constexpr int kB = D / 32;
@@ -240,7 +259,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) kv4_attn_kernel(con
             total += sm.scan[w];
         }
         const int64_t all = total * n_seg;
-        const int64_t share = max(static_cast<int64_t>(kMinShare), (all + gridDim.x - 1) / gridDim.x);
+        const int64_t share = share_of(all, gridDim.x);
         x = share * blockIdx.x;
         x_end = min(x + share, all);
         if (x >= x_end) return;
@@ -604,6 +623,8 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) kv4_attn_kernel(con
             }
         }
 
+        // the second kernel's blocks may start as these finish
+        asm volatile("griddepcontrol.launch_dependents;");
         // this warp's result: O in true units relative to 2^M, into its own ring
         float* mine = reinterpret_cast<float*>(sm.ring[warp][0]);
 #pragma unroll
@@ -654,13 +675,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) kv4_attn_kernel(con
                     part[kRows * D + kRows + r] = lt;
                 }
             } else {
-                const Row w = row_of(p, r0 + r);
-                const int64_t row = (static_cast<int64_t>(b) * p.Sq + w.i) * p.Hq + hk * p.G + w.h;
-                const float inv = lt == 0.0f ? 0.0f : 1.0f / lt;
-                const __nv_bfloat162 lo = __floats2bfloat162_rn(a.x * inv, a.y * inv), hi = __floats2bfloat162_rn(a.z * inv, a.w * inv);
-                *reinterpret_cast<uint2*>(p.o + row * D + 4 * d4) =
-                    make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
-                if (p.lse && d4 == 0) p.lse[row] = lt == 0.0f ? -INFINITY : (m + __log2f(lt)) * 0.6931471805599453f;
+                write_row<D>(p, b, hk, r0 + r, d4, a, m, lt);
             }
         }
         // the merge buffer becomes the ring of the next segment
@@ -671,14 +686,28 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) kv4_attn_kernel(con
 }
 
 // Joins the parts of the segments that several blocks worked on, and writes the
-// rows of empty sequences.  One block per segment.
-template <int D, int NT>
+// rows of empty sequences.  A block takes kPer rows of a segment: a warp a row
+// weighs the parts, then kSlices groups of kPer * D / 4 threads each add every
+// kSlices-th part, so that a row split over all resident blocks still waits for
+// few loads in turn (8 segments of 38 parts: 24 us with one thread adding all of
+// an element's parts, 9 us so).  One row a block where segments are few, four
+// where they are many and their parts few (16 sequences, 64 segments: 20.7 us
+// for the whole call with one row a block, 19.4 us with four).  Launched to
+// overlap the end of the first kernel: what precedes the wait depends on the
+// lengths alone.
+template <int D, int NT, int kPer>
 __global__ void __launch_bounds__(kThreads) kv4_join_kernel(const Params p, int n_blocks) {
-    constexpr int kRows = 8 * NT;
+    constexpr int kRows = 8 * NT, kLanes = D / 4, kSlices = kThreads / (kLanes * kPer);
     __shared__ int64_t warp_sum[2][kWarps];
-    const int tid = threadIdx.x, lane = tid & 31;
+    __shared__ float row_m[kPer], row_l[kPer];
+    __shared__ float fac[kPer][kMaxBlocks];
+    __shared__ float4 red[kSlices][kPer * kLanes];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int n_seg = p.Hkv * p.n_rt;
     const int b = blockIdx.x / n_seg, seg = blockIdx.x - b * n_seg;
+    const int r_first = blockIdx.y * kPer;
+    const int hk = seg / p.n_rt, r0 = (seg % p.n_rt) * kRows;
+    if (r0 + r_first >= p.Sq * p.G) return;
     int64_t before = 0, total = 0;
     for (int i = tid; i < p.B; i += kThreads) {
         const int n = seq_groups(p, i);
@@ -690,8 +719,8 @@ __global__ void __launch_bounds__(kThreads) kv4_join_kernel(const Params p, int 
         total += __shfl_xor_sync(0xFFFFFFFFu, total, o);
     }
     if (lane == 0) {
-        warp_sum[0][tid >> 5] = before;
-        warp_sum[1][tid >> 5] = total;
+        warp_sum[0][warp] = before;
+        warp_sum[1][warp] = total;
     }
     __syncthreads();
     before = total = 0;
@@ -700,42 +729,64 @@ __global__ void __launch_bounds__(kThreads) kv4_join_kernel(const Params p, int 
         total += warp_sum[1][w];
     }
     const int ng = seq_groups(p, b);
-    const int64_t all = total * n_seg;
-    const int64_t share = max(static_cast<int64_t>(kMinShare), (all + n_blocks - 1) / n_blocks);
+    const int64_t share = share_of(total * n_seg, n_blocks);
     const int64_t s0 = before * n_seg + static_cast<int64_t>(seg) * ng;
     const int c0 = static_cast<int>(s0 / share), c1 = ng ? static_cast<int>((s0 + ng - 1) / share) : c0 - 1;
     if (c0 == c1) return;  // one block wrote the result
-    const int hk = seg / p.n_rt, r0 = (seg % p.n_rt) * kRows;
-    const int n_rows = min(kRows, p.Sq * p.G - r0);
-    for (int e = tid; e < n_rows * (D / 4); e += kThreads) {
-        const int r = e / (D / 4), d4 = e % (D / 4);
-        float m = kNoMax, lt = 0.0f;
-        float4 a = make_float4(0, 0, 0, 0);
-        // the segment starts in block c0 (its second part unless the block starts
-        // with it) and is the first part of every later block
-        auto part_of = [&](int c) {
-            return p.partial + (2 * static_cast<int64_t>(c) + (c == c0 ? 1 : 0)) * (kRows * (D + 2));
-        };
-#pragma unroll 4
-        for (int c = c0; c <= c1; ++c) m = fmaxf(m, part_of(c)[kRows * D + r]);
-#pragma unroll 4
-        for (int c = c0; c <= c1; ++c) {
-            const float* part = part_of(c);
-            const float f = ex2(part[kRows * D + r] - m);
-            lt = fmaf(f, part[kRows * D + kRows + r], lt);
-            const float4 v = reinterpret_cast<const float4*>(part)[r * (D / 4) + d4];
-            a.x = fmaf(f, v.x, a.x);
-            a.y = fmaf(f, v.y, a.y);
-            a.z = fmaf(f, v.z, a.z);
-            a.w = fmaf(f, v.w, a.w);
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+
+    // the segment starts in block c0, as its second part, and is the first part
+    // of every later block
+    const int n_parts = c1 - c0 + 1;
+    auto part_of = [&](int j) {
+        return p.partial + (2 * static_cast<int64_t>(c0 + j) + (j == 0 ? 1 : 0)) * (kRows * (D + 2));
+    };
+    if (warp < kPer) {
+        const int r = r_first + warp;
+        float m = kNoMax, l = 0.0f;
+        for (int j = lane; j < n_parts; j += 32) {
+            const float mj = part_of(j)[kRows * D + r];
+            fac[warp][j] = mj;
+            m = fmaxf(m, mj);
         }
-        const Row w = row_of(p, r0 + r);
-        const int64_t row = (static_cast<int64_t>(b) * p.Sq + w.i) * p.Hq + hk * p.G + w.h;
-        const float inv = lt == 0.0f ? 0.0f : 1.0f / lt;
-        const __nv_bfloat162 lo = __floats2bfloat162_rn(a.x * inv, a.y * inv), hi = __floats2bfloat162_rn(a.z * inv, a.w * inv);
-        *reinterpret_cast<uint2*>(p.o + row * D + 4 * d4) =
-            make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
-        if (p.lse && d4 == 0) p.lse[row] = lt == 0.0f ? -INFINITY : (m + __log2f(lt)) * 0.6931471805599453f;
+        for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+        for (int j = lane; j < n_parts; j += 32) {
+            const float f = ex2(fac[warp][j] - m);
+            fac[warp][j] = f;
+            l = fmaf(f, part_of(j)[kRows * D + kRows + r], l);
+        }
+        for (int o = 16; o; o >>= 1) l += __shfl_xor_sync(0xFFFFFFFFu, l, o);
+        if (lane == 0) {
+            row_m[warp] = m;
+            row_l[warp] = l;
+        }
+    }
+    __syncthreads();
+
+    const int e = tid % (kPer * kLanes), slice = tid / (kPer * kLanes);
+    const int k = e / kLanes, d4 = e % kLanes, r = r_first + k;
+    float4 a = make_float4(0, 0, 0, 0);
+#pragma unroll 4
+    for (int j = slice; j < n_parts; j += kSlices) {
+        const float f = fac[k][j];
+        const float4 v = reinterpret_cast<const float4*>(part_of(j))[r * kLanes + d4];
+        a.x = fmaf(f, v.x, a.x);
+        a.y = fmaf(f, v.y, a.y);
+        a.z = fmaf(f, v.z, a.z);
+        a.w = fmaf(f, v.w, a.w);
+    }
+    red[slice][e] = a;
+    __syncthreads();
+    if (slice == 0 && r0 + r < p.Sq * p.G) {
+#pragma unroll
+        for (int i = 1; i < kSlices; ++i) {
+            const float4 v = red[i][e];
+            a.x += v.x;
+            a.y += v.y;
+            a.z += v.z;
+            a.w += v.w;
+        }
+        write_row<D>(p, b, hk, r0 + r, d4, a, row_m[k], row_l[k]);
     }
 }
 
@@ -756,8 +807,18 @@ cudaError_t launch(Params p, int n_whole, cudaStream_t st) {
     kv4_attn_kernel<D, NT><<<blocks, kThreads, smem, st>>>(p);
     e = cudaGetLastError();
     if (e != cudaSuccess || !p.partial) return e;
-    kv4_join_kernel<D, NT><<<n_whole, kThreads, 0, st>>>(p, blocks);
-    return cudaGetLastError();
+    cudaLaunchConfig_t cfg{};
+    const bool many = n_whole >= kManySegments;
+    cfg.gridDim = dim3(static_cast<unsigned>(n_whole), static_cast<unsigned>(8 * NT / (many ? 4 : 1)));
+    cfg.blockDim = dim3(kThreads);
+    cfg.stream = st;
+    cudaLaunchAttribute at{};
+    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &at;
+    cfg.numAttrs = 1;
+    return many ? cudaLaunchKernelEx(&cfg, kv4_join_kernel<D, NT, 4>, p, blocks)
+                : cudaLaunchKernelEx(&cfg, kv4_join_kernel<D, NT, 1>, p, blocks);
 }
 
 }  // namespace

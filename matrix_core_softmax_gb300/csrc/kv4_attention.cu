@@ -60,8 +60,13 @@ namespace fsa {
 namespace {
 
 constexpr int kWarps = 8, kThreads = 32 * kWarps;
-constexpr int kStages = 3;
-constexpr int kMaxBlocks = 304;   // two blocks on each of 152 SMs
+constexpr int kStages = 2;        // (three: 1 % slower, the merge and the ring leave less L1)
+constexpr int kResident = 304;    // two blocks on each of 152 SMs
+constexpr int kMaxBlocks = 2 * kResident;
+// Shares beyond this many groups are halved, so that SMs that read faster take
+// more of them (64 x 32768 keys: 234 against 239 us; with small shares the
+// further parts cost more than that: 131072 keys of one sequence 69 against 55).
+constexpr int64_t kLongShare = 1024;
 constexpr int kMinShare = kWarps; // groups of a block, at least one a warp
 constexpr int kWholeGroups = 16;  // longest segment (groups) that one block takes whole
 constexpr int kManySegments = 64; // from here on the join takes four rows a block
@@ -797,13 +802,20 @@ bool takes_whole(int page_size, int max_pages) {
     return static_cast<int64_t>(max_pages) * (page_size / kKv4Group) <= kWholeGroups;
 }
 
+// Blocks of the split form.
+template <int NT>
+int stream_blocks(int64_t segments, int page_size, int max_pages) {
+    const int64_t most = segments * max_pages * (page_size / kKv4Group);
+    return (most >= kLongShare * kResident ? kMaxBlocks : kResident) / NT;
+}
+
 template <int D, int NT>
 cudaError_t launch(Params p, int n_whole, cudaStream_t st) {
     const size_t smem = sizeof(Smem<D, NT>);
     static KernelSetup setup;
     cudaError_t e = setup(reinterpret_cast<const void*>(kv4_attn_kernel<D, NT>), static_cast<int>(smem), 0);
     if (e != cudaSuccess) return e;
-    const int blocks = p.partial ? kMaxBlocks / NT : n_whole;
+    const int blocks = p.partial ? stream_blocks<NT>(n_whole, p.page_size, p.max_pages) : n_whole;
     kv4_attn_kernel<D, NT><<<blocks, kThreads, smem, st>>>(p);
     e = cudaGetLastError();
     if (e != cudaSuccess || !p.partial) return e;

@@ -15,7 +15,13 @@
 //
 //   warps 0-3 / 4-7  softmax of tile 0 / tile 1 (thread = row = TMEM lane);
 //   warp 8           TMA of Q and the K ring; warp 10 of the V ring;
-//   warp 9           TMEM allocator and the issuer of every product.
+//   warp 9           TMEM allocator and the issuer of every product;
+//   warp 11          finds the CTA's next pair of tiles.
+// A CTA stays on its SM: when it has taken a pair, warp 11 cancels the launch of
+// a CTA that has not started yet and takes over its number, so pairs (the
+// longest of a sequence first) go to whichever SM is free, and the next pair's Q,
+// K and first scores are under way while the softmax warps still write the last
+// one's output.
 // TMEM: S0, S1 (128 columns each, P overlays the first 64 of its S in bf16),
 // O0, O1 (D columns each).
 //
@@ -44,7 +50,7 @@ namespace {
 
 constexpr int kKStages = 2, kVStages = 2;
 constexpr int kThreads = 384;
-constexpr int kWarpLoad = 8, kWarpMma = 9, kWarpLoadV = 10;
+constexpr int kWarpLoad = 8, kWarpMma = 9, kWarpLoadV = 10, kWarpPlan = 11;
 // launched at 168 registers per thread; helpers drop to 32, softmax takes 232
 constexpr int kLaunchRegs = 168, kSoftmaxRegs = 232, kHelperRegs = 40;
 static_assert(2 * 128 * kSoftmaxRegs + 128 * kHelperRegs <= kThreads * kLaunchRegs,
@@ -56,20 +62,27 @@ constexpr uint32_t kColO = 256;        // S0 at 0, S1 at 128, O0 at 256, O1 at 3
 constexpr float kNoMax = -1e30f;
 constexpr float kLag = 8.0f;           // how far the reference may lag behind the maximum (log2)
 
+// A pair of query tiles of one key head: sequence bounds, first token of the pair
+// in its sequence, key head (-1: no more work).
+struct Item {
+    int q0, nq, k0, nk, tok0, hk;
+};
+
 struct __align__(1024) Smem {
     uint8_t q[2][kTileBytes];
     uint8_t k[kKStages][kTileBytes];
     uint8_t v[kVStages][kTileBytes];
-    uint64_t bar_q;
+    uint4 next;  // the launch control's answer
+    uint64_t next_full;
+    uint64_t item_full[2], item_empty[2];
+    uint64_t q_full, q_empty;
     uint64_t k_full[kKStages], k_empty[kKStages];
     uint64_t v_full[kVStages], v_empty[kVStages], v_clean[kVStages];
     uint64_t s_full[2], p_full[2], o_full[2];
     uint64_t drain;
+    Item item[2];
     uint32_t tmem_base;
     int abort;
-    int scan[kThreads / 32];
-    int first_bad;
-    int seq, tile;  // this CTA's sequence (-1: none) and pair of tiles in it
 };
 
 static_assert(sizeof(Smem) <= 232448, "shared memory beyond the 227 KB a CTA may use");
@@ -89,63 +102,90 @@ __device__ __forceinline__ void raise_abort(Smem& sm, const Params& p) {
     atomicOr(p.err_word, kErrTimeout);
 }
 
-// Finds the sequence and the pair of query tiles of CTA number `idx`: sequence
-// after sequence, the last pair (the longest one when causal) first.  Sequences
-// from the first wrong bound on have none.
-__device__ __forceinline__ void find_work(Smem& sm, const Params& p, int idx, bool report) {
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int per = (p.B + kThreads - 1) / kThreads;
-    const int b0 = min(tid * per, p.B), b1 = min(b0 + per, p.B);
-    const int rows = 2 * p.n_tok;
-    int bad = p.B, sum = 0;
-    int q0 = b0 < p.B ? __ldg(p.cu_q + b0) : 0, k0 = b0 < p.B ? __ldg(p.cu_k + b0) : 0;
-    for (int b = b0; b < b1; ++b) {
-        const int q1 = __ldg(p.cu_q + b + 1), k1 = __ldg(p.cu_k + b + 1);
-        if (q0 < 0 || q1 < q0 || q1 > p.Tq || k0 < 0 || k1 < k0 || k1 > p.Tk) bad = min(bad, b);
-        if (b < bad) sum += (q1 - q0 + rows - 1) / rows;
-        q0 = q1;
-        k0 = k1;
-    }
-    if (bad < p.B) atomicMin(&sm.first_bad, bad);
-    int inc = sum;
-    for (int o = 1; o < 32; o <<= 1) {
-        const int x = __shfl_up_sync(0xFFFFFFFFu, inc, o);
-        if (lane >= o) inc += x;
-    }
-    if (lane == 31) sm.scan[warp] = inc;
-    __syncthreads();
-    int before = inc - sum;
-    for (int w = 0; w < warp; ++w) before += sm.scan[w];
-    // counts of threads behind the first wrong bound are off, but their
-    // sequences are behind it, too
-    if (idx >= before && idx < before + sum) {
-        int b = b0, at = before;
-        int q = __ldg(p.cu_q + b);
-        while (true) {
-            const int q1 = __ldg(p.cu_q + b + 1);
-            const int n = (q1 - q + rows - 1) / rows;
-            if (idx < at + n) {
-                if (b < sm.first_bad) {
-                    sm.seq = b;
-                    sm.tile = n - 1 - (idx - at);
-                }
-                break;
-            }
-            at += n;
-            q = q1;
-            ++b;
+// Where the plan warp's search for pair numbers stands: sequence b, whose first
+// pair has the number `first`.
+struct Cursor {
+    int b, first;
+};
+
+// Finds pair number idx, by the whole warp: sequence after sequence, 32 at a time
+// from the cursor on (numbers grow from call to call as a rule), the last pair
+// of a sequence (the longest one when causal) first.  Sequences from the first
+// wrong bound on have none.  False: no such pair.
+__device__ __forceinline__ bool find_pair(const Params& p, int idx, Cursor& at, Item& it) {
+    const int lane = threadIdx.x & 31, rows = 2 * p.n_tok;
+    if (idx < at.first) at = {0, 0};
+    while (at.b < p.B) {
+        const int b = min(at.b + lane, p.B - 1);
+        const int q0 = __ldg(p.cu_q + b), q1 = __ldg(p.cu_q + b + 1), k0 = __ldg(p.cu_k + b), k1 = __ldg(p.cu_k + b + 1);
+        const bool bad = q0 < 0 || q1 < q0 || q1 > p.Tq || k0 < 0 || k1 < k0 || k1 > p.Tk;
+        const unsigned wrong = __ballot_sync(0xFFFFFFFFu, bad);
+        const int good = min(p.B - at.b, wrong ? __ffs(wrong) - 1 : 32);  // sequences of this window
+        const int n = lane < good ? (q1 - q0 + rows - 1) / rows : 0;
+        int inc = n;
+        for (int o = 1; o < 32; o <<= 1) {
+            const int x = __shfl_up_sync(0xFFFFFFFFu, inc, o);
+            if (lane >= o) inc += x;
         }
+        const unsigned has = __ballot_sync(0xFFFFFFFFu, idx < at.first + inc);
+        if (has) {
+            const int src = __ffs(has) - 1;
+            const int last = at.first + inc - 1;  // number of the sequence's first pair of tokens
+            it.q0 = __shfl_sync(0xFFFFFFFFu, q0, src);
+            it.nq = __shfl_sync(0xFFFFFFFFu, q1, src) - it.q0;
+            it.k0 = __shfl_sync(0xFFFFFFFFu, k0, src);
+            it.nk = __shfl_sync(0xFFFFFFFFu, k1, src) - it.k0;
+            it.tok0 = (__shfl_sync(0xFFFFFFFFu, last, src) - idx) * rows;
+            return true;
+        }
+        if (good < min(32, p.B - at.b)) {
+            if (lane == 0) atomicOr(p.err_word, kErrBadIndex);
+            return false;
+        }
+        at.first += __shfl_sync(0xFFFFFFFFu, inc, 31);
+        at.b += 32;
     }
-    if (tid == 0 && report && sm.first_bad < p.B) atomicOr(p.err_word, kErrBadIndex);
+    return false;
+}
+
+// Asks the hardware for a CTA of this grid that has not started: its number, or
+// that there is none, arrives in `answer` and on `bar`.
+__device__ __forceinline__ void ask_next_cta(uint4* answer, uint64_t* bar) {
+    asm volatile("clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(
+                     smem_u32(answer)),
+                 "r"(smem_u32(bar))
+                 : "memory");
+}
+__device__ __forceinline__ int next_cta(const uint4* answer) {  // -1: none
+    uint32_t ok, x;
+    asm volatile(
+        "{\n\t.reg .b128 h;\n\t.reg .pred p;\n\t"
+        "ld.shared.b128 h, [%2];\n\t"
+        "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, h;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t"
+        "mov.u32 %1, 0;\n\t"
+        "@p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %1, h;\n\t}"
+        : "=r"(ok), "=r"(x)
+        : "r"(smem_u32(answer))
+        : "memory");
+    return ok ? static_cast<int>(x) : -1;
+}
+
+// Key tiles that query tile i of an item works on: those that its last token sees.
+__device__ __forceinline__ int key_tiles(const Params& p, const Item& it, int i) {
+    const int first = it.tok0 + i * p.n_tok, last = min(first + p.n_tok, it.nq) - 1;
+    const int see = first >= it.nq ? 0 : p.causal ? min(it.nk, max(0, it.nk - it.nq + 1 + last)) : it.nk;
+    return (see + kTile - 1) / kTile;
 }
 
 // One key tile t for this thread's row: scores out of TMEM, the maximum, the
-// rare rescale of O, P back into TMEM.  `lim`: keys the row sees in all;
+// rare rescale of O, P back into TMEM.  `lim`: keys the row sees in all; `ph`:
+// phase of s_full;
 // `masked`: some row of the tile sees less than this whole key tile.
 template <int D>
-__device__ __forceinline__ bool softmax_tile(Smem& sm, const Params& p, int t, int i, uint32_t s_col, uint32_t o_col, int lim,
-                                             bool masked, float& m, float& l) {
-    const bool ok = mbar_wait(&sm.s_full[i], t & 1, p.timeout_ns, &sm.abort);
+__device__ __forceinline__ bool softmax_tile(Smem& sm, const Params& p, int t, int i, uint32_t ph, uint32_t s_col, uint32_t o_col,
+                                             int lim, bool masked, float& m, float& l) {
+    const bool ok = mbar_wait(&sm.s_full[i], ph, p.timeout_ns, &sm.abort);
     tc_fence_after();
     uint32_t s0[32], s1[32], s2[32], s3[32];
     float top;
@@ -245,13 +285,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     Smem& sm = *reinterpret_cast<Smem*>(smem_raw);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     constexpr int n_atoms = D / 64;
-    const int idx = blockIdx.x / p.Hkv, hk = blockIdx.x - idx * p.Hkv;
 
     if (tid == 0) {
         sm.abort = 0;
-        sm.first_bad = p.B;
-        sm.seq = -1;
-        mbar_init(&sm.bar_q, 1);
+        mbar_init(&sm.next_full, 1);
+        mbar_init(&sm.q_full, 1);
+        mbar_init(&sm.q_empty, 1);
         for (int i = 0; i < kKStages; ++i) {
             mbar_init(&sm.k_full[i], 1);
             mbar_init(&sm.k_empty[i], 1);
@@ -262,6 +301,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(&sm.v_clean[i], 1);
         }
         for (int i = 0; i < 2; ++i) {
+            mbar_init(&sm.item_full[i], 1);
+            mbar_init(&sm.item_empty[i], 11);  // every warp but the plan warp
             mbar_init(&sm.s_full[i], 1);
             mbar_init(&sm.p_full[i], 4);  // one arrival per softmax warp
             mbar_init(&sm.o_full[i], 1);
@@ -269,8 +310,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_init(&sm.drain, 1);
         fence_mbar_init();
     }
-    __syncthreads();
-    find_work(sm, p, idx, blockIdx.x == 0);
     if (warp == kWarpMma) {
         tmem_alloc(&sm.tmem_base, kTmemCols);
         tmem_relinquish();
@@ -279,58 +318,101 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = sm.tmem_base;
-    const int b = sm.seq;
 
-    if (b >= 0) {
-        const int q0 = __ldg(p.cu_q + b), nq = __ldg(p.cu_q + b + 1) - q0;
-        const int k0 = __ldg(p.cu_k + b), nk = __ldg(p.cu_k + b + 1) - k0;
-        const int tok0 = sm.tile * 2 * p.n_tok;  // first token of the pair in its sequence
-        // key tiles of query tile i: those that its last token sees
-        int n_t[2];
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const int first = tok0 + i * p.n_tok, last = min(first + p.n_tok, nq) - 1;
-            const int see = first >= nq ? 0 : p.causal ? min(nk, max(0, nk - nq + 1 + last)) : nk;
-            n_t[i] = (see + kTile - 1) / kTile;
-        }
-        const int n_max = max(n_t[0], n_t[1]);  // (a missing second tile has none)
-        const int t_ragged = (nk % kTile) ? nk / kTile : -1;  // key tile that ends inside, if any
+    auto wait = [&](uint64_t* bar, uint32_t phase) {
+        return __all_sync(0xFFFFFFFFu, mbar_wait(bar, phase & 1u, p.timeout_ns, &sm.abort)) != 0;
+    };
+    // the n-th item of this CTA; false: no more, or a wait ran out
+    auto take = [&](int n, Item& it, bool& ok) {
+        ok = wait(&sm.item_full[n & 1], n >> 1);
+        if (!ok) return false;
+        it = sm.item[n & 1];
+        return it.hk >= 0;
+    };
+    auto give_back = [&](int n) { warp_arrive(&sm.item_empty[n & 1]); };
 
-        if (warp == kWarpLoad || warp == kWarpLoadV) {
-            warpgroup_reg_dec<kHelperRegs>();
-            const bool is_k = warp == kWarpLoad;
-            const int stages = is_k ? kKStages : kVStages;
-            uint64_t* full = is_k ? sm.k_full : sm.v_full;
-            uint64_t* empty = is_k ? sm.k_empty : sm.v_empty;
-            const CUtensorMap* map = is_k ? &tm_k : &tm_v;
-            bool ok = true;
-            bool q_issued = false;
-            int issued = 0, st = 0;
-            uint32_t ph = 0;
-            if (lane == 0 && is_k && n_max > 0) {
-                const int n_q = n_t[1] > 0 ? 2 : 1;
-                mbar_arrive_expect_tx(&sm.bar_q, n_q * n_atoms * p.G * p.n_tok * 128);
-                for (int i = 0; i < n_q; ++i)
-                    for (int a = 0; a < n_atoms; ++a)
-                        tma_load_3d(sm.q[i] + a * kAtom, &tm_q, &sm.bar_q, 64 * a, hk * p.G, q0 + tok0 + i * p.n_tok);
-                q_issued = true;
+    if (warp == kWarpPlan) {
+        warpgroup_reg_dec<kHelperRegs>();
+        Cursor at{0, 0};
+        int cta = blockIdx.x, n = 0;
+        uint32_t asked = 0;  // phase of next_full
+        bool ok = true;
+        while (true) {
+            // the next number is asked for while this one is looked up
+            if (cta >= 0 && lane == 0) {
+                mbar_arrive_expect_tx(&sm.next_full, 16);
+                ask_next_cta(&sm.next, &sm.next_full);
             }
+            Item it{};
+            it.hk = -1;
+            bool have = false;
+            if (cta >= 0) {
+                const int idx = cta / p.Hkv;
+                have = find_pair(p, idx, at, it);
+                it.hk = have ? cta - idx * p.Hkv : -1;
+            }
+            if (have || cta < 0) {
+                if (n >= 2) ok = wait(&sm.item_empty[n & 1], (n >> 1) + 1);
+                if (ok && lane == 0) {
+                    sm.item[n & 1] = it;
+                    mbar_arrive(&sm.item_full[n & 1]);
+                }
+                ++n;
+            }
+            if (cta < 0) break;
+            int dummy = 0;  // (an answer under way is waited for in any case)
+            const bool got = __all_sync(0xFFFFFFFFu, mbar_wait(&sm.next_full, asked, p.timeout_ns, &dummy)) != 0;
+            asked ^= 1u;
+            ok = ok && got;
+            if (!ok) break;
+            cta = next_cta(&sm.next);
+            fence_async_smem();
+            __syncwarp();
+        }
+        if (!ok && lane == 0) raise_abort(sm, p);
+    } else if (warp == kWarpLoad || warp == kWarpLoadV) {
+        warpgroup_reg_dec<kHelperRegs>();
+        const bool is_k = warp == kWarpLoad;
+        const int stages = is_k ? kKStages : kVStages;
+        uint64_t* full = is_k ? sm.k_full : sm.v_full;
+        uint64_t* empty = is_k ? sm.k_empty : sm.v_empty;
+        const CUtensorMap* map = is_k ? &tm_k : &tm_v;
+        int issued = 0, st = 0, n_q = 0;  // key tiles and query pairs loaded so far, stage of the next
+        uint32_t ph = 0;
+        bool ok = true;
+        Item it;
+        for (int n = 0; take(n, it, ok); ++n) {
+            const int n0 = key_tiles(p, it, 0), n1 = key_tiles(p, it, 1), n_max = max(n0, n1);
+            if (is_k && n_max > 0) {
+                if (n_q > 0) ok = wait(&sm.q_empty, n_q - 1);
+                if (!ok) break;
+                if (lane == 0) {
+                    const int tiles = n1 > 0 ? 2 : 1;
+                    mbar_arrive_expect_tx(&sm.q_full, tiles * n_atoms * p.G * p.n_tok * 128);
+                    for (int i = 0; i < tiles; ++i)
+                        for (int a = 0; a < n_atoms; ++a)
+                            tma_load_3d(sm.q[i] + a * kAtom, &tm_q, &sm.q_full, 64 * a, it.hk * p.G,
+                                        it.q0 + it.tok0 + i * p.n_tok);
+                }
+                ++n_q;
+            }
+            const int t_ragged = (it.nk % kTile) ? it.nk / kTile : -1;  // key tile that ends inside, if any
             for (int t = 0; t < n_max; ++t) {
-                if (t >= stages) ok = mbar_wait(&empty[st], ph ^ 1u, p.timeout_ns, &sm.abort);
-                ok = __all_sync(0xFFFFFFFFu, ok);
+                if (issued >= stages) ok = wait(&empty[st], ph ^ 1u);
                 if (!ok) break;
                 uint8_t* dst = is_k ? sm.k[st] : sm.v[st];
                 if (lane == 0) {
                     mbar_arrive_expect_tx(&full[st], kAtom * n_atoms);
-                    for (int a = 0; a < n_atoms; ++a) tma_load_3d(dst + a * kAtom, map, &full[st], 64 * a, hk, k0 + t * kTile);
+                    for (int a = 0; a < n_atoms; ++a)
+                        tma_load_3d(dst + a * kAtom, map, &full[st], 64 * a, it.hk, it.k0 + t * kTile);
                 }
-                issued = t + 1;
+                ++issued;
                 if (!is_k && t == t_ragged) {
                     // the rows behind the sequence's last key belong to others: a
                     // weight of zero does not hide a NaN, so they become zeros
-                    ok = __all_sync(0xFFFFFFFFu, mbar_wait(&full[st], ph, p.timeout_ns, &sm.abort));
+                    ok = wait(&full[st], ph);
                     if (!ok) break;
-                    const int r0 = nk - t * kTile;
+                    const int r0 = it.nk - t * kTile;
                     for (int a = 0; a < n_atoms; ++a)
                         for (int e = r0 * 8 + lane; e < kTile * 8; e += 32)
                             reinterpret_cast<uint4*>(dst + a * kAtom)[e] = make_uint4(0, 0, 0, 0);
@@ -343,115 +425,141 @@ __global__ void __launch_bounds__(kThreads, 1)
                     ph ^= 1u;
                 }
             }
-            if (lane == 0) {
-                if (!ok) raise_abort(sm, p);
-                if (sm.abort) {
-                    // let the copies still in flight land before the CTA exits
-                    int dummy = 0;
-                    if (q_issued) mbar_wait(&sm.bar_q, 0, p.timeout_ns, &dummy);
-                    for (int t = max(0, issued - stages); t < issued; ++t)
-                        mbar_wait(&full[t % stages], (t / stages) & 1, p.timeout_ns, &dummy);
-                }
+            if (!ok) break;
+            give_back(n);
+        }
+        if (lane == 0) {
+            if (!ok) raise_abort(sm, p);
+            if (sm.abort) {
+                // let the copies still in flight land before the CTA exits
+                int dummy = 0;
+                if (n_q > 0) mbar_wait(&sm.q_full, (n_q - 1) & 1, p.timeout_ns, &dummy);
+                for (int t = max(0, issued - stages); t < issued; ++t)
+                    mbar_wait(&full[t % stages], (t / stages) & 1, p.timeout_ns, &dummy);
             }
-        } else if (warp == kWarpMma) {
-            warpgroup_reg_dec<kHelperRegs>();
+        }
+    } else if (warp == kWarpMma) {
+        warpgroup_reg_dec<kHelperRegs>();
+        // the whole warp walks this, one elected lane issues.  Descriptors: + 2
+        // advances a K-major operand by one 16-element K step, + kAtom / 16 by one
+        // swizzle atom; V is MN-major, 64-wide d atoms kAtom apart (LBO), 8-key
+        // groups 1024 apart (SBO), one 16-key step 2048 bytes
+        constexpr uint32_t id_qk = idesc_bf16(128, 128, 0, 0), id_pv = idesc_bf16(128, D, 0, 1);
+        const uint32_t tm = __shfl_sync(0xFFFFFFFFu, tmem, 0);
+        const uint64_t dq = smem_desc(smem_u32(sm.q[0]), 16, 1024, SWZ_128B);
+        const uint64_t dk = smem_desc(smem_u32(sm.k[0]), 16, 1024, SWZ_128B);
+        const uint64_t dv = smem_desc(smem_u32(sm.v[0]), kAtom, 1024, SWZ_128B);
+        auto scores = [&](int i, int st) {
+            const uint64_t a = dq + (kTileBytes >> 4) * i, bk = dk + (kTileBytes >> 4) * st;
+#pragma unroll
+            for (int kk = 0; kk < D / 16; ++kk) {
+                const uint32_t off = (kk >> 2) * (kAtom >> 4) + 2 * (kk & 3);
+                mma_bf16_one(tm + 128 * i, a + off, bk + off, id_qk, kk > 0 ? 1u : 0u);
+            }
+            tc_commit_one(&sm.s_full[i]);
+        };
+        auto values = [&](int i, int st, bool add) {
+            const uint64_t bv = dv + (kTileBytes >> 4) * st;
+#pragma unroll
+            for (int kk = 0; kk < 8; ++kk)
+                mma_bf16_tmem_a_one(tm + kColO + 128 * i, tm + 128 * i + 8 * kk, bv + 128 * kk, id_pv,
+                                    (add || kk > 0) ? 1u : 0u);
+        };
+        int tiles = 0, n_q = 0;      // key tiles and query pairs used so far
+        uint32_t p_ph[2] = {0, 0};   // phases of p_full
+        uint32_t clean_ph = 0;       // phases of v_clean, a bit per stage
+        bool ok = true;
+        Item it;
+        for (int n = 0; take(n, it, ok); ++n) {
+            const int n_t[2] = {key_tiles(p, it, 0), key_tiles(p, it, 1)};
+            const int n_max = max(n_t[0], n_t[1]);
+            const int t_ragged = (it.nk % kTile) ? it.nk / kTile : -1;
             if (n_max > 0) {
-                // the whole warp walks this, one elected lane issues.  Descriptors:
-                // + 2 advances a K-major operand by one 16-element K step, + kAtom /
-                // 16 by one swizzle atom; V is MN-major, 64-wide d atoms kAtom apart
-                // (LBO), 8-key groups 1024 apart (SBO), one 16-key step 2048 bytes
-                constexpr uint32_t id_qk = idesc_bf16(128, 128, 0, 0), id_pv = idesc_bf16(128, D, 0, 1);
-                const uint32_t tm = __shfl_sync(0xFFFFFFFFu, tmem, 0);
-                const uint64_t dq = smem_desc(smem_u32(sm.q[0]), 16, 1024, SWZ_128B);
-                const uint64_t dk = smem_desc(smem_u32(sm.k[0]), 16, 1024, SWZ_128B);
-                const uint64_t dv = smem_desc(smem_u32(sm.v[0]), kAtom, 1024, SWZ_128B);
-                auto scores = [&](int i, int t) {
-                    const uint64_t a = dq + (kTileBytes >> 4) * i, bk = dk + (kTileBytes >> 4) * (t % kKStages);
+                ok = wait(&sm.q_full, n_q) && wait(&sm.k_full[tiles % kKStages], tiles / kKStages);
+                if (!ok) break;
+                tc_fence_after();
+                if (n_t[0] > 0) scores(0, tiles % kKStages);
+                if (n_t[1] > 0) scores(1, tiles % kKStages);
+                tc_commit_one(&sm.k_empty[tiles % kKStages]);
+                if (n_max == 1) tc_commit_one(&sm.q_empty);
+                ++n_q;
+            }
+            for (int t = 0; ok && t < n_max; ++t, ++tiles) {
+                const int sv = tiles % kVStages, sk = (tiles + 1) % kKStages;
+                bool have_v = false, have_k = false;
 #pragma unroll
-                    for (int kk = 0; kk < D / 16; ++kk) {
-                        const uint32_t off = (kk >> 2) * (kAtom >> 4) + 2 * (kk & 3);
-                        mma_bf16_one(tm + 128 * i, a + off, bk + off, id_qk, kk > 0 ? 1u : 0u);
-                    }
-                    tc_commit_one(&sm.s_full[i]);
-                };
-                auto values = [&](int i, int t) {
-                    const uint64_t bv = dv + (kTileBytes >> 4) * (t % kVStages);
-#pragma unroll
-                    for (int kk = 0; kk < 8; ++kk)
-                        mma_bf16_tmem_a_one(tm + kColO + 128 * i, tm + 128 * i + 8 * kk, bv + 128 * kk, id_pv,
-                                            (t > 0 || kk > 0) ? 1u : 0u);
-                };
-                auto wait = [&](uint64_t* bar, int phase) {
-                    return __all_sync(0xFFFFFFFFu, mbar_wait(bar, phase & 1, p.timeout_ns, &sm.abort)) != 0;
-                };
-                bool ok = wait(&sm.bar_q, 0) && wait(&sm.k_full[0], 0);
-                if (ok) {
-                    tc_fence_after();
-                    if (n_t[0] > 0) scores(0, 0);
-                    if (n_t[1] > 0) scores(1, 0);
-                    tc_commit_one(&sm.k_empty[0]);
-                }
-                for (int t = 0; ok && t < n_max; ++t) {
-                    bool have_v = false, have_k = false;
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        if (!ok || t >= n_t[i]) continue;
-                        ok = wait(&sm.p_full[i], t);
-                        if (ok && !have_v) {
-                            ok = wait(&sm.v_full[t % kVStages], t / kVStages) &&
-                                 (t != t_ragged || wait(&sm.v_clean[t % kVStages], 0));
-                            have_v = true;
+                for (int i = 0; i < 2; ++i) {
+                    if (!ok || t >= n_t[i]) continue;
+                    ok = wait(&sm.p_full[i], p_ph[i]);
+                    p_ph[i] ^= 1u;
+                    if (ok && !have_v) {
+                        ok = wait(&sm.v_full[sv], tiles / kVStages);
+                        if (ok && t == t_ragged) {
+                            ok = wait(&sm.v_clean[sv], clean_ph >> sv);
+                            clean_ph ^= 1u << sv;
                         }
+                        have_v = true;
+                    }
+                    if (!ok) continue;
+                    tc_fence_after();
+                    values(i, sv, t > 0);
+                    if (t + 1 == n_t[i]) {
+                        tc_commit_one(&sm.o_full[i]);
+                        continue;
+                    }
+                    if (!have_k) {
+                        ok = wait(&sm.k_full[sk], (tiles + 1) / kKStages);
+                        have_k = true;
                         if (!ok) continue;
                         tc_fence_after();
-                        values(i, t);
-                        if (t + 1 == n_t[i]) {
-                            tc_commit_one(&sm.o_full[i]);
-                            continue;
-                        }
-                        if (!have_k) {
-                            ok = wait(&sm.k_full[(t + 1) % kKStages], (t + 1) / kKStages);
-                            have_k = true;
-                            if (!ok) continue;
-                            tc_fence_after();
-                        }
-                        scores(i, t + 1);
                     }
-                    if (!ok) break;
-                    tc_commit_one(&sm.v_empty[t % kVStages]);
-                    if (t + 1 < n_max) tc_commit_one(&sm.k_empty[(t + 1) % kKStages]);
+                    scores(i, sk);
                 }
-                if (!ok) {
-                    if (lane == 0) raise_abort(sm, p);
-                    int dummy = 0;
-                    tc_commit_one(&sm.drain);  // wait until every product issued has retired
-                    mbar_wait(&sm.drain, 0, p.timeout_ns, &dummy);
-                }
+                if (!ok) break;
+                tc_commit_one(&sm.v_empty[sv]);
+                if (t + 1 < n_max) tc_commit_one(&sm.k_empty[sk]);
+                if (t + 2 == n_max) tc_commit_one(&sm.q_empty);
             }
-        } else if (warp < 8) {
-            warpgroup_reg_inc<kSoftmaxRegs>();
-            const int i = warp >> 2, r = tid & 127;
-            const uint32_t lane_addr = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
-            const uint32_t s_col = lane_addr + 128 * i, o_col = lane_addr + kColO + 128 * i;
-            const int first = tok0 + i * p.n_tok;
-            const int tl = r / p.G, h = r - tl * p.G, tok = first + tl;
-            const bool row_valid = tl < p.n_tok && tok < nq;
+            if (!ok) break;
+            give_back(n);
+        }
+        if (!ok) {
+            if (lane == 0) raise_abort(sm, p);
+            int dummy = 0;
+            tc_commit_one(&sm.drain);  // wait until every product issued has retired
+            mbar_wait(&sm.drain, 0, p.timeout_ns, &dummy);
+        }
+    } else {
+        warpgroup_reg_inc<kSoftmaxRegs>();
+        const int i = warp >> 2, r = tid & 127;
+        const uint32_t lane_addr = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+        const uint32_t s_col = lane_addr + 128 * i, o_col = lane_addr + kColO + 128 * i;
+        const int tl = r / p.G, h = r - tl * p.G;
+        uint32_t s_ph = 0, o_ph = 0;
+        bool ok = true;
+        Item it;
+        for (int n = 0; take(n, it, ok); ++n) {
+            const int n_t = key_tiles(p, it, i);
+            const int first = it.tok0 + i * p.n_tok, tok = first + tl;
+            const bool row_valid = tl < p.n_tok && tok < it.nq;
             // keys that this row and the tile's first row see
-            const int lim = p.causal ? min(nk, nk - nq + 1 + tok) : nk;
-            const int lim0 = p.causal ? min(nk, nk - nq + 1 + first) : nk;
+            const int lim = p.causal ? min(it.nk, it.nk - it.nq + 1 + tok) : it.nk;
+            const int lim0 = p.causal ? min(it.nk, it.nk - it.nq + 1 + first) : it.nk;
             float m = kNoMax, l = 0.0f;
-            bool ok = true;
-            for (int t = 0; ok && t < n_t[i]; ++t)
-                ok = softmax_tile<D>(sm, p, t, i, s_col, o_col, lim, (t + 1) * kTile > lim0, m, l);
-            if (ok && n_t[i] > 0) ok = __all_sync(0xFFFFFFFFu, mbar_wait(&sm.o_full[i], 0, p.timeout_ns, &sm.abort));
-            if (!ok) raise_abort(sm, p);
-            if (ok && first < nq) {
-                const int64_t row = static_cast<int64_t>(q0 + tok) * p.Hq + hk * p.G + h;
+            for (int t = 0; ok && t < n_t; ++t, s_ph ^= 1u)
+                ok = softmax_tile<D>(sm, p, t, i, s_ph, s_col, o_col, lim, (t + 1) * kTile > lim0, m, l);
+            if (ok && n_t > 0) {
+                ok = wait(&sm.o_full[i], o_ph);
+                o_ph ^= 1u;
+            }
+            if (!ok) break;
+            if (first < it.nq) {
+                const int64_t row = static_cast<int64_t>(it.q0 + tok) * p.Hq + it.hk * p.G + h;
                 const float inv = l == 0.0f ? 0.0f : 1.0f / l;
                 tc_fence_after();
                 for (int c = 0; c < D / 32; ++c) {
                     uint32_t rr[32];
-                    if (n_t[i] > 0) {
+                    if (n_t > 0) {
                         tmem_ld32(o_col + 32 * c, rr);
                         tmem_ld_wait();
                         tmem_reg_dep(rr);
@@ -472,9 +580,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 if (row_valid && p.lse) p.lse[row] = l == 0.0f ? -INFINITY : (m + __log2f(l)) * 0.6931471805599453f;
             }
-        } else {
-            warpgroup_reg_dec<kHelperRegs>();
+            give_back(n);
         }
+        if (!ok) raise_abort(sm, p);
     }
 
     tc_fence_before();

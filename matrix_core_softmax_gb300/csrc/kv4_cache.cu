@@ -23,6 +23,7 @@ namespace fsa {
 namespace {
 
 constexpr int kThreads = 256;
+constexpr int kTokens = kThreads / 4;  // tokens of a block, all of one head
 
 // Byte address of the group and the row in it that slot s of head h lives in.
 __device__ __forceinline__ int64_t group_of(int64_t s, int h, int H, int page_size, int gbytes, int* row) {
@@ -41,12 +42,12 @@ __global__ void __launch_bounds__(kThreads) kv4_append_kernel(
     constexpr Kv4Layout L = kv4_layout(D);
     const bool is_v = blockIdx.y != 0;
     const int t = threadIdx.x & 3;
-    const int64_t row_id = blockIdx.x * static_cast<int64_t>(kThreads / 4) + (threadIdx.x >> 2);
+    const unsigned chunk = blockIdx.x / H;
+    const int h = blockIdx.x - chunk * H;
+    const int64_t tok = chunk * static_cast<int64_t>(kTokens) + (threadIdx.x >> 2);
     // a quad's four lanes take the same way through every branch, so the
     // shuffles below name the quad
-    if (row_id >= T * H) return;
-    const int64_t tok = row_id / H;
-    const int h = static_cast<int>(row_id - tok * H);
+    if (tok >= T) return;
     const int64_t s = __ldg(slots + tok);
     if (s < 0) return;
     if (s >= capacity) {
@@ -113,10 +114,10 @@ __global__ void __launch_bounds__(kThreads) kv4_read_kernel(
     constexpr Kv4Layout L = kv4_layout(D);
     const bool is_v = blockIdx.y != 0;
     const int t = threadIdx.x & 3;
-    const int64_t row_id = blockIdx.x * static_cast<int64_t>(kThreads / 4) + (threadIdx.x >> 2);
-    if (row_id >= T * H) return;
-    const int64_t tok = row_id / H;
-    const int h = static_cast<int>(row_id - tok * H);
+    const unsigned chunk = blockIdx.x / H;
+    const int h = blockIdx.x - chunk * H;
+    const int64_t tok = chunk * static_cast<int64_t>(kTokens) + (threadIdx.x >> 2);
+    if (tok >= T) return;
     const int64_t s = __ldg(slots + tok);
     uint32_t w[kB] = {}, sc = 0;
     if (s >= capacity && t == 0) atomicOr(err_word, kErrBadIndex);
@@ -152,8 +153,13 @@ __global__ void __launch_bounds__(kThreads) kv4_read_kernel(
     }
 }
 
-dim3 grid_of(int64_t rows) {
-    return dim3(static_cast<unsigned>((rows + kThreads / 4 - 1) / (kThreads / 4)), 2);
+// Blocks of the heads of one token chunk are neighbours, so a token's rows are
+// read or written together.
+cudaError_t grid_of(const Kv4Rows& a, dim3* grid) {
+    const int64_t blocks = (a.T + kTokens - 1) / kTokens * a.H;
+    if (blocks > 0x7FFFFFFF) return cudaErrorInvalidValue;
+    *grid = dim3(static_cast<unsigned>(blocks), 2);
+    return cudaSuccess;
 }
 
 }  // namespace
@@ -161,7 +167,9 @@ dim3 grid_of(int64_t rows) {
 cudaError_t launch_kv4_append(const Kv4Rows& a, uint8_t* cache, cudaStream_t st) {
     const uint16_t* k = static_cast<const uint16_t*>(a.k);
     const uint16_t* v = static_cast<const uint16_t*>(a.v);
-    const dim3 grid = grid_of(a.T * a.H);
+    dim3 grid;
+    const cudaError_t e = grid_of(a, &grid);
+    if (e != cudaSuccess) return e;
     if (a.D == 128)
         kv4_append_kernel<128><<<grid, kThreads, 0, st>>>(k, v, a.k_stride, a.v_stride, a.slots, a.T, a.H, cache,
                                                           a.capacity, a.page_size, a.err_word);
@@ -174,7 +182,9 @@ cudaError_t launch_kv4_append(const Kv4Rows& a, uint8_t* cache, cudaStream_t st)
 cudaError_t launch_kv4_read(const Kv4Rows& a, const uint8_t* cache, cudaStream_t st) {
     uint16_t* k = static_cast<uint16_t*>(const_cast<void*>(a.k));
     uint16_t* v = static_cast<uint16_t*>(const_cast<void*>(a.v));
-    const dim3 grid = grid_of(a.T * a.H);
+    dim3 grid;
+    const cudaError_t e = grid_of(a, &grid);
+    if (e != cudaSuccess) return e;
     if (a.D == 128)
         kv4_read_kernel<128><<<grid, kThreads, 0, st>>>(cache, a.slots, a.T, a.H, a.capacity, a.page_size, k, v,
                                                         a.k_stride, a.v_stride, a.err_word);

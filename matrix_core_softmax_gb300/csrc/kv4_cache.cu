@@ -33,6 +33,39 @@ __device__ __forceinline__ int64_t group_of(int64_t s, int h, int H, int page_si
     return ((page * H + h) * (page_size / kKv4Group) + (r / kKv4Group)) * gbytes;
 }
 
+__device__ __forceinline__ uint32_t max16x2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("max.u16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+
+// X + 127 of the scale rule for a block whose largest magnitude has the bf16
+// pattern `amax`: e - 2, one more beyond 1.5 * 2^e (the 0x3F carries into the
+// exponent from mantissa 0x41 on), at least 0 -- where every subnormal lands.
+__device__ __forceinline__ uint32_t e2m1_scale_byte(uint32_t amax) {
+    return static_cast<uint32_t>(max(static_cast<int>((amax + 0x3Fu) >> 7) - 2, 0));
+}
+
+// Eight bf16 values (four pairs) times f, rounded to E2M1 codes, value i in
+// nibble i.  (f is a power of two and no product leaves FP32's normal range.)
+__device__ __forceinline__ uint32_t e2m1x8(const uint32_t (&u)[4], float f) {
+    float2 v[4];
+    const float2 f2 = make_float2(f, f);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        v[i] = __fmul2_rn(make_float2(__uint_as_float(u[i] << 16), __uint_as_float(u[i] & 0xFFFF0000u)), f2);
+    uint32_t r;
+    asm("{\n.reg .b8 a, b, c, d;\n"
+        "cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n"
+        "cvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n"
+        "cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n"
+        "cvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n"
+        "mov.b32 %0, {a, b, c, d};\n}"
+        : "=r"(r)
+        : "f"(v[0].x), "f"(v[0].y), "f"(v[1].x), "f"(v[1].y), "f"(v[2].x), "f"(v[2].y), "f"(v[3].x), "f"(v[3].y));
+    return r;
+}
+
 template <int D>
 __global__ void __launch_bounds__(kThreads) kv4_append_kernel(
     const uint16_t* __restrict__ k, const uint16_t* __restrict__ v, int64_t k_stride, int64_t v_stride,
@@ -63,19 +96,13 @@ __global__ void __launch_bounds__(kThreads) kv4_append_kernel(
 #pragma unroll
     for (int b = 0; b < kB; ++b) {
         const uint32_t u[4] = {x[b].x, x[b].y, x[b].z, x[b].w};
-        uint32_t m = 0;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) m = max(m, max(u[i] & 0x7FFFu, (u[i] >> 16) & 0x7FFFu));
-        m = max(m, __shfl_xor_sync(quad, m, 1));
-        m = max(m, __shfl_xor_sync(quad, m, 2));
-        const int X = mx_scale_exp(m, fmt_consts(ELEM_E2M1));
-        const float f = pow2_neg(X);
-        uint32_t c = 0;
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            c |= (cvt_e2m1x2(__uint_as_float(u[i] << 16) * f, __uint_as_float(u[i] & 0xFFFF0000u) * f) & 0xFFu) << (8 * i);
-        w[b] = c;
-        sc |= static_cast<uint32_t>(X + 127) << (8 * b);
+        // magnitudes of bf16 values order like their bit patterns
+        uint32_t m = max16x2(max16x2(u[0] & 0x7FFF7FFFu, u[1] & 0x7FFF7FFFu), max16x2(u[2] & 0x7FFF7FFFu, u[3] & 0x7FFF7FFFu));
+        m = max16x2(m, __shfl_xor_sync(quad, m, 1));
+        m = max16x2(m, __shfl_xor_sync(quad, m, 2));
+        const uint32_t byte = e2m1_scale_byte(max(m & 0xFFFFu, m >> 16));
+        w[b] = e2m1x8(u, __uint_as_float((254u - byte) << 23));
+        sc |= byte << (8 * b);
     }
     int row;
     uint8_t* g = cache + group_of(s, h, H, page_size, kv4_group_bytes(D), &row);

@@ -8,6 +8,7 @@ loaded, every call raises.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import threading
 
@@ -510,8 +511,10 @@ def kv4_read(cache, slots, *, out_k=None, out_v=None, stream=None):
     return out_k, out_v
 
 
+@functools.lru_cache(maxsize=1024)
 def kv4_attention_workspace_size(B: int, Sq: int, n_heads: int, n_kv_heads: int, D: int, page_size: int,
                                  max_pages: int) -> int:
+    """Bytes of workspace of kv4_attention_fwd (fsa_kv4_attention_workspace_size)."""
     return int(load().fsa_kv4_attention_workspace_size(B, Sq, n_heads, n_kv_heads, D, page_size, max_pages))
 
 
@@ -551,15 +554,14 @@ def kv4_attention_fwd(q, cache, page_table, seq_lens, *, out=None, return_lse: b
         _plain(lse, "lse", torch.float32, (B, Sq, Hq), dev)
     elif return_lse:
         lse = torch.empty((B, Sq, Hq), dtype=torch.float32, device=cache.device)
-    lib = load()
-    ws, ws_bytes = None, lib.fsa_kv4_attention_workspace_size(B, Sq, Hq, Hkv, D, page_size, max_pages)
+    ws, ws_bytes = None, kv4_attention_workspace_size(B, Sq, Hq, Hkv, D, page_size, max_pages)
     if workspace is not None:
         if not workspace.is_contiguous() or workspace.get_device() != dev:
             raise ValueError(f"workspace must be a contiguous tensor on cuda:{dev}")
         ws, ws_bytes = workspace, workspace.numel() * workspace.element_size()
     elif ws_bytes:
         ws = torch.empty(ws_bytes, dtype=torch.uint8, device=cache.device)
-    _check(lib.fsa_kv4_attention_fwd(q.data_ptr(), q_stride, cache.data_ptr(), page_table.data_ptr(), seq_lens.data_ptr(),
+    _check(load().fsa_kv4_attention_fwd(q.data_ptr(), q_stride, cache.data_ptr(), page_table.data_ptr(), seq_lens.data_ptr(),
                                      o.data_ptr(), None if lse is None else lse.data_ptr(), B, Sq, Hq, Hkv, D, pages,
                                      page_size, max_pages, sm_scale, None if ws is None else ws.data_ptr(), ws_bytes,
                                      _raw_stream(dev)), "fsa_kv4_attention_fwd")

@@ -37,15 +37,19 @@
 // scaled by a power of two to [1, 2) per row, in which f16 holds a bf16 value
 // exactly down to 2^-14 of the row's largest and to 2^-25 of it below.
 //
-// Work split.  The cache's groups of all (sequence, key head, 16-row tile)
-// segments form one line, cut into equal shares, one per resident block: long
-// contexts spread over the GPU, ragged batches balance, and a block leaves at
-// most two unfinished segments (the one it starts in and the one it ends in) to
-// the second kernel, which joins them.  Where no sequence can be longer than
-// kWholeGroups groups a block takes one whole segment and there is no second
-// kernel.  Each of a block's eight warps runs its own ring of bulk copies, one
-// 32-key group (4352 bytes at D = 128) a copy, and its own softmax state; a
-// segment's end joins the eight.
+// Work split.  The cache's groups of all (sequence, key head, 8- or 16-row tile)
+// segments form one line, cut into equal shares, one per resident block, and a
+// share into equal parts, one per warp: long contexts spread over the GPU and
+// ragged batches balance.  A warp runs along its part on its own: a ring of
+// bulk copies (one 32-key group, 4352 bytes at D = 128, a copy) that reaches
+// over the segments' ends, its own softmax state, and the output of every
+// segment that lies in its part as a whole.  Of the others it leaves at most
+// two pieces, the segment it starts in and the one it ends in; the block joins
+// its warps' pieces, leaves at most two of its own, and a second kernel joins
+// those.  (With blocks that walked over segments together and met at each end,
+// 64 ragged sequences of up to 2000 keys took 40.7 us.)  Where no sequence can
+// be longer than kWholeGroups groups a block takes one segment and there is no
+// second kernel.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -59,7 +63,8 @@
 namespace fsa {
 namespace {
 
-constexpr int kWarps = 8, kThreads = 32 * kWarps;
+constexpr int kSplitWarps = 8;    // warps of a block of the split form and of the join
+constexpr int kJoinThreads = 256;
 constexpr int kStages = 2;        // (three: 1 % slower, the merge and the ring leave less L1)
 constexpr int kResident = 304;    // two blocks on each of 152 SMs
 constexpr int kMaxBlocks = 2 * kResident;
@@ -67,9 +72,19 @@ constexpr int kMaxBlocks = 2 * kResident;
 // more of them (64 x 32768 keys: 234 against 239 us; with small shares the
 // further parts cost more than that: 131072 keys of one sequence 69 against 55).
 constexpr int64_t kLongShare = 1024;
-constexpr int kMinShare = kWarps; // groups of a block, at least one a warp
-constexpr int kWholeGroups = 16;  // longest segment (groups) that one block takes whole
-constexpr int kManySegments = 64; // from here on the join takes four rows a block
+constexpr int kMinShare = kSplitWarps; // groups of a block, at least one a warp
+// A block takes a whole segment up to this many groups, twice as many where
+// there are many segments.  8 key heads of D = 128, whole against split: one
+// sequence of 1000 keys 8.4 / 9.2 us, of 2000 12.8 / 10.0; 64 sequences of up to
+// 1000 keys 19.9 / 24.2, of up to 2000 29.6 / 31.5, of up to 4000 50 / 47.
+constexpr int kWholeGroups = 32;
+constexpr int kManySegments = 64; // from here on the join takes four rows a block, too
+// More whole segments than fit the GPU in blocks of eight warps run in blocks of
+// four: twice as many segments at a time wait for their first keys.  8 key
+// heads, four warps against eight: 64 sequences of up to 500 keys 10.7 / 14.6 us,
+// of up to 1000 16.0 / 20.4, of up to 2000 29.6 / 30.1; 8 sequences of up to 1000
+// 10.2 / 9.0, of up to 2000 16.6 / 13.4.
+constexpr int kFewWarps = 8, kManyWarps = 4;
 constexpr uint32_t kNoGroup = 0xFFFFFFFFu;
 constexpr float kNoMax = -1e30f;
 constexpr float kLag = 4.0f;      // how far M may lag behind (log2)
@@ -90,15 +105,24 @@ struct Params {
     unsigned int* err_word;
 };
 
-template <int D, int NT>
+// A piece of a segment: what one warp made of the groups of it in its part.
+struct Piece {
+    int64_t seg_x;  // the segment's first group on the line
+    int b, seg, ng; // sequence (-1: no piece), segment of it, its groups
+};
+
+template <int D, int NT, int kWarps>
 struct __align__(128) Smem {
-    uint8_t ring[kWarps][kStages][kv4_group_bytes(D)];
+    static constexpr int kPitch = D + 4;  // floats of a row of a piece
+    uint8_t ring[kWarps][kStages][kv4_group_bytes(D)];  // in the end: the warp's last piece
+    float first[kWarps][8 * NT][kPitch];                // the segment a warp starts in
     float4 kscale[kWarps][kKv4Group];      // 2^X of the key blocks, by row position
     float2 ykey[kWarps][kKv4Group];        // -y and 2^y of each key, by row position
     uint32_t vscale[kWarps][4][2][2][4];   // f16 pairs: [t][16-key step][half][block]
     uint64_t full[kWarps][kStages];
-    float m[kWarps][8 * NT], l[kWarps][8 * NT];
-    int64_t scan[kThreads];
+    float m[kWarps][2][8 * NT], l[kWarps][2][8 * NT];
+    Piece piece[kWarps][2];  // [0] in first, [1] in ring
+    int64_t scan[kWarps];
     int64_t first_x;
     int first_b;
     int abort;
@@ -177,6 +201,13 @@ struct Row {
 };
 __device__ __forceinline__ Row row_of(const Params& p, int r) { return {r / p.G, r % p.G}; }
 
+// Segment of a sequence of ng-group segments that its group `rel` lies in (a
+// 64-bit division takes 1 us, and every warp waits for two of these).
+__device__ __forceinline__ int segment_at(int64_t rel, int ng) {
+    if (rel <= 0x7FFFFFFF) return static_cast<int>(static_cast<uint32_t>(rel) / static_cast<uint32_t>(ng));
+    return static_cast<int>(rel / ng);
+}
+
 // Groups of a block's share of `all` groups.
 __device__ __forceinline__ int64_t share_of(int64_t all, int n_blocks) {
     return max(static_cast<int64_t>(kMinShare), (all + n_blocks - 1) / n_blocks);
@@ -195,32 +226,41 @@ __device__ __forceinline__ void write_row(const Params& p, int b, int hk, int r,
     if (p.lse && d4 == 0) p.lse[row] = l == 0.0f ? -INFINITY : (m + __log2f(l)) * 0.6931471805599453f;
 }
 
-template <int D, int NT>
-__global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) kv4_attn_kernel(const Params p) {
+// kWhole: a block takes one segment, without a walk over sequences, segments
+// that end inside a warp's part or pieces left to the second kernel; the short
+// calls that it serves wait for the kernel's instructions, too (300 keys: 7.5 us
+// with the general form).
+template <int D, int NT, bool kWhole, int kWarps>
+__global__ void __launch_bounds__(32 * kWarps, (NT == 1 ? 16 : 8) / kWarps) kv4_attn_kernel(const Params p) {
+    constexpr int kThreads = 32 * kWarps;
     constexpr int kB = D / 32;
     constexpr int kGroupBytes = kv4_group_bytes(D);
     constexpr Kv4Layout L = kv4_layout(D);
     constexpr int kRows = 8 * NT;
-    constexpr int kPitch = D + 4;  // floats of a row in the merge buffer
-    static_assert(kRows * kPitch * 4 <= kStages * kGroupBytes, "merge buffer exceeds a warp's ring");
+    constexpr int kPitch = Smem<D, NT, kWarps>::kPitch;
+    static_assert(kRows * kPitch * 4 <= kStages * kGroupBytes, "a piece exceeds a warp's ring");
     extern __shared__ __align__(128) uint8_t smem_raw[];
-    Smem<D, NT>& sm = *reinterpret_cast<Smem<D, NT>*>(smem_raw);
+    Smem<D, NT, kWarps>& sm = *reinterpret_cast<Smem<D, NT, kWarps>*>(smem_raw);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int g = lane >> 2, t = lane & 3;
 
     if (tid == 0) sm.abort = 0;
+    if (lane < 2) sm.piece[warp][lane].b = -1;
     if (lane < kStages) mbar_init(&sm.full[warp][lane], 1);
     fence_mbar_init();
 
     // this block's share [x, x_end) of the line of groups, and where it starts:
     // sequence b, its first group at x_seq
     int64_t x, x_end, x_seq;
-    int b;
+    int b, len;
     const int n_seg = p.Hkv * p.n_rt;  // segments of a sequence
-    if (!p.partial) {
+    if constexpr (kWhole) {
         __syncthreads();
         b = blockIdx.x / n_seg;
-        const int ng = seq_groups(p, b);
+        bool bad;
+        len = seq_len(p, b, &bad);
+        const int ng = (len + kKv4Group - 1) / kKv4Group;
+        if (bad && tid == 0) atomicOr(p.err_word, kErrBadIndex);
         const int seg = blockIdx.x - b * n_seg;
         x_seq = 0;
         x = static_cast<int64_t>(seg) * ng;
@@ -236,9 +276,6 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) kv4_attn_kernel(con
                     if (p.lse && e % D == 0) p.lse[row] = -INFINITY;
                 }
             }
-            bool bad;
-            seq_len(p, b, &bad);
-            if (bad && tid == 0) atomicOr(p.err_word, kErrBadIndex);
             return;
         }
     } else {
@@ -283,60 +320,81 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) kv4_attn_kernel(con
         __syncthreads();
         b = sm.first_b;
         x_seq = sm.first_x;
+        bool bad;
+        len = seq_len(p, b, &bad);
     }
-    const int64_t x_begin = x;
     const int gpp = p.page_size / kKv4Group;
-    int st = 0;              // stage of the next group, and its phase
-    uint32_t ph = 0;
+    // this warp's part [pos, pos_end) of the share
+    const int64_t pos_begin = x + (x_end - x) * warp / kWarps, pos_end = x + (x_end - x) * (warp + 1) / kWarps;
+    const int count = static_cast<int>(pos_end - pos_begin);
+
+    // copies, by the warp's group number j
+    uint32_t ids = 0;        // lane i: the cache's group number of the warp's group 32 n + i
     uint32_t bad_stage = 0;  // stages whose group has no page
-
-    while (x < x_end) {
-        bool bad_len;
-        const int len = seq_len(p, b, &bad_len), ng = (len + kKv4Group - 1) / kKv4Group;
-        if (ng == 0 || x >= x_seq + static_cast<int64_t>(ng) * n_seg) {
-            x_seq += static_cast<int64_t>(ng) * n_seg;
-            ++b;
-            continue;
-        }
-        if (!p.partial && bad_len && tid == 0) atomicOr(p.err_word, kErrBadIndex);
-        const int seg = static_cast<int>((x - x_seq) / ng);
-        const int64_t seg_x = x_seq + static_cast<int64_t>(seg) * ng;
-        const int g0 = static_cast<int>(x - seg_x);                                       // first group of the part
-        const int g1 = static_cast<int>(min(static_cast<int64_t>(ng), x_end - seg_x));    // end of the part
-        const int hk = seg / p.n_rt, r0 = (seg % p.n_rt) * kRows;
-        const int n_rows = min(kRows, p.Sq * p.G - r0);
-
-        const int count = g1 - g0 > warp ? (g1 - g0 - warp + kWarps - 1) / kWarps : 0;  // this warp's groups
-        const int* table = p.page_table + static_cast<int64_t>(b) * p.max_pages;
-        uint32_t ids = 0;  // lane j: the cache's group number of the warp's group 32 n + j
-        int st_in = st;    // stage of the next copy
-        auto issue = [&](int j) {
-            if ((j & 31) == 0) {
-                const int gi = g0 + warp + kWarps * (j + lane), pi = gi / gpp;
-                ids = kNoGroup;
-                if (j + lane < count) {
-                    const int page = __ldg(table + pi);
-                    if (page >= 0 && page < p.num_pages)  // (a 16 TB cache would have 2^32 groups)
-                        ids = (static_cast<uint32_t>(page) * p.Hkv + hk) * gpp + (gi - pi * gpp);
-                    else
-                        atomicOr(p.err_word, kErrBadIndex);
-                }
-            }
-            const uint32_t id = __shfl_sync(0xFFFFFFFFu, ids, j & 31);
-            bad_stage &= ~(1u << st_in);
-            if (id == kNoGroup) bad_stage |= 1u << st_in;
-            if (lane == 0) {
-                if (id == kNoGroup) {
-                    mbar_arrive(&sm.full[warp][st_in]);
+    int ib = b;              // sequence that the next ids are looked for from,
+    int64_t ix = x_seq;      // its first group and the groups of its segments
+    int ing = (len + kKv4Group - 1) / kKv4Group;
+    auto issue = [&](int j) {
+        if ((j & 31) == 0) {
+            const int64_t pos = pos_begin + j + lane;
+            ids = kNoGroup;
+            if (pos < pos_end) {
+                int seg, gi;
+                if constexpr (kWhole) {
+                    seg = blockIdx.x - b * n_seg;
+                    gi = static_cast<int>(pos - x);
                 } else {
-                    mbar_arrive_expect_tx(&sm.full[warp][st_in], kGroupBytes);
-                    bulk_load(sm.ring[warp][st_in], p.cache + static_cast<uint64_t>(id) * kGroupBytes, kGroupBytes,
-                              &sm.full[warp][st_in]);
+                    while (pos >= ix + static_cast<int64_t>(ing) * n_seg) {
+                        ix += static_cast<int64_t>(ing) * n_seg;
+                        ing = seq_groups(p, ++ib);
+                    }
+                    seg = segment_at(pos - ix, ing);
+                    gi = static_cast<int>(pos - ix - static_cast<int64_t>(seg) * ing);
                 }
+                const int pi = gi / gpp;
+                const int page = __ldg(p.page_table + static_cast<int64_t>(ib) * p.max_pages + pi);
+                if (page >= 0 && page < p.num_pages)  // (a 9 TB cache would have 2^32 groups)
+                    ids = (static_cast<uint32_t>(page) * p.Hkv + seg / p.n_rt) * gpp + (gi - pi * gpp);
+                else
+                    atomicOr(p.err_word, kErrBadIndex);
             }
-            if (++st_in == kStages) st_in = 0;
-        };
-        for (int j = 0; j < min(count, kStages); ++j) issue(j);
+            if constexpr (!kWhole) {
+            const int last = min(31, count - 1 - j);
+            ib = __shfl_sync(0xFFFFFFFFu, ib, last);
+            ix = __shfl_sync(0xFFFFFFFFu, ix, last);
+            ing = __shfl_sync(0xFFFFFFFFu, ing, last);
+            }
+        }
+        const uint32_t id = __shfl_sync(0xFFFFFFFFu, ids, j & 31);
+        const int st = j % kStages;
+        bad_stage &= ~(1u << st);
+        if (id == kNoGroup) bad_stage |= 1u << st;
+        if (lane == 0) {
+            if (id == kNoGroup) {
+                mbar_arrive(&sm.full[warp][st]);
+            } else {
+                mbar_arrive_expect_tx(&sm.full[warp][st], kGroupBytes);
+                bulk_load(sm.ring[warp][st], p.cache + static_cast<uint64_t>(id) * kGroupBytes, kGroupBytes, &sm.full[warp][st]);
+            }
+        }
+    };
+    for (int j = 0; j < min(count, kStages); ++j) issue(j);
+
+    int i = 0;  // the warp's groups done
+    bool ok = true;
+    while (ok && i < count) {
+        const int64_t pos = pos_begin + i;
+        int ng = (len + kKv4Group - 1) / kKv4Group;
+        while (!kWhole && pos >= x_seq + static_cast<int64_t>(ng) * n_seg) {
+            x_seq += static_cast<int64_t>(ng) * n_seg;
+            bool bad;
+            len = seq_len(p, ++b, &bad);
+            ng = (len + kKv4Group - 1) / kKv4Group;
+        }
+        const int seg = kWhole ? blockIdx.x - b * n_seg : segment_at(pos - x_seq, ng);
+        const int64_t seg_x = x_seq + static_cast<int64_t>(seg) * ng;
+        const int i_end = kWhole ? count : static_cast<int>(min(seg_x + ng, pos_end) - pos_begin);  // end of the segment's groups
+        const int hk = seg / p.n_rt, r0 = (seg % p.n_rt) * kRows;
 
         // the query rows as B fragments, in f16 relative to each row's largest
         uint32_t qf[NT][kB][4];
@@ -384,15 +442,14 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) kv4_attn_kernel(con
 #pragma unroll
         for (int n = 0; n < NT; ++n) M[n][0] = M[n][1] = kNoMax;
         uint32_t R02 = 0, R13 = 0;  // largest value scale bytes so far
-        bool ok = true;
-        int i = 0;
 
-        for (; i < count; ++i) {
-            ok = __all_sync(0xFFFFFFFFu, mbar_wait(&sm.full[warp][st], ph, p.timeout_ns, &sm.abort));
+        for (; i < i_end; ++i) {
+            const int st = i % kStages;
+            ok = __all_sync(0xFFFFFFFFu, mbar_wait(&sm.full[warp][st], (i / kStages) & 1, p.timeout_ns, &sm.abort));
             if (!ok) break;
             if (!((bad_stage >> st) & 1u)) {
                 const uint8_t* buf = sm.ring[warp][st];
-                const int key0 = (g0 + warp + kWarps * i) * kKv4Group;
+                const int key0 = static_cast<int>(pos_begin + i - seg_x) * kKv4Group;
 
                 // scales: lane = key.  A zero scale byte (2^-127, a zero block as a
                 // rule) counts as zero.  Value scale bytes as 16-bit pairs, blocks 0
@@ -607,86 +664,112 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) kv4_attn_kernel(con
             }
             __syncwarp();
             if (i + kStages < count) issue(i + kStages);
-            if (++st == kStages) {
-                st = 0;
-                ph ^= 1u;
-            }
         }
-        if (!ok) {
-            // give up: let this warp's copies in flight land, then leave together
-            if (lane == 0) {
-                sm.abort = 1;
-                atomicOr(p.err_word, kErrTimeout);
-            }
-            int dummy = 0;
-            for (int j = i; j < min(count, i + kStages); ++j) {
-                mbar_wait(&sm.full[warp][st], ph, p.timeout_ns, &dummy);
-                if (++st == kStages) {
-                    st = 0;
-                    ph ^= 1u;
-                }
-            }
-        }
+        if (!ok) break;
 
-        // the second kernel's blocks may start as these finish
-        asm volatile("griddepcontrol.launch_dependents;");
-        // this warp's result: O in true units relative to 2^M, into its own ring
-        float* mine = reinterpret_cast<float*>(sm.ring[warp][0]);
+        // O in true units relative to 2^M
 #pragma unroll
-        for (int n = 0; n < NT; ++n) {
+        for (int c = 0; c < kB; ++c) {
+            const float f0 = 1.0f / static_cast<float>(1 << kHeadroom);
+            const float f1 = pow2f(static_cast<int>(((c & 1 ? R13 : R02) >> (16 * (c >> 1))) & 0xFFu) - 127);
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    O[n][c][0][e] = O[n][c][0][e] * f0 * f1;
+                    O[n][c][1][e] = O[n][c][1][e] * f0 * f1;
+                }
+        }
+        // written where the segment is complete, kept as a piece where it is not
+        const bool complete = !kWhole && seg_x >= pos_begin && seg_x + ng <= pos_end;
+        const int slot = kWhole || i == count ? 1 : 0;  // (the ring is free at the end only)
+        float* piece = slot ? reinterpret_cast<float*>(sm.ring[warp][0]) : &sm.first[warp][0][0];
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
-                for (int o = 4; o < 32; o <<= 1) l[n][j] += __shfl_xor_sync(0xFFFFFFFFu, l[n][j], o);
-                if (g == 0) {
-                    sm.m[warp][8 * n + 2 * t + j] = M[n][j];
-                    sm.l[warp][8 * n + 2 * t + j] = l[n][j];
+                const int r = 8 * n + 2 * t + j;
+                float lt = l[n][j];
+                for (int o = 4; o < 32; o <<= 1) lt += __shfl_xor_sync(0xFFFFFFFFu, lt, o);
+                if (!complete) {
+                    if (g == 0) {
+                        sm.m[warp][slot][r] = M[n][j];
+                        sm.l[warp][slot][r] = lt;
+                    }
+#pragma unroll
+                    for (int c = 0; c < kB; ++c)
+                        *reinterpret_cast<float4*>(piece + r * kPitch + 32 * c + 4 * g) =
+                            make_float4(O[n][c][0][j], O[n][c][0][2 + j], O[n][c][1][j], O[n][c][1][2 + j]);
+                } else if (r0 + r < p.Sq * p.G) {
+#pragma unroll
+                    for (int c = 0; c < kB; ++c)
+                        write_row<D>(p, b, hk, r0 + r, 8 * c + g,
+                                     make_float4(O[n][c][0][j], O[n][c][0][2 + j], O[n][c][1][j], O[n][c][1][2 + j]), M[n][j], lt);
                 }
             }
-#pragma unroll
-            for (int c = 0; c < kB; ++c) {
-                const float f0 = 1.0f / static_cast<float>(1 << kHeadroom), f1 = pow2f(static_cast<int>(((c & 1 ? R13 : R02) >> (16 * (c >> 1))) & 0xFFu) - 127);
-#pragma unroll
-                for (int j = 0; j < 2; ++j)
-                    *reinterpret_cast<float4*>(mine + (8 * n + 2 * t + j) * kPitch + 32 * c + 4 * g) =
-                        make_float4(O[n][c][0][j] * f0 * f1, O[n][c][0][2 + j] * f0 * f1, O[n][c][1][j] * f0 * f1,
-                                    O[n][c][1][2 + j] * f0 * f1);
-            }
+        if (!complete && lane == 0) sm.piece[warp][slot] = {seg_x, b, seg, ng};
+    }
+    if (!ok) {
+        // give up: let this warp's copies in flight land, then leave together
+        if (lane == 0) {
+            sm.abort = 1;
+            atomicOr(p.err_word, kErrTimeout);
         }
-        __syncthreads();
-        if (sm.abort) return;
-        const bool whole = g0 == 0 && g1 == ng;
-        float* part = nullptr;
-        if (!whole) part = p.partial + (2 * static_cast<int64_t>(blockIdx.x) + (seg_x < x_begin ? 0 : 1)) * (kRows * (D + 2));
+        int dummy = 0;
+        for (int j = i; j < min(count, i + kStages); ++j)
+            mbar_wait(&sm.full[warp][j % kStages], (j / kStages) & 1, p.timeout_ns, &dummy);
+    }
+    // the second kernel's blocks may start as these finish
+    if constexpr (!kWhole) asm volatile("griddepcontrol.launch_dependents;");
+    __syncthreads();
+    if (sm.abort) return;
+
+    // join the warps' pieces, segment after segment: bit k of a mask is piece k & 1
+    // of warp k / 2
+    const Piece& own = sm.piece[(lane >> 1) % kWarps][lane & 1];
+    const int own_b = lane < 2 * kWarps ? own.b : -1;
+    const int64_t own_x = own.seg_x;
+    unsigned left = __ballot_sync(0xFFFFFFFFu, own_b >= 0);
+    while (left) {
+        const int k0 = __ffs(left) - 1;
+        const int64_t seg_x = __shfl_sync(0xFFFFFFFFu, own_x, k0);
+        const unsigned group = __ballot_sync(0xFFFFFFFFu, own_b >= 0 && own_x == seg_x);
+        left &= ~group;
+        const Piece pc = sm.piece[k0 >> 1][k0 & 1];
+        const int hk = pc.seg / p.n_rt, r0 = (pc.seg % p.n_rt) * kRows;
+        const int n_rows = min(kRows, p.Sq * p.G - r0);
+        const bool whole = kWhole || (seg_x >= x && seg_x + pc.ng <= x_end);
+        float* part = whole ? nullptr : p.partial + (2 * static_cast<int64_t>(blockIdx.x) + (seg_x < x ? 0 : 1)) * (kRows * (D + 2));
         for (int e = tid; e < n_rows * (D / 4); e += kThreads) {
             const int r = e / (D / 4), d4 = e % (D / 4);
+            // (selected rather than branched on, so that the loads overlap; unrolled
+            // no further, since a short call waits for the instructions themselves)
             float m = kNoMax, lt = 0.0f;
-#pragma unroll
-            for (int w = 0; w < kWarps; ++w) m = fmaxf(m, sm.m[w][r]);
-            float4 a = make_float4(0, 0, 0, 0);
-#pragma unroll
-            for (int w = 0; w < kWarps; ++w) {
-                const float f = ex2(sm.m[w][r] - m);
-                lt = fmaf(f, sm.l[w][r], lt);
-                const float4 v = *reinterpret_cast<const float4*>(reinterpret_cast<const float*>(sm.ring[w][0]) + r * kPitch + 4 * d4);
-                a.x = fmaf(f, v.x, a.x);
-                a.y = fmaf(f, v.y, a.y);
-                a.z = fmaf(f, v.z, a.z);
-                a.w = fmaf(f, v.w, a.w);
+            float4 v = make_float4(0, 0, 0, 0);
+#pragma unroll 4
+            for (int k = kWhole ? 1 : 0; k < 2 * kWarps; k += kWhole ? 2 : 1) m = fmaxf(m, (group >> k) & 1u ? sm.m[k >> 1][k & 1][r] : kNoMax);
+#pragma unroll 4
+            for (int k = kWhole ? 1 : 0; k < 2 * kWarps; k += kWhole ? 2 : 1) {
+                const bool in = (group >> k) & 1u;
+                const float* src = (k & 1) ? reinterpret_cast<const float*>(sm.ring[k >> 1][0]) : &sm.first[k >> 1][0][0];
+                const float4 y = in ? *reinterpret_cast<const float4*>(src + r * kPitch + 4 * d4) : make_float4(0, 0, 0, 0);
+                const float f = in ? ex2(sm.m[k >> 1][k & 1][r] - m) : 0.0f;
+                lt = fmaf(f, in ? sm.l[k >> 1][k & 1][r] : 0.0f, lt);
+                v.x = fmaf(f, y.x, v.x);
+                v.y = fmaf(f, y.y, v.y);
+                v.z = fmaf(f, y.z, v.z);
+                v.w = fmaf(f, y.w, v.w);
             }
-            if (!whole) {
-                reinterpret_cast<float4*>(part)[r * (D / 4) + d4] = a;
+            if (whole) {
+                write_row<D>(p, pc.b, hk, r0 + r, d4, v, m, lt);
+            } else {
+                reinterpret_cast<float4*>(part)[r * (D / 4) + d4] = v;
                 if (d4 == 0) {
                     part[kRows * D + r] = m;
                     part[kRows * D + kRows + r] = lt;
                 }
-            } else {
-                write_row<D>(p, b, hk, r0 + r, d4, a, m, lt);
             }
         }
-        // the merge buffer becomes the ring of the next segment
-        fence_async_smem();
-        __syncthreads();
-        x = seg_x + g1;
     }
 }
 
@@ -701,9 +784,9 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) kv4_attn_kernel(con
 // overlap the end of the first kernel: what precedes the wait depends on the
 // lengths alone.
 template <int D, int NT, int kPer>
-__global__ void __launch_bounds__(kThreads) kv4_join_kernel(const Params p, int n_blocks) {
-    constexpr int kRows = 8 * NT, kLanes = D / 4, kSlices = kThreads / (kLanes * kPer);
-    __shared__ int64_t warp_sum[2][kWarps];
+__global__ void __launch_bounds__(kJoinThreads) kv4_join_kernel(const Params p, int n_blocks) {
+    constexpr int kRows = 8 * NT, kLanes = D / 4, kSlices = kJoinThreads / (kLanes * kPer);
+    __shared__ int64_t warp_sum[2][kJoinThreads / 32];
     __shared__ float row_m[kPer], row_l[kPer];
     __shared__ float fac[kPer][kMaxBlocks];
     __shared__ float4 red[kSlices][kPer * kLanes];
@@ -714,7 +797,7 @@ __global__ void __launch_bounds__(kThreads) kv4_join_kernel(const Params p, int 
     const int hk = seg / p.n_rt, r0 = (seg % p.n_rt) * kRows;
     if (r0 + r_first >= p.Sq * p.G) return;
     int64_t before = 0, total = 0;
-    for (int i = tid; i < p.B; i += kThreads) {
+    for (int i = tid; i < p.B; i += kJoinThreads) {
         const int n = seq_groups(p, i);
         total += n;
         if (i < b) before += n;
@@ -729,7 +812,7 @@ __global__ void __launch_bounds__(kThreads) kv4_join_kernel(const Params p, int 
     }
     __syncthreads();
     before = total = 0;
-    for (int w = 0; w < kWarps; ++w) {
+    for (int w = 0; w < kJoinThreads / 32; ++w) {
         before += warp_sum[0][w];
         total += warp_sum[1][w];
     }
@@ -798,8 +881,13 @@ __global__ void __launch_bounds__(kThreads) kv4_join_kernel(const Params p, int 
 // Query rows of a block: 8 or, beyond 8 rows to a key head, 16.
 int row_tiles(int rows) { return rows <= 8 ? 1 : 2; }
 
-bool takes_whole(int page_size, int max_pages) {
-    return static_cast<int64_t>(max_pages) * (page_size / kKv4Group) <= kWholeGroups;
+bool takes_whole(int64_t segments, int page_size, int max_pages) {
+    return static_cast<int64_t>(max_pages) * (page_size / kKv4Group) <= (segments >= kManySegments ? 2 : 1) * kWholeGroups;
+}
+
+int64_t segments_of(int B, int Sq, int Hq, int Hkv) {
+    const int rows = Sq * (Hq / Hkv), per = 8 * row_tiles(rows);
+    return static_cast<int64_t>(B) * Hkv * ((rows + per - 1) / per);
 }
 
 // Blocks of the split form.
@@ -809,20 +897,34 @@ int stream_blocks(int64_t segments, int page_size, int max_pages) {
     return (most >= kLongShare * kResident ? kMaxBlocks : kResident) / NT;
 }
 
+// The whole form in blocks of W warps.
+template <int D, int NT, int W>
+cudaError_t launch_whole(const Params& p, int segments, cudaStream_t st) {
+    static KernelSetup setup;
+    constexpr int smem = sizeof(Smem<D, NT, W>);
+    const cudaError_t e = setup(reinterpret_cast<const void*>(kv4_attn_kernel<D, NT, true, W>), smem, 0);
+    if (e != cudaSuccess) return e;
+    kv4_attn_kernel<D, NT, true, W><<<segments, 32 * W, smem, st>>>(p);
+    return cudaGetLastError();
+}
+
 template <int D, int NT>
 cudaError_t launch(Params p, int n_whole, cudaStream_t st) {
-    const size_t smem = sizeof(Smem<D, NT>);
-    static KernelSetup setup;
-    cudaError_t e = setup(reinterpret_cast<const void*>(kv4_attn_kernel<D, NT>), static_cast<int>(smem), 0);
-    if (e != cudaSuccess) return e;
-    const int blocks = p.partial ? stream_blocks<NT>(n_whole, p.page_size, p.max_pages) : n_whole;
-    kv4_attn_kernel<D, NT><<<blocks, kThreads, smem, st>>>(p);
-    e = cudaGetLastError();
-    if (e != cudaSuccess || !p.partial) return e;
-    cudaLaunchConfig_t cfg{};
     const bool many = n_whole >= kManySegments;
+    if (!p.partial)
+        return n_whole > kResident / NT ? launch_whole<D, NT, kManyWarps>(p, n_whole, st)
+                                        : launch_whole<D, NT, kFewWarps>(p, n_whole, st);
+    static KernelSetup setup;
+    constexpr int W = kSplitWarps, smem = sizeof(Smem<D, NT, W>);
+    cudaError_t e = setup(reinterpret_cast<const void*>(kv4_attn_kernel<D, NT, false, W>), smem, 0);
+    if (e != cudaSuccess) return e;
+    const int blocks = stream_blocks<NT>(n_whole, p.page_size, p.max_pages);
+    kv4_attn_kernel<D, NT, false, W><<<blocks, 32 * W, smem, st>>>(p);
+    e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(static_cast<unsigned>(n_whole), static_cast<unsigned>(8 * NT / (many ? 4 : 1)));
-    cfg.blockDim = dim3(kThreads);
+    cfg.blockDim = dim3(kJoinThreads);
     cfg.stream = st;
     cudaLaunchAttribute at{};
     at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -835,8 +937,8 @@ cudaError_t launch(Params p, int n_whole, cudaStream_t st) {
 
 }  // namespace
 
-size_t kv4_attention_workspace_bytes(int, int Sq, int Hq, int Hkv, int D, int page_size, int max_pages) {
-    if (takes_whole(page_size, max_pages)) return 0;
+size_t kv4_attention_workspace_bytes(int B, int Sq, int Hq, int Hkv, int D, int page_size, int max_pages) {
+    if (takes_whole(segments_of(B, Sq, Hq, Hkv), page_size, max_pages)) return 0;
     const int nt = row_tiles(Sq * (Hq / Hkv));
     return static_cast<size_t>(kMaxBlocks / nt) * 2 * (8 * nt) * (D + 2) * sizeof(float);
 }
@@ -849,7 +951,8 @@ cudaError_t launch_kv4_attention(const Kv4AttnLaunch& a, cudaStream_t st) {
     p.seq_lens = a.seq_lens;
     p.o = static_cast<uint16_t*>(a.o);
     p.lse = a.lse;
-    p.partial = takes_whole(a.page_size, a.max_pages) ? nullptr : static_cast<float*>(a.workspace);
+    const int64_t segments = segments_of(a.B, a.Sq, a.Hq, a.Hkv);
+    p.partial = takes_whole(segments, a.page_size, a.max_pages) ? nullptr : static_cast<float*>(a.workspace);
     p.q_stride = a.q_stride;
     p.num_pages = a.num_pages;
     p.B = a.B;
@@ -864,7 +967,6 @@ cudaError_t launch_kv4_attention(const Kv4AttnLaunch& a, cudaStream_t st) {
     p.c = static_cast<float>(static_cast<double>(a.sm_scale) * 1.4426950408889634);
     p.timeout_ns = a.timeout_ns;
     p.err_word = a.err_word;
-    const int64_t segments = static_cast<int64_t>(a.B) * a.Hkv * p.n_rt;
     if (segments > 0x7FFFFFFF) return cudaErrorInvalidValue;
     const int n = static_cast<int>(segments);
     if (a.D == 128) return nt == 1 ? launch<128, 1>(p, n, st) : launch<128, 2>(p, n, st);

@@ -517,8 +517,9 @@ __global__ void __launch_bounds__(32 * kWarps, (NT == 1 ? 16 : 8) / kWarps) kv4_
                 }
                 __syncwarp();
 
-                // scores: position r of tile mt is key 16 mt + swap_pos(r)
-                float s[NT][2][4];
+                // scores: position r of tile mt is key 16 mt + swap_pos(r); a pair of
+                // columns (query rows) at a time
+                float2 s[NT][2][2];
 #pragma unroll
                 for (int mt = 0; mt < 2; ++mt) {
                     uint32_t ka[kB], kb[kB];
@@ -535,8 +536,6 @@ __global__ void __launch_bounds__(32 * kWarps, (NT == 1 ? 16 : 8) / kWarps) kv4_
                     const float4 fa4 = sm.kscale[warp][16 * mt + g], fb4 = sm.kscale[warp][16 * mt + 8 + g];
                     const float fa[4] = {fa4.x, fa4.y, fa4.z, fa4.w}, fb[4] = {fb4.x, fb4.y, fb4.z, fb4.w};
 #pragma unroll
-                    for (int n = 0; n < NT; ++n) s[n][mt][0] = s[n][mt][1] = s[n][mt][2] = s[n][mt][3] = 0.0f;
-#pragma unroll
                     for (int c = 0; c < kB; ++c) {
                         uint32_t xa[4], xb[4];
                         e2m1x8_to_f16(ka[c], xa);
@@ -546,17 +545,16 @@ __global__ void __launch_bounds__(32 * kWarps, (NT == 1 ? 16 : 8) / kWarps) kv4_
                             float acc[4];
                             mma_f16_zero(acc, xa[0], xb[0], xa[1], xb[1], qf[n][c][0], qf[n][c][1]);
                             mma_f16(acc, xa[2], xb[2], xa[3], xb[3], qf[n][c][2], qf[n][c][3]);
-                            s[n][mt][0] = fmaf(acc[0], fa[c], s[n][mt][0]);
-                            s[n][mt][1] = fmaf(acc[1], fa[c], s[n][mt][1]);
-                            s[n][mt][2] = fmaf(acc[2], fb[c], s[n][mt][2]);
-                            s[n][mt][3] = fmaf(acc[3], fb[c], s[n][mt][3]);
+                            const float2 a0 = make_float2(acc[0], acc[1]), a1 = make_float2(acc[2], acc[3]);
+                            const float2 f0 = make_float2(fa[c], fa[c]), f1 = make_float2(fb[c], fb[c]);
+                            s[n][mt][0] = c == 0 ? __fmul2_rn(a0, f0) : __ffma2_rn(a0, f0, s[n][mt][0]);
+                            s[n][mt][1] = c == 0 ? __fmul2_rn(a1, f1) : __ffma2_rn(a1, f1, s[n][mt][1]);
                         }
                     }
                 }
 
                 // s - y in log2, masked; the running maximum
                 float y2[2][2];
-                bool grew = false;
 #pragma unroll
                 for (int mt = 0; mt < 2; ++mt)
 #pragma unroll
@@ -565,8 +563,7 @@ __global__ void __launch_bounds__(32 * kWarps, (NT == 1 ? 16 : 8) / kWarps) kv4_
                         y2[mt][h] = yy.y;
 #pragma unroll
                         for (int n = 0; n < NT; ++n)
-#pragma unroll
-                            for (int j = 0; j < 2; ++j) s[n][mt][2 * h + j] = fmaf(s[n][mt][2 * h + j], cs[n][j], yy.x);
+                            s[n][mt][h] = __ffma2_rn(s[n][mt][h], make_float2(cs[n][0], cs[n][1]), make_float2(yy.x, yy.x));
                     }
                 if (key0 + kKv4Group > all_see) {
 #pragma unroll
@@ -575,20 +572,20 @@ __global__ void __launch_bounds__(32 * kWarps, (NT == 1 ? 16 : 8) / kWarps) kv4_
                         for (int h = 0; h < 2; ++h) {
                             const int key = key0 + 16 * mt + 8 * h + swap_pos(g);
 #pragma unroll
-                            for (int n = 0; n < NT; ++n)
-#pragma unroll
-                                for (int j = 0; j < 2; ++j)
-                                    if (key >= seen[n][j]) s[n][mt][2 * h + j] = -INFINITY;
+                            for (int n = 0; n < NT; ++n) {
+                                if (key >= seen[n][0]) s[n][mt][h].x = -INFINITY;
+                                if (key >= seen[n][1]) s[n][mt][h].y = -INFINITY;
+                            }
                         }
                 }
                 float top[NT][2];
+                bool grew = false;
 #pragma unroll
-                for (int n = 0; n < NT; ++n)
-#pragma unroll
-                    for (int j = 0; j < 2; ++j) {
-                        top[n][j] = fmaxf(fmaxf(s[n][0][j], s[n][0][2 + j]), fmaxf(s[n][1][j], s[n][1][2 + j]));
-                        grew |= top[n][j] > M[n][j] + kLag;
-                    }
+                for (int n = 0; n < NT; ++n) {
+                    top[n][0] = fmaxf(fmaxf(s[n][0][0].x, s[n][0][1].x), fmaxf(s[n][1][0].x, s[n][1][1].x));
+                    top[n][1] = fmaxf(fmaxf(s[n][0][0].y, s[n][0][1].y), fmaxf(s[n][1][0].y, s[n][1][1].y));
+                    grew |= top[n][0] > M[n][0] + kLag || top[n][1] > M[n][1] + kLag;
+                }
                 if (__any_sync(0xFFFFFFFFu, grew)) {
 #pragma unroll
                     for (int n = 0; n < NT; ++n)
@@ -612,16 +609,20 @@ __global__ void __launch_bounds__(32 * kWarps, (NT == 1 ? 16 : 8) / kWarps) kv4_
                 // weights, transposed into B fragments (keys along k)
                 uint32_t pf[NT][2][2];
 #pragma unroll
-                for (int n = 0; n < NT; ++n)
+                for (int n = 0; n < NT; ++n) {
+                    float2 lv = make_float2(l[n][0], l[n][1]);
 #pragma unroll
                     for (int mt = 0; mt < 2; ++mt)
 #pragma unroll
                         for (int h = 0; h < 2; ++h) {
-                            const float p0 = ex2(s[n][mt][2 * h] - M[n][0]), p1 = ex2(s[n][mt][2 * h + 1] - M[n][1]);
-                            l[n][0] = fmaf(p0, y2[mt][h], l[n][0]);
-                            l[n][1] = fmaf(p1, y2[mt][h], l[n][1]);
-                            pf[n][mt][h] = transpose8x8(f16x2(p0, p1));
+                            const float2 d = __fadd2_rn(s[n][mt][h], make_float2(-M[n][0], -M[n][1]));
+                            const float2 w = make_float2(ex2(d.x), ex2(d.y));
+                            lv = __ffma2_rn(w, make_float2(y2[mt][h], y2[mt][h]), lv);
+                            pf[n][mt][h] = transpose8x8(f16x2(w.x, w.y));
                         }
+                    l[n][0] = lv.x;
+                    l[n][1] = lv.y;
+                }
                 // O^T += V^T P^T: k of a step = positions 2t, 2t + 1, 8 + 2t, 9 + 2t
 #pragma unroll
                 for (int ks = 0; ks < 2; ++ks) {

@@ -407,14 +407,13 @@ def bf16_attention_fwd(q, k, v, *, out=None, stream=None):
 # ---- four-bit key/value cache and packed sequences --------------------------
 
 
-# These calls are short (a decoding step makes one per layer), so the checks look
-# at each tensor once and the current stream's handle is fetched directly.
+# These calls are short (a decoding step makes several per layer), so the checks
+# look at each property of a tensor once, and the current device and stream are
+# read directly.
 
 _raw_stream = torch._C._cuda_getCurrentRawStream
-
-
-def _elsewhere(t: torch.Tensor, stream) -> bool:
-    return stream is not None or t.get_device() != torch.cuda.current_device()
+_device = torch._C._cuda_getDevice
+_bf16, _f32, _i32, _i64, _u8 = torch.bfloat16, torch.float32, torch.int32, torch.int64, torch.uint8
 
 
 def _on(t: torch.Tensor, stream):
@@ -428,25 +427,19 @@ def _on(t: torch.Tensor, stream):
 
 def _heads(t: torch.Tensor, name: str, shape, dev: int):
     """A CUDA bf16 tensor [..., heads, D] of the given shape whose heads are
-    contiguous; returns its token stride (a lone token has none of its own)."""
-    H, D = shape[-2:]
-    if t.dtype != torch.bfloat16 or t.get_device() != dev or t.shape != shape:
-        raise ValueError(f"{name} must be a bf16 tensor {list(shape)} on cuda:{dev}")
+    contiguous; returns its strides."""
     st = t.stride()
-    if st[-1] != 1 or (st[-2] != D and H > 1):
+    if t.dtype is not _bf16 or t.shape != shape or t.get_device() != dev:
+        raise ValueError(f"{name} must be a bf16 tensor {list(shape)} on cuda:{dev}")
+    if st[-1] != 1 or (st[-2] != shape[-1] and shape[-2] > 1):
         raise ValueError(f"the heads of {name} must be contiguous")
-    return st[0] if shape[0] > 1 else H * D
+    return st
 
 
 def _plain(t: torch.Tensor, name: str, dtype, shape, dev: int):
-    if t.dtype != dtype or t.get_device() != dev or t.shape != shape or not t.is_contiguous():
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != dev or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous {dtype} tensor {list(shape)} on cuda:{dev}")
     return t
-
-
-def _need_cuda(t: torch.Tensor, name: str):
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
 
 
 def kv4_new_cache(num_pages: int, page_size: int, n_kv_heads: int, D: int, device="cuda") -> torch.Tensor:
@@ -460,10 +453,10 @@ def kv4_new_cache(num_pages: int, page_size: int, n_kv_heads: int, D: int, devic
 
 def _kv4(cache: torch.Tensor):
     """(pages, heads, page_size, D) of a cache tensor."""
-    if cache.dtype != torch.uint8 or not cache.is_cuda or cache.dim() != 4 or not cache.is_contiguous():
+    if cache.dtype is not _u8 or cache.get_device() < 0 or cache.dim() != 4 or not cache.is_contiguous():
         raise ValueError("cache must be a contiguous CUDA uint8 tensor [pages, heads, page_size / 32, 34 * D]")
     pages, heads, groups, last = cache.shape
-    if last != 34 * 128 and last != 34 * 64:
+    if last != 4352 and last != 2176:
         raise ValueError("the last dimension of a cache is 34 * D with D 64 or 128")
     return pages, heads, 32 * groups, last // 34
 
@@ -473,13 +466,16 @@ def kv4_append(cache, k, v, slots, stream=None):
     contiguous, any token stride), into the cache at `slots`, int64 [T] =
     page * page_size + token; a negative slot skips its token."""
     pages, H, page_size, D = _kv4(cache)
-    if _elsewhere(cache, stream):
+    dev = cache.get_device()
+    if stream is not None or dev != _device():
         with _on(cache, stream):
             return kv4_append(cache, k, v, slots)
-    dev = cache.get_device()
     T = slots.numel()
-    _plain(slots, "slots", torch.int64, (T,), dev)
-    ks, vs = _heads(k, "k", (T, H, D), dev), _heads(v, "v", (T, H, D), dev)
+    shape = (T, H, D)
+    _plain(slots, "slots", _i64, (T,), dev)
+    ks, vs = _heads(k, "k", shape, dev)[0], _heads(v, "v", shape, dev)[0]
+    if T < 2:  # (a lone token's stride is arbitrary)
+        ks = vs = H * D
     _check(load().fsa_kv4_append(k.data_ptr(), v.data_ptr(), ks, vs, slots.data_ptr(), T, H, D, cache.data_ptr(), pages,
                                  page_size, _raw_stream(dev)), "fsa_kv4_append")
 
@@ -490,22 +486,24 @@ def kv4_read(cache, slots, *, out_k=None, out_v=None, stream=None):
     out_v: written instead of new tensors (heads contiguous, tokens that do not
     overlap)."""
     pages, H, page_size, D = _kv4(cache)
-    if _elsewhere(cache, stream):
+    dev = cache.get_device()
+    if stream is not None or dev != _device():
         with _on(cache, stream):
             return kv4_read(cache, slots, out_k=out_k, out_v=out_v)
-    dev = cache.get_device()
     T = slots.numel()
-    _plain(slots, "slots", torch.int64, (T,), dev)
     shape = (T, H, D)
+    _plain(slots, "slots", _i64, (T,), dev)
     ks = vs = H * D
     if out_k is None:
-        out_k = torch.empty(shape, dtype=torch.bfloat16, device=cache.device)
+        out_k = torch.empty(shape, dtype=_bf16, device=cache.device)
     else:
-        ks = _heads(out_k, "out_k", shape, dev)
+        st = _heads(out_k, "out_k", shape, dev)
+        ks = st[0] if T > 1 else ks
     if out_v is None:
-        out_v = torch.empty(shape, dtype=torch.bfloat16, device=cache.device)
+        out_v = torch.empty(shape, dtype=_bf16, device=cache.device)
     else:
-        vs = _heads(out_v, "out_v", shape, dev)
+        st = _heads(out_v, "out_v", shape, dev)
+        vs = st[0] if T > 1 else vs
     _check(load().fsa_kv4_read(cache.data_ptr(), pages, page_size, slots.data_ptr(), T, H, D, out_k.data_ptr(),
                                out_v.data_ptr(), ks, vs, _raw_stream(dev)), "fsa_kv4_read")
     return out_k, out_v
@@ -529,38 +527,36 @@ def kv4_attention_fwd(q, cache, page_table, seq_lens, *, out=None, return_lse: b
     workspace: uint8 tensor of kv4_attention_workspace_size bytes for callers
     that keep one; calls that may overlap need their own."""
     pages, Hkv, page_size, D = _kv4(cache)
-    if _elsewhere(cache, stream):
+    dev = cache.get_device()
+    if stream is not None or dev != _device():
         with _on(cache, stream):
             return kv4_attention_fwd(q, cache, page_table, seq_lens, out=out, return_lse=return_lse, lse=lse,
                                      sm_scale=sm_scale, workspace=workspace)
-    dev = cache.get_device()
     if q.dim() != 4 or page_table.dim() != 2:
         raise ValueError("q must be [B, Sq, n_heads, D] and page_table [B, max_pages]")
     shape = q.shape
-    B, Sq, Hq, _ = shape
-    if Hkv == 0 or Hq % Hkv or shape[3] != D or B * Sq * Hq == 0:
+    B, Sq, Hq, Dq = shape
+    if Hkv == 0 or Dq != D or Hq % Hkv or B * Sq * Hq == 0:
         raise ValueError(f"q must be a non-empty tensor [B, Sq, n_heads, {D}] with a multiple of {Hkv} heads")
-    q_stride = _heads(q, "q", shape, dev)
-    if Sq > 1:
-        if B > 1 and q_stride != Sq * q.stride(1):
-            raise ValueError("the tokens of q must lie at one distance")
-        q_stride = q.stride(1)
+    st = _heads(q, "q", shape, dev)
+    q_stride = st[1] if Sq > 1 else st[0] if B > 1 else Hq * D
+    if B > 1 and st[0] != Sq * q_stride:
+        raise ValueError("the tokens of q must lie at one distance")
     max_pages = page_table.shape[1]
-    _plain(page_table, "page_table", torch.int32, (B, max_pages), dev)
-    _plain(seq_lens, "seq_lens", torch.int32, (B,), dev)
-    o = torch.empty(shape, dtype=torch.bfloat16, device=cache.device) if out is None else \
-        _plain(out, "out", torch.bfloat16, shape, dev)
+    _plain(page_table, "page_table", _i32, (B, max_pages), dev)
+    _plain(seq_lens, "seq_lens", _i32, (B,), dev)
+    o = torch.empty(shape, dtype=_bf16, device=cache.device) if out is None else _plain(out, "out", _bf16, shape, dev)
     if lse is not None:
-        _plain(lse, "lse", torch.float32, (B, Sq, Hq), dev)
+        _plain(lse, "lse", _f32, (B, Sq, Hq), dev)
     elif return_lse:
-        lse = torch.empty((B, Sq, Hq), dtype=torch.float32, device=cache.device)
+        lse = torch.empty((B, Sq, Hq), dtype=_f32, device=cache.device)
     ws, ws_bytes = None, kv4_attention_workspace_size(B, Sq, Hq, Hkv, D, page_size, max_pages)
     if workspace is not None:
         if not workspace.is_contiguous() or workspace.get_device() != dev:
             raise ValueError(f"workspace must be a contiguous tensor on cuda:{dev}")
         ws, ws_bytes = workspace, workspace.numel() * workspace.element_size()
     elif ws_bytes:
-        ws = torch.empty(ws_bytes, dtype=torch.uint8, device=cache.device)
+        ws = torch.empty(ws_bytes, dtype=_u8, device=cache.device)
     _check(load().fsa_kv4_attention_fwd(q.data_ptr(), q_stride, cache.data_ptr(), page_table.data_ptr(), seq_lens.data_ptr(),
                                      o.data_ptr(), None if lse is None else lse.data_ptr(), B, Sq, Hq, Hkv, D, pages,
                                      page_size, max_pages, sm_scale, None if ws is None else ws.data_ptr(), ws_bytes,
@@ -576,12 +572,13 @@ def varlen_attention_fwd(q, k, v, cu_seqlens_q, cu_seqlens_k=None, *, causal: bo
     default the same) int32 [B + 1].  Returns o [Tq, n_heads, D], with
     return_lse also the log-sum-exps, float32 [Tq, n_heads].  Rows outside every
     sequence are not written (a new output leaves them undefined)."""
-    _need_cuda(q, "q")
-    if _elsewhere(q, stream):
+    dev = q.get_device()
+    if dev < 0:
+        raise ValueError("q must be a CUDA tensor")
+    if stream is not None or dev != _device():
         with _on(q, stream):
             return varlen_attention_fwd(q, k, v, cu_seqlens_q, cu_seqlens_k, causal=causal, out=out,
                                         return_lse=return_lse, lse=lse, sm_scale=sm_scale)
-    dev = q.get_device()
     if q.dim() != 3 or k.dim() != 3:
         raise ValueError("q must be [Tq, n_heads, D], k and v [Tk, n_kv_heads, D]")
     cu_k = cu_seqlens_q if cu_seqlens_k is None else cu_seqlens_k
@@ -590,19 +587,22 @@ def varlen_attention_fwd(q, k, v, cu_seqlens_q, cu_seqlens_k=None, *, causal: bo
     Tk, Hkv, Dk = kshape
     if D != Dk or Hkv == 0 or Hq == 0 or Hq % Hkv:
         raise ValueError("k and v must be [Tk, n_kv_heads, D] with q's D and a head count that divides q's")
-    qs, ks, vs = _heads(q, "q", qshape, dev), _heads(k, "k", kshape, dev), _heads(v, "v", kshape, dev)
+    qs, ks, vs = _heads(q, "q", qshape, dev)[0], _heads(k, "k", kshape, dev)[0], _heads(v, "v", kshape, dev)[0]
+    if Tq < 2:  # (a lone token's stride is arbitrary)
+        qs = Hq * D
+    if Tk < 2:
+        ks = vs = Hkv * D
     nb = cu_seqlens_q.numel()
     if nb < 2:
         raise ValueError("cu_seqlens_q must have B + 1 >= 2 entries")
-    _plain(cu_seqlens_q, "cu_seqlens_q", torch.int32, (nb,), dev)
+    _plain(cu_seqlens_q, "cu_seqlens_q", _i32, (nb,), dev)
     if cu_seqlens_k is not None:
-        _plain(cu_k, "cu_seqlens_k", torch.int32, (nb,), dev)
-    o = torch.empty(qshape, dtype=torch.bfloat16, device=q.device) if out is None else \
-        _plain(out, "out", torch.bfloat16, qshape, dev)
+        _plain(cu_k, "cu_seqlens_k", _i32, (nb,), dev)
+    o = torch.empty(qshape, dtype=_bf16, device=q.device) if out is None else _plain(out, "out", _bf16, qshape, dev)
     if lse is not None:
-        _plain(lse, "lse", torch.float32, (Tq, Hq), dev)
+        _plain(lse, "lse", _f32, (Tq, Hq), dev)
     elif return_lse:
-        lse = torch.empty((Tq, Hq), dtype=torch.float32, device=q.device)
+        lse = torch.empty((Tq, Hq), dtype=_f32, device=q.device)
     _check(load().fsa_varlen_attention_fwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), qs, ks, vs, cu_seqlens_q.data_ptr(),
                                            cu_k.data_ptr(), o.data_ptr(), None if lse is None else lse.data_ptr(), nb - 1,
                                            Tq, Tk, Hq, Hkv, D, 1 if causal else 0, sm_scale, _raw_stream(dev)),

@@ -18,8 +18,8 @@
 //   warp 9           TMEM allocator and the issuer of every product;
 //   warp 11          finds the CTA's next pair of tiles.
 // A CTA stays on its SM: when it has taken a pair, warp 11 cancels the launch of
-// a CTA that has not started yet and takes over its number, so pairs (the
-// longest of a sequence first) go to whichever SM is free, and the next pair's Q,
+// a CTA that has not started yet and takes over its number, so pairs (those of
+// most keys first) go to whichever SM is free, and the next pair's Q,
 // K and first scores are under way while the softmax warps still write the last
 // one's output.
 // TMEM: S0, S1 (128 columns each, P overlays the first 64 of its S in bf16),
@@ -50,6 +50,7 @@ namespace {
 
 constexpr int kKStages = 2, kVStages = 2;
 constexpr int kThreads = 384;
+constexpr unsigned kSms = 152;
 constexpr int kWarpLoad = 8, kWarpMma = 9, kWarpLoadV = 10, kWarpPlan = 11;
 // launched at 168 registers per thread; helpers drop to 32, softmax takes 232
 constexpr int kLaunchRegs = 168, kSoftmaxRegs = 232, kHelperRegs = 40;
@@ -102,16 +103,17 @@ __device__ __forceinline__ void raise_abort(Smem& sm, const Params& p) {
     atomicOr(p.err_word, kErrTimeout);
 }
 
-// Where the plan warp's search for pair numbers stands: sequence b, whose first
-// pair has the number `first`.
+// Where the plan warp's search for pair numbers stands: 32 sequences from b on,
+// whose pairs' numbers begin with `first`.
 struct Cursor {
     int b, first;
 };
 
-// Finds pair number idx, by the whole warp: sequence after sequence, 32 at a time
-// from the cursor on (numbers grow from call to call as a rule), the last pair
-// of a sequence (the longest one when causal) first.  Sequences from the first
-// wrong bound on have none.  False: no such pair.
+// Finds pair number idx, by the whole warp: 32 sequences after 32 from the cursor
+// on (numbers grow from call to call as a rule), among the pairs of these the
+// one with the most key tiles first, so that no long one is left for the end
+// (eight ragged sequences in the order of the pack: SMs idle a tenth of the
+// time).  Sequences from the first wrong bound on have none.  False: no such pair.
 __device__ __forceinline__ bool find_pair(const Params& p, int idx, Cursor& at, Item& it) {
     const int lane = threadIdx.x & 31, rows = 2 * p.n_tok;
     if (idx < at.first) at = {0, 0};
@@ -121,28 +123,55 @@ __device__ __forceinline__ bool find_pair(const Params& p, int idx, Cursor& at, 
         const bool bad = q0 < 0 || q1 < q0 || q1 > p.Tq || k0 < 0 || k1 < k0 || k1 > p.Tk;
         const unsigned wrong = __ballot_sync(0xFFFFFFFFu, bad);
         const int good = min(p.B - at.b, wrong ? __ffs(wrong) - 1 : 32);  // sequences of this window
-        const int n = lane < good ? (q1 - q0 + rows - 1) / rows : 0;
-        int inc = n;
-        for (int o = 1; o < 32; o <<= 1) {
-            const int x = __shfl_up_sync(0xFFFFFFFFu, inc, o);
-            if (lane >= o) inc += x;
-        }
-        const unsigned has = __ballot_sync(0xFFFFFFFFu, idx < at.first + inc);
-        if (has) {
-            const int src = __ffs(has) - 1;
-            const int last = at.first + inc - 1;  // number of the sequence's first pair of tokens
+        const int nq = q1 - q0, nk = k1 - k0;
+        const int n = lane < good ? (nq + rows - 1) / rows : 0;
+        const int local = idx - at.first, total = __reduce_add_sync(0xFFFFFFFFu, n);
+        if (local < total) {
+            // pairs of this lane's sequence that see at least `tiles` key tiles: the
+            // later ones, from the one whose last token sees key 128 (tiles - 1) on
+            auto longer = [&](int tiles) {
+                const int key = kTile * (tiles - 1);
+                if (tiles <= 0 || n == 0) return n;
+                if (nk <= key) return 0;
+                const int token = key - (nk - nq);
+                return !p.causal || token < 0 ? n : n - token / rows;
+            };
+            // the length of pair idx: the largest with more than `local` pairs that
+            // long (where every CTA starts at once the order is of no use, and the
+            // 0.7 us of the search would stand before the first load)
+            int more = 0, same = n;
+            if (gridDim.x > kSms) {
+                int lo = 0, hi = __reduce_max_sync(0xFFFFFFFFu, n ? nk / kTile + 2 : 1);
+                while (hi - lo > 1) {
+                    const int mid = (lo + hi) / 2;
+                    if (__reduce_add_sync(0xFFFFFFFFu, longer(mid)) > local)
+                        lo = mid;
+                    else
+                        hi = mid;
+                }
+                more = longer(lo + 1);
+                same = longer(lo) - more;
+            }
+            int inc = same;
+            for (int o = 1; o < 32; o <<= 1) {
+                const int x = __shfl_up_sync(0xFFFFFFFFu, inc, o);
+                if (lane >= o) inc += x;
+            }
+            const int rest = local - __reduce_add_sync(0xFFFFFFFFu, more);
+            const int src = __ffs(__ballot_sync(0xFFFFFFFFu, rest < inc)) - 1;
+            const int pair = n - 1 - more - (rest - (inc - same));
             it.q0 = __shfl_sync(0xFFFFFFFFu, q0, src);
-            it.nq = __shfl_sync(0xFFFFFFFFu, q1, src) - it.q0;
+            it.nq = __shfl_sync(0xFFFFFFFFu, nq, src);
             it.k0 = __shfl_sync(0xFFFFFFFFu, k0, src);
-            it.nk = __shfl_sync(0xFFFFFFFFu, k1, src) - it.k0;
-            it.tok0 = (__shfl_sync(0xFFFFFFFFu, last, src) - idx) * rows;
+            it.nk = __shfl_sync(0xFFFFFFFFu, nk, src);
+            it.tok0 = __shfl_sync(0xFFFFFFFFu, pair, src) * rows;
             return true;
         }
         if (good < min(32, p.B - at.b)) {
             if (lane == 0) atomicOr(p.err_word, kErrBadIndex);
             return false;
         }
-        at.first += __shfl_sync(0xFFFFFFFFu, inc, 31);
+        at.first += total;
         at.b += 32;
     }
     return false;

@@ -361,7 +361,11 @@ FSA_API fsa_status fsa_mma_rate_probe(int kind, int ctas, int iters, double *flo
  *   and d + 1; byte g (D/16) + 2 b + j of a value row d = 32 b + 4 g + 2 j and
  *   d + 1.
  * D in {64, 128}; page_size a positive multiple of 32, at most 65536;
- * H_kv in 1 .. 65535; num_pages in 1 .. 2^31 - 1.
+ * H_kv in 1 .. 65535; num_pages in 1 .. 2^31 - 1; at most 2^32 - 2 groups.
+ *
+ * These entry points take no library workspace and allocate nothing, except
+ * that the first call of the library on a device allocates its error word:
+ * make one call before capturing a graph.
  */
 
 /* Bytes of one page; 0 for invalid arguments. */
@@ -379,7 +383,8 @@ FSA_API uint64_t fsa_kv4_page_bytes(int H_kv, int page_size, int D);
  *        twice holds a mixture of the two tokens.  A slot beyond the cache is
  *        skipped and reported by fsa_get_device_error as
  *        FSA_ERR_INVALID_ARGUMENT.
- * T in 0 .. 2^31 - 1.  Writes only the given slots' bytes.
+ * T in 0 .. 2^31 - 1, ceil(T / 64) * H_kv < 2^31.  Writes only the given
+ * slots' bytes.
  */
 FSA_API fsa_status fsa_kv4_append(const void *k, const void *v, int64_t k_stride, int64_t v_stride,
                                   const int64_t *slots, int64_t T, int H_kv, int D, void *cache,
@@ -414,6 +419,7 @@ FSA_API fsa_status fsa_kv4_read(const void *cache, int64_t num_pages, int page_s
  *  - Products in f16 with FP32 accumulation: q is scaled by a power of two per
  *    row, softmax weights are rounded to f16 (relative to the largest product
  *    of weight and value scale); sums are FP32.
+ *  - o and lse must not overlap q or the cache.
  *  - workspace: device buffer of fsa_kv4_attention_workspace_size() bytes,
  *    256-byte aligned, contents arbitrary; NULL when that size is 0.  Calls
  *    that may overlap need workspaces of their own.
@@ -421,8 +427,9 @@ FSA_API fsa_status fsa_kv4_read(const void *cache, int64_t num_pages, int page_s
  *    cache skipped with all of its keys; both are reported by
  *    fsa_get_device_error as FSA_ERR_INVALID_ARGUMENT.
  * Requirements: B, Sq, Hq, Hkv >= 1, Hkv divides Hq, B <= 65535, Hkv <= 65535,
- * Sq * Hq / Hkv <= 65535, D in {64, 128}, max_pages >= 1, max_pages *
- * page_size <= 2^30, and a cache as above.
+ * Sq * Hq / Hkv <= 65535, B * Hkv * ceil(Sq * Hq / Hkv / 8) < 2^31, D in
+ * {64, 128}, max_pages >= 1, max_pages * page_size <= 2^30, and a cache as
+ * above.
  */
 FSA_API fsa_status fsa_kv4_attention_fwd(const void *q, int64_t q_stride, const void *cache,
                                          const int32_t *page_table, const int32_t *seq_lens, void *o,
@@ -455,8 +462,10 @@ FSA_API uint64_t fsa_kv4_attention_workspace_size(int B, int Sq, int Hq, int Hkv
  * it does not reach its outputs.  Bounds that decrease or leave 0 .. Tq or
  * 0 .. Tk are reported by fsa_get_device_error as FSA_ERR_INVALID_ARGUMENT,
  * and the sequences from the first wrong bound on are skipped.
- * Requirements: B >= 1, Tq, Tk in 0 .. 2^30, Hkv divides Hq, Hkv <= 65535,
- * Hq / Hkv <= 128, (Tq / 128 + B) * Hkv <= 2^31 / 256, D in {64, 128}.
+ * o and lse must not overlap q, k or v.
+ * Requirements: B >= 1, Tq, Tk in 0 .. 2^26, Hkv divides Hq, Hkv <= 65535,
+ * G = Hq / Hkv <= 128, (Tq / (2 floor(128 / G)) + B) * Hkv < 2^31, D in
+ * {64, 128}.
  */
 FSA_API fsa_status fsa_varlen_attention_fwd(const void *q, const void *k, const void *v,
                                             int64_t q_stride, int64_t k_stride, int64_t v_stride,

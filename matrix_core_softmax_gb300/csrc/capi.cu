@@ -454,7 +454,9 @@ namespace {
 fsa_status check_kv4(const void* cache, int64_t num_pages, int page_size, int H_kv, int D) {
     if (!cache || !aligned16(cache)) return FSA_ERR_INVALID_ARGUMENT;
     if (D != 64 && D != 128) return FSA_ERR_UNSUPPORTED;
-    if (num_pages < 1 || num_pages > INT32_MAX || fsa_kv4_page_bytes(H_kv, page_size, D) == 0)
+    // (groups are numbered in 32 bits: 2^32 of them would be 9 TB)
+    if (num_pages < 1 || num_pages > INT32_MAX || fsa_kv4_page_bytes(H_kv, page_size, D) == 0 ||
+        num_pages * H_kv * (page_size / 32) >= int64_t{UINT32_MAX})
         return FSA_ERR_INVALID_ARGUMENT;
     return FSA_OK;
 }
@@ -465,7 +467,7 @@ fsa_status kv4_rows(const void* k, const void* v, int64_t k_stride, int64_t v_st
                     int H_kv, int D, const void* cache, int64_t num_pages, int page_size, int64_t least, Kv4Rows* a) {
     fsa_status s = check_kv4(cache, num_pages, page_size, H_kv, D);
     if (s != FSA_OK) return s;
-    if (T < 0 || T > INT32_MAX) return FSA_ERR_INVALID_ARGUMENT;
+    if (T < 0 || T > INT32_MAX || (T + 63) / 64 * H_kv > INT32_MAX) return FSA_ERR_INVALID_ARGUMENT;
     if (T > 0 && (!k || !v || !slots || !aligned16(k) || !aligned16(v) || (reinterpret_cast<uintptr_t>(slots) & 7) ||
                   !token_stride_ok(k_stride, least) || !token_stride_ok(v_stride, least)))
         return FSA_ERR_INVALID_ARGUMENT;
@@ -510,7 +512,8 @@ fsa_status check_kv4_attention(int B, int Sq, int Hq, int Hkv, int D, int page_s
     if (D != 64 && D != 128) return FSA_ERR_UNSUPPORTED;
     if (B < 1 || B > 65535 || Sq < 1 || Hq < 1 || Hkv < 1 || Hkv > 65535 || Hq % Hkv != 0 ||
         static_cast<int64_t>(Sq) * (Hq / Hkv) > 65535 || max_pages < 1 ||
-        fsa_kv4_page_bytes(Hkv, page_size, D) == 0 || static_cast<int64_t>(max_pages) * page_size > (1 << 30))
+        fsa_kv4_page_bytes(Hkv, page_size, D) == 0 || static_cast<int64_t>(max_pages) * page_size > (1 << 30) ||
+        static_cast<int64_t>(B) * Hkv * ((static_cast<int64_t>(Sq) * (Hq / Hkv) + 7) / 8) > INT32_MAX)
         return FSA_ERR_INVALID_ARGUMENT;
     return FSA_OK;
 }
@@ -569,9 +572,11 @@ fsa_status fsa_varlen_attention_fwd(const void* q, const void* k, const void* v,
                                     int B, int Tq, int Tk, int Hq, int Hkv, int D, int causal, float sm_scale,
                                     void* stream) {
     if (D != 64 && D != 128) return FSA_ERR_UNSUPPORTED;
-    if (B < 1 || Tq < 0 || Tk < 0 || Tq > (1 << 30) || Tk > (1 << 30) || Hq < 1 || Hkv < 1 || Hkv > 65535 ||
+    // (with more keys one pair of query tiles could outlast the kernel's bounded waits)
+    if (B < 1 || Tq < 0 || Tk < 0 || Tq > (1 << 26) || Tk > (1 << 26) || Hq < 1 || Hkv < 1 || Hkv > 65535 ||
         Hq % Hkv != 0 || Hq / Hkv > 128 || (causal != 0 && causal != 1) || !std::isfinite(sm_scale))
         return FSA_ERR_INVALID_ARGUMENT;
+    if ((Tq / (2 * (128 / (Hq / Hkv))) + static_cast<int64_t>(B)) * Hkv > INT32_MAX) return FSA_ERR_INVALID_ARGUMENT;
     if (!cu_q || !cu_k || (reinterpret_cast<uintptr_t>(cu_q) & 3) || (reinterpret_cast<uintptr_t>(cu_k) & 3) ||
         (reinterpret_cast<uintptr_t>(lse) & 3))
         return FSA_ERR_INVALID_ARGUMENT;

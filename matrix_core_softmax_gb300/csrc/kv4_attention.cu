@@ -968,7 +968,6 @@ cudaError_t launch_kv4_attention(const Kv4AttnLaunch& a, cudaStream_t st) {
     p.c = static_cast<float>(static_cast<double>(a.sm_scale) * 1.4426950408889634);
     p.timeout_ns = a.timeout_ns;
     p.err_word = a.err_word;
-    if (segments > 0x7FFFFFFF) return cudaErrorInvalidValue;
     const int n = static_cast<int>(segments);
     if (a.D == 128) return nt == 1 ? launch<128, 1>(p, n, st) : launch<128, 2>(p, n, st);
     return nt == 1 ? launch<64, 1>(p, n, st) : launch<64, 2>(p, n, st);

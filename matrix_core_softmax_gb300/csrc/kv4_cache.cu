@@ -182,21 +182,14 @@ __global__ void __launch_bounds__(kThreads) kv4_read_kernel(
 
 // Blocks of the heads of one token chunk are neighbours, so a token's rows are
 // read or written together.
-cudaError_t grid_of(const Kv4Rows& a, dim3* grid) {
-    const int64_t blocks = (a.T + kTokens - 1) / kTokens * a.H;
-    if (blocks > 0x7FFFFFFF) return cudaErrorInvalidValue;
-    *grid = dim3(static_cast<unsigned>(blocks), 2);
-    return cudaSuccess;
-}
+dim3 grid_of(const Kv4Rows& a) { return dim3(static_cast<unsigned>((a.T + kTokens - 1) / kTokens * a.H), 2); }
 
 }  // namespace
 
 cudaError_t launch_kv4_append(const Kv4Rows& a, uint8_t* cache, cudaStream_t st) {
     const uint16_t* k = static_cast<const uint16_t*>(a.k);
     const uint16_t* v = static_cast<const uint16_t*>(a.v);
-    dim3 grid;
-    const cudaError_t e = grid_of(a, &grid);
-    if (e != cudaSuccess) return e;
+    const dim3 grid = grid_of(a);
     if (a.D == 128)
         kv4_append_kernel<128><<<grid, kThreads, 0, st>>>(k, v, a.k_stride, a.v_stride, a.slots, a.T, a.H, cache,
                                                           a.capacity, a.page_size, a.err_word);
@@ -209,9 +202,7 @@ cudaError_t launch_kv4_append(const Kv4Rows& a, uint8_t* cache, cudaStream_t st)
 cudaError_t launch_kv4_read(const Kv4Rows& a, const uint8_t* cache, cudaStream_t st) {
     uint16_t* k = static_cast<uint16_t*>(const_cast<void*>(a.k));
     uint16_t* v = static_cast<uint16_t*>(const_cast<void*>(a.v));
-    dim3 grid;
-    const cudaError_t e = grid_of(a, &grid);
-    if (e != cudaSuccess) return e;
+    const dim3 grid = grid_of(a);
     if (a.D == 128)
         kv4_read_kernel<128><<<grid, kThreads, 0, st>>>(cache, a.slots, a.T, a.H, a.capacity, a.page_size, k, v,
                                                         a.k_stride, a.v_stride, a.err_word);

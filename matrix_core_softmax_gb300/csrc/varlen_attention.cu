@@ -632,7 +632,6 @@ cudaError_t launch(const VarlenLaunch& a, const Params& p, cudaStream_t st) {
     if (e != cudaSuccess) return e;
     // a sequence of n tokens has at most n / (2 n_tok) + 1 pairs
     const int64_t pairs = a.Tq / (2 * p.n_tok) + static_cast<int64_t>(a.B);
-    if (pairs * a.Hkv > 0x7FFFFFFF) return cudaErrorInvalidValue;
     varlen_attn_kernel<D><<<static_cast<unsigned>(pairs * a.Hkv), kThreads, smem, st>>>(*a.tm_q, *a.tm_k, *a.tm_v, p);
     return cudaGetLastError();
 }

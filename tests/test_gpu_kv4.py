@@ -150,6 +150,13 @@ CASES = [
     ([4097], 1, 40, 8, 128, 64),
     ([3000], 9, 12, 1, 64, 32),                       # 108 rows
     ([70] * 40, 1, 3, 3, 128, 32),
+    ([0, 700, 0, 0, 33, 1, 2500, 64, 0], 1, 6, 3, 128, 64),    # empty sequences inside and at the end
+    ([17 * i % 400 for i in range(64)], 1, 8, 8, 64, 32),       # more whole segments than fit at once
+    ([13 * i % 300 for i in range(64)], 3, 32, 8, 128, 64),     # the same with 12 rows
+    ([311 * i % 3000 for i in range(50)], 1, 4, 2, 64, 128),    # segments that end inside every warp's part
+    ([0] * 7, 2, 4, 2, 64, 32),
+    ([3, 0, 5] * 700, 1, 2, 1, 64, 32),                         # more sequences than a block has threads
+    ([40000, 5], 1, 3, 1, 64, 256),
 ]
 
 
@@ -215,6 +222,33 @@ def test_attention_query_sizes(fsa, amp):
     sm = 0.125 if amp < 2 else 2.0 ** -58
     o, lse = fsa.kv4_attention_fwd(q, cache, table, n, sm_scale=sm, return_lse=True)
     _check_sequences(fsa, o, lse, q, held, sm)
+
+
+@pytest.mark.parametrize("Hkv,D,Sq", [(8, 128, 1), (2, 64, 3)])
+def test_attention_with_a_wide_page_table(fsa, Hkv, D, Sq):
+    """Room for far longer sequences than there are: the work is cut for the long
+    ones (half shares), most blocks have none."""
+    lens, page, B = [60, 0, 900, 3] * 16, 64, 64
+    cache, table, n, held = _sequences(fsa, lens, Hkv, D, page, seed=10)
+    wide = torch.full((B, 40960 // page), -7, dtype=torch.int32, device="cuda")
+    wide[:, :table.shape[1]] = table
+    q = to_dev(_bits((B, Sq, 4 * Hkv, D), 11, 2.0))
+    o, lse = fsa.kv4_attention_fwd(q, cache, wide, n, return_lse=True)
+    assert fsa.get_device_error() == 0
+    _check_sequences(fsa, o, lse, q, held, ref.default_scale(D))
+
+
+@pytest.mark.parametrize("seed", range(8))
+def test_attention_of_random_shapes(fsa, seed):
+    rng = np.random.default_rng(1000 + seed)
+    D, page = int(rng.choice([64, 128])), 32 * int(rng.integers(1, 9))
+    Hkv, G, Sq, B = (int(rng.integers(1, m)) for m in (5, 18, 6, 12))
+    lens = [int(x) for x in (rng.random(B) ** 2 * rng.choice([40, 700, 6000])).astype(int)]
+    cache, table, n, held = _sequences(fsa, lens, Hkv, D, page, seed=seed, kscale=float(rng.choice([0.3, 1, 3])))
+    q = to_dev(_bits((B, Sq, G * Hkv, D), seed, 1.5))
+    o, lse = fsa.kv4_attention_fwd(q, cache, table, n, return_lse=True)
+    assert fsa.get_device_error() == 0
+    _check_sequences(fsa, o, lse, q, held, ref.default_scale(D))
 
 
 def test_attention_strides_outputs_and_workspace(fsa):

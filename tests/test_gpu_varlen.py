@@ -67,6 +67,20 @@ def test_matches_64_bits(fsa, case, causal):
     assert torch.equal(o, fsa.varlen_attention_fwd(q, k, v, cq, ck, causal=causal))
 
 
+@pytest.mark.parametrize("seed", range(8))
+def test_random_shapes(fsa, seed):
+    rng = np.random.default_rng(2000 + seed)
+    D, causal = int(rng.choice([64, 128])), bool(rng.random() < 0.7)
+    Hkv, G, B = (int(rng.integers(1, m)) for m in (5, 18, 40))
+    nq = [int(x) for x in (rng.random(B) ** 2 * rng.choice([20, 300, 1200])).astype(int)]
+    nk = [max(0, n + int(rng.integers(-20, 500) if rng.random() < 0.6 else 0)) for n in nq]
+    q, k, v = _bf16((sum(nq), G * Hkv, D), seed, 2.0), _bf16((sum(nk), Hkv, D), seed + 50), _bf16((sum(nk), Hkv, D), seed + 90)
+    cq, ck = _cu(nq), _cu(nk)
+    o, lse = fsa.varlen_attention_fwd(q, k, v, cq, ck, causal=causal, return_lse=True)
+    assert fsa.get_device_error() == 0
+    _check(o, lse, q, k, v, cq, ck, causal, ref.default_scale(D))
+
+
 @pytest.mark.parametrize("kind", ["growing", "huge", "zero", "sink"])
 def test_score_ranges(fsa, kind):
     n, Hq, Hkv, D = 700, 4, 2, 64

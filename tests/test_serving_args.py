@@ -38,7 +38,8 @@ def _read(lib, k=256, v=256, ks=128, vs=128, slots=256, T=4, H=2, D=64, cache=25
 def test_rows_refused(lib, call):
     for bad in [dict(k=0), dict(v=0), dict(slots=0), dict(cache=0), dict(k=8), dict(v=24), dict(cache=8), dict(slots=260),
                 dict(ks=100), dict(vs=-128), dict(T=-1), dict(T=1 << 31), dict(H=0), dict(pages=0), dict(pages=1 << 31),
-                dict(page=48), dict(page=0), dict(ks=1 << 36)]:
+                dict(page=48), dict(page=0), dict(ks=1 << 36),
+                dict(pages=(1 << 31) - 1, page=128), dict(T=(1 << 31) - 1, H=65, ks=65 * 64, vs=65 * 64)]:
         assert call(lib, **bad) == INVALID, bad
     assert call(lib, D=96) == UNSUPPORTED
     assert call(lib, T=0, k=0, v=0, slots=0) == 0        # nothing to do: no device needed
@@ -58,7 +59,8 @@ def test_cache_attention_refused(lib):
     for bad in [dict(q=0), dict(cache=0), dict(table=0), dict(lens=0), dict(o=0), dict(q=8), dict(o=8), dict(cache=4),
                 dict(table=258), dict(lens=258), dict(lse=258), dict(qs=4), dict(qs=-8), dict(B=0), dict(B=65536), dict(Sq=0),
                 dict(Hq=5), dict(Hkv=0), dict(Hq=0), dict(pages=0), dict(page=40), dict(max_pages=0),
-                dict(max_pages=1 << 26), dict(Sq=40000), dict(sm=float("nan")), dict(sm=float("inf"))]:
+                dict(max_pages=1 << 26), dict(Sq=40000), dict(B=65535, Hkv=65535, Hq=65535),
+                dict(pages=1 << 30, page=64), dict(sm=float("nan")), dict(sm=float("inf"))]:
         assert _attend(lib, **bad) == INVALID, bad
     assert _attend(lib, D=80) == UNSUPPORTED
 
@@ -84,7 +86,7 @@ def _varlen(lib, q=256, k=256, v=256, qs=256, ks=128, vs=128, cq=256, ck=256, o=
 def test_varlen_refused(lib):
     for bad in [dict(q=0), dict(k=0), dict(v=0), dict(o=0), dict(cq=0), dict(ck=0), dict(q=8), dict(k=8), dict(v=8), dict(o=8),
                 dict(cq=258), dict(ck=2), dict(lse=2), dict(qs=248), dict(ks=64), dict(vs=132), dict(B=0), dict(Tq=-1),
-                dict(Tk=-1), dict(Tq=(1 << 30) + 1), dict(Hq=5), dict(Hkv=0), dict(Hq=258, Hkv=2, qs=258 * 64), dict(causal=2),
+                dict(Tk=-1), dict(Tq=(1 << 26) + 1), dict(Tk=(1 << 26) + 1), dict(B=1 << 30), dict(Hq=5), dict(Hkv=0), dict(Hq=258, Hkv=2, qs=258 * 64), dict(causal=2),
                 dict(sm=float("inf"))]:
         assert _varlen(lib, **bad) == INVALID, bad
     assert _varlen(lib, D=96) == UNSUPPORTED

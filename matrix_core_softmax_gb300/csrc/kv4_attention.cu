@@ -25,7 +25,7 @@
 //    weight fragment per 32-channel block.
 //
 // Weights.  With X the scale exponent of a key's value block b, R_b the largest
-// one so far and y = min_b (R_b - X_b) (at most 24) the kernel takes
+// one so far and y = min_b (R_b - X_b) (at most 96) the kernel takes
 //   p = 2^(s - y - M)  rounded to f16, M the running maximum of s - y,
 //   w_b = p 2^(y - (R_b - X_b) + 11),
 //   O_b += sum w_b code,  l += p 2^y (before the rounding),
@@ -33,9 +33,14 @@
 // and neither a large nor a small value row leaves f16's range; a weight's
 // error is 2^-11 of itself or 2^-25 of that largest product.  M and R_b follow
 // lazily (M may lag by 2^4, which the 2^11 leaves room for), so O is rescaled
-// only when one of them really grows.  O, l and the scores are FP32.  q is
+// only when one of them really grows.  Where the R_b grow, s - y of every key
+// before falls by the least of the steps and M with it (else the keys after a
+// large value of little weight would have p far below 1), down to 2^-96 of its
+// peak at most, which keeps l in range.  O, l and the scores are FP32.  q is
 // scaled by a power of two to [1, 2) per row, in which f16 holds a bf16 value
 // exactly down to 2^-14 of the row's largest and to 2^-25 of it below.
+// Pieces of a row are kept as their own output and its log-sum-exp, not as
+// unnormalised sums, whose scale 2^(M + R_b) may lie outside of FP32.
 //
 // Work split.  The cache's groups of all (sequence, key head, 8- or 16-row tile)
 // segments form one line, cut into equal shares, one per resident block, and a
@@ -65,13 +70,8 @@ namespace {
 
 constexpr int kSplitWarps = 8;    // warps of a block of the split form and of the join
 constexpr int kJoinThreads = 256;
-constexpr int kStages = 2;        // (three: 1 % slower, the merge and the ring leave less L1)
-constexpr int kResident = 304;    // two blocks on each of 152 SMs
-constexpr int kMaxBlocks = 2 * kResident;
-// Shares beyond this many groups are halved, so that SMs that read faster take
-// more of them (64 x 32768 keys: 234 against 239 us; with small shares the
-// further parts cost more than that: 131072 keys of one sequence 69 against 55).
-constexpr int64_t kLongShare = 1024;
+constexpr int kStages = 2;        // (three: 1 % slower, they leave less L1)
+constexpr int kBlocks = 304;      // of the split form: two on each of 152 SMs
 constexpr int kMinShare = kSplitWarps; // groups of a block, at least one a warp
 // A block takes a whole segment up to this many groups, twice as many where
 // there are many segments.  8 key heads of D = 128, whole against split: one
@@ -88,6 +88,7 @@ constexpr int kFewWarps = 8, kManyWarps = 4;
 constexpr uint32_t kNoGroup = 0xFFFFFFFFu;
 constexpr float kNoMax = -1e30f;
 constexpr float kLag = 4.0f;      // how far M may lag behind (log2)
+constexpr unsigned kMostY = 96;   // largest y
 constexpr int kHeadroom = 11;     // weights carry 2^11: 2^11 * 2^4 = 2^15 < 65504
 
 struct Params {
@@ -97,7 +98,7 @@ struct Params {
     const int* seq_lens;
     uint16_t* o;
     float* lse;
-    float* partial;  // [block][2][8 NT rows][D + 2], or null: whole segments
+    float* partial;  // [block][2]: 8 NT rows of D, then their log2-sum-exp2; null: whole segments
     int64_t q_stride, num_pages;
     int B, Sq, Hq, Hkv, G, n_rt, page_size, max_pages;
     float c;  // sm_scale * log2(e)
@@ -120,7 +121,8 @@ struct __align__(128) Smem {
     float2 ykey[kWarps][kKv4Group];        // -y and 2^y of each key, by row position
     uint32_t vscale[kWarps][4][2][2][4];   // f16 pairs: [t][16-key step][half][block]
     uint64_t full[kWarps][kStages];
-    float m[kWarps][2][8 * NT], l[kWarps][2][8 * NT];
+    float lse2[kWarps][2][8 * NT];  // log2-sum-exp2 of the pieces' rows
+    float peak[kWarps][8 * NT];     // largest M so far
     Piece piece[kWarps][2];  // [0] in first, [1] in ring
     int64_t scan[kWarps];
     int64_t first_x;
@@ -213,17 +215,15 @@ __device__ __forceinline__ int64_t share_of(int64_t all, int n_blocks) {
     return max(static_cast<int64_t>(kMinShare), (all + n_blocks - 1) / n_blocks);
 }
 
-// Four channels of row r of a segment from their weighted sum and the row's
-// maximum and weight sum.
+// Four channels of row r of a segment, and the row's log-sum-exp from its log2.
 template <int D>
-__device__ __forceinline__ void write_row(const Params& p, int b, int hk, int r, int d4, float4 a, float m, float l) {
+__device__ __forceinline__ void write_row(const Params& p, int b, int hk, int r, int d4, float4 a, float lse2) {
     const Row w = row_of(p, r);
     const int64_t row = (static_cast<int64_t>(b) * p.Sq + w.i) * p.Hq + hk * p.G + w.h;
-    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-    const __nv_bfloat162 lo = __floats2bfloat162_rn(a.x * inv, a.y * inv), hi = __floats2bfloat162_rn(a.z * inv, a.w * inv);
+    const __nv_bfloat162 lo = __floats2bfloat162_rn(a.x, a.y), hi = __floats2bfloat162_rn(a.z, a.w);
     *reinterpret_cast<uint2*>(p.o + row * D + 4 * d4) =
         make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
-    if (p.lse && d4 == 0) p.lse[row] = l == 0.0f ? -INFINITY : (m + __log2f(l)) * 0.6931471805599453f;
+    if (p.lse && d4 == 0) p.lse[row] = lse2 < 0.5f * kNoMax ? -INFINITY : lse2 * 0.6931471805599453f;
 }
 
 // kWhole: a block takes one segment, without a walk over sequences, segments
@@ -440,7 +440,9 @@ __global__ void __launch_bounds__(32 * kWarps, (NT == 1 ? 16 : 8) / kWarps) kv4_
         float O[NT][kB][2][4] = {};
         float M[NT][2], l[NT][2] = {};
 #pragma unroll
-        for (int n = 0; n < NT; ++n) M[n][0] = M[n][1] = kNoMax;
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) M[n][j] = sm.peak[warp][8 * n + 2 * t + j] = kNoMax;
         uint32_t R02 = 0, R13 = 0;  // largest value scale bytes so far
 
         for (; i < i_end; ++i) {
@@ -482,26 +484,38 @@ __global__ void __launch_bounds__(32 * kWarps, (NT == 1 ? 16 : 8) / kWarps) kv4_
                             n02 = max16x2(n02, __shfl_xor_sync(0xFFFFFFFFu, n02, o));
                             n13 = max16x2(n13, __shfl_xor_sync(0xFFFFFFFFu, n13, o));
                         }
+                        int d[kB], least = 255;
 #pragma unroll
                         for (int c = 0; c < kB; ++c) {
                             const int sh = 16 * (c >> 1);
-                            const int d = static_cast<int>(((c & 1 ? R13 : R02) >> sh) & 0xFFu) -
-                                          static_cast<int>(((c & 1 ? n13 : n02) >> sh) & 0xFFu);
-                            const float f = ex2(static_cast<float>(d));
-#pragma unroll
-                            for (int n = 0; n < NT; ++n)
-#pragma unroll
-                                for (int e = 0; e < 4; ++e) {
-                                    O[n][c][0][e] *= f;
-                                    O[n][c][1][e] *= f;
-                                }
+                            d[c] = static_cast<int>(((c & 1 ? n13 : n02) >> sh) & 0xFFu) -
+                                   static_cast<int>(((c & 1 ? R13 : R02) >> sh) & 0xFFu);
+                            least = min(least, d[c]);
                         }
+#pragma unroll
+                        for (int n = 0; n < NT; ++n)
+#pragma unroll
+                            for (int j = 0; j < 2; ++j) {
+                                const float to = fmaxf(M[n][j] - least, sm.peak[warp][8 * n + 2 * t + j] - static_cast<float>(kMostY));
+                                const float drop = fmaxf(M[n][j] - to, 0.0f);
+                                M[n][j] -= drop;
+                                l[n][j] *= ex2(drop);
+#pragma unroll
+                                for (int c = 0; c < kB; ++c) {
+                                    const float f = ex2(drop - static_cast<float>(d[c]));
+#pragma unroll
+                                    for (int h = 0; h < 2; ++h) {
+                                        O[n][c][h][j] *= f;
+                                        O[n][c][h][2 + j] *= f;
+                                    }
+                                }
+                            }
                         R02 = n02;
                         R13 = n13;
                     }
                     const uint32_t z02 = R02 - v02, z13 = R13 - v13;  // no borrow: R is the larger in every half
                     const uint32_t zm = D == 128 ? min16x2(z02, z13) : min(z02, z13);
-                    const uint32_t y = D == 128 ? min(min(zm & 0xFFFFu, zm >> 16), 24u) : min(zm, 24u);
+                    const uint32_t y = D == 128 ? min(min(zm & 0xFFFFu, zm >> 16), kMostY) : min(zm, kMostY);
                     sm.ykey[warp][pos] = make_float2(-static_cast<float>(y), __uint_as_float((127u + y) << 23));
                     // f16 2^(kHeadroom - (z - y)), zero where that has no exponent left
                     const uint32_t top = (15 + kHeadroom + y) * 0x00010001u;
@@ -595,6 +609,8 @@ __global__ void __launch_bounds__(32 * kWarps, (NT == 1 ? 16 : 8) / kWarps) kv4_
                             for (int o = 4; o < 32; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
                             m = fmaxf(m, M[n][j]);
                             const float f = ex2(M[n][j] - m);
+                            float& peak = sm.peak[warp][8 * n + 2 * t + j];  // (the lanes of a column write the same)
+                            peak = fmaxf(peak, m);
                             M[n][j] = m;
                             l[n][j] *= f;
 #pragma unroll
@@ -668,19 +684,26 @@ __global__ void __launch_bounds__(32 * kWarps, (NT == 1 ? 16 : 8) / kWarps) kv4_
         }
         if (!ok) break;
 
-        // O in true units relative to 2^M
+        // the outputs of this part, and their log-sum-exp
+        float L2[NT][2];
 #pragma unroll
-        for (int c = 0; c < kB; ++c) {
-            const float f0 = 1.0f / static_cast<float>(1 << kHeadroom);
-            const float f1 = pow2f(static_cast<int>(((c & 1 ? R13 : R02) >> (16 * (c >> 1))) & 0xFFu) - 127);
+        for (int n = 0; n < NT; ++n)
 #pragma unroll
-            for (int n = 0; n < NT; ++n)
+            for (int j = 0; j < 2; ++j) {
+                float lt = l[n][j];
+                for (int o = 4; o < 32; o <<= 1) lt += __shfl_xor_sync(0xFFFFFFFFu, lt, o);
+                L2[n][j] = lt == 0.0f ? kNoMax : M[n][j] + __log2f(lt);
+                const float inv = lt == 0.0f ? 0.0f : 1.0f / (lt * static_cast<float>(1 << kHeadroom));
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    O[n][c][0][e] = O[n][c][0][e] * f0 * f1;
-                    O[n][c][1][e] = O[n][c][1][e] * f0 * f1;
+                for (int c = 0; c < kB; ++c) {
+                    const float f = pow2f(static_cast<int>(((c & 1 ? R13 : R02) >> (16 * (c >> 1))) & 0xFFu) - 127);
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        O[n][c][h][j] = O[n][c][h][j] * inv * f;
+                        O[n][c][h][2 + j] = O[n][c][h][2 + j] * inv * f;
+                    }
                 }
-        }
+            }
         // written where the segment is complete, kept as a piece where it is not
         const bool complete = !kWhole && seg_x >= pos_begin && seg_x + ng <= pos_end;
         const int slot = kWhole || i == count ? 1 : 0;  // (the ring is free at the end only)
@@ -690,13 +713,8 @@ __global__ void __launch_bounds__(32 * kWarps, (NT == 1 ? 16 : 8) / kWarps) kv4_
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
                 const int r = 8 * n + 2 * t + j;
-                float lt = l[n][j];
-                for (int o = 4; o < 32; o <<= 1) lt += __shfl_xor_sync(0xFFFFFFFFu, lt, o);
                 if (!complete) {
-                    if (g == 0) {
-                        sm.m[warp][slot][r] = M[n][j];
-                        sm.l[warp][slot][r] = lt;
-                    }
+                    if (g == 0) sm.lse2[warp][slot][r] = L2[n][j];
 #pragma unroll
                     for (int c = 0; c < kB; ++c)
                         *reinterpret_cast<float4*>(piece + r * kPitch + 32 * c + 4 * g) =
@@ -705,7 +723,7 @@ __global__ void __launch_bounds__(32 * kWarps, (NT == 1 ? 16 : 8) / kWarps) kv4_
 #pragma unroll
                     for (int c = 0; c < kB; ++c)
                         write_row<D>(p, b, hk, r0 + r, 8 * c + g,
-                                     make_float4(O[n][c][0][j], O[n][c][0][2 + j], O[n][c][1][j], O[n][c][1][2 + j]), M[n][j], lt);
+                                     make_float4(O[n][c][0][j], O[n][c][0][2 + j], O[n][c][1][j], O[n][c][1][2 + j]), L2[n][j]);
                 }
             }
         if (!complete && lane == 0) sm.piece[warp][slot] = {seg_x, b, seg, ng};
@@ -740,35 +758,36 @@ __global__ void __launch_bounds__(32 * kWarps, (NT == 1 ? 16 : 8) / kWarps) kv4_
         const int hk = pc.seg / p.n_rt, r0 = (pc.seg % p.n_rt) * kRows;
         const int n_rows = min(kRows, p.Sq * p.G - r0);
         const bool whole = kWhole || (seg_x >= x && seg_x + pc.ng <= x_end);
-        float* part = whole ? nullptr : p.partial + (2 * static_cast<int64_t>(blockIdx.x) + (seg_x < x ? 0 : 1)) * (kRows * (D + 2));
+        float* part = whole ? nullptr : p.partial + (2 * static_cast<int64_t>(blockIdx.x) + (seg_x < x ? 0 : 1)) * (kRows * (D + 1));
         for (int e = tid; e < n_rows * (D / 4); e += kThreads) {
             const int r = e / (D / 4), d4 = e % (D / 4);
             // (selected rather than branched on, so that the loads overlap; unrolled
             // no further, since a short call waits for the instructions themselves)
-            float m = kNoMax, lt = 0.0f;
+            float m = kNoMax, sum = 0.0f;
             float4 v = make_float4(0, 0, 0, 0);
 #pragma unroll 4
-            for (int k = kWhole ? 1 : 0; k < 2 * kWarps; k += kWhole ? 2 : 1) m = fmaxf(m, (group >> k) & 1u ? sm.m[k >> 1][k & 1][r] : kNoMax);
+            for (int k = kWhole ? 1 : 0; k < 2 * kWarps; k += kWhole ? 2 : 1)
+                m = fmaxf(m, (group >> k) & 1u ? sm.lse2[k >> 1][k & 1][r] : kNoMax);
 #pragma unroll 4
             for (int k = kWhole ? 1 : 0; k < 2 * kWarps; k += kWhole ? 2 : 1) {
                 const bool in = (group >> k) & 1u;
                 const float* src = (k & 1) ? reinterpret_cast<const float*>(sm.ring[k >> 1][0]) : &sm.first[k >> 1][0][0];
                 const float4 y = in ? *reinterpret_cast<const float4*>(src + r * kPitch + 4 * d4) : make_float4(0, 0, 0, 0);
-                const float f = in ? ex2(sm.m[k >> 1][k & 1][r] - m) : 0.0f;
-                lt = fmaf(f, in ? sm.l[k >> 1][k & 1][r] : 0.0f, lt);
+                const float f = in ? ex2(sm.lse2[k >> 1][k & 1][r] - m) : 0.0f;
+                sum += f;
                 v.x = fmaf(f, y.x, v.x);
                 v.y = fmaf(f, y.y, v.y);
                 v.z = fmaf(f, y.z, v.z);
                 v.w = fmaf(f, y.w, v.w);
             }
+            const float inv = 1.0f / sum;
+            v = make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv);
+            m += __log2f(sum);
             if (whole) {
-                write_row<D>(p, pc.b, hk, r0 + r, d4, v, m, lt);
+                write_row<D>(p, pc.b, hk, r0 + r, d4, v, m);
             } else {
                 reinterpret_cast<float4*>(part)[r * (D / 4) + d4] = v;
-                if (d4 == 0) {
-                    part[kRows * D + r] = m;
-                    part[kRows * D + kRows + r] = lt;
-                }
+                if (d4 == 0) part[kRows * D + r] = m;
             }
         }
     }
@@ -778,18 +797,18 @@ __global__ void __launch_bounds__(32 * kWarps, (NT == 1 ? 16 : 8) / kWarps) kv4_
 // rows of empty sequences.  A block takes kPer rows of a segment: a warp a row
 // weighs the parts, then kSlices groups of kPer * D / 4 threads each add every
 // kSlices-th part, so that a row split over all resident blocks still waits for
-// few loads in turn (8 segments of 38 parts: 24 us with one thread adding all of
-// an element's parts, 9 us so).  One row a block where segments are few, four
-// where they are many and their parts few (16 sequences, 64 segments: 20.7 us
-// for the whole call with one row a block, 19.4 us with four).  Launched to
+// few loads in turn (8 segments of 38 parts: 12 us less than with one thread
+// adding all of an element's parts).  One row a block where segments are few,
+// four where they are many and their parts few (16 sequences, 64 segments: 20.7
+// us for the whole call with one row a block, 18.7 with four).  Launched to
 // overlap the end of the first kernel: what precedes the wait depends on the
 // lengths alone.
 template <int D, int NT, int kPer>
 __global__ void __launch_bounds__(kJoinThreads) kv4_join_kernel(const Params p, int n_blocks) {
     constexpr int kRows = 8 * NT, kLanes = D / 4, kSlices = kJoinThreads / (kLanes * kPer);
     __shared__ int64_t warp_sum[2][kJoinThreads / 32];
-    __shared__ float row_m[kPer], row_l[kPer];
-    __shared__ float fac[kPer][kMaxBlocks];
+    __shared__ float row_lse2[kPer], row_inv[kPer];
+    __shared__ float fac[kPer][kBlocks];
     __shared__ float4 red[kSlices][kPer * kLanes];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int n_seg = p.Hkv * p.n_rt;
@@ -828,26 +847,26 @@ __global__ void __launch_bounds__(kJoinThreads) kv4_join_kernel(const Params p, 
     // of every later block
     const int n_parts = c1 - c0 + 1;
     auto part_of = [&](int j) {
-        return p.partial + (2 * static_cast<int64_t>(c0 + j) + (j == 0 ? 1 : 0)) * (kRows * (D + 2));
+        return p.partial + (2 * static_cast<int64_t>(c0 + j) + (j == 0 ? 1 : 0)) * (kRows * (D + 1));
     };
     if (warp < kPer) {
         const int r = r_first + warp;
-        float m = kNoMax, l = 0.0f;
+        float m = kNoMax, sum = 0.0f;
         for (int j = lane; j < n_parts; j += 32) {
-            const float mj = part_of(j)[kRows * D + r];
-            fac[warp][j] = mj;
-            m = fmaxf(m, mj);
+            const float x = part_of(j)[kRows * D + r];
+            fac[warp][j] = x;
+            m = fmaxf(m, x);
         }
         for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
         for (int j = lane; j < n_parts; j += 32) {
             const float f = ex2(fac[warp][j] - m);
             fac[warp][j] = f;
-            l = fmaf(f, part_of(j)[kRows * D + kRows + r], l);
+            sum += f;
         }
-        for (int o = 16; o; o >>= 1) l += __shfl_xor_sync(0xFFFFFFFFu, l, o);
+        for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
         if (lane == 0) {
-            row_m[warp] = m;
-            row_l[warp] = l;
+            row_lse2[warp] = n_parts ? m + __log2f(sum) : kNoMax;
+            row_inv[warp] = n_parts ? 1.0f / sum : 0.0f;
         }
     }
     __syncthreads();
@@ -875,7 +894,8 @@ __global__ void __launch_bounds__(kJoinThreads) kv4_join_kernel(const Params p, 
             a.z += v.z;
             a.w += v.w;
         }
-        write_row<D>(p, b, hk, r0 + r, d4, a, row_m[k], row_l[k]);
+        const float inv = row_inv[k];
+        write_row<D>(p, b, hk, r0 + r, d4, make_float4(a.x * inv, a.y * inv, a.z * inv, a.w * inv), row_lse2[k]);
     }
 }
 
@@ -889,13 +909,6 @@ bool takes_whole(int64_t segments, int page_size, int max_pages) {
 int64_t segments_of(int B, int Sq, int Hq, int Hkv) {
     const int rows = Sq * (Hq / Hkv), per = 8 * row_tiles(rows);
     return static_cast<int64_t>(B) * Hkv * ((rows + per - 1) / per);
-}
-
-// Blocks of the split form.
-template <int NT>
-int stream_blocks(int64_t segments, int page_size, int max_pages) {
-    const int64_t most = segments * max_pages * (page_size / kKv4Group);
-    return (most >= kLongShare * kResident ? kMaxBlocks : kResident) / NT;
 }
 
 // The whole form in blocks of W warps.
@@ -913,13 +926,13 @@ template <int D, int NT>
 cudaError_t launch(Params p, int n_whole, cudaStream_t st) {
     const bool many = n_whole >= kManySegments;
     if (!p.partial)
-        return n_whole > kResident / NT ? launch_whole<D, NT, kManyWarps>(p, n_whole, st)
+        return n_whole > kBlocks / NT ? launch_whole<D, NT, kManyWarps>(p, n_whole, st)
                                         : launch_whole<D, NT, kFewWarps>(p, n_whole, st);
     static KernelSetup setup;
     constexpr int W = kSplitWarps, smem = sizeof(Smem<D, NT, W>);
     cudaError_t e = setup(reinterpret_cast<const void*>(kv4_attn_kernel<D, NT, false, W>), smem, 0);
     if (e != cudaSuccess) return e;
-    const int blocks = stream_blocks<NT>(n_whole, p.page_size, p.max_pages);
+    constexpr int blocks = kBlocks / NT;
     kv4_attn_kernel<D, NT, false, W><<<blocks, 32 * W, smem, st>>>(p);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
@@ -941,7 +954,7 @@ cudaError_t launch(Params p, int n_whole, cudaStream_t st) {
 size_t kv4_attention_workspace_bytes(int B, int Sq, int Hq, int Hkv, int D, int page_size, int max_pages) {
     if (takes_whole(segments_of(B, Sq, Hq, Hkv), page_size, max_pages)) return 0;
     const int nt = row_tiles(Sq * (Hq / Hkv));
-    return static_cast<size_t>(kMaxBlocks / nt) * 2 * (8 * nt) * (D + 2) * sizeof(float);
+    return static_cast<size_t>(kBlocks / nt) * 2 * (8 * nt) * (D + 1) * sizeof(float);
 }
 
 cudaError_t launch_kv4_attention(const Kv4AttnLaunch& a, cudaStream_t st) {

@@ -173,15 +173,17 @@ def test_attention_matches_the_held_values(fsa, case):
 
 
 @pytest.mark.parametrize("kind", ["sink", "value_outlier", "block_outlier", "tiny_values", "huge_keys", "zero_keys",
-                                  "growing", "one_hot"])
+                                  "growing", "one_hot", "late_outlier", "outliers_growing", "zero_then_large"])
 def test_attention_over_uneven_rows(fsa, kind):
     """Rows of very different sizes: weights that span the range of f16, value
     scales that differ between tokens and between the blocks of a token."""
     lens, Hq, Hkv, D, page = [700, 96], 8, 2, 128, 64
+    queries = _values(_bits((2, 1, Hq, D), 6)).reshape(2, Hkv, Hq // Hkv, D)
 
     def edit(k, v):
-        for a, c in zip(k, v):
+        for b, (a, c) in enumerate(zip(k, v)):
             ka, va = _values(a), _values(c)
+            away = -queries[b].sum(1) * np.sqrt(D) / D     # a key that every head scores about -1
             if kind == "sink":
                 ka[0] *= 12
                 va[0] *= 2.0 ** -10
@@ -202,6 +204,16 @@ def test_attention_over_uneven_rows(fsa, kind):
                 va *= np.exp2(np.linspace(-12, 12, len(va)))[:, None, None]
             elif kind == "one_hot":
                 ka[len(ka) // 2] *= 100
+            elif kind == "late_outlier":      # weight 2^-20 or so, value 2^20: counts as much as the others
+                ka[-40] = 14 * away
+                va[-40] *= 2.0 ** 20
+            elif kind == "outliers_growing":  # the same again and again, each larger and further off
+                for i in range(1, 9):
+                    ka[i * len(ka) // 9] = 8 * i * away
+                    va[i * len(ka) // 9] *= 2.0 ** (11 * i)
+            elif kind == "zero_then_large":   # no values at all at first
+                va[:len(va) // 2] = 0
+                va[len(va) // 2:] *= 2.0 ** 100
             a[:] = fsa_inputs.to_bf16_bits(ka.astype(np.float32))
             c[:] = fsa_inputs.to_bf16_bits(va.astype(np.float32))
     cache, table, n, held = _sequences(fsa, lens, Hkv, D, page, seed=3, edit=edit)

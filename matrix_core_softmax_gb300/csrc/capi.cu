@@ -454,7 +454,7 @@ namespace {
 fsa_status check_kv4(const void* cache, int64_t num_pages, int page_size, int H_kv, int D) {
     if (!cache || !aligned16(cache)) return FSA_ERR_INVALID_ARGUMENT;
     if (D != 64 && D != 128) return FSA_ERR_UNSUPPORTED;
-    // (groups are numbered in 32 bits: 2^32 of them would be 9 TB)
+    // (groups are numbered in 32 bits, two numbers set aside: 2^32 of them would be 9 TB)
     if (num_pages < 1 || num_pages > INT32_MAX || fsa_kv4_page_bytes(H_kv, page_size, D) == 0 ||
         num_pages * H_kv * (page_size / 32) >= int64_t{UINT32_MAX})
         return FSA_ERR_INVALID_ARGUMENT;

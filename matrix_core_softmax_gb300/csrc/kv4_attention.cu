@@ -43,8 +43,9 @@
 // unnormalised sums, whose scale 2^(M + R_b) may lie outside of FP32.
 //
 // Work split.  The cache's groups of all (sequence, key head, 8- or 16-row tile)
-// segments form one line, cut into equal shares, one per resident block, and a
-// share into equal parts, one per warp: long contexts spread over the GPU and
+// segments form one line (kSegmentCost places before each segment's groups),
+// cut into equal shares, one per resident block, and a share into equal parts,
+// one per warp: long contexts spread over the GPU and
 // ragged batches balance.  A warp runs along its part on its own: a ring of
 // bulk copies (one 32-key group, 4352 bytes at D = 128, a copy) that reaches
 // over the segments' ends, its own softmax state, and the output of every
@@ -72,7 +73,7 @@ constexpr int kSplitWarps = 8;    // warps of a block of the split form and of t
 constexpr int kJoinThreads = 256;
 constexpr int kStages = 2;        // (three: 1 % slower, they leave less L1)
 constexpr int kBlocks = 304;      // of the split form: two on each of 152 SMs
-constexpr int kMinShare = kSplitWarps; // groups of a block, at least one a warp
+constexpr int kMinShare = kSplitWarps; // places of a block, at least one a warp
 // A block takes a whole segment up to this many groups, twice as many where
 // there are many segments.  8 key heads of D = 128, whole against split: one
 // sequence of 1000 keys 8.4 / 9.2 us, of 2000 12.8 / 10.0; 64 sequences of up to
@@ -85,7 +86,13 @@ constexpr int kManySegments = 64; // from here on the join takes four rows a blo
 // of up to 1000 16.0 / 20.4, of up to 2000 29.6 / 30.1; 8 sequences of up to 1000
 // 10.2 / 9.0, of up to 2000 16.6 / 13.4.
 constexpr int kFewWarps = 8, kManyWarps = 4;
-constexpr uint32_t kNoGroup = 0xFFFFFFFFu;
+// A segment takes this many places of the line before its groups, for what a
+// warp spends on taking it up and writing it (some 3 us, against 1.9 us for a
+// group beside 15 other warps; without them the warps that meet many short
+// sequences finished last, 75 us against 56 for the others on 64 ragged
+// sequences of up to 8000 keys).
+constexpr int kSegmentCost = 3;
+constexpr uint32_t kNoGroup = 0xFFFFFFFFu, kNoPlace = 0xFFFFFFFEu;
 constexpr float kNoMax = -1e30f;
 constexpr float kLag = 4.0f;      // how far M may lag behind (log2)
 constexpr unsigned kMostY = 96;   // largest y
@@ -108,7 +115,7 @@ struct Params {
 
 // A piece of a segment: what one warp made of the groups of it in its part.
 struct Piece {
-    int64_t seg_x;  // the segment's first group on the line
+    int64_t seg_x;  // the place of the segment's first group
     int b, seg, ng; // sequence (-1: no piece), segment of it, its groups
 };
 
@@ -190,6 +197,8 @@ __device__ __forceinline__ int seq_groups(const Params& p, int b) {
     bool bad;
     return (seq_len(p, b, &bad) + kKv4Group - 1) / kKv4Group;
 }
+// Places on the line of a segment of ng groups (of the split form).
+__device__ __forceinline__ int places_of(int ng) { return ng ? ng + kSegmentCost : 0; }
 
 // Row position of a key in its group and back (an involution within each 8):
 // position r of a 16-row tile is key r with its low bit flipped by bit 1, so
@@ -203,14 +212,14 @@ struct Row {
 };
 __device__ __forceinline__ Row row_of(const Params& p, int r) { return {r / p.G, r % p.G}; }
 
-// Segment of a sequence of ng-group segments that its group `rel` lies in (a
-// 64-bit division takes 1 us, and every warp waits for two of these).
-__device__ __forceinline__ int segment_at(int64_t rel, int ng) {
-    if (rel <= 0x7FFFFFFF) return static_cast<int>(static_cast<uint32_t>(rel) / static_cast<uint32_t>(ng));
-    return static_cast<int>(rel / ng);
+// Segment of a sequence with segments of `places` places that its place `rel`
+// lies in (a 64-bit division takes 1 us, and every warp waits for two of these).
+__device__ __forceinline__ int segment_at(int64_t rel, int places) {
+    if (rel <= 0x7FFFFFFF) return static_cast<int>(static_cast<uint32_t>(rel) / static_cast<uint32_t>(places));
+    return static_cast<int>(rel / places);
 }
 
-// Groups of a block's share of `all` groups.
+// Places of a block's share of a line of `all` places.
 __device__ __forceinline__ int64_t share_of(int64_t all, int n_blocks) {
     return max(static_cast<int64_t>(kMinShare), (all + n_blocks - 1) / n_blocks);
 }
@@ -249,8 +258,8 @@ __global__ void __launch_bounds__(32 * kWarps, (NT == 1 ? 16 : 8) / kWarps) kv4_
     if (lane < kStages) mbar_init(&sm.full[warp][lane], 1);
     fence_mbar_init();
 
-    // this block's share [x, x_end) of the line of groups, and where it starts:
-    // sequence b, its first group at x_seq
+    // this block's share [x, x_end) of the line, and where it starts: sequence b,
+    // whose places begin at x_seq
     int64_t x, x_end, x_seq;
     int b, len;
     const int n_seg = p.Hkv * p.n_rt;  // segments of a sequence
@@ -284,7 +293,7 @@ __global__ void __launch_bounds__(32 * kWarps, (NT == 1 ? 16 : 8) / kWarps) kv4_
         int64_t sum = 0;
         for (int i = b0; i < b1; ++i) {
             bool bad;
-            sum += (seq_len(p, i, &bad) + kKv4Group - 1) / kKv4Group;
+            sum += places_of((seq_len(p, i, &bad) + kKv4Group - 1) / kKv4Group);
             if (bad && blockIdx.x == 0) atomicOr(p.err_word, kErrBadIndex);
         }
         // inclusive scan over the warp, then over the warps
@@ -309,7 +318,7 @@ __global__ void __launch_bounds__(32 * kWarps, (NT == 1 ? 16 : 8) / kWarps) kv4_
             int i = b0;
             int64_t at = before * n_seg;
             while (true) {
-                const int64_t next = at + static_cast<int64_t>(seq_groups(p, i)) * n_seg;
+                const int64_t next = at + static_cast<int64_t>(places_of(seq_groups(p, i))) * n_seg;
                 if (x < next) break;
                 at = next;
                 ++i;
@@ -324,75 +333,91 @@ __global__ void __launch_bounds__(32 * kWarps, (NT == 1 ? 16 : 8) / kWarps) kv4_
         len = seq_len(p, b, &bad);
     }
     const int gpp = p.page_size / kKv4Group;
-    // this warp's part [pos, pos_end) of the share
+    // this warp's part of the share
     const int64_t pos_begin = x + (x_end - x) * warp / kWarps, pos_end = x + (x_end - x) * (warp + 1) / kWarps;
     const int count = static_cast<int>(pos_end - pos_begin);
 
-    // copies, by the warp's group number j
-    uint32_t ids = 0;        // lane i: the cache's group number of the warp's group 32 n + i
+    // copies: the next place to look at, and the copies issued so far (copy k in
+    // stage k mod kStages)
+    int next = 0, n_in = 0;
+    uint32_t ids = 0;        // lane i: the cache's group number at place 32 n + i of the part
     uint32_t bad_stage = 0;  // stages whose group has no page
     int ib = b;              // sequence that the next ids are looked for from,
-    int64_t ix = x_seq;      // its first group and the groups of its segments
+    int64_t ix = x_seq;      // where its places begin, and the groups of its segments
     int ing = (len + kKv4Group - 1) / kKv4Group;
-    auto issue = [&](int j) {
-        if ((j & 31) == 0) {
-            const int64_t pos = pos_begin + j + lane;
-            ids = kNoGroup;
-            if (pos < pos_end) {
-                int seg, gi;
-                if constexpr (kWhole) {
-                    seg = blockIdx.x - b * n_seg;
-                    gi = static_cast<int>(pos - x);
-                } else {
-                    while (pos >= ix + static_cast<int64_t>(ing) * n_seg) {
-                        ix += static_cast<int64_t>(ing) * n_seg;
-                        ing = seq_groups(p, ++ib);
+    auto issue = [&]() {
+        while (next < count) {
+            if ((next & 31) == 0) {
+                const int64_t pos = pos_begin + next + lane;
+                ids = kNoPlace;
+                if (pos < pos_end) {
+                    int seg, gi;
+                    if constexpr (kWhole) {
+                        seg = blockIdx.x - b * n_seg;
+                        gi = static_cast<int>(pos - x);
+                    } else {
+                        while (pos >= ix + static_cast<int64_t>(places_of(ing)) * n_seg) {
+                            ix += static_cast<int64_t>(places_of(ing)) * n_seg;
+                            ing = seq_groups(p, ++ib);
+                        }
+                        seg = segment_at(pos - ix, places_of(ing));
+                        gi = static_cast<int>(pos - ix - static_cast<int64_t>(seg) * places_of(ing)) - kSegmentCost;
                     }
-                    seg = segment_at(pos - ix, ing);
-                    gi = static_cast<int>(pos - ix - static_cast<int64_t>(seg) * ing);
+                    if (gi >= 0) {
+                        const int pi = gi / gpp;
+                        const int page = __ldg(p.page_table + static_cast<int64_t>(ib) * p.max_pages + pi);
+                        ids = kNoGroup;
+                        if (page >= 0 && page < p.num_pages)  // (a 9 TB cache would have 2^32 - 2 groups)
+                            ids = (static_cast<uint32_t>(page) * p.Hkv + seg / p.n_rt) * gpp + (gi - pi * gpp);
+                        else
+                            atomicOr(p.err_word, kErrBadIndex);
+                    }
                 }
-                const int pi = gi / gpp;
-                const int page = __ldg(p.page_table + static_cast<int64_t>(ib) * p.max_pages + pi);
-                if (page >= 0 && page < p.num_pages)  // (a 9 TB cache would have 2^32 groups)
-                    ids = (static_cast<uint32_t>(page) * p.Hkv + seg / p.n_rt) * gpp + (gi - pi * gpp);
-                else
-                    atomicOr(p.err_word, kErrBadIndex);
+                if constexpr (!kWhole) {
+                    const int last = min(31, count - 1 - next);
+                    ib = __shfl_sync(0xFFFFFFFFu, ib, last);
+                    ix = __shfl_sync(0xFFFFFFFFu, ix, last);
+                    ing = __shfl_sync(0xFFFFFFFFu, ing, last);
+                }
             }
-            if constexpr (!kWhole) {
-            const int last = min(31, count - 1 - j);
-            ib = __shfl_sync(0xFFFFFFFFu, ib, last);
-            ix = __shfl_sync(0xFFFFFFFFu, ix, last);
-            ing = __shfl_sync(0xFFFFFFFFu, ing, last);
+            const uint32_t id = __shfl_sync(0xFFFFFFFFu, ids, next & 31);
+            ++next;
+            if (!kWhole && id == kNoPlace) continue;
+            const int st = n_in % kStages;
+            ++n_in;
+            bad_stage &= ~(1u << st);
+            if (id == kNoGroup) bad_stage |= 1u << st;
+            if (lane == 0) {
+                if (id == kNoGroup) {
+                    mbar_arrive(&sm.full[warp][st]);
+                } else {
+                    mbar_arrive_expect_tx(&sm.full[warp][st], kGroupBytes);
+                    bulk_load(sm.ring[warp][st], p.cache + static_cast<uint64_t>(id) * kGroupBytes, kGroupBytes, &sm.full[warp][st]);
+                }
             }
-        }
-        const uint32_t id = __shfl_sync(0xFFFFFFFFu, ids, j & 31);
-        const int st = j % kStages;
-        bad_stage &= ~(1u << st);
-        if (id == kNoGroup) bad_stage |= 1u << st;
-        if (lane == 0) {
-            if (id == kNoGroup) {
-                mbar_arrive(&sm.full[warp][st]);
-            } else {
-                mbar_arrive_expect_tx(&sm.full[warp][st], kGroupBytes);
-                bulk_load(sm.ring[warp][st], p.cache + static_cast<uint64_t>(id) * kGroupBytes, kGroupBytes, &sm.full[warp][st]);
-            }
+            return;
         }
     };
-    for (int j = 0; j < min(count, kStages); ++j) issue(j);
+#pragma unroll 1
+    for (int k = 0; k < kStages; ++k) issue();
 
-    int i = 0;  // the warp's groups done
+    int i = 0, n_out = 0;  // places passed, groups done
     bool ok = true;
     while (ok && i < count) {
         const int64_t pos = pos_begin + i;
         int ng = (len + kKv4Group - 1) / kKv4Group;
-        while (!kWhole && pos >= x_seq + static_cast<int64_t>(ng) * n_seg) {
-            x_seq += static_cast<int64_t>(ng) * n_seg;
+        while (!kWhole && pos >= x_seq + static_cast<int64_t>(places_of(ng)) * n_seg) {
+            x_seq += static_cast<int64_t>(places_of(ng)) * n_seg;
             bool bad;
             len = seq_len(p, ++b, &bad);
             ng = (len + kKv4Group - 1) / kKv4Group;
         }
-        const int seg = kWhole ? blockIdx.x - b * n_seg : segment_at(pos - x_seq, ng);
-        const int64_t seg_x = x_seq + static_cast<int64_t>(seg) * ng;
+        const int seg = kWhole ? blockIdx.x - b * n_seg : segment_at(pos - x_seq, places_of(ng));
+        const int64_t seg_x = kWhole ? x : x_seq + static_cast<int64_t>(seg) * places_of(ng) + kSegmentCost;
+        if (!kWhole && pos < seg_x) {
+            i = static_cast<int>(min(seg_x, pos_end) - pos_begin);
+            continue;
+        }
         const int i_end = kWhole ? count : static_cast<int>(min(seg_x + ng, pos_end) - pos_begin);  // end of the segment's groups
         const int hk = seg / p.n_rt, r0 = (seg % p.n_rt) * kRows;
 
@@ -446,8 +471,8 @@ __global__ void __launch_bounds__(32 * kWarps, (NT == 1 ? 16 : 8) / kWarps) kv4_
         uint32_t R02 = 0, R13 = 0;  // largest value scale bytes so far
 
         for (; i < i_end; ++i) {
-            const int st = i % kStages;
-            ok = __all_sync(0xFFFFFFFFu, mbar_wait(&sm.full[warp][st], (i / kStages) & 1, p.timeout_ns, &sm.abort));
+            const int st = n_out % kStages;
+            ok = __all_sync(0xFFFFFFFFu, mbar_wait(&sm.full[warp][st], (n_out / kStages) & 1, p.timeout_ns, &sm.abort));
             if (!ok) break;
             if (!((bad_stage >> st) & 1u)) {
                 const uint8_t* buf = sm.ring[warp][st];
@@ -680,7 +705,8 @@ __global__ void __launch_bounds__(32 * kWarps, (NT == 1 ? 16 : 8) / kWarps) kv4_
                 }
             }
             __syncwarp();
-            if (i + kStages < count) issue(i + kStages);
+            ++n_out;
+            issue();
         }
         if (!ok) break;
 
@@ -735,8 +761,7 @@ __global__ void __launch_bounds__(32 * kWarps, (NT == 1 ? 16 : 8) / kWarps) kv4_
             atomicOr(p.err_word, kErrTimeout);
         }
         int dummy = 0;
-        for (int j = i; j < min(count, i + kStages); ++j)
-            mbar_wait(&sm.full[warp][j % kStages], (j / kStages) & 1, p.timeout_ns, &dummy);
+        for (int k = n_out; k < n_in; ++k) mbar_wait(&sm.full[warp][k % kStages], (k / kStages) & 1, p.timeout_ns, &dummy);
     }
     // the second kernel's blocks may start as these finish
     if constexpr (!kWhole) asm volatile("griddepcontrol.launch_dependents;");
@@ -818,7 +843,7 @@ __global__ void __launch_bounds__(kJoinThreads) kv4_join_kernel(const Params p, 
     if (r0 + r_first >= p.Sq * p.G) return;
     int64_t before = 0, total = 0;
     for (int i = tid; i < p.B; i += kJoinThreads) {
-        const int n = seq_groups(p, i);
+        const int n = places_of(seq_groups(p, i));
         total += n;
         if (i < b) before += n;
     }
@@ -838,7 +863,7 @@ __global__ void __launch_bounds__(kJoinThreads) kv4_join_kernel(const Params p, 
     }
     const int ng = seq_groups(p, b);
     const int64_t share = share_of(total * n_seg, n_blocks);
-    const int64_t s0 = before * n_seg + static_cast<int64_t>(seg) * ng;
+    const int64_t s0 = before * n_seg + static_cast<int64_t>(seg) * places_of(ng) + kSegmentCost;
     const int c0 = static_cast<int>(s0 / share), c1 = ng ? static_cast<int>((s0 + ng - 1) / share) : c0 - 1;
     if (c0 == c1) return;  // one block wrote the result
     asm volatile("griddepcontrol.wait;" ::: "memory");

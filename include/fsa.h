@@ -427,9 +427,10 @@ FSA_API fsa_status fsa_kv4_read(const void *cache, int64_t num_pages, int page_s
  *    cache skipped with all of its keys; both are reported by
  *    fsa_get_device_error as FSA_ERR_INVALID_ARGUMENT.
  * Requirements: B, Sq, Hq, Hkv >= 1, Hkv divides Hq, B <= 65535, Hkv <= 65535,
- * Sq * Hq / Hkv <= 65535, B * Hkv * ceil(Sq * Hq / Hkv / 8) < 2^31, D in
- * {64, 128}, max_pages >= 1, max_pages * page_size <= 2^30, and a cache as
- * above.
+ * Sq * Hq / Hkv <= 65535, D in {64, 128}, max_pages >= 1, max_pages *
+ * page_size <= 2^30, a cache as above, and for the row tiles T = B * Hkv *
+ * ceil(Sq * Hq / Hkv / 8): T < 2^31, T * (max_pages * page_size / 32 + 4) <=
+ * 2^40.
  */
 FSA_API fsa_status fsa_kv4_attention_fwd(const void *q, int64_t q_stride, const void *cache,
                                          const int32_t *page_table, const int32_t *seq_lens, void *o,

@@ -512,8 +512,12 @@ fsa_status check_kv4_attention(int B, int Sq, int Hq, int Hkv, int D, int page_s
     if (D != 64 && D != 128) return FSA_ERR_UNSUPPORTED;
     if (B < 1 || B > 65535 || Sq < 1 || Hq < 1 || Hkv < 1 || Hkv > 65535 || Hq % Hkv != 0 ||
         static_cast<int64_t>(Sq) * (Hq / Hkv) > 65535 || max_pages < 1 ||
-        fsa_kv4_page_bytes(Hkv, page_size, D) == 0 || static_cast<int64_t>(max_pages) * page_size > (1 << 30) ||
-        static_cast<int64_t>(B) * Hkv * ((static_cast<int64_t>(Sq) * (Hq / Hkv) + 7) / 8) > INT32_MAX)
+        fsa_kv4_page_bytes(Hkv, page_size, D) == 0 || static_cast<int64_t>(max_pages) * page_size > (1 << 30))
+        return FSA_ERR_INVALID_ARGUMENT;
+    // (eight-row tiles of all sequences and key heads number the blocks of a grid;
+    // a warp counts the 32-key groups of its part in 32 bits)
+    const int64_t tiles = static_cast<int64_t>(B) * Hkv * ((static_cast<int64_t>(Sq) * (Hq / Hkv) + 7) / 8);
+    if (tiles > INT32_MAX || tiles > (int64_t{1} << 40) / (max_pages * static_cast<int64_t>(page_size / 32) + 4))
         return FSA_ERR_INVALID_ARGUMENT;
     return FSA_OK;
 }

@@ -827,7 +827,8 @@ __global__ void __launch_bounds__(32 * kWarps, (NT == 1 ? 16 : 8) / kWarps) kv4_
 // four where they are many and their parts few (16 sequences, 64 segments: 20.7
 // us for the whole call with one row a block, 18.7 with four).  Launched to
 // overlap the end of the first kernel: what precedes the wait depends on the
-// lengths alone.
+// lengths alone, and every block waits before it ends, so that this kernel's end
+// is the first one's, too.
 template <int D, int NT, int kPer>
 __global__ void __launch_bounds__(kJoinThreads) kv4_join_kernel(const Params p, int n_blocks) {
     constexpr int kRows = 8 * NT, kLanes = D / 4, kSlices = kJoinThreads / (kLanes * kPer);
@@ -840,7 +841,10 @@ __global__ void __launch_bounds__(kJoinThreads) kv4_join_kernel(const Params p, 
     const int b = blockIdx.x / n_seg, seg = blockIdx.x - b * n_seg;
     const int r_first = blockIdx.y * kPer;
     const int hk = seg / p.n_rt, r0 = (seg % p.n_rt) * kRows;
-    if (r0 + r_first >= p.Sq * p.G) return;
+    if (r0 + r_first >= p.Sq * p.G) {
+        asm volatile("griddepcontrol.wait;" ::: "memory");
+        return;
+    }
     int64_t before = 0, total = 0;
     for (int i = tid; i < p.B; i += kJoinThreads) {
         const int n = places_of(seq_groups(p, i));
@@ -865,8 +869,8 @@ __global__ void __launch_bounds__(kJoinThreads) kv4_join_kernel(const Params p, 
     const int64_t share = share_of(total * n_seg, n_blocks);
     const int64_t s0 = before * n_seg + static_cast<int64_t>(seg) * places_of(ng) + kSegmentCost;
     const int c0 = static_cast<int>(s0 / share), c1 = ng ? static_cast<int>((s0 + ng - 1) / share) : c0 - 1;
-    if (c0 == c1) return;  // one block wrote the result
     asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (c0 == c1) return;  // one block wrote the result
 
     // the segment starts in block c0, as its second part, and is the first part
     // of every later block
@@ -970,8 +974,10 @@ cudaError_t launch(Params p, int n_whole, cudaStream_t st) {
     at.val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = &at;
     cfg.numAttrs = 1;
-    return many ? cudaLaunchKernelEx(&cfg, kv4_join_kernel<D, NT, 4>, p, blocks)
-                : cudaLaunchKernelEx(&cfg, kv4_join_kernel<D, NT, 1>, p, blocks);
+    e = many ? cudaLaunchKernelEx(&cfg, kv4_join_kernel<D, NT, 4>, p, blocks)
+             : cudaLaunchKernelEx(&cfg, kv4_join_kernel<D, NT, 1>, p, blocks);
+    if (e != cudaSuccess) cudaGetLastError();
+    return e;
 }
 
 }  // namespace

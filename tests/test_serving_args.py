@@ -60,6 +60,7 @@ def test_cache_attention_refused(lib):
                 dict(table=258), dict(lens=258), dict(lse=258), dict(qs=4), dict(qs=-8), dict(B=0), dict(B=65536), dict(Sq=0),
                 dict(Hq=5), dict(Hkv=0), dict(Hq=0), dict(pages=0), dict(page=40), dict(max_pages=0),
                 dict(max_pages=1 << 26), dict(Sq=40000), dict(B=65535, Hkv=65535, Hq=65535),
+                dict(B=65535, Hkv=8, Hq=8, max_pages=1 << 25),
                 dict(pages=1 << 30, page=64), dict(sm=float("nan")), dict(sm=float("inf"))]:
         assert _attend(lib, **bad) == INVALID, bad
     assert _attend(lib, D=80) == UNSUPPORTED

@@ -280,6 +280,22 @@ def test_attention_strides_outputs_and_workspace(fsa):
     assert (ws[need + 256:] == 0xFF).all()
 
 
+def test_sequences_that_share_pages(fsa):
+    # two continuations of one prefix, and a page that a sequence holds twice
+    Hq, Hkv, D, page = 8, 2, 128, 32
+    cache, table, _, held = _sequences(fsa, [300], Hkv, D, page, seed=17)
+    k, v = held[0]
+    t = table[0, :10].repeat(3, 1)
+    t[1, 9] = t[0, 2]                      # 9 common pages, another last one
+    t[2, 1:4] = t[2, 0]
+    n = torch.tensor([300, 310, 128], dtype=torch.int32, device="cuda")
+    q = to_dev(_bits((3, 1, Hq, D), 18))
+    o, lse = fsa.kv4_attention_fwd(q, cache, t, n, return_lse=True)
+    assert fsa.get_device_error() == 0
+    rows = [(k, v), *((torch.cat([x[:288], x[64:86]]) for x in (k, v)),), *((torch.cat([x[:32]] * 4) for x in (k, v)),)]
+    _check_sequences(fsa, o, lse, q, [tuple(r) for r in rows], ref.default_scale(D))
+
+
 def test_bad_pages_and_lengths_are_reported(fsa):
     lens, Hq, Hkv, D, page = [100, 100, 64], 4, 1, 128, 32
     cache, table, n, held = _sequences(fsa, lens, Hkv, D, page, seed=15)

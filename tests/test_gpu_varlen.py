@@ -153,6 +153,21 @@ def test_bad_bounds_are_reported(fsa):
             assert torch.equal(out[:20], good[:20])
 
 
+def test_a_bad_bound_behind_long_sequences(fsa):
+    # more pairs of query tiles than SMs: the sequences before the wrong bound are
+    # whole, the others left alone
+    Hq = Hkv = 16
+    lens = [2000, 1500, 300, 700]
+    q, k, v = (_bf16((sum(lens), Hq, 64), 40 + i) for i in range(3))
+    good = fsa.varlen_attention_fwd(q, k, v, _cu(lens))
+    bad = _cu(lens)
+    bad[3] = 3000
+    out = torch.full_like(q, 3.0)
+    fsa.varlen_attention_fwd(q, k, v, bad, _cu(lens), out=out)
+    assert fsa.get_device_error() == 1 and fsa.get_device_error() == 0
+    assert torch.equal(out[:3500], good[:3500]) and (out[3500:] == 3).all()
+
+
 def test_streams_and_graphs(fsa):
     Hq, Hkv, D = 8, 2, 128
     runs = []

@@ -69,10 +69,16 @@
 namespace fsa {
 namespace {
 
-constexpr int kSplitWarps = 8;    // warps of a block of the split form and of the join
+// Warps of a block of the split form: two blocks of eight on an SM, or, where a
+// warp's part may be kLongPart groups or more, one of sixteen, whose warps share
+// the SM evenly (of two blocks the first is served first, and a later one that
+// lags is the call's end).  64 sequences of up to 32768 keys 208.6 us with eight,
+// 199.5 with sixteen, of up to 8000 64.0 / 62.6; 16 of up to 8000 24.0 / 25.9,
+// one of 4000 11.2 / 11.5.
+constexpr int kSplitWarps = 8, kLongWarps = 16, kLongPart = 32;
 constexpr int kJoinThreads = 256;
 constexpr int kStages = 2;        // (three: 1 % slower, they leave less L1)
-constexpr int kBlocks = 304;      // of the split form: two on each of 152 SMs
+constexpr int kBlocks = 304;      // of eight warps: two on each of 152 SMs
 constexpr int kMinShare = kSplitWarps; // places of a block, at least one a warp
 // A block takes a whole segment up to this many groups, twice as many where
 // there are many segments.  8 key heads of D = 128, whole against split: one
@@ -768,12 +774,12 @@ __global__ void __launch_bounds__(32 * kWarps, (NT == 1 ? 16 : 8) / kWarps) kv4_
     __syncthreads();
     if (sm.abort) return;
 
-    // join the warps' pieces, segment after segment: bit k of a mask is piece k & 1
-    // of warp k / 2
+    // join the warps' pieces: bit k of a mask is piece k & 1 of warp k / 2
     const Piece& own = sm.piece[(lane >> 1) % kWarps][lane & 1];
     const int own_b = lane < 2 * kWarps ? own.b : -1;
     const int64_t own_x = own.seg_x;
     unsigned left = __ballot_sync(0xFFFFFFFFu, own_b >= 0);
+    int turn = warp;  // rows until this warp's next
     while (left) {
         const int k0 = __ffs(left) - 1;
         const int64_t seg_x = __shfl_sync(0xFFFFFFFFu, own_x, k0);
@@ -784,35 +790,76 @@ __global__ void __launch_bounds__(32 * kWarps, (NT == 1 ? 16 : 8) / kWarps) kv4_
         const int n_rows = min(kRows, p.Sq * p.G - r0);
         const bool whole = kWhole || (seg_x >= x && seg_x + pc.ng <= x_end);
         float* part = whole ? nullptr : p.partial + (2 * static_cast<int64_t>(blockIdx.x) + (seg_x < x ? 0 : 1)) * (kRows * (D + 1));
-        for (int e = tid; e < n_rows * (D / 4); e += kThreads) {
-            const int r = e / (D / 4), d4 = e % (D / 4);
-            // (selected rather than branched on, so that the loads overlap; unrolled
-            // no further, since a short call waits for the instructions themselves)
-            float m = kNoMax, sum = 0.0f;
-            float4 v = make_float4(0, 0, 0, 0);
-#pragma unroll 4
-            for (int k = kWhole ? 1 : 0; k < 2 * kWarps; k += kWhole ? 2 : 1)
-                m = fmaxf(m, (group >> k) & 1u ? sm.lse2[k >> 1][k & 1][r] : kNoMax);
-#pragma unroll 4
-            for (int k = kWhole ? 1 : 0; k < 2 * kWarps; k += kWhole ? 2 : 1) {
-                const bool in = (group >> k) & 1u;
-                const float* src = (k & 1) ? reinterpret_cast<const float*>(sm.ring[k >> 1][0]) : &sm.first[k >> 1][0][0];
-                const float4 y = in ? *reinterpret_cast<const float4*>(src + r * kPitch + 4 * d4) : make_float4(0, 0, 0, 0);
-                const float f = in ? ex2(sm.lse2[k >> 1][k & 1][r] - m) : 0.0f;
-                sum += f;
-                v.x = fmaf(f, y.x, v.x);
-                v.y = fmaf(f, y.y, v.y);
-                v.z = fmaf(f, y.z, v.z);
-                v.w = fmaf(f, y.w, v.w);
+        if constexpr (!kWhole && NT == 1) {
+            // the rows of all segments go around the warps (one segment after the
+            // other by the whole block held the blocks with many of them up by 20
+            // us); with 16 rows or one segment a block that is no gain
+            int r = turn;
+            for (; r < n_rows; r += kWarps) {
+                const bool in = (group >> lane) & 1u;
+                const float x2 = in ? sm.lse2[(lane >> 1) % kWarps][lane & 1][r] : kNoMax;
+                float m = x2;
+                for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+                const float f = in ? ex2(x2 - m) : 0.0f;
+                float sum = f;
+                for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
+                float4 v = make_float4(0, 0, 0, 0);
+                for (unsigned rest = group; rest; rest &= rest - 1) {
+                    const int k = __ffs(rest) - 1;
+                    const float fk = __shfl_sync(0xFFFFFFFFu, f, k);
+                    const float* src = (k & 1) ? reinterpret_cast<const float*>(sm.ring[k >> 1][0]) : &sm.first[k >> 1][0][0];
+                    if (lane < D / 4) {
+                        const float4 y = *reinterpret_cast<const float4*>(src + r * kPitch + 4 * lane);
+                        v.x = fmaf(fk, y.x, v.x);
+                        v.y = fmaf(fk, y.y, v.y);
+                        v.z = fmaf(fk, y.z, v.z);
+                        v.w = fmaf(fk, y.w, v.w);
+                    }
+                }
+                const float inv = 1.0f / sum;
+                v = make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv);
+                m += __log2f(sum);
+                if (lane < D / 4) {
+                    if (whole) {
+                        write_row<D>(p, pc.b, hk, r0 + r, lane, v, m);
+                    } else {
+                        reinterpret_cast<float4*>(part)[r * (D / 4) + lane] = v;
+                        if (lane == 0) part[kRows * D + r] = m;
+                    }
+                }
             }
-            const float inv = 1.0f / sum;
-            v = make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv);
-            m += __log2f(sum);
-            if (whole) {
-                write_row<D>(p, pc.b, hk, r0 + r, d4, v, m);
-            } else {
-                reinterpret_cast<float4*>(part)[r * (D / 4) + d4] = v;
-                if (d4 == 0) part[kRows * D + r] = m;
+            turn = r - n_rows;
+        } else {
+            for (int e = tid; e < n_rows * (D / 4); e += kThreads) {
+                const int r = e / (D / 4), d4 = e % (D / 4);
+                // (selected rather than branched on, so that the loads overlap; unrolled
+                // no further, since a short call waits for the instructions themselves)
+                float m = kNoMax, sum = 0.0f;
+                float4 v = make_float4(0, 0, 0, 0);
+#pragma unroll 4
+                for (int k = kWhole ? 1 : 0; k < 2 * kWarps; k += kWhole ? 2 : 1)
+                    m = fmaxf(m, (group >> k) & 1u ? sm.lse2[k >> 1][k & 1][r] : kNoMax);
+#pragma unroll 4
+                for (int k = kWhole ? 1 : 0; k < 2 * kWarps; k += kWhole ? 2 : 1) {
+                    const bool in = (group >> k) & 1u;
+                    const float* src = (k & 1) ? reinterpret_cast<const float*>(sm.ring[k >> 1][0]) : &sm.first[k >> 1][0][0];
+                    const float4 y = in ? *reinterpret_cast<const float4*>(src + r * kPitch + 4 * d4) : make_float4(0, 0, 0, 0);
+                    const float f = in ? ex2(sm.lse2[k >> 1][k & 1][r] - m) : 0.0f;
+                    sum += f;
+                    v.x = fmaf(f, y.x, v.x);
+                    v.y = fmaf(f, y.y, v.y);
+                    v.z = fmaf(f, y.z, v.z);
+                    v.w = fmaf(f, y.w, v.w);
+                }
+                const float inv = 1.0f / sum;
+                v = make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv);
+                m += __log2f(sum);
+                if (whole) {
+                    write_row<D>(p, pc.b, hk, r0 + r, d4, v, m);
+                } else {
+                    reinterpret_cast<float4*>(part)[r * (D / 4) + d4] = v;
+                    if (d4 == 0) part[kRows * D + r] = m;
+                }
             }
         }
     }
@@ -951,22 +998,20 @@ cudaError_t launch_whole(const Params& p, int segments, cudaStream_t st) {
     return cudaGetLastError();
 }
 
-template <int D, int NT>
-cudaError_t launch(Params p, int n_whole, cudaStream_t st) {
-    const bool many = n_whole >= kManySegments;
-    if (!p.partial)
-        return n_whole > kBlocks / NT ? launch_whole<D, NT, kManyWarps>(p, n_whole, st)
-                                        : launch_whole<D, NT, kFewWarps>(p, n_whole, st);
+// The split form in `blocks` blocks of W warps, and the join.
+template <int D, int NT, int W>
+cudaError_t launch_split(const Params& p, int segments, int blocks, cudaStream_t st) {
     static KernelSetup setup;
-    constexpr int W = kSplitWarps, smem = sizeof(Smem<D, NT, W>);
+    constexpr int smem = sizeof(Smem<D, NT, W>);
+    static_assert(smem <= 232448, "shared memory beyond the 227 KB a block may use");
     cudaError_t e = setup(reinterpret_cast<const void*>(kv4_attn_kernel<D, NT, false, W>), smem, 0);
     if (e != cudaSuccess) return e;
-    constexpr int blocks = kBlocks / NT;
     kv4_attn_kernel<D, NT, false, W><<<blocks, 32 * W, smem, st>>>(p);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
+    const bool many = segments >= kManySegments;
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(static_cast<unsigned>(n_whole), static_cast<unsigned>(8 * NT / (many ? 4 : 1)));
+    cfg.gridDim = dim3(static_cast<unsigned>(segments), static_cast<unsigned>(8 * NT / (many ? 4 : 1)));
     cfg.blockDim = dim3(kJoinThreads);
     cfg.stream = st;
     cudaLaunchAttribute at{};
@@ -978,6 +1023,19 @@ cudaError_t launch(Params p, int n_whole, cudaStream_t st) {
              : cudaLaunchKernelEx(&cfg, kv4_join_kernel<D, NT, 1>, p, blocks);
     if (e != cudaSuccess) cudaGetLastError();
     return e;
+}
+
+template <int D, int NT>
+cudaError_t launch(const Params& p, int segments, cudaStream_t st) {
+    if (!p.partial)
+        return segments > kBlocks / NT ? launch_whole<D, NT, kManyWarps>(p, segments, st)
+                                       : launch_whole<D, NT, kFewWarps>(p, segments, st);
+    if constexpr (NT == 1) {
+        const int64_t most = static_cast<int64_t>(segments) * p.max_pages * (p.page_size / kKv4Group);
+        if (most >= static_cast<int64_t>(kLongPart) * kBlocks * kSplitWarps)
+            return launch_split<D, NT, kLongWarps>(p, segments, kBlocks * kSplitWarps / kLongWarps, st);
+    }
+    return launch_split<D, NT, kSplitWarps>(p, segments, kBlocks / NT, st);
 }
 
 }  // namespace

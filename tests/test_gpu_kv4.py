@@ -250,6 +250,19 @@ def test_attention_with_a_wide_page_table(fsa, Hkv, D, Sq):
     _check_sequences(fsa, o, lse, q, held, ref.default_scale(D))
 
 
+@pytest.mark.parametrize("Hkv,D,G", [(3, 128, 5), (3, 64, 8), (3, 128, 1)])
+def test_attention_over_long_parts(fsa, Hkv, D, G):
+    # blocks of sixteen warps: long sequences, short ones between them
+    lens, page = [9000, 40, 0, 7000, 1, 700, 12000], 128
+    cache, table, n, held = _sequences(fsa, lens, Hkv, D, page, seed=14)
+    wide = torch.full((len(lens), 163840 // page), -1, dtype=torch.int32, device="cuda")
+    wide[:, :table.shape[1]] = table
+    q = to_dev(_bits((len(lens), 1, G * Hkv, D), 15, 2.0))
+    o, lse = fsa.kv4_attention_fwd(q, cache, wide, n, return_lse=True)
+    assert fsa.get_device_error() == 0
+    _check_sequences(fsa, o, lse, q, held, ref.default_scale(D))
+
+
 @pytest.mark.parametrize("seed", range(8))
 def test_attention_of_random_shapes(fsa, seed):
     rng = np.random.default_rng(1000 + seed)

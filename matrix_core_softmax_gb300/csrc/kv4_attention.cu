@@ -73,7 +73,7 @@ namespace {
 // warp's part may be kLongPart groups or more, one of sixteen, whose warps share
 // the SM evenly (of two blocks the first is served first, and a later one that
 // lags is the call's end).  64 sequences of up to 32768 keys 208.6 us with eight,
-// 199.5 with sixteen, of up to 8000 64.0 / 62.6; 16 of up to 8000 24.0 / 25.9,
+// 199.8 with sixteen, of up to 8000 64.0 / 62.6; 16 of up to 8000 24.0 / 25.9,
 // one of 4000 11.2 / 11.5.
 constexpr int kSplitWarps = 8, kLongWarps = 16, kLongPart = 32;
 constexpr int kJoinThreads = 256;
@@ -82,8 +82,9 @@ constexpr int kBlocks = 304;      // of eight warps: two on each of 152 SMs
 constexpr int kMinShare = kSplitWarps; // places of a block, at least one a warp
 // A block takes a whole segment up to this many groups, twice as many where
 // there are many segments.  8 key heads of D = 128, whole against split: one
-// sequence of 1000 keys 8.4 / 9.2 us, of 2000 12.8 / 10.0; 64 sequences of up to
-// 1000 keys 19.9 / 24.2, of up to 2000 29.6 / 31.5, of up to 4000 50 / 47.
+// sequence of 1000 keys 8.9 / 9.4 us, of 2000 13.2 / 9.8; 16 sequences of up to
+// 2000 keys 13.6 / 15.0, 32 of them 17.3 / 19.3, 64 30.1 / 27.6, 256 79.6 / 80.2;
+// 16 of up to 4000 22.1 / 19.4, 64 of them 44.3 / 41.9.
 constexpr int kWholeGroups = 32;
 constexpr int kManySegments = 64; // from here on the join takes four rows a block, too
 // More whole segments than fit the GPU in blocks of eight warps run in blocks of

@@ -44,15 +44,15 @@
 //
 // Work split.  The cache's groups of all (sequence, key head, 8- or 16-row tile)
 // segments form one line (kSegmentCost places before each segment's groups),
-// cut into equal shares, one per resident block, and a share into equal parts,
-// one per warp: long contexts spread over the GPU and
+// cut into equal shares, one per team of eight warps (two on an SM), and a share
+// into equal parts, one per warp: long contexts spread over the GPU and
 // ragged batches balance.  A warp runs along its part on its own: a ring of
 // bulk copies (one 32-key group, 4352 bytes at D = 128, a copy) that reaches
 // over the segments' ends, its own softmax state, and the output of every
 // segment that lies in its part as a whole.  Of the others it leaves at most
-// two pieces, the segment it starts in and the one it ends in; the block joins
+// two pieces, the segment it starts in and the one it ends in; the team joins
 // its warps' pieces, leaves at most two of its own, and a second kernel joins
-// those.  (With blocks that walked over segments together and met at each end,
+// those.  (With teams that walked over segments together and met at each end,
 // 64 ragged sequences of up to 2000 keys took 40.7 us.)  Where no sequence can
 // be longer than kWholeGroups groups a block takes one segment and there is no
 // second kernel.
@@ -69,17 +69,19 @@
 namespace fsa {
 namespace {
 
-// Warps of a block of the split form: two blocks of eight on an SM, or, where a
-// warp's part may be kLongPart groups or more, one of sixteen, whose warps share
-// the SM evenly (of two blocks the first is served first, and a later one that
-// lags is the call's end).  64 sequences of up to 32768 keys 208.6 us with eight,
-// 199.8 with sixteen, of up to 8000 64.0 / 62.6; 16 of up to 8000 24.0 / 25.9,
-// one of 4000 11.2 / 11.5.
-constexpr int kSplitWarps = 8, kLongWarps = 16, kLongPart = 32;
+// Warps that share a part of the line of the split form, a team: one a block and
+// two blocks on an SM, or, where a warp's part may be kLongPart groups or more,
+// two a block.  (Of two blocks on an SM the first is served first, 8 of the 152
+// SMs get two of the first ones or two of the later ones, and the later ones are
+// the call's end; the warps of one block are served evenly.  But the second kernel
+// cannot start before a block ends.)  One team a block / two, 8 key heads: 64
+// sequences of up to 32768 keys 208.6 / 198 us, of up to 8000 64.0 / 62.0, of up
+// to 4000 41.5 / 40.8; 16 of up to 8000 24.0 / 25.5, of up to 4000 19.3 / 21.4.
+constexpr int kTeamWarps = 8, kLongPart = 16;
 constexpr int kJoinThreads = 256;
 constexpr int kStages = 2;        // (three: 1 % slower, they leave less L1)
-constexpr int kBlocks = 304;      // of eight warps: two on each of 152 SMs
-constexpr int kMinShare = kSplitWarps; // places of a block, at least one a warp
+constexpr int kTeams = 304;       // of the split form: two on each of 152 SMs
+constexpr int kMinShare = kTeamWarps; // places of a team, at least one a warp
 // A block takes a whole segment up to this many groups, twice as many where
 // there are many segments.  8 key heads of D = 128, whole against split: one
 // sequence of 1000 keys 8.9 / 9.4 us, of 2000 13.2 / 9.8; 16 sequences of up to
@@ -112,7 +114,7 @@ struct Params {
     const int* seq_lens;
     uint16_t* o;
     float* lse;
-    float* partial;  // [block][2]: 8 NT rows of D, then their log2-sum-exp2; null: whole segments
+    float* partial;  // [team][2]: 8 NT rows of D, then their log2-sum-exp2; null: whole segments
     int64_t q_stride, num_pages;
     int B, Sq, Hq, Hkv, G, n_rt, page_size, max_pages;
     float c;  // sm_scale * log2(e)
@@ -226,9 +228,9 @@ __device__ __forceinline__ int segment_at(int64_t rel, int places) {
     return static_cast<int>(rel / places);
 }
 
-// Places of a block's share of a line of `all` places.
-__device__ __forceinline__ int64_t share_of(int64_t all, int n_blocks) {
-    return max(static_cast<int64_t>(kMinShare), (all + n_blocks - 1) / n_blocks);
+// Places of a team's share of a line of `all` places.
+__device__ __forceinline__ int64_t share_of(int64_t all, int n_teams) {
+    return max(static_cast<int64_t>(kMinShare), (all + n_teams - 1) / n_teams);
 }
 
 // Four channels of row r of a segment, and the row's log-sum-exp from its log2.
@@ -246,9 +248,10 @@ __device__ __forceinline__ void write_row(const Params& p, int b, int hk, int r,
 // that end inside a warp's part or pieces left to the second kernel; the short
 // calls that it serves wait for the kernel's instructions, too (300 keys: 7.5 us
 // with the general form).
-template <int D, int NT, bool kWhole, int kWarps>
-__global__ void __launch_bounds__(32 * kWarps, (NT == 1 ? 16 : 8) / kWarps) kv4_attn_kernel(const Params p) {
-    constexpr int kThreads = 32 * kWarps;
+template <int D, int NT, bool kWhole, int kWarps, int kBlockTeams>
+__global__ void __launch_bounds__(32 * kWarps * kBlockTeams, (NT == 1 ? 16 : 8) / (kWarps * kBlockTeams))
+    kv4_attn_kernel(const Params p) {
+    constexpr int kThreads = 32 * kWarps;  // of a team
     constexpr int kB = D / 32;
     constexpr int kGroupBytes = kv4_group_bytes(D);
     constexpr Kv4Layout L = kv4_layout(D);
@@ -256,22 +259,30 @@ __global__ void __launch_bounds__(32 * kWarps, (NT == 1 ? 16 : 8) / kWarps) kv4_
     constexpr int kPitch = Smem<D, NT, kWarps>::kPitch;
     static_assert(kRows * kPitch * 4 <= kStages * kGroupBytes, "a piece exceeds a warp's ring");
     extern __shared__ __align__(128) uint8_t smem_raw[];
-    Smem<D, NT, kWarps>& sm = *reinterpret_cast<Smem<D, NT, kWarps>*>(smem_raw);
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int block_team = kBlockTeams == 1 ? 0 : static_cast<int>(threadIdx.x) / kThreads;
+    const int tid = threadIdx.x - block_team * kThreads, warp = tid >> 5, lane = tid & 31;
     const int g = lane >> 2, t = lane & 3;
+    const int team = blockIdx.x + gridDim.x * block_team;  // few teams' work goes to as many SMs
+    Smem<D, NT, kWarps>& sm = reinterpret_cast<Smem<D, NT, kWarps>*>(smem_raw)[block_team];
+    auto sync = [&]() {
+        if constexpr (kBlockTeams == 1)
+            __syncthreads();
+        else
+            asm volatile("bar.sync %0, %1;" ::"r"(1 + block_team), "n"(kThreads) : "memory");
+    };
 
     if (tid == 0) sm.abort = 0;
     if (lane < 2) sm.piece[warp][lane].b = -1;
     if (lane < kStages) mbar_init(&sm.full[warp][lane], 1);
     fence_mbar_init();
 
-    // this block's share [x, x_end) of the line, and where it starts: sequence b,
+    // this team's share [x, x_end) of the line, and where it starts: sequence b,
     // whose places begin at x_seq
     int64_t x, x_end, x_seq;
     int b, len;
     const int n_seg = p.Hkv * p.n_rt;  // segments of a sequence
     if constexpr (kWhole) {
-        __syncthreads();
+        sync();
         b = blockIdx.x / n_seg;
         bool bad;
         len = seq_len(p, b, &bad);
@@ -301,7 +312,7 @@ __global__ void __launch_bounds__(32 * kWarps, (NT == 1 ? 16 : 8) / kWarps) kv4_
         for (int i = b0; i < b1; ++i) {
             bool bad;
             sum += places_of((seq_len(p, i, &bad) + kKv4Group - 1) / kKv4Group);
-            if (bad && blockIdx.x == 0) atomicOr(p.err_word, kErrBadIndex);
+            if (bad && team == 0) atomicOr(p.err_word, kErrBadIndex);
         }
         // inclusive scan over the warp, then over the warps
         int64_t inc = sum;
@@ -310,15 +321,15 @@ __global__ void __launch_bounds__(32 * kWarps, (NT == 1 ? 16 : 8) / kWarps) kv4_
             if (lane >= o) inc += v;
         }
         if (lane == 31) sm.scan[warp] = inc;
-        __syncthreads();
+        sync();
         int64_t before = inc - sum, total = 0;
         for (int w = 0; w < kWarps; ++w) {
             if (w < warp) before += sm.scan[w];
             total += sm.scan[w];
         }
         const int64_t all = total * n_seg;
-        const int64_t share = share_of(all, gridDim.x);
-        x = share * blockIdx.x;
+        const int64_t share = share_of(all, gridDim.x * kBlockTeams);
+        x = share * team;
         x_end = min(x + share, all);
         if (x >= x_end) return;
         if (before * n_seg <= x && x < (before + sum) * n_seg) {
@@ -333,7 +344,7 @@ __global__ void __launch_bounds__(32 * kWarps, (NT == 1 ? 16 : 8) / kWarps) kv4_
             sm.first_b = i;
             sm.first_x = at;
         }
-        __syncthreads();
+        sync();
         b = sm.first_b;
         x_seq = sm.first_x;
         bool bad;
@@ -772,7 +783,7 @@ __global__ void __launch_bounds__(32 * kWarps, (NT == 1 ? 16 : 8) / kWarps) kv4_
     }
     // the second kernel's blocks may start as these finish
     if constexpr (!kWhole) asm volatile("griddepcontrol.launch_dependents;");
-    __syncthreads();
+    sync();
     if (sm.abort) return;
 
     // join the warps' pieces: bit k of a mask is piece k & 1 of warp k / 2
@@ -790,10 +801,10 @@ __global__ void __launch_bounds__(32 * kWarps, (NT == 1 ? 16 : 8) / kWarps) kv4_
         const int hk = pc.seg / p.n_rt, r0 = (pc.seg % p.n_rt) * kRows;
         const int n_rows = min(kRows, p.Sq * p.G - r0);
         const bool whole = kWhole || (seg_x >= x && seg_x + pc.ng <= x_end);
-        float* part = whole ? nullptr : p.partial + (2 * static_cast<int64_t>(blockIdx.x) + (seg_x < x ? 0 : 1)) * (kRows * (D + 1));
+        float* part = whole ? nullptr : p.partial + (2 * static_cast<int64_t>(team) + (seg_x < x ? 0 : 1)) * (kRows * (D + 1));
         if constexpr (!kWhole && NT == 1) {
             // the rows of all segments go around the warps (one segment after the
-            // other by the whole block held the blocks with many of them up by 20
+            // other by the whole team held the teams with many of them up by 20
             // us); with 16 rows or one segment a block that is no gain
             int r = turn;
             for (; r < n_rows; r += kWarps) {
@@ -866,10 +877,10 @@ __global__ void __launch_bounds__(32 * kWarps, (NT == 1 ? 16 : 8) / kWarps) kv4_
     }
 }
 
-// Joins the parts of the segments that several blocks worked on, and writes the
+// Joins the parts of the segments that several teams worked on, and writes the
 // rows of empty sequences.  A block takes kPer rows of a segment: a warp a row
 // weighs the parts, then kSlices groups of kPer * D / 4 threads each add every
-// kSlices-th part, so that a row split over all resident blocks still waits for
+// kSlices-th part, so that a row split over all teams still waits for
 // few loads in turn (8 segments of 38 parts: 12 us less than with one thread
 // adding all of an element's parts).  One row a block where segments are few,
 // four where they are many and their parts few (16 sequences, 64 segments: 20.7
@@ -878,11 +889,11 @@ __global__ void __launch_bounds__(32 * kWarps, (NT == 1 ? 16 : 8) / kWarps) kv4_
 // lengths alone, and every block waits before it ends, so that this kernel's end
 // is the first one's, too.
 template <int D, int NT, int kPer>
-__global__ void __launch_bounds__(kJoinThreads) kv4_join_kernel(const Params p, int n_blocks) {
+__global__ void __launch_bounds__(kJoinThreads) kv4_join_kernel(const Params p, int n_teams) {
     constexpr int kRows = 8 * NT, kLanes = D / 4, kSlices = kJoinThreads / (kLanes * kPer);
     __shared__ int64_t warp_sum[2][kJoinThreads / 32];
     __shared__ float row_lse2[kPer], row_inv[kPer];
-    __shared__ float fac[kPer][kBlocks];
+    __shared__ float fac[kPer][kTeams];
     __shared__ float4 red[kSlices][kPer * kLanes];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int n_seg = p.Hkv * p.n_rt;
@@ -914,14 +925,14 @@ __global__ void __launch_bounds__(kJoinThreads) kv4_join_kernel(const Params p, 
         total += warp_sum[1][w];
     }
     const int ng = seq_groups(p, b);
-    const int64_t share = share_of(total * n_seg, n_blocks);
+    const int64_t share = share_of(total * n_seg, n_teams);
     const int64_t s0 = before * n_seg + static_cast<int64_t>(seg) * places_of(ng) + kSegmentCost;
     const int c0 = static_cast<int>(s0 / share), c1 = ng ? static_cast<int>((s0 + ng - 1) / share) : c0 - 1;
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    if (c0 == c1) return;  // one block wrote the result
+    if (c0 == c1) return;  // one team wrote the result
 
-    // the segment starts in block c0, as its second part, and is the first part
-    // of every later block
+    // the segment starts in team c0's share, as its second part, and is the first
+    // part of every later team
     const int n_parts = c1 - c0 + 1;
     auto part_of = [&](int j) {
         return p.partial + (2 * static_cast<int64_t>(c0 + j) + (j == 0 ? 1 : 0)) * (kRows * (D + 1));
@@ -993,21 +1004,21 @@ template <int D, int NT, int W>
 cudaError_t launch_whole(const Params& p, int segments, cudaStream_t st) {
     static KernelSetup setup;
     constexpr int smem = sizeof(Smem<D, NT, W>);
-    const cudaError_t e = setup(reinterpret_cast<const void*>(kv4_attn_kernel<D, NT, true, W>), smem, 0);
+    const cudaError_t e = setup(reinterpret_cast<const void*>(kv4_attn_kernel<D, NT, true, W, 1>), smem, 0);
     if (e != cudaSuccess) return e;
-    kv4_attn_kernel<D, NT, true, W><<<segments, 32 * W, smem, st>>>(p);
+    kv4_attn_kernel<D, NT, true, W, 1><<<segments, 32 * W, smem, st>>>(p);
     return cudaGetLastError();
 }
 
-// The split form in `blocks` blocks of W warps, and the join.
-template <int D, int NT, int W>
-cudaError_t launch_split(const Params& p, int segments, int blocks, cudaStream_t st) {
+// The split form in blocks of T teams, and the join.
+template <int D, int NT, int T>
+cudaError_t launch_split(const Params& p, int segments, cudaStream_t st) {
     static KernelSetup setup;
-    constexpr int smem = sizeof(Smem<D, NT, W>);
+    constexpr int n_teams = kTeams / NT, smem = T * sizeof(Smem<D, NT, kTeamWarps>);
     static_assert(smem <= 232448, "shared memory beyond the 227 KB a block may use");
-    cudaError_t e = setup(reinterpret_cast<const void*>(kv4_attn_kernel<D, NT, false, W>), smem, 0);
+    cudaError_t e = setup(reinterpret_cast<const void*>(kv4_attn_kernel<D, NT, false, kTeamWarps, T>), smem, 0);
     if (e != cudaSuccess) return e;
-    kv4_attn_kernel<D, NT, false, W><<<blocks, 32 * W, smem, st>>>(p);
+    kv4_attn_kernel<D, NT, false, kTeamWarps, T><<<n_teams / T, 32 * kTeamWarps * T, smem, st>>>(p);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     const bool many = segments >= kManySegments;
@@ -1020,8 +1031,8 @@ cudaError_t launch_split(const Params& p, int segments, int blocks, cudaStream_t
     at.val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = &at;
     cfg.numAttrs = 1;
-    e = many ? cudaLaunchKernelEx(&cfg, kv4_join_kernel<D, NT, 4>, p, blocks)
-             : cudaLaunchKernelEx(&cfg, kv4_join_kernel<D, NT, 1>, p, blocks);
+    e = many ? cudaLaunchKernelEx(&cfg, kv4_join_kernel<D, NT, 4>, p, n_teams)
+             : cudaLaunchKernelEx(&cfg, kv4_join_kernel<D, NT, 1>, p, n_teams);
     if (e != cudaSuccess) cudaGetLastError();
     return e;
 }
@@ -1029,14 +1040,13 @@ cudaError_t launch_split(const Params& p, int segments, int blocks, cudaStream_t
 template <int D, int NT>
 cudaError_t launch(const Params& p, int segments, cudaStream_t st) {
     if (!p.partial)
-        return segments > kBlocks / NT ? launch_whole<D, NT, kManyWarps>(p, segments, st)
+        return segments > kTeams / NT ? launch_whole<D, NT, kManyWarps>(p, segments, st)
                                        : launch_whole<D, NT, kFewWarps>(p, segments, st);
     if constexpr (NT == 1) {
         const int64_t most = static_cast<int64_t>(segments) * p.max_pages * (p.page_size / kKv4Group);
-        if (most >= static_cast<int64_t>(kLongPart) * kBlocks * kSplitWarps)
-            return launch_split<D, NT, kLongWarps>(p, segments, kBlocks * kSplitWarps / kLongWarps, st);
+        if (most >= static_cast<int64_t>(kLongPart) * kTeams * kTeamWarps) return launch_split<D, NT, 2>(p, segments, st);
     }
-    return launch_split<D, NT, kSplitWarps>(p, segments, kBlocks / NT, st);
+    return launch_split<D, NT, 1>(p, segments, st);
 }
 
 }  // namespace
@@ -1044,7 +1054,7 @@ cudaError_t launch(const Params& p, int segments, cudaStream_t st) {
 size_t kv4_attention_workspace_bytes(int B, int Sq, int Hq, int Hkv, int D, int page_size, int max_pages) {
     if (takes_whole(segments_of(B, Sq, Hq, Hkv), page_size, max_pages)) return 0;
     const int nt = row_tiles(Sq * (Hq / Hkv));
-    return static_cast<size_t>(kBlocks / nt) * 2 * (8 * nt) * (D + 1) * sizeof(float);
+    return static_cast<size_t>(kTeams / nt) * 2 * (8 * nt) * (D + 1) * sizeof(float);
 }
 
 cudaError_t launch_kv4_attention(const Kv4AttnLaunch& a, cudaStream_t st) {

@@ -252,7 +252,7 @@ def test_attention_with_a_wide_page_table(fsa, Hkv, D, Sq):
 
 @pytest.mark.parametrize("Hkv,D,G", [(3, 128, 5), (3, 64, 8), (3, 128, 1)])
 def test_attention_over_long_parts(fsa, Hkv, D, G):
-    # blocks of sixteen warps: long sequences, short ones between them
+    # two teams of warps a block: long sequences, short ones between them
     lens, page = [9000, 40, 0, 7000, 1, 700, 12000], 128
     cache, table, n, held = _sequences(fsa, lens, Hkv, D, page, seed=14)
     wide = torch.full((len(lens), 163840 // page), -1, dtype=torch.int32, device="cuda")

@@ -52,7 +52,7 @@ constexpr int kKStages = 2, kVStages = 2;
 constexpr int kThreads = 384;
 constexpr unsigned kSms = 152;
 constexpr int kWarpLoad = 8, kWarpMma = 9, kWarpLoadV = 10, kWarpPlan = 11;
-// launched at 168 registers per thread; helpers drop to 32, softmax takes 232
+// launched at 168 registers per thread; helpers drop to 40, softmax takes 232
 constexpr int kLaunchRegs = 168, kSoftmaxRegs = 232, kHelperRegs = 40;
 static_assert(2 * 128 * kSoftmaxRegs + 128 * kHelperRegs <= kThreads * kLaunchRegs,
               "register split exceeds the launch allocation");

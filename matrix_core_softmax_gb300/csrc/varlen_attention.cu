@@ -29,10 +29,15 @@
 //   Q0 K(0), Q1 K(0), then per key tile t
 //   P0 V(t), Q0 K(t+1), P1 V(t), Q1 K(t+1)
 // so while one tile's softmax works on its scores the other tile's two products
-// run.  A score product's commit also says that the tile's P V before it has
-// finished, so between s_full and p_full a softmax thread owns its row of O and
-// may rescale it: that happens only when the running maximum is passed by more
-// than 2^8 (weights up to 2^8 are exact enough in bf16, sums are FP32).
+// run.  P is handed over in halves of 64 keys, so that P V begins under the second
+// half's exponentials: a step is bound by this chain, from scores to weights to
+// the next scores, as much as by the products (16 prompts of up to 1000 tokens
+// 73.5 -> 70.3 us with the halves and V waited for ahead of P, 24 of up to 2000 at
+// D = 64 208 -> 197; quarters no better).  A score product's commit also says that
+// the tile's P V before it has finished, so between s_full and p_half a softmax
+// thread owns its row of O and may rescale it: that happens only when the running
+// maximum is passed by more than 2^8 (weights up to 2^8 are exact enough in bf16,
+// sums are FP32).
 //
 // Exponentials: 128 x 128 per tile and product pair are 512 clocks of the
 // SFU (32 a clock and SM, measured) against 1024 clocks of the tensor core at
@@ -80,7 +85,7 @@ struct __align__(1024) Smem {
     uint64_t q_full, q_empty;
     uint64_t k_full[kKStages], k_empty[kKStages];
     uint64_t v_full[kVStages], v_empty[kVStages], v_clean[kVStages];
-    uint64_t s_full[2], p_full[2], o_full[2];
+    uint64_t s_full[2], p_half[2], p_full[2], o_full[2];
     uint64_t drain;
     Item item[2];
     uint32_t tmem_base;
@@ -250,10 +255,11 @@ __device__ __forceinline__ bool softmax_tile(Smem& sm, const Params& p, int t, i
         tmem_reg_dep(s3);
         if (masked) {
             const int n_valid = lim - t * kTile;
-            mask32(s0, n_valid);
-            mask32(s1, n_valid - 32);
-            mask32(s2, n_valid - 64);
-            mask32(s3, n_valid - 96);
+            const int least = __reduce_min_sync(0xFFFFFFFFu, n_valid);  // of the warp's rows
+            if (least < 32) mask32(s0, n_valid);
+            if (least < 64) mask32(s1, n_valid - 32);
+            if (least < 96) mask32(s2, n_valid - 64);
+            if (least < 128) mask32(s3, n_valid - 96);
         }
         top = fmaxf(fmaxf(max32(s0), max32(s1)), fmaxf(max32(s2), max32(s3)));
     }
@@ -287,6 +293,9 @@ __device__ __forceinline__ bool softmax_tile(Smem& sm, const Params& p, int t, i
             lo[16 + j] = w1[j];
         }
         tmem_st32(s_col, lo);
+        tmem_st_wait();
+        tc_fence_before();
+        warp_arrive(&sm.p_half[i]);
         l += exp32(s2, p.c, m, w0);
         l += exp32(s3, p.c, m, w1);
 #pragma unroll
@@ -334,7 +343,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(&sm.item_full[i], 1);
             mbar_init(&sm.item_empty[i], 11);  // every warp but the plan warp
             mbar_init(&sm.s_full[i], 1);
-            mbar_init(&sm.p_full[i], 4);  // one arrival per softmax warp
+            mbar_init(&sm.p_half[i], 4);  // one arrival per softmax warp
+            mbar_init(&sm.p_full[i], 4);
             mbar_init(&sm.o_full[i], 1);
         }
         mbar_init(&sm.drain, 1);
@@ -488,10 +498,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             tc_commit_one(&sm.s_full[i]);
         };
-        auto values = [&](int i, int st, bool add) {
+        auto values = [&](int i, int st, int half, bool add) {
             const uint64_t bv = dv + (kTileBytes >> 4) * st;
 #pragma unroll
-            for (int kk = 0; kk < 8; ++kk)
+            for (int kk = 4 * half; kk < 4 * half + 4; ++kk)
                 mma_bf16_tmem_a_one(tm + kColO + 128 * i, tm + 128 * i + 8 * kk, bv + 128 * kk, id_pv,
                                     (add || kk > 0) ? 1u : 0u);
         };
@@ -516,23 +526,26 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             for (int t = 0; ok && t < n_max; ++t, ++tiles) {
                 const int sv = tiles % kVStages, sk = (tiles + 1) % kKStages;
-                bool have_v = false, have_k = false;
+                // (before the weights, so that these are waited for alone: a wait takes
+                // some 100 clocks even when there is nothing to wait for)
+                ok = wait(&sm.v_full[sv], tiles / kVStages);
+                if (ok && t == t_ragged) {
+                    ok = wait(&sm.v_clean[sv], clean_ph >> sv);
+                    clean_ph ^= 1u << sv;
+                }
+                bool have_k = false;
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
                     if (!ok || t >= n_t[i]) continue;
-                    ok = wait(&sm.p_full[i], p_ph[i]);
-                    p_ph[i] ^= 1u;
-                    if (ok && !have_v) {
-                        ok = wait(&sm.v_full[sv], tiles / kVStages);
-                        if (ok && t == t_ragged) {
-                            ok = wait(&sm.v_clean[sv], clean_ph >> sv);
-                            clean_ph ^= 1u << sv;
-                        }
-                        have_v = true;
-                    }
+                    ok = wait(&sm.p_half[i], p_ph[i]);
                     if (!ok) continue;
                     tc_fence_after();
-                    values(i, sv, t > 0);
+                    values(i, sv, 0, t > 0);
+                    ok = wait(&sm.p_full[i], p_ph[i]);
+                    p_ph[i] ^= 1u;
+                    if (!ok) continue;
+                    tc_fence_after();
+                    values(i, sv, 1, true);
                     if (t + 1 == n_t[i]) {
                         tc_commit_one(&sm.o_full[i]);
                         continue;

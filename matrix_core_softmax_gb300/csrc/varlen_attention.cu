@@ -224,6 +224,7 @@ __device__ __forceinline__ bool softmax_tile(Smem& sm, const Params& p, int t, i
     tc_fence_after();
     uint32_t s0[32], s1[32], s2[32], s3[32];
     float top;
+    bool half = false;  // no row of the warp sees the tile's second 64 keys
 #ifdef FSA_HAVE_TMEM_REDUCE
     if (!masked) {
         float r0, r1, r2, r3;
@@ -244,24 +245,28 @@ __device__ __forceinline__ bool softmax_tile(Smem& sm, const Params& p, int t, i
     } else
 #endif
     {
+        const int n_valid = masked ? lim - t * kTile : kTile;
+        half = __reduce_max_sync(0xFFFFFFFFu, n_valid) <= 64;
         tmem_ld32(s_col, s0);
         tmem_ld32(s_col + 32, s1);
-        tmem_ld32(s_col + 64, s2);
-        tmem_ld32(s_col + 96, s3);
+        if (!half) {
+            tmem_ld32(s_col + 64, s2);
+            tmem_ld32(s_col + 96, s3);
+        }
         tmem_ld_wait();
         tmem_reg_dep(s0);
         tmem_reg_dep(s1);
         tmem_reg_dep(s2);
         tmem_reg_dep(s3);
-        if (masked) {
-            const int n_valid = lim - t * kTile;
-            const int least = __reduce_min_sync(0xFFFFFFFFu, n_valid);  // of the warp's rows
-            if (least < 32) mask32(s0, n_valid);
-            if (least < 64) mask32(s1, n_valid - 32);
+        const int least = __reduce_min_sync(0xFFFFFFFFu, n_valid);  // of the warp's rows
+        if (least < 32) mask32(s0, n_valid);
+        if (least < 64) mask32(s1, n_valid - 32);
+        top = fmaxf(max32(s0), max32(s1));
+        if (!half) {
             if (least < 96) mask32(s2, n_valid - 64);
             if (least < 128) mask32(s3, n_valid - 96);
+            top = fmaxf(top, fmaxf(max32(s2), max32(s3)));
         }
-        top = fmaxf(fmaxf(max32(s0), max32(s1)), fmaxf(max32(s2), max32(s3)));
     }
     top *= p.c;
     const bool grew = top > m + kLag;
@@ -282,32 +287,36 @@ __device__ __forceinline__ bool softmax_tile(Smem& sm, const Params& p, int t, i
             }
         }
     }
-    uint32_t lo[32], hi[32];
-    {
-        uint32_t w0[16], w1[16];
-        l += exp32(s0, p.c, m, w0);
-        l += exp32(s1, p.c, m, w1);
+    // the weights of 64 keys
+    auto weights = [&](const uint32_t (&a)[32], const uint32_t (&b)[32], uint32_t col) {
+        uint32_t w0[16], w1[16], w[32];
+        l += exp32(a, p.c, m, w0);
+        l += exp32(b, p.c, m, w1);
 #pragma unroll
         for (int j = 0; j < 16; ++j) {
-            lo[j] = w0[j];
-            lo[16 + j] = w1[j];
+            w[j] = w0[j];
+            w[16 + j] = w1[j];
         }
-        tmem_st32(s_col, lo);
+        tmem_st32(col, w);
+    };
+    auto hand_over = [&](uint64_t* bar) {
         tmem_st_wait();
         tc_fence_before();
-        warp_arrive(&sm.p_half[i]);
-        l += exp32(s2, p.c, m, w0);
-        l += exp32(s3, p.c, m, w1);
-#pragma unroll
-        for (int j = 0; j < 16; ++j) {
-            hi[j] = w0[j];
-            hi[16 + j] = w1[j];
-        }
-        tmem_st32(s_col + 32, hi);
+        warp_arrive(bar);
+    };
+    if (half) {
+        // (a branch around the second half alone cost all tiles 3 % at D = 64)
+        uint32_t none[32] = {};
+        tmem_st32(s_col + 32, none);
+        weights(s0, s1, s_col);
+        hand_over(&sm.p_half[i]);
+        hand_over(&sm.p_full[i]);
+    } else {
+        weights(s0, s1, s_col);
+        hand_over(&sm.p_half[i]);
+        weights(s2, s3, s_col + 32);
+        hand_over(&sm.p_full[i]);
     }
-    tmem_st_wait();
-    tc_fence_before();
-    warp_arrive(&sm.p_full[i]);
     return __all_sync(0xFFFFFFFFu, ok);
 }
 

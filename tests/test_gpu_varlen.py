@@ -67,6 +67,19 @@ def test_matches_64_bits(fsa, case, causal):
     assert torch.equal(o, fsa.varlen_attention_fwd(q, k, v, cq, ck, causal=causal))
 
 
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("Hq,Hkv,D", [(4, 2, 128), (8, 1, 64), (1, 1, 128)])
+def test_ends_of_key_halves(fsa, Hq, Hkv, D, causal):
+    # keys that end at, before and behind each 64th, under one and many query tokens
+    nk = [n + d for n in (64, 128, 192, 256, 320) for d in (-1, 0, 1)] + [32, 33, 96, 97, 160]
+    nq = [(1, 64, 5, n)[i % 4] if n >= 64 else n for i, n in enumerate(nk)]
+    q, k, v = _bf16((sum(nq), Hq, D), 21, 2.0), _bf16((sum(nk), Hkv, D), 22), _bf16((sum(nk), Hkv, D), 23)
+    cq, ck = _cu(nq), _cu(nk)
+    o, lse = fsa.varlen_attention_fwd(q, k, v, cq, ck, causal=causal, return_lse=True)
+    assert fsa.get_device_error() == 0
+    _check(o, lse, q, k, v, cq, ck, causal, ref.default_scale(D))
+
+
 @pytest.mark.parametrize("seed", range(8))
 def test_random_shapes(fsa, seed):
     rng = np.random.default_rng(2000 + seed)

@@ -418,7 +418,8 @@ FSA_API fsa_status fsa_kv4_read(const void *cache, int64_t num_pages, int page_s
  * no key gets o = 0 and lse = -infinity.
  *  - Products in f16 with FP32 accumulation: q is scaled by a power of two per
  *    row, softmax weights are rounded to f16 (relative to the largest product
- *    of weight and value scale); sums are FP32.
+ *    of weight and value scale, a scale counting as 2^-90 of the row's largest at
+ *    least); sums are FP32.
  *  - o and lse must not overlap q or the cache.
  *  - workspace: device buffer of fsa_kv4_attention_workspace_size() bytes,
  *    256-byte aligned, contents arbitrary; NULL when that size is 0.  Calls

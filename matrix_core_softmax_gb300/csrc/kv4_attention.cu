@@ -25,7 +25,7 @@
 //    weight fragment per 32-channel block.
 //
 // Weights.  With X the scale exponent of a key's value block b, R_b the largest
-// one so far and y = min_b (R_b - X_b) (at most 96) the kernel takes
+// one so far and y = min_b (R_b - X_b) (at most 90) the kernel takes
 //   p = 2^(s - y - M)  rounded to f16, M the running maximum of s - y,
 //   w_b = p 2^(y - (R_b - X_b) + 11),
 //   O_b += sum w_b code,  l += p 2^y (before the rounding),
@@ -35,10 +35,13 @@
 // lazily (M may lag by 2^4, which the 2^11 leaves room for), so O is rescaled
 // only when one of them really grows.  Where the R_b grow, s - y of every key
 // before falls by the least of the steps and M with it (else the keys after a
-// large value of little weight would have p far below 1), down to 2^-96 of its
-// peak at most, which keeps l in range.  O, l and the scores are FP32.  q is
-// scaled by a power of two to [1, 2) per row, in which f16 holds a bf16 value
-// exactly down to 2^-14 of the row's largest and to 2^-25 of it below.
+// large value of little weight would have p far below 1), but only as far as
+// keeps l below 2^100: a key without value that leads the others by 2^g has
+// added 2^min(g, 90) to it.  A later key adds less than 2^(4 + 90), so a lane's
+// share of 2^30 keys stays below 2^122 and a row's sum below 2^125.  O, l and
+// the scores are FP32.  q is scaled by a power of two to [1, 2) per row, in
+// which f16 holds a bf16 value exactly down to 2^-14 of the row's largest and to
+// 2^-25 of it below.
 // Pieces of a row are kept as their own output and its log-sum-exp, not as
 // unnormalised sums, whose scale 2^(M + R_b) may lie outside of FP32.
 //
@@ -104,8 +107,10 @@ constexpr int kSegmentCost = 3;
 constexpr uint32_t kNoGroup = 0xFFFFFFFFu, kNoPlace = 0xFFFFFFFEu;
 constexpr float kNoMax = -1e30f;
 constexpr float kLag = 4.0f;      // how far M may lag behind (log2)
-constexpr unsigned kMostY = 96;   // largest y
+constexpr unsigned kMostY = 90;   // largest y
+constexpr int kMostL = 100;       // l is not rescaled to 2^100 or more
 constexpr int kHeadroom = 11;     // weights carry 2^11: 2^11 * 2^4 = 2^15 < 65504
+constexpr float kUnit = 1.0f / (1 << kHeadroom);
 
 struct Params {
     const uint16_t* q;
@@ -138,7 +143,6 @@ struct __align__(128) Smem {
     uint32_t vscale[kWarps][4][2][2][4];   // f16 pairs: [t][16-key step][half][block]
     uint64_t full[kWarps][kStages];
     float lse2[kWarps][2][8 * NT];  // log2-sum-exp2 of the pieces' rows
-    float peak[kWarps][8 * NT];     // largest M so far
     Piece piece[kWarps][2];  // [0] in first, [1] in ring
     int64_t scan[kWarps];
     int64_t first_x;
@@ -485,7 +489,7 @@ __global__ void __launch_bounds__(32 * kWarps * kBlockTeams, (NT == 1 ? 16 : 8) 
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
-            for (int j = 0; j < 2; ++j) M[n][j] = sm.peak[warp][8 * n + 2 * t + j] = kNoMax;
+            for (int j = 0; j < 2; ++j) M[n][j] = kNoMax;
         uint32_t R02 = 0, R13 = 0;  // largest value scale bytes so far
 
         for (; i < i_end; ++i) {
@@ -539,9 +543,18 @@ __global__ void __launch_bounds__(32 * kWarps * kBlockTeams, (NT == 1 ? 16 : 8) 
                         for (int n = 0; n < NT; ++n)
 #pragma unroll
                             for (int j = 0; j < 2; ++j) {
-                                const float to = fmaxf(M[n][j] - least, sm.peak[warp][8 * n + 2 * t + j] - static_cast<float>(kMostY));
-                                const float drop = fmaxf(M[n][j] - to, 0.0f);
-                                M[n][j] -= drop;
+                                // l < 2^(exp - 126) in every lane of the column.  (Rolled and unrolled: 64 x
+                                // 32768 keys 197.6 / 199.0 us, but one of 300 6.7 / 6.5)
+                                int exp = __float_as_int(l[n][j]) >> 23;
+#pragma unroll (kWhole ? 3 : 1)
+                                for (int o = 4; o < 32; o <<= 1) exp = max(exp, __shfl_xor_sync(0xFFFFFFFFu, exp, o));
+                                const int room = min(least, max(kMostL + 126 - exp, 0));
+                                float to = M[n][j] - static_cast<float>(room), drop = M[n][j] - to;
+                                if (drop > static_cast<float>(room + 1)) {  // an M of 2^25 or more takes no small steps
+                                    to = M[n][j];
+                                    drop = 0.0f;
+                                }
+                                M[n][j] = to;
                                 l[n][j] *= ex2(drop);
 #pragma unroll
                                 for (int c = 0; c < kB; ++c) {
@@ -652,8 +665,6 @@ __global__ void __launch_bounds__(32 * kWarps * kBlockTeams, (NT == 1 ? 16 : 8) 
                             for (int o = 4; o < 32; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
                             m = fmaxf(m, M[n][j]);
                             const float f = ex2(M[n][j] - m);
-                            float& peak = sm.peak[warp][8 * n + 2 * t + j];  // (the lanes of a column write the same)
-                            peak = fmaxf(peak, m);
                             M[n][j] = m;
                             l[n][j] *= f;
 #pragma unroll
@@ -737,10 +748,10 @@ __global__ void __launch_bounds__(32 * kWarps * kBlockTeams, (NT == 1 ? 16 : 8) 
                 float lt = l[n][j];
                 for (int o = 4; o < 32; o <<= 1) lt += __shfl_xor_sync(0xFFFFFFFFu, lt, o);
                 L2[n][j] = lt == 0.0f ? kNoMax : M[n][j] + __log2f(lt);
-                const float inv = lt == 0.0f ? 0.0f : 1.0f / (lt * static_cast<float>(1 << kHeadroom));
+                const float inv = lt == 0.0f ? 0.0f : 1.0f / lt;
 #pragma unroll
                 for (int c = 0; c < kB; ++c) {
-                    const float f = pow2f(static_cast<int>(((c & 1 ? R13 : R02) >> (16 * (c >> 1))) & 0xFFu) - 127);
+                    const float f = kUnit * pow2f(static_cast<int>(((c & 1 ? R13 : R02) >> (16 * (c >> 1))) & 0xFFu) - 127);  // exact
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
                         O[n][c][h][j] = O[n][c][h][j] * inv * f;

@@ -1,0 +1,64 @@
+"""The serving operators on finite inputs of extreme range, against 64 bits."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import fsa_inputs
+import serving_ref as ref
+from gpu_util import to_dev
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def fsa():
+    import __graft_entry__
+    __graft_entry__.build()
+    import matrix_core_softmax_gb300 as m
+    return m
+
+
+def _bits(x):
+    return fsa_inputs.to_bf16_bits(np.asarray(x, np.float32))
+
+
+def _cached(fsa, k, v, page=64):
+    """One sequence's rows [n, Hkv, D] (float64) in a cache, pages in reverse order:
+    cache, page table, length and the held rows."""
+    n, H, D = k.shape
+    pages = -(-n // page)
+    cache = fsa.kv4_new_cache(pages, page, H, D)
+    table = torch.arange(pages - 1, -1, -1, dtype=torch.int32, device="cuda")[None].contiguous()
+    j = torch.arange(n, device="cuda")
+    kb, vb = _bits(k), _bits(v)
+    fsa.kv4_append(cache, to_dev(kb), to_dev(vb), table[0, j // page].long() * page + j % page)
+    held = tuple(torch.from_numpy(ref.held_rows(x)) for x in (kb, vb))
+    return cache, table, torch.tensor([n], dtype=torch.int32, device="cuda"), held
+
+
+# A key without a value whose score leads by `lead` (log2), then values 2^growth
+# larger.  1024 keys: a block takes the segment, four groups a warp; 160000: two
+# groups a warp of the split form.
+@pytest.mark.parametrize("n", [1024, 160000])
+@pytest.mark.parametrize("lead,growth", [(64, 70), (100, 40), (90, 36), (100, 10), (40, 100), (87, 42), (110, 96)])
+def test_a_leading_key_without_value_before_larger_values(fsa, n, lead, growth):
+    D, page, G = 64, 64, 4
+    rng = np.random.default_rng(n + lead)
+    u = rng.choice([-1.0, 1.0], D)
+    k = np.zeros((n, 1, D))
+    v = np.rint(rng.uniform(1, 7, (n, 1, D))) / 4
+    group = np.arange(n) // 32
+    leaders = (np.arange(n) % 32 == 7) & (group % 2 == 0)
+    k[leaders, 0] = 1.5 * u
+    v[leaders] = 0
+    v[group % 2 == 1] *= 2.0 ** growth
+    cache, table, lens, (hk, hv) = _cached(fsa, k, v, page)
+    q = np.array([1.0, 0.75, 0.5, -1.0])[None, None, :, None] * u
+    sm = float(np.float32(lead * math.log(2) / (1.5 * D)))
+    qb = to_dev(_bits(q))
+    o, lse = fsa.kv4_attention_fwd(qb, cache, table, lens, sm_scale=sm, return_lse=True)
+    assert fsa.get_device_error() == 0
+    r = ref.attend(qb[0].double().cpu(), hk, hv, torch.tensor([n - 1]), sm)
+    ref.check(o[0].cpu(), lse[0].cpu(), r, ref.F16)

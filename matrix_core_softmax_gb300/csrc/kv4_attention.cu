@@ -105,7 +105,7 @@ constexpr int kFewWarps = 8, kManyWarps = 4;
 // sequences of up to 8000 keys).
 constexpr int kSegmentCost = 3;
 constexpr uint32_t kNoGroup = 0xFFFFFFFFu, kNoPlace = 0xFFFFFFFEu;
-constexpr float kNoMax = -1e30f;
+constexpr float kNoMax = -3.402823466e38f;  // of a row without keys: the least finite value, below every score
 constexpr float kLag = 4.0f;      // how far M may lag behind (log2)
 constexpr unsigned kMostY = 90;   // largest y
 constexpr int kMostL = 100;       // l is not rescaled to 2^100 or more
@@ -245,7 +245,7 @@ __device__ __forceinline__ void write_row(const Params& p, int b, int hk, int r,
     const __nv_bfloat162 lo = __floats2bfloat162_rn(a.x, a.y), hi = __floats2bfloat162_rn(a.z, a.w);
     *reinterpret_cast<uint2*>(p.o + row * D + 4 * d4) =
         make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
-    if (p.lse && d4 == 0) p.lse[row] = lse2 < 0.5f * kNoMax ? -INFINITY : lse2 * 0.6931471805599453f;
+    if (p.lse && d4 == 0) p.lse[row] = lse2 == kNoMax ? -INFINITY : lse2 * 0.6931471805599453f;
 }
 
 // kWhole: a block takes one segment, without a walk over sequences, segments

@@ -62,3 +62,26 @@ def test_a_leading_key_without_value_before_larger_values(fsa, n, lead, growth):
     assert fsa.get_device_error() == 0
     r = ref.attend(qb[0].double().cpu(), hk, hv, torch.tensor([n - 1]), sm)
     ref.check(o[0].cpu(), lse[0].cpu(), r, ref.F16)
+
+
+# One channel carries the scores, so that they are exact: of all keys one wins.
+# What a row then gets is that key's value, whatever the scores' size.
+@pytest.mark.parametrize("size", [2.0 ** 40, 2.0 ** 64, 2.0 ** 115], ids=["2^40", "2^64", "2^115"])
+@pytest.mark.parametrize("sign", [1, -1])
+@pytest.mark.parametrize("n", [1, 300, 5000])
+def test_cache_scores_far_from_zero(fsa, n, sign, size):
+    D, G = 128, 4
+    rng = np.random.default_rng(n)
+    k, q = np.zeros((n, 1, D)), np.zeros((1, 1, G, D))
+    k[:, 0, 5] = np.where(sign > 0, 1.0, 4.0) * math.sqrt(size)
+    win = n // 3
+    k[win, 0, 5] = np.where(sign > 0, 4.0, 1.0) * math.sqrt(size)
+    q[..., 5] = sign * math.sqrt(size)
+    v = np.rint(rng.uniform(-4, 4, (n, 1, D)))
+    cache, table, lens, (hk, hv) = _cached(fsa, k, v)
+    o, lse = fsa.kv4_attention_fwd(to_dev(_bits(q)), cache, table, lens, sm_scale=0.5, return_lse=True)
+    assert fsa.get_device_error() == 0
+    want = hv[win, 0]
+    assert torch.equal(o.double().cpu()[0, 0], want.expand(G, D))
+    s = 0.5 * float(hk[win, 0, 5]) * sign * float(torch.tensor(math.sqrt(size)).bfloat16())
+    assert (lse.double().cpu() - s).abs().max() <= 2.0 ** -21 * abs(s)

@@ -111,6 +111,13 @@ constexpr unsigned kMostY = 90;   // largest y
 constexpr int kMostL = 100;       // l is not rescaled to 2^100 or more
 constexpr int kHeadroom = 11;     // weights carry 2^11: 2^11 * 2^4 = 2^15 < 65504
 constexpr float kUnit = 1.0f / (1 << kHeadroom);
+// A key's products of codes and the scaled q, below 2^11 in sum, take the key
+// scales over 2^kKeyShift and the scores the rest: scales go up to 2^126, and
+// nothing on the way to a score of normal size leaves FP32's range.  (kKeyUnit
+// takes the scale byte's one away, too.)
+constexpr int kKeyShift = 9;
+constexpr int kMostE = 240;       // largest exponent that q is scaled by: below 2^15 in f16
+constexpr float kKeyUnit = 0.5f / (1 << kKeyShift);
 
 struct Params {
     const uint16_t* q;
@@ -445,7 +452,7 @@ __global__ void __launch_bounds__(32 * kWarps * kBlockTeams, (NT == 1 ? 16 : 8) 
 
         // the query rows as B fragments, in f16 relative to each row's largest
         uint32_t qf[NT][kB][4];
-        float cs[NT][2];      // sm log2(e) 2^e of the rows of this lane's columns
+        float cs[NT][2];      // sm log2(e) 2^(e + kKeyShift) of the rows of this lane's columns
         int seen[NT][2];      // keys that they see
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
@@ -466,7 +473,7 @@ __global__ void __launch_bounds__(32 * kWarps * kBlockTeams, (NT == 1 ? 16 : 8) 
             }
             mx = max(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 1));
             mx = max(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 2));
-            const int E = min(max(static_cast<int>(mx >> 7), 1), 253);
+            const int E = min(max(static_cast<int>(mx >> 7), 1), kMostE);
             const float f = __int_as_float((254 - E) << 23);
 #pragma unroll
             for (int c = 0; c < kB; ++c) {
@@ -477,7 +484,7 @@ __global__ void __launch_bounds__(32 * kWarps * kBlockTeams, (NT == 1 ? 16 : 8) 
             }
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
-                cs[n][j] = p.c * __int_as_float(__shfl_sync(0xFFFFFFFFu, E, 8 * t + 4 * j) << 23);
+                cs[n][j] = p.c * __int_as_float((__shfl_sync(0xFFFFFFFFu, E, 8 * t + 4 * j) + kKeyShift) << 23);
                 const int rr = r0 + 8 * n + 2 * t + j;
                 seen[n][j] = rr < p.Sq * p.G ? len - p.Sq + 1 + rr / p.G : 0;
             }
@@ -500,8 +507,9 @@ __global__ void __launch_bounds__(32 * kWarps * kBlockTeams, (NT == 1 ? 16 : 8) 
                 const uint8_t* buf = sm.ring[warp][st];
                 const int key0 = static_cast<int>(pos_begin + i - seg_x) * kKv4Group;
 
-                // scales: lane = key.  A zero scale byte (2^-127, a zero block as a
-                // rule) counts as zero.  Value scale bytes as 16-bit pairs, blocks 0
+                // scales: lane = key.  2^(X - kKeyShift) of the key blocks, from the bytes
+                // plus one, so that byte 0 (2^-127) has an exponent, too (the largest that
+                // the cache is given is 253).  Value scale bytes as 16-bit pairs, blocks 0
                 // and 2, 1 and 3.
                 {
                     const int pos = swap_pos(lane);
@@ -515,10 +523,11 @@ __global__ void __launch_bounds__(32 * kWarps * kBlockTeams, (NT == 1 ? 16 : 8) 
                     }
                     if (key0 + lane >= len) vs = 0;
                     float kf[4];
-                    kf[0] = __uint_as_float((ks & 0xFFu) << 23);
-                    kf[1] = __uint_as_float((ks << 15) & 0x7F800000u);
-                    kf[2] = __uint_as_float((ks << 7) & 0x7F800000u);
-                    kf[3] = __uint_as_float((ks >> 1) & 0x7F800000u);
+                    ks += D == 128 ? 0x01010101u : 0x0101u;
+                    kf[0] = __uint_as_float((ks & 0xFFu) << 23) * kKeyUnit;
+                    kf[1] = __uint_as_float((ks << 15) & 0x7F800000u) * kKeyUnit;
+                    kf[2] = __uint_as_float((ks << 7) & 0x7F800000u) * kKeyUnit;
+                    kf[3] = __uint_as_float((ks >> 1) & 0x7F800000u) * kKeyUnit;
                     if (D == 128)
                         sm.kscale[warp][pos] = make_float4(kf[0], kf[1], kf[2], kf[3]);
                     else

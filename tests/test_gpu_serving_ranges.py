@@ -85,3 +85,33 @@ def test_cache_scores_far_from_zero(fsa, n, sign, size):
     assert torch.equal(o.double().cpu()[0, 0], want.expand(G, D))
     s = 0.5 * float(hk[win, 0, 5]) * sign * float(torch.tensor(math.sqrt(size)).bfloat16())
     assert (lse.double().cpu() - s).abs().max() <= 2.0 ** -21 * abs(s)
+
+
+# Keys and queries at opposite ends of bf16's exponents, scores of normal size
+@pytest.mark.parametrize("e", [126, 118, 100, -100, -119, -124, -127, -130])
+@pytest.mark.parametrize("n,D", [(200, 64), (3000, 128)])
+def test_cache_keys_at_the_ends_of_the_exponents(fsa, n, D, e):
+    rng = np.random.default_rng(n)
+    k = np.clip(rng.standard_normal((n, 2, D)), -1.9, 1.9) * 2.0 ** e
+    v = rng.standard_normal((n, 2, D))
+    q = np.clip(rng.standard_normal((1, 1, 10, D)), -1.9, 1.9) * 2.0 ** min(-e, 126)
+    cache, table, lens, (hk, hv) = _cached(fsa, k, v)
+    qb = to_dev(_bits(q))
+    sm = 0.3 * 2.0 ** (-e - min(-e, 126))
+    o, lse = fsa.kv4_attention_fwd(qb, cache, table, lens, sm_scale=sm, return_lse=True)
+    assert fsa.get_device_error() == 0
+    r = ref.attend(qb[0].double().cpu(), hk, hv, torch.tensor([n - 1]), float(np.float32(sm)))
+    ref.check(o[0].cpu(), lse[0].cpu(), r, ref.F16)
+
+
+@pytest.mark.parametrize("e", [125, -110, -126, -130])
+def test_cache_values_at_the_ends_of_the_exponents(fsa, e):
+    n, D = 700, 128
+    rng = np.random.default_rng(5)
+    k, v = rng.standard_normal((n, 2, D)), np.clip(rng.standard_normal((n, 2, D)), -1.9, 1.9) * 2.0 ** e
+    cache, table, lens, (hk, hv) = _cached(fsa, k, v)
+    qb = to_dev(_bits(rng.standard_normal((1, 1, 6, D))))
+    o, lse = fsa.kv4_attention_fwd(qb, cache, table, lens, return_lse=True)
+    assert fsa.get_device_error() == 0
+    r = ref.attend(qb[0].double().cpu(), hk, hv, torch.tensor([n - 1]), ref.default_scale(D))
+    ref.check(o[0].cpu(), lse[0].cpu(), r, ref.F16)

@@ -321,6 +321,13 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32
         FSA_W8(0), FSA_W8(8), FSA_W8(16), FSA_W8(24)
         : "memory");
 }
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+        "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+        FSA_W8(0), FSA_W8(8)
+        : "memory");
+}
 // 32 columns from four groups of eight registers (columns 8g .. 8g + 7).
 __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&a)[8], const uint32_t (&b)[8],
                                           const uint32_t (&c)[8], const uint32_t (&d)[8]) {

@@ -65,8 +65,13 @@ constexpr int kAtom = 128 * 128;       // 128 rows x 128 bytes (64 bf16)
 constexpr int kTileBytes = 2 * kAtom;  // 128 rows x 128 bf16
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kColO = 256;        // S0 at 0, S1 at 128, O0 at 256, O1 at 384
-constexpr float kNoMax = -1e30f;
+constexpr float kNoMax = -3.402823466e38f;  // before a row's first key: the least finite value
 constexpr float kLag = 8.0f;           // how far the reference may lag behind the maximum (log2)
+// A weight is 2^(s c - m) in one rounding, m the rounded reference: all weights of
+// the row are off by the same 2^d, |d| <= 2^-25 |m|, which cancels in the output
+// while it stays in range.  From scores of this size on (d = 8) both are rounded
+// before they are subtracted.
+constexpr float kFar = 268435456.0f;
 
 // A pair of query tiles of one key head: sequence bounds, first token of the pair
 // in its sequence, key head (-1: no more work).
@@ -213,6 +218,50 @@ __device__ __forceinline__ int key_tiles(const Params& p, const Item& it, int i)
     return (see + kTile - 1) / kTile;
 }
 
+// O of this thread's row times f.
+template <int D>
+__device__ __forceinline__ void rescale_output(uint32_t o_col, float f) {
+    uint32_t rr[32];
+    for (int c = 0; c < D / 32; ++c) {
+        tmem_ld32(o_col + 32 * c, rr);
+        tmem_ld_wait();
+        tmem_reg_dep(rr);
+#pragma unroll
+        for (int j = 0; j < 32; ++j) rr[j] = __float_as_uint(__uint_as_float(rr[j]) * f);
+        tmem_st32(o_col + 32 * c, rr);
+    }
+}
+
+// The rest of softmax_tile, reading the scores once more, where some row's are
+// beyond kFar (`far`: this row's); the other rows' arithmetic is the same as there.
+template <int D>
+__device__ __forceinline__ void far_tile(Smem& sm, const Params& p, int t, int i, uint32_t s_col, uint32_t o_col, int n_valid,
+                                         float top, bool far, float& m, float& l) {
+    const float mn = top > m + kLag ? top : m, f = ex2(m - mn);
+    l *= f;
+    m = mn;
+    if (t > 0) rescale_output<D>(o_col, f);
+#pragma unroll 1
+    for (int c = 0; c < 4; ++c) {
+        uint32_t s[32], w[16];
+        tmem_ld32(s_col + 32 * c, s);
+        tmem_ld_wait();
+        tmem_reg_dep(s);
+        mask32(s, n_valid - 32 * c);
+        if (far) {
+#pragma unroll
+            for (int j = 0; j < 32; ++j) s[j] = __float_as_uint(__fsub_rn(__fmul_rn(__uint_as_float(s[j]), p.c), m));
+        }
+        l += exp32(s, far ? 1.0f : p.c, far ? 0.0f : m, w);
+        tmem_st16(s_col + 16 * c, w);  // (ends below the next 32 scores)
+        if (c & 1) {
+            tmem_st_wait();
+            tc_fence_before();
+            warp_arrive(c == 1 ? &sm.p_half[i] : &sm.p_full[i]);
+        }
+    }
+}
+
 // One key tile t for this thread's row: scores out of TMEM, the maximum, the
 // rare rescale of O, P back into TMEM.  `lim`: keys the row sees in all; `ph`:
 // phase of s_full;
@@ -269,23 +318,17 @@ __device__ __forceinline__ bool softmax_tile(Smem& sm, const Params& p, int t, i
         }
     }
     top *= p.c;
-    const bool grew = top > m + kLag;
-    if (__any_sync(0xFFFFFFFFu, grew)) {
+    const bool grew = top > m + kLag, far = fabsf(top) >= kFar && top >= kNoMax;
+    if (__any_sync(0xFFFFFFFFu, grew || far)) {
+        if (__builtin_expect(__any_sync(0xFFFFFFFFu, far), 0)) {
+            far_tile<D>(sm, p, t, i, s_col, o_col, masked ? lim - t * kTile : kTile, top, far, m, l);
+            return __all_sync(0xFFFFFFFFu, ok);
+        }
         const float mn = grew ? top : m;
         const float f = ex2(m - mn);
         l *= f;
         m = mn;
-        if (t > 0) {  // O holds the tiles before t
-            uint32_t rr[32];
-            for (int c = 0; c < D / 32; ++c) {
-                tmem_ld32(o_col + 32 * c, rr);
-                tmem_ld_wait();
-                tmem_reg_dep(rr);
-#pragma unroll
-                for (int j = 0; j < 32; ++j) rr[j] = __float_as_uint(__uint_as_float(rr[j]) * f);
-                tmem_st32(o_col + 32 * c, rr);
-            }
-        }
+        if (t > 0) rescale_output<D>(o_col, f);  // O holds the tiles before t
     }
     // the weights of 64 keys
     auto weights = [&](const uint32_t (&a)[32], const uint32_t (&b)[32], uint32_t col) {
@@ -359,6 +402,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_init(&sm.drain, 1);
         fence_mbar_init();
     }
+    // rows behind a query tile's last whole token are loaded by no copy: zeros, so
+    // that their scores are none that would have to be followed
+#pragma unroll 1
+    for (int e = tid + p.G * p.n_tok * 8; e < kTile * 8; e += kThreads)
+#pragma unroll 1
+        for (int a = 0; a < 2 * n_atoms; ++a)
+            reinterpret_cast<uint4*>(sm.q[a / n_atoms] + a % n_atoms * kAtom)[e] = make_uint4(0, 0, 0, 0);
+    if (p.G * p.n_tok < kTile) fence_async_smem();
     if (warp == kWarpMma) {
         tmem_alloc(&sm.tmem_base, kTmemCols);
         tmem_relinquish();

@@ -87,6 +87,42 @@ def test_cache_scores_far_from_zero(fsa, n, sign, size):
     assert (lse.double().cpu() - s).abs().max() <= 2.0 ** -21 * abs(s)
 
 
+@pytest.mark.parametrize("size", [2.0 ** 24, 2.0 ** 40, 2.0 ** 64, 2.0 ** 116], ids=["2^24", "2^40", "2^64", "2^116"])
+@pytest.mark.parametrize("sign", [1, -1])
+@pytest.mark.parametrize("n,causal", [(1, True), (300, True), (300, False), (1500, True)])
+def test_packed_scores_far_from_zero(fsa, n, causal, sign, size):
+    D, Hq, Hkv = 64, 6, 2
+    g = torch.Generator().manual_seed(n)
+    k, q = torch.zeros(n, Hkv, D), torch.zeros(n, Hq, D)
+    root = math.sqrt(size)
+    # scores in steps (the sizes are even powers, so k = root * step / 128 is a bf16 value
+    # and equal scores are those of equal steps): the largest is another from row to row
+    step = torch.randperm(n, generator=g) % 120 + 128
+    k[:, :, 9] = root * step[:, None] / 128
+    q[:, :, 9] = sign * root * 1.25
+    v = torch.randn(n, Hkv, D, generator=g)
+    q, k, v = (x.bfloat16().cuda() for x in (q, k, v))
+    cu = torch.tensor([0, n], dtype=torch.int32, device="cuda")
+    o, lse = fsa.varlen_attention_fwd(q, k, v, cu, causal=causal, sm_scale=0.35, return_lse=True)
+    assert fsa.get_device_error() == 0
+    # the keys of the largest score share the weight; the others' lies below 2^-1000
+    # of it or so at these sizes (2^24: steps of 2^17 * 1.25 * 0.35)
+    s = sign * step.double()
+    seen = torch.ones(n, n).tril() if causal else torch.ones(n, n)
+    s = torch.where(seen > 0, s, -math.inf)
+    w = (s == s.max(1, keepdim=True).values).double()
+    w /= w.sum(1, keepdim=True)
+    vv = v.double().cpu()
+    want = torch.stack([w @ vv[:, h // (Hq // Hkv)] for h in range(Hq)], 1)
+    big = torch.stack([w @ vv[:, h // (Hq // Hkv)].abs() for h in range(Hq)], 1)
+    # equal weights, one rounding of them to bf16 and one of the result
+    assert ((o.double().cpu() - want).abs() <= 2.0 ** -7 * big).all()
+    top = s.max(1).values / 128 * float(torch.tensor(root).bfloat16()) * float(q[0, 0, 9].abs()) * 0.35
+    assert torch.isfinite(lse).all()
+    err = (lse.double().cpu() - top[:, None]).abs()
+    assert (err <= 2.0 ** -21 * top.abs()[:, None] + math.log(n) + 2.0 ** -10).all()
+
+
 # Keys and queries at opposite ends of bf16's exponents, scores of normal size
 @pytest.mark.parametrize("e", [126, 118, 100, -100, -119, -124, -127, -130])
 @pytest.mark.parametrize("n,D", [(200, 64), (3000, 128)])

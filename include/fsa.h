@@ -79,7 +79,9 @@ typedef enum {
 #define FSA_DEBUG_SKIP_KV_ARRIVE 0x1 /* the loader never signals KV tile 1:
                                         the consumers' bounded waits run out,
                                         the kernel exits cleanly and the error
-                                        word reads FSA_ERR_TIMEOUT */
+                                        word reads FSA_ERR_TIMEOUT (attention
+                                        over the four-bit cache: no warp sees
+                                        its second group of keys) */
 
 typedef struct {
     /* Score scale; <= 0 selects 1/sqrt(D). */
@@ -440,6 +442,14 @@ FSA_API fsa_status fsa_kv4_attention_fwd(const void *q, int64_t q_stride, const 
                                          float sm_scale, void *workspace, uint64_t workspace_bytes,
                                          void *stream);
 
+/* As fsa_kv4_attention_fwd; of *opt (NULL: all zero) sm_scale, workspace,
+ * workspace_bytes, wait_timeout_ms and debug_flags are used. */
+FSA_API fsa_status fsa_kv4_attention_fwd_ex(const void *q, int64_t q_stride, const void *cache,
+                                            const int32_t *page_table, const int32_t *seq_lens,
+                                            void *o, float *lse, int B, int Sq, int Hq, int Hkv,
+                                            int D, int64_t num_pages, int page_size, int max_pages,
+                                            const fsa_options *opt, void *stream);
+
 /* Bytes of device workspace that fsa_kv4_attention_fwd needs (0: none, and for
  * invalid arguments). */
 FSA_API uint64_t fsa_kv4_attention_workspace_size(int B, int Sq, int Hq, int Hkv, int D,
@@ -474,6 +484,15 @@ FSA_API fsa_status fsa_varlen_attention_fwd(const void *q, const void *k, const 
                                             const int32_t *cu_q, const int32_t *cu_k, void *o,
                                             float *lse, int B, int Tq, int Tk, int Hq, int Hkv,
                                             int D, int causal, float sm_scale, void *stream);
+
+/* As fsa_varlen_attention_fwd; of *opt (NULL: all zero) sm_scale,
+ * wait_timeout_ms and debug_flags are used. */
+FSA_API fsa_status fsa_varlen_attention_fwd_ex(const void *q, const void *k, const void *v,
+                                               int64_t q_stride, int64_t k_stride,
+                                               int64_t v_stride, const int32_t *cu_q,
+                                               const int32_t *cu_k, void *o, float *lse, int B,
+                                               int Tq, int Tk, int Hq, int Hkv, int D, int causal,
+                                               const fsa_options *opt, void *stream);
 
 /* Synchronises `stream`, then reads and clears the device error words of the
  * current device (the allocating entry points' word and, once that entry

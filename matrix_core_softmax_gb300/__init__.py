@@ -33,7 +33,8 @@ EXPORTS = ("fsa_quantize_mx", "fsa_attention_fwd", "fsa_attention_fwd_ex",
            "fsa_cross_attention_prepare", "fsa_cross_attention_run",
            "fsa_attention_fwd_host", "fsa_cross_attention_fwd_host", "fsa_mma_rate_probe",
            "fsa_kv4_page_bytes", "fsa_kv4_append", "fsa_kv4_read", "fsa_kv4_attention_fwd",
-           "fsa_kv4_attention_workspace_size", "fsa_varlen_attention_fwd")
+           "fsa_kv4_attention_workspace_size", "fsa_varlen_attention_fwd", "fsa_kv4_attention_fwd_ex",
+           "fsa_varlen_attention_fwd_ex")
 
 
 class FsaError(RuntimeError):
@@ -126,6 +127,12 @@ def load(path: str | None = None):
             lib.fsa_kv4_attention_fwd.restype = I
             lib.fsa_varlen_attention_fwd.argtypes = [V, V, V, I64, I64, I64, V, V, V, V, I, I, I, I, I, I, I, F, V]
             lib.fsa_varlen_attention_fwd.restype = I
+            lib.fsa_kv4_attention_fwd_ex.argtypes = [V, I64, V, V, V, V, V, I, I, I, I, I, I64, I, I,
+                                                     ctypes.POINTER(Options), V]
+            lib.fsa_kv4_attention_fwd_ex.restype = I
+            lib.fsa_varlen_attention_fwd_ex.argtypes = [V, V, V, I64, I64, I64, V, V, V, V, I, I, I, I, I, I, I,
+                                                        ctypes.POINTER(Options), V]
+            lib.fsa_varlen_attention_fwd_ex.restype = I
             lib.fsa_get_device_error.argtypes = [V]
             lib.fsa_get_device_error.restype = I
             lib.fsa_status_string.argtypes = [I]
@@ -517,7 +524,7 @@ def kv4_attention_workspace_size(B: int, Sq: int, n_heads: int, n_kv_heads: int,
 
 
 def kv4_attention_fwd(q, cache, page_table, seq_lens, *, out=None, return_lse: bool = False, lse=None,
-                      sm_scale: float = 0.0, workspace=None, stream=None):
+                      sm_scale: float = 0.0, workspace=None, wait_timeout_ms: int = 0, debug_flags: int = 0, stream=None):
     """fsa_kv4_attention_fwd: attention of q, CUDA bf16 [B, Sq, n_heads, D] (the
     last Sq tokens of each sequence, already in the cache; heads contiguous, all
     tokens at one distance), over the four-bit cache.  page_table int32 [B,
@@ -525,13 +532,15 @@ def kv4_attention_fwd(q, cache, page_table, seq_lens, *, out=None, return_lse: b
     included).  Returns o [B, Sq, n_heads, D], with return_lse also the
     log-sum-exps, float32 [B, Sq, n_heads] (written into `lse` if given).
     workspace: uint8 tensor of kv4_attention_workspace_size bytes for callers
-    that keep one; calls that may overlap need their own."""
+    that keep one; calls that may overlap need their own.  wait_timeout_ms: limit
+    of the kernels' bounded waits (0: 2000)."""
     pages, Hkv, page_size, D = _kv4(cache)
     dev = cache.get_device()
     if stream is not None or dev != _device():
         with _on(cache, stream):
             return kv4_attention_fwd(q, cache, page_table, seq_lens, out=out, return_lse=return_lse, lse=lse,
-                                     sm_scale=sm_scale, workspace=workspace)
+                                     sm_scale=sm_scale, workspace=workspace, wait_timeout_ms=wait_timeout_ms,
+                                     debug_flags=debug_flags)
     if q.dim() != 4 or page_table.dim() != 2:
         raise ValueError("q must be [B, Sq, n_heads, D] and page_table [B, max_pages]")
     shape = q.shape
@@ -557,28 +566,36 @@ def kv4_attention_fwd(q, cache, page_table, seq_lens, *, out=None, return_lse: b
         ws, ws_bytes = workspace, workspace.numel() * workspace.element_size()
     elif ws_bytes:
         ws = torch.empty(ws_bytes, dtype=_u8, device=cache.device)
-    _check(load().fsa_kv4_attention_fwd(q.data_ptr(), q_stride, cache.data_ptr(), page_table.data_ptr(), seq_lens.data_ptr(),
-                                     o.data_ptr(), None if lse is None else lse.data_ptr(), B, Sq, Hq, Hkv, D, pages,
-                                     page_size, max_pages, sm_scale, None if ws is None else ws.data_ptr(), ws_bytes,
-                                     _raw_stream(dev)), "fsa_kv4_attention_fwd")
+    args = (q.data_ptr(), q_stride, cache.data_ptr(), page_table.data_ptr(), seq_lens.data_ptr(), o.data_ptr(),
+            None if lse is None else lse.data_ptr(), B, Sq, Hq, Hkv, D, pages, page_size, max_pages)
+    if wait_timeout_ms or debug_flags:
+        opt = Options(sm_scale=sm_scale, workspace=None if ws is None else ws.data_ptr(), workspace_bytes=ws_bytes,
+                      wait_timeout_ms=wait_timeout_ms, debug_flags=debug_flags)
+        _check(load().fsa_kv4_attention_fwd_ex(*args, ctypes.byref(opt), _raw_stream(dev)), "fsa_kv4_attention_fwd_ex")
+    else:
+        _check(load().fsa_kv4_attention_fwd(*args, sm_scale, None if ws is None else ws.data_ptr(), ws_bytes,
+                                            _raw_stream(dev)), "fsa_kv4_attention_fwd")
     return (o, lse) if return_lse else o
 
 
 def varlen_attention_fwd(q, k, v, cu_seqlens_q, cu_seqlens_k=None, *, causal: bool = True, out=None,
-                         return_lse: bool = False, lse=None, sm_scale: float = 0.0, stream=None):
+                         return_lse: bool = False, lse=None, sm_scale: float = 0.0, wait_timeout_ms: int = 0,
+                         debug_flags: int = 0, stream=None):
     """fsa_varlen_attention_fwd: BF16 attention over packed sequences.  q CUDA
     bf16 [Tq, n_heads, D], k and v [Tk, n_kv_heads, D] (heads contiguous, any
     token stride that keeps tokens apart); cu_seqlens_q and cu_seqlens_k (by
     default the same) int32 [B + 1].  Returns o [Tq, n_heads, D], with
     return_lse also the log-sum-exps, float32 [Tq, n_heads].  Rows outside every
-    sequence are not written (a new output leaves them undefined)."""
+    sequence are not written (a new output leaves them undefined).
+    wait_timeout_ms: limit of the kernel's bounded waits (0: 2000)."""
     dev = q.get_device()
     if dev < 0:
         raise ValueError("q must be a CUDA tensor")
     if stream is not None or dev != _device():
         with _on(q, stream):
             return varlen_attention_fwd(q, k, v, cu_seqlens_q, cu_seqlens_k, causal=causal, out=out,
-                                        return_lse=return_lse, lse=lse, sm_scale=sm_scale)
+                                        return_lse=return_lse, lse=lse, sm_scale=sm_scale,
+                                        wait_timeout_ms=wait_timeout_ms, debug_flags=debug_flags)
     if q.dim() != 3 or k.dim() != 3:
         raise ValueError("q must be [Tq, n_heads, D], k and v [Tk, n_kv_heads, D]")
     cu_k = cu_seqlens_q if cu_seqlens_k is None else cu_seqlens_k
@@ -603,10 +620,14 @@ def varlen_attention_fwd(q, k, v, cu_seqlens_q, cu_seqlens_k=None, *, causal: bo
         _plain(lse, "lse", _f32, (Tq, Hq), dev)
     elif return_lse:
         lse = torch.empty((Tq, Hq), dtype=_f32, device=q.device)
-    _check(load().fsa_varlen_attention_fwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), qs, ks, vs, cu_seqlens_q.data_ptr(),
-                                           cu_k.data_ptr(), o.data_ptr(), None if lse is None else lse.data_ptr(), nb - 1,
-                                           Tq, Tk, Hq, Hkv, D, 1 if causal else 0, sm_scale, _raw_stream(dev)),
-           "fsa_varlen_attention_fwd")
+    args = (q.data_ptr(), k.data_ptr(), v.data_ptr(), qs, ks, vs, cu_seqlens_q.data_ptr(), cu_k.data_ptr(), o.data_ptr(),
+            None if lse is None else lse.data_ptr(), nb - 1, Tq, Tk, Hq, Hkv, D, 1 if causal else 0)
+    if wait_timeout_ms or debug_flags:
+        opt = Options(sm_scale=sm_scale, wait_timeout_ms=wait_timeout_ms, debug_flags=debug_flags)
+        _check(load().fsa_varlen_attention_fwd_ex(*args, ctypes.byref(opt), _raw_stream(dev)),
+               "fsa_varlen_attention_fwd_ex")
+    else:
+        _check(load().fsa_varlen_attention_fwd(*args, sm_scale, _raw_stream(dev)), "fsa_varlen_attention_fwd")
     return (o, lse) if return_lse else o
 
 

@@ -461,6 +461,10 @@ fsa_status check_kv4(const void* cache, int64_t num_pages, int page_size, int H_
     return FSA_OK;
 }
 
+uint64_t wait_limit_ns(const fsa_options& op) {
+    return static_cast<uint64_t>(op.wait_timeout_ms > 0 ? op.wait_timeout_ms : 2000) * 1000000ull;
+}
+
 bool token_stride_ok(int64_t stride, int64_t least) { return stride >= least && stride % 8 == 0 && stride < (int64_t{1} << 36); }
 
 fsa_status kv4_rows(const void* k, const void* v, int64_t k_stride, int64_t v_stride, const int64_t* slots, int64_t T,
@@ -533,16 +537,29 @@ fsa_status fsa_kv4_attention_fwd(const void* q, int64_t q_stride, const void* ca
                                  const int32_t* seq_lens, void* o, float* lse, int B, int Sq, int Hq, int Hkv, int D,
                                  int64_t num_pages, int page_size, int max_pages, float sm_scale, void* workspace,
                                  uint64_t workspace_bytes, void* stream) {
+    fsa_options op{};
+    op.sm_scale = sm_scale;
+    op.workspace = workspace;
+    op.workspace_bytes = workspace_bytes;
+    return fsa_kv4_attention_fwd_ex(q, q_stride, cache, page_table, seq_lens, o, lse, B, Sq, Hq, Hkv, D, num_pages,
+                                    page_size, max_pages, &op, stream);
+}
+
+fsa_status fsa_kv4_attention_fwd_ex(const void* q, int64_t q_stride, const void* cache, const int32_t* page_table,
+                                    const int32_t* seq_lens, void* o, float* lse, int B, int Sq, int Hq, int Hkv, int D,
+                                    int64_t num_pages, int page_size, int max_pages, const fsa_options* opt,
+                                    void* stream) {
+    const fsa_options op = opt ? *opt : fsa_options{};
     fsa_status s = check_kv4_attention(B, Sq, Hq, Hkv, D, page_size, max_pages);
     if (s != FSA_OK) return s;
     s = check_kv4(cache, num_pages, page_size, Hkv, D);
     if (s != FSA_OK) return s;
     if (!q || !o || !page_table || !seq_lens || !aligned16(q) || !aligned16(o) ||
         (reinterpret_cast<uintptr_t>(page_table) & 3) || (reinterpret_cast<uintptr_t>(seq_lens) & 3) ||
-        (reinterpret_cast<uintptr_t>(lse) & 3) || !token_stride_ok(q_stride, 0) || !std::isfinite(sm_scale))
+        (reinterpret_cast<uintptr_t>(lse) & 3) || !token_stride_ok(q_stride, 0) || !std::isfinite(op.sm_scale))
         return FSA_ERR_INVALID_ARGUMENT;
     const uint64_t need = kv4_attention_workspace_bytes(B, Sq, Hq, Hkv, D, page_size, max_pages);
-    if (need && (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255) || workspace_bytes < need))
+    if (need && (!op.workspace || (reinterpret_cast<uintptr_t>(op.workspace) & 255) || op.workspace_bytes < need))
         return FSA_ERR_INVALID_ARGUMENT;
     int dev;
     DeviceState* ds;
@@ -556,7 +573,7 @@ fsa_status fsa_kv4_attention_fwd(const void* q, int64_t q_stride, const void* ca
     a.seq_lens = seq_lens;
     a.o = o;
     a.lse = lse;
-    a.workspace = workspace;
+    a.workspace = op.workspace;
     a.num_pages = num_pages;
     a.B = B;
     a.Sq = Sq;
@@ -565,8 +582,9 @@ fsa_status fsa_kv4_attention_fwd(const void* q, int64_t q_stride, const void* ca
     a.D = D;
     a.page_size = page_size;
     a.max_pages = max_pages;
-    a.sm_scale = sm_scale > 0.0f ? sm_scale : 1.0f / std::sqrt(static_cast<float>(D));
-    a.timeout_ns = 2000000000ull;
+    a.sm_scale = op.sm_scale > 0.0f ? op.sm_scale : 1.0f / std::sqrt(static_cast<float>(D));
+    a.timeout_ns = wait_limit_ns(op);
+    a.debug_flags = op.debug_flags;
     a.err_word = ds->err;
     return launch_kv4_attention(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? FSA_OK : FSA_ERR_CUDA;
 }
@@ -575,10 +593,21 @@ fsa_status fsa_varlen_attention_fwd(const void* q, const void* k, const void* v,
                                     int64_t v_stride, const int32_t* cu_q, const int32_t* cu_k, void* o, float* lse,
                                     int B, int Tq, int Tk, int Hq, int Hkv, int D, int causal, float sm_scale,
                                     void* stream) {
+    fsa_options op{};
+    op.sm_scale = sm_scale;
+    return fsa_varlen_attention_fwd_ex(q, k, v, q_stride, k_stride, v_stride, cu_q, cu_k, o, lse, B, Tq, Tk, Hq, Hkv, D,
+                                       causal, &op, stream);
+}
+
+fsa_status fsa_varlen_attention_fwd_ex(const void* q, const void* k, const void* v, int64_t q_stride, int64_t k_stride,
+                                       int64_t v_stride, const int32_t* cu_q, const int32_t* cu_k, void* o, float* lse,
+                                       int B, int Tq, int Tk, int Hq, int Hkv, int D, int causal,
+                                       const fsa_options* opt, void* stream) {
+    const fsa_options op = opt ? *opt : fsa_options{};
     if (D != 64 && D != 128) return FSA_ERR_UNSUPPORTED;
     // (with more keys one pair of query tiles could outlast the kernel's bounded waits)
     if (B < 1 || Tq < 0 || Tk < 0 || Tq > (1 << 26) || Tk > (1 << 26) || Hq < 1 || Hkv < 1 || Hkv > 65535 ||
-        Hq % Hkv != 0 || Hq / Hkv > 128 || (causal != 0 && causal != 1) || !std::isfinite(sm_scale))
+        Hq % Hkv != 0 || Hq / Hkv > 128 || (causal != 0 && causal != 1) || !std::isfinite(op.sm_scale))
         return FSA_ERR_INVALID_ARGUMENT;
     if ((Tq / (2 * (128 / (Hq / Hkv))) + static_cast<int64_t>(B)) * Hkv > INT32_MAX) return FSA_ERR_INVALID_ARGUMENT;
     if (!cu_q || !cu_k || (reinterpret_cast<uintptr_t>(cu_q) & 3) || (reinterpret_cast<uintptr_t>(cu_k) & 3) ||
@@ -619,8 +648,9 @@ fsa_status fsa_varlen_attention_fwd(const void* q, const void* k, const void* v,
     a.Hkv = Hkv;
     a.D = D;
     a.causal = causal;
-    a.sm_scale = sm_scale > 0.0f ? sm_scale : 1.0f / std::sqrt(static_cast<float>(D));
-    a.timeout_ns = 2000000000ull;
+    a.sm_scale = op.sm_scale > 0.0f ? op.sm_scale : 1.0f / std::sqrt(static_cast<float>(D));
+    a.timeout_ns = wait_limit_ns(op);
+    a.debug_flags = op.debug_flags;
     a.err_word = ds->err;
     return launch_varlen_attention(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? FSA_OK : FSA_ERR_CUDA;
 }

@@ -133,6 +133,7 @@ struct Kv4AttnLaunch {
     int B, Sq, Hq, Hkv, D, page_size, max_pages;
     float sm_scale;
     uint64_t timeout_ns;
+    int debug_flags;
     unsigned int* err_word;
 };
 size_t kv4_attention_workspace_bytes(int B, int Sq, int Hq, int Hkv, int D, int page_size, int max_pages);
@@ -151,6 +152,7 @@ struct VarlenLaunch {
     int causal;
     float sm_scale;
     uint64_t timeout_ns;
+    int debug_flags;
     unsigned int* err_word;
 };
 cudaError_t launch_varlen_attention(const VarlenLaunch& a, cudaStream_t st);

@@ -132,6 +132,7 @@ struct Params {
     float c;  // sm_scale * log2(e)
     uint64_t timeout_ns;
     unsigned int* err_word;
+    int skip;  // test use: a warp's second group never arrives
 };
 
 // A piece of a segment: what one warp made of the groups of it in its part.
@@ -284,7 +285,7 @@ __global__ void __launch_bounds__(32 * kWarps * kBlockTeams, (NT == 1 ? 16 : 8) 
 
     if (tid == 0) sm.abort = 0;
     if (lane < 2) sm.piece[warp][lane].b = -1;
-    if (lane < kStages) mbar_init(&sm.full[warp][lane], 1);
+    if (lane < kStages) mbar_init(&sm.full[warp][lane], lane == 1 && p.skip ? 2 : 1);
     fence_mbar_init();
 
     // this team's share [x, x_end) of the line, and where it starts: sequence b,
@@ -1100,6 +1101,7 @@ cudaError_t launch_kv4_attention(const Kv4AttnLaunch& a, cudaStream_t st) {
     p.max_pages = a.max_pages;
     p.c = static_cast<float>(static_cast<double>(a.sm_scale) * 1.4426950408889634);
     p.timeout_ns = a.timeout_ns;
+    p.skip = a.debug_flags & 1;
     p.err_word = a.err_word;
     const int n = static_cast<int>(segments);
     if (a.D == 128) return nt == 1 ? launch<128, 1>(p, n, st) : launch<128, 2>(p, n, st);

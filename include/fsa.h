@@ -498,8 +498,9 @@ FSA_API fsa_status fsa_varlen_attention_fwd_ex(const void *q, const void *k, con
  * current device (the allocating entry points' word and, once that entry
  * point has run there, fsa_attention_fwd_noalloc's): FSA_OK, FSA_ERR_TIMEOUT,
  * FSA_ERR_INVALID_ARGUMENT if a kernel met a slot, page or sequence bound
- * outside its buffer, or FSA_ERR_CUDA if the sync itself failed.  Allocates no
- * device memory. */
+ * outside its buffer, or FSA_ERR_CUDA if the sync itself failed or a kernel
+ * could not start its work.  Of several, a timeout is returned first, then
+ * FSA_ERR_CUDA.  Allocates no device memory. */
 FSA_API fsa_status fsa_get_device_error(void *stream);
 
 /* Static description of a status code. */

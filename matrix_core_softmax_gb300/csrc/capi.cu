@@ -875,9 +875,7 @@ fsa_status fsa_get_device_error(void* stream) {
         }
         w |= x;
     }
-    if (w & kErrTimeout) return FSA_ERR_TIMEOUT;
-    if (w & kErrBadIndex) return FSA_ERR_INVALID_ARGUMENT;
-    return w ? FSA_ERR_CUDA : FSA_OK;
+    return error_word_status(w);
 }
 
 void fsa_release_workspace(void) {

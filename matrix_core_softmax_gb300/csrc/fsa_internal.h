@@ -5,6 +5,8 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include "fsa.h"
+
 namespace fsa {
 
 // Element formats (match fsa_elem).
@@ -166,5 +168,13 @@ cudaError_t launch_mma_probe(int kind, int ctas, int iters, uint64_t timeout_ns,
 constexpr unsigned int kErrTimeout = 1u;
 constexpr unsigned int kErrMisaligned = 2u;  // shared-memory base not 1024-byte aligned
 constexpr unsigned int kErrBadIndex = 4u;    // a slot, page or sequence bound outside its buffer
+
+// What several calls may have left in one word: whatever kept a kernel from
+// computing at all comes before an index that was skipped.
+constexpr fsa_status error_word_status(unsigned int w) {
+    if (w & kErrTimeout) return FSA_ERR_TIMEOUT;
+    if (w & ~kErrBadIndex) return FSA_ERR_CUDA;
+    return w ? FSA_ERR_INVALID_ARGUMENT : FSA_OK;
+}
 
 }  // namespace fsa

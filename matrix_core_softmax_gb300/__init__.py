@@ -545,8 +545,8 @@ def kv4_attention_fwd(q, cache, page_table, seq_lens, *, out=None, return_lse: b
         raise ValueError("q must be [B, Sq, n_heads, D] and page_table [B, max_pages]")
     shape = q.shape
     B, Sq, Hq, Dq = shape
-    if Hkv == 0 or Dq != D or Hq % Hkv or B * Sq * Hq == 0:
-        raise ValueError(f"q must be a non-empty tensor [B, Sq, n_heads, {D}] with a multiple of {Hkv} heads")
+    if Hkv == 0 or Dq != D or Hq % Hkv or Sq * Hq == 0:
+        raise ValueError(f"q must be [B, Sq, n_heads, {D}] with a query token and a multiple of {Hkv} heads")
     st = _heads(q, "q", shape, dev)
     q_stride = st[1] if Sq > 1 else st[0] if B > 1 else Hq * D
     if B > 1 and st[0] != Sq * q_stride:
@@ -559,6 +559,8 @@ def kv4_attention_fwd(q, cache, page_table, seq_lens, *, out=None, return_lse: b
         _plain(lse, "lse", _f32, (B, Sq, Hq), dev)
     elif return_lse:
         lse = torch.empty((B, Sq, Hq), dtype=_f32, device=cache.device)
+    if B == 0:
+        return (o, lse) if return_lse else o
     ws, ws_bytes = None, kv4_attention_workspace_size(B, Sq, Hq, Hkv, D, page_size, max_pages)
     if workspace is not None:
         if not workspace.is_contiguous() or workspace.get_device() != dev:

@@ -41,3 +41,21 @@ def test_packed_attention_options(lib):
                                                D, 1, opt, None)
     assert call(_opt(sm_scale=float("inf"))) == INVALID
     assert call(None, k=8) == INVALID and call(None, D=96) == UNSUPPORTED
+
+
+@pytest.mark.parametrize("page", [32, 64, 256])
+@pytest.mark.parametrize("D", [64, 128])
+def test_workspace_on_both_sides_of_the_split(lib, page, D):
+    # up to 1024 keys a block takes a segment, up to 2048 from 64 segments on; longer
+    # tables are split and joined through the workspace
+    def size(B, Sq, Hq, Hkv, keys):
+        return lib.fsa_kv4_attention_workspace_size(B, Sq, Hq, Hkv, D, page, keys // page)
+    for B, Hkv in ((1, 1), (7, 9), (63, 1)):
+        assert size(B, 1, 4 * Hkv, Hkv, 1024) == 0
+        assert size(B, 1, 4 * Hkv, Hkv, 1024 + 256) > 0
+    for B, Hkv in ((8, 8), (64, 1)):
+        assert size(B, 1, 4 * Hkv, Hkv, 2048) == 0
+        assert size(B, 1, 4 * Hkv, Hkv, 2048 + 256) > 0
+    # pieces of at most two segments of 8 or 16 rows a team, in FP32 with their log-sum-exp
+    assert size(1, 1, 8, 1, 131072) == 304 * 2 * 8 * (D + 1) * 4
+    assert size(1, 5, 8, 1, 131072) == 152 * 2 * 16 * (D + 1) * 4

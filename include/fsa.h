@@ -419,7 +419,8 @@ FSA_API fsa_status fsa_kv4_read(const void *cache, int64_t num_pages, int page_s
  * 1/sqrt(D)), o = softmax(s) v^ on the cached values as held.  A row that sees
  * no key gets o = 0 and lse = -infinity.
  *  - Products in f16 with FP32 accumulation: q is scaled by a power of two per
- *    row, softmax weights are rounded to f16 (relative to the largest product
+ *    row (an element is exact down to 2^-14 of the row's largest and rounded to
+ *    2^-25 of it below), softmax weights are rounded to f16 (relative to the largest product
  *    of weight and value scale, a scale counting as 2^-90 of the row's largest at
  *    least); sums are FP32.
  *  - o and lse must not overlap q or the cache.

@@ -30,6 +30,13 @@ __host__ __device__ constexpr Kv4Layout kv4_layout(int D) {
     return {kKv4Group * D / 2, kKv4Group * D, kKv4Group * (D + D / 32), D / 2, D / 32};
 }
 
+// Packed unsigned 16-bit maximum.
+__device__ __forceinline__ uint32_t max16x2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("max.u16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+
 // Eight E2M1 codes of a word to four f16 pairs (exact); pair i from byte i.
 __device__ __forceinline__ void e2m1x8_to_f16(uint32_t w, uint32_t (&r)[4]) {
     asm("{\n.reg .b8 a, b, c, d;\n"

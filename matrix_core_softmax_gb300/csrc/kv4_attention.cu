@@ -57,8 +57,8 @@
 // its warps' pieces, leaves at most two of its own, and a second kernel joins
 // those.  (With teams that walked over segments together and met at each end,
 // 64 ragged sequences of up to 2000 keys took 40.7 us.)  Where no sequence can
-// be longer than kWholeGroups groups a block takes one segment and there is no
-// second kernel.
+// be longer than kWholeGroups groups, or twice as many with many segments, a block
+// takes one segment and there is no second kernel.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -77,32 +77,35 @@ namespace {
 // two a block.  (Of two blocks on an SM the first is served first, 8 of the 152
 // SMs get two of the first ones or two of the later ones, and the later ones are
 // the call's end; the warps of one block are served evenly.  But the second kernel
-// cannot start before a block ends.)  One team a block / two, 8 key heads: 64
-// sequences of up to 32768 keys 208.6 / 198 us, of up to 8000 64.0 / 62.0, of up
-// to 4000 41.5 / 40.8; 16 of up to 8000 24.0 / 25.5, of up to 4000 19.3 / 21.4.
+// cannot start before a block ends.)  One team a block / two, 32 / 8 heads of 128:
+// 64 sequences of up to 32768 keys 208.6 / 198.3 us, of up to 8000 64.7 / 62.3, of
+// up to 4000 42.2 / 41.4; 16 of up to 8000 24.1 / 25.6, of up to 4000 19.2 / 21.6.
 constexpr int kTeamWarps = 8, kLongPart = 16;
 constexpr int kJoinThreads = 256;
 constexpr int kStages = 2;        // (three: 1 % slower, they leave less L1)
 constexpr int kTeams = 304;       // of the split form: two on each of 152 SMs
 constexpr int kMinShare = kTeamWarps; // places of a team, at least one a warp
 // A block takes a whole segment up to this many groups, twice as many where
-// there are many segments.  8 key heads of D = 128, whole against split: one
-// sequence of 1000 keys 8.9 / 9.4 us, of 2000 13.2 / 9.8; 16 sequences of up to
-// 2000 keys 13.6 / 15.0, 32 of them 17.3 / 19.3, 64 30.1 / 27.6, 256 79.6 / 80.2;
-// 16 of up to 4000 22.1 / 19.4, 64 of them 44.3 / 41.9.
+// there are many segments.  32 / 8 heads of 128, whole / split: one sequence of
+// 1000 keys 9.3 / 9.6 us, of 2000 13.9 / 9.9; 16 of up to 1000 9.6 / 13.2, 64 of
+// them 16.6 / 20.4, 256 48.0 / 49.8; up to 2000 keys: 8 sequences 14.0 / 13.5, 16
+// 14.0 / 15.2, 32 17.5 / 19.4, 64 30.1 / 27.6, 128 45.6 / 46.4, 256 79.8 / 78.7 (no
+// clear side: the longest segment sets the whole form's time); 16 of up to 4000
+// 22.8 / 19.3, 64 of them 44.6 / 41.3.
 constexpr int kWholeGroups = 32;
 constexpr int kManySegments = 64; // from here on the join takes four rows a block, too
 // More whole segments than fit the GPU in blocks of eight warps run in blocks of
-// four: twice as many segments at a time wait for their first keys.  8 key
-// heads, four warps against eight: 64 sequences of up to 500 keys 10.7 / 14.6 us,
-// of up to 1000 16.0 / 20.4, of up to 2000 29.6 / 30.1; 8 sequences of up to 1000
-// 10.2 / 9.0, of up to 2000 16.6 / 13.4.
+// four: twice as many segments at a time wait for their first keys.  32 / 8 heads
+// of 128, four warps / eight: 64 sequences of up to 500 keys 11.2 / 15.6 us, of up
+// to 1000 16.6 / 21.6, of up to 2000 30.1 / 31.5; 32 of up to 1000 12.3 / 12.2; 8 of
+// up to 1000 10.8 / 9.6, of up to 2000 17.2 / 14.0.
 constexpr int kFewWarps = 8, kManyWarps = 4;
 // A segment takes this many places of the line before its groups, for what a
-// warp spends on taking it up and writing it (some 3 us, against 1.9 us for a
-// group beside 15 other warps; without them the warps that meet many short
-// sequences finished last, 75 us against 56 for the others on 64 ragged
-// sequences of up to 8000 keys).
+// warp spends on taking it up and writing it and for the joins of its pieces
+// (without them the warps that meet many short sequences finished last).  One,
+// two and three places, 32 / 8 heads: 64 sequences of up to 8000 keys 70.0 / 62.7 /
+// 62.3 us, at D = 64 51.7 / 46.9 / 44.0, of up to 4000 44.1 / 41.3 / 41.4, of up to
+// 32768 200.5 / 199.4 / 198.3; 16 of up to 4000 with four queries 30.9 / 29.6 / 28.9.
 constexpr int kSegmentCost = 3;
 constexpr uint32_t kNoGroup = 0xFFFFFFFFu, kNoPlace = 0xFFFFFFFEu;
 constexpr float kNoMax = -3.402823466e38f;  // of a row without keys: the least finite value, below every score
@@ -158,12 +161,6 @@ struct __align__(128) Smem {
     int abort;
 };
 
-__device__ __forceinline__ float ex2(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-
 __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                         uint32_t b1) {
     asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
@@ -178,15 +175,10 @@ __device__ __forceinline__ void mma_f16_zero(float (&c)[4], uint32_t a0, uint32_
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
 }
 
-// Packed unsigned 16-bit minimum and maximum.
+// Packed unsigned 16-bit minimum.
 __device__ __forceinline__ uint32_t min16x2(uint32_t a, uint32_t b) {
     uint32_t r;
     asm("min.u16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-    return r;
-}
-__device__ __forceinline__ uint32_t max16x2(uint32_t a, uint32_t b) {
-    uint32_t r;
-    asm("max.u16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
     return r;
 }
 

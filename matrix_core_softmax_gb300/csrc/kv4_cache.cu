@@ -33,12 +33,6 @@ __device__ __forceinline__ int64_t group_of(int64_t s, int h, int H, int page_si
     return ((page * H + h) * (page_size / kKv4Group) + (r / kKv4Group)) * gbytes;
 }
 
-__device__ __forceinline__ uint32_t max16x2(uint32_t a, uint32_t b) {
-    uint32_t r;
-    asm("max.u16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-    return r;
-}
-
 // X + 127 of the scale rule for a block whose largest magnitude has the bf16
 // pattern `amax`: e - 2, one more beyond 1.5 * 2^e (the 0x3F carries into the
 // exponent from mantissa 0x41 on), at least 0 -- where every subnormal lands.

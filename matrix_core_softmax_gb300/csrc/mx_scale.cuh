@@ -1,6 +1,7 @@
 // mx_scale.cuh -- the block scale rule of the MX element types (E8M0 scales:
-// the smallest power of two 2^X with amax <= max_elem * 2^X), shared by the
-// quantizer and the four-bit key/value cache.
+// the smallest power of two 2^X with amax <= max_elem * 2^X), for the quantizer,
+// and powers of two, for it and the four-bit key/value cache (whose kernels have
+// the rule in a closed form for E2M1).
 #pragma once
 #include <cstdint>
 

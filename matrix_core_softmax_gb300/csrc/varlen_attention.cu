@@ -32,8 +32,8 @@
 // run.  P is handed over in halves of 64 keys, so that P V begins under the second
 // half's exponentials: a step is bound by this chain, from scores to weights to
 // the next scores, as much as by the products (16 prompts of up to 1000 tokens
-// 73.5 -> 70.3 us with the halves and V waited for ahead of P, 24 of up to 2000 at
-// D = 64 208 -> 197; quarters no better).  A score product's commit also says that
+// 73.5 -> 71 us with the halves and V waited for ahead of P, 24 of up to 2000 at
+// D = 64 208 -> 199, 32 / 8 heads; quarters no better).  A score product's commit also says that
 // the tile's P V before it has finished, so between s_full and p_half a softmax
 // thread owns its row of O and may rescale it: that happens only when the running
 // maximum is passed by more than 2^8 (weights up to 2^8 are exact enough in bf16,

@@ -115,12 +115,11 @@ constexpr int kMostL = 100;       // l is not rescaled to 2^100 or more
 constexpr int kHeadroom = 11;     // weights carry 2^11: 2^11 * 2^4 = 2^15 < 65504
 constexpr float kUnit = 1.0f / (1 << kHeadroom);
 // A key's products of codes and the scaled q, below 2^11 in sum, take the key
-// scales over 2^kKeyShift and the scores the rest: scales go up to 2^126, and
-// nothing on the way to a score of normal size leaves FP32's range.  (kKeyUnit
-// takes the scale byte's one away, too.)
-constexpr int kKeyShift = 9;
+// scales over 2^kKeyShift and the scores the rest: scales go up to 2^127, and
+// nothing on the way to a score of normal size leaves FP32's range.
+constexpr int kKeyShift = 10;
+constexpr float kKeyUnit = 1.0f / (1 << kKeyShift);
 constexpr int kMostE = 240;       // largest exponent that q is scaled by: below 2^15 in f16
-constexpr float kKeyUnit = 0.5f / (1 << kKeyShift);
 
 struct Params {
     const uint16_t* q;
@@ -500,10 +499,9 @@ __global__ void __launch_bounds__(32 * kWarps * kBlockTeams, (NT == 1 ? 16 : 8) 
                 const uint8_t* buf = sm.ring[warp][st];
                 const int key0 = static_cast<int>(pos_begin + i - seg_x) * kKv4Group;
 
-                // scales: lane = key.  2^(X - kKeyShift) of the key blocks, from the bytes
-                // plus one, so that byte 0 (2^-127) has an exponent, too (the largest that
-                // the cache is given is 253).  Value scale bytes as 16-bit pairs, blocks 0
-                // and 2, 1 and 3.
+                // scales: lane = key.  2^(X - kKeyShift) of the key blocks (byte 0, 2^-127, is
+                // the one without an exponent field).  Value scale bytes as 16-bit pairs,
+                // blocks 0 and 2, 1 and 3.
                 {
                     const int pos = swap_pos(lane);
                     uint32_t ks, vs;
@@ -516,11 +514,10 @@ __global__ void __launch_bounds__(32 * kWarps * kBlockTeams, (NT == 1 ? 16 : 8) 
                     }
                     if (key0 + lane >= len) vs = 0;
                     float kf[4];
-                    ks += D == 128 ? 0x01010101u : 0x0101u;
-                    kf[0] = __uint_as_float((ks & 0xFFu) << 23) * kKeyUnit;
-                    kf[1] = __uint_as_float((ks << 15) & 0x7F800000u) * kKeyUnit;
-                    kf[2] = __uint_as_float((ks << 7) & 0x7F800000u) * kKeyUnit;
-                    kf[3] = __uint_as_float((ks >> 1) & 0x7F800000u) * kKeyUnit;
+                    kf[0] = __uint_as_float(max((ks & 0xFFu) << 23, 0x00400000u)) * kKeyUnit;
+                    kf[1] = __uint_as_float(max((ks << 15) & 0x7F800000u, 0x00400000u)) * kKeyUnit;
+                    kf[2] = __uint_as_float(max((ks << 7) & 0x7F800000u, 0x00400000u)) * kKeyUnit;
+                    kf[3] = __uint_as_float(max((ks >> 1) & 0x7F800000u, 0x00400000u)) * kKeyUnit;
                     if (D == 128)
                         sm.kscale[warp][pos] = make_float4(kf[0], kf[1], kf[2], kf[3]);
                     else

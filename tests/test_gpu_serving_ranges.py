@@ -151,3 +151,26 @@ def test_cache_values_at_the_ends_of_the_exponents(fsa, e):
     assert fsa.get_device_error() == 0
     r = ref.attend(qb[0].double().cpu(), hk, hv, torch.tensor([n - 1]), ref.default_scale(D))
     ref.check(o[0].cpu(), lse[0].cpu(), r, ref.F16)
+
+
+# The layout is public: a cache that its owner filled, with the scale bytes that
+# fsa_kv4_append never writes (2^127)
+@pytest.mark.parametrize("n,D", [(200, 64), (3000, 128)])
+def test_a_cache_with_the_largest_scales(fsa, n, D):
+    page, H = 64, 2
+    pages = -(-n // page)
+    rng = np.random.default_rng(n)
+    c = np.zeros((pages, H, page // 32, 34 * D), np.uint8)
+    nibbles = np.array([0, 1, 2, 8, 9, 10], np.uint8)  # 0, 0.5, 1 and their negatives
+    c[..., :32 * D] = rng.choice(nibbles, c[..., :32 * D].shape) | (rng.choice(nibbles, c[..., :32 * D].shape) << 4)
+    c[..., 32 * D:33 * D] = rng.choice(np.array([0, 1, 126, 253, 254], np.uint8), c[..., 32 * D:33 * D].shape)
+    c[..., 33 * D:] = rng.integers(120, 135, c[..., 33 * D:].shape)
+    cache = torch.from_numpy(c).cuda()
+    table = torch.arange(pages, dtype=torch.int32, device="cuda")[None]
+    hk, hv = (torch.from_numpy(x) for x in ref.cache_rows(cache, list(range(n))))
+    q = to_dev(_bits(np.clip(rng.standard_normal((1, 1, 8, D)), -1.9, 1.9) * 2.0 ** -126))
+    o, lse = fsa.kv4_attention_fwd(q, cache, table, torch.tensor([n], dtype=torch.int32, device="cuda"), sm_scale=0.25,
+                                   return_lse=True)
+    assert fsa.get_device_error() == 0
+    r = ref.attend(q[0].double().cpu(), hk, hv, torch.tensor([n - 1]), 0.25)
+    ref.check(o[0].cpu(), lse[0].cpu(), r, ref.F16)

@@ -423,6 +423,7 @@ FSA_API fsa_status fsa_kv4_read(const void *cache, int64_t num_pages, int page_s
  *    2^-25 of it below), softmax weights are rounded to f16 (relative to the largest product
  *    of weight and value scale, a scale counting as 2^-90 of the row's largest at
  *    least); sums are FP32.
+ *  - The scores, and q . k^ itself, must lie in FP32's range.
  *  - o and lse must not overlap q or the cache.
  *  - workspace: device buffer of fsa_kv4_attention_workspace_size() bytes,
  *    256-byte aligned, contents arbitrary; NULL when that size is 0.  Calls
@@ -471,8 +472,9 @@ FSA_API uint64_t fsa_kv4_attention_workspace_size(int B, int Sq, int Hq, int Hkv
  *     NULL.  Rows outside every sequence are left as they were; a row that
  *     sees no key gets o = 0 and lse = -infinity.
  * Same arithmetic as fsa_bf16_attention_fwd (FP32 scores and sums, BF16
- * weights).  The tokens of a sequence must be finite; what stands outside of
- * it does not reach its outputs.  Bounds that decrease or leave 0 .. Tq or
+ * weights).  The tokens of a sequence must be finite and its products q . k and
+ * scores lie in FP32's range; what stands outside of it does not reach its
+ * outputs.  Bounds that decrease or leave 0 .. Tq or
  * 0 .. Tk are reported by fsa_get_device_error as FSA_ERR_INVALID_ARGUMENT,
  * and the sequences from the first wrong bound on are skipped.
  * o and lse must not overlap q, k or v.

@@ -497,6 +497,82 @@ FSA_API fsa_status fsa_varlen_attention_fwd_ex(const void *q, const void *k, con
                                                int Tq, int Tk, int Hq, int Hkv, int D, int causal,
                                                const fsa_options *opt, void *stream);
 
+/*
+ * Products of matrices in MX formats, for the projections of a language model (an
+ * addition of this library; the pages have no counterpart).
+ *
+ * An operand is a matrix of `rows` rows of `cols` elements, E2M1 or E4M3, that
+ * share one E8M0 scale for 32 elements of a row:
+ *  codes: [rows][pitch] bytes, 32-byte aligned, pitch = ceil(cols / 128) * 64 for
+ *    E2M1 (two to a byte, low nibble first) or * 128 for E4M3; codes behind cols
+ *    are zero.
+ *  scales: [ceil(rows / 128)][ceil(cols / 128)][512] bytes (X + 127), 16-byte
+ *    aligned: that of row r and block b (32 elements) is byte (r % 32) * 16 +
+ *    (r % 128 / 32) * 4 + b % 4 of [r / 128][b / 4].  Those of blocks behind cols
+ *    are 127, those of rows behind the last are not read for any output and left
+ *    as they were.
+ * A slice of whole 128-row groups of an operand is an operand.
+ * rows in 0 .. 2^30, cols in 1 .. 2^20; FSA_ELEM_E2M3: FSA_ERR_UNSUPPORTED.
+ *
+ * These entry points take no workspace and allocate nothing, except that the first
+ * call of the library on a device allocates its error word: make one call before
+ * capturing a graph.
+ */
+
+/*
+ * fsa_mx_pack -- quantizes bf16 rows x[rows][cols], x_stride elements apart (0
+ * repeats a row), into an operand, by fsa_quantize_mx's rule.  Rows on 16 bytes
+ * (pointer, and a stride that is a multiple of 8) are read in whole vectors,
+ * others element by element.
+ */
+FSA_API fsa_status fsa_mx_pack(const void *x, int64_t x_stride, int64_t rows, int64_t cols, int elem,
+                               uint8_t *codes, uint8_t *scales, void *stream);
+
+/*
+ * fsa_mx_unpack -- an operand's values as bf16 out[rows][cols], out_stride (at
+ * least cols) elements apart.  Exact, except that a value below bf16's normal range
+ * is rounded and one of 2^128 or more (fsa_mx_pack makes them of blocks whose
+ * largest magnitude is 1.75 * 2^127 or more in E2M1) reads as infinity.
+ */
+FSA_API fsa_status fsa_mx_unpack(const uint8_t *codes, const uint8_t *scales, int64_t rows,
+                                 int64_t cols, int elem, void *out, int64_t out_stride, void *stream);
+
+/*
+ * fsa_rms_norm_mx -- root-mean-square norm of rows, with the residual's addition
+ * before it, into an operand:
+ *   h = x + residual, rounded to bf16 and stored in sum (residual NULL: h = x, and
+ *       sum is not used);
+ *   y = h / sqrt(mean of h^2 over the row + eps) * gain, in FP32, quantized as by
+ *       fsa_mx_pack without a rounding to bf16 between.
+ *  x, residual: bf16 [rows][cols], x_stride and residual_stride elements apart;
+ *  gain: bf16 [cols]; sum: bf16, sum_stride (at least cols) elements apart; it may be
+ *  x or residual itself (same address and stride), and overlap nothing else.
+ * h and y must be finite; the squares' sum may pass FP32's range.  eps > 0.
+ * cols in 1 .. 32768.
+ */
+FSA_API fsa_status fsa_rms_norm_mx(const void *x, int64_t x_stride, const void *residual,
+                                   int64_t residual_stride, const void *gain, float eps, int64_t rows,
+                                   int64_t cols, int elem, void *sum, int64_t sum_stride,
+                                   uint8_t *codes, uint8_t *scales, void *stream);
+
+/*
+ * fsa_mx_linear -- y[t][n] = sum over k of x[t][k] w[n][k] of two operands: T tokens'
+ * activations and the N rows of a weight, both with K columns.
+ *  x_elem, w_elem: E2M1 and E2M1, E4M3 and E2M1, or E4M3 and E4M3 (E2M1 and E4M3:
+ *  FSA_ERR_UNSUPPORTED).
+ *  y: bf16 [T][N], y_stride (at least N) elements apart; must not overlap the
+ *  operands.  FP32 sums in an order that depends on T, N, K and the types only, one
+ *  rounding; the held values' products and sums must lie in FP32's range.
+ *  opt: NULL, or wait_timeout_ms and debug_flags (stage 1 of a tile's ring never
+ *  arrives) are used.
+ * ceil(T / 128) * ceil(N / 128) <= 2^27.  A bounded wait that ran out is reported by
+ * fsa_get_device_error.
+ */
+FSA_API fsa_status fsa_mx_linear(const uint8_t *x_codes, const uint8_t *x_scales, int x_elem,
+                                 const uint8_t *w_codes, const uint8_t *w_scales, int w_elem, int64_t T,
+                                 int64_t N, int64_t K, void *y, int64_t y_stride,
+                                 const fsa_options *opt, void *stream);
+
 /* Synchronises `stream`, then reads and clears the device error words of the
  * current device (the allocating entry points' word and, once that entry
  * point has run there, fsa_attention_fwd_noalloc's): FSA_OK, FSA_ERR_TIMEOUT,

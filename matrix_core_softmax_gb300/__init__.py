@@ -11,6 +11,7 @@ import ctypes
 import functools
 import os
 import threading
+from typing import NamedTuple
 
 import torch
 
@@ -34,7 +35,7 @@ EXPORTS = ("fsa_quantize_mx", "fsa_attention_fwd", "fsa_attention_fwd_ex",
            "fsa_attention_fwd_host", "fsa_cross_attention_fwd_host", "fsa_mma_rate_probe",
            "fsa_kv4_page_bytes", "fsa_kv4_append", "fsa_kv4_read", "fsa_kv4_attention_fwd",
            "fsa_kv4_attention_workspace_size", "fsa_varlen_attention_fwd", "fsa_kv4_attention_fwd_ex",
-           "fsa_varlen_attention_fwd_ex")
+           "fsa_varlen_attention_fwd_ex", "fsa_mx_pack", "fsa_mx_unpack", "fsa_rms_norm_mx", "fsa_mx_linear")
 
 
 class FsaError(RuntimeError):
@@ -133,6 +134,14 @@ def load(path: str | None = None):
             lib.fsa_varlen_attention_fwd_ex.argtypes = [V, V, V, I64, I64, I64, V, V, V, V, I, I, I, I, I, I, I,
                                                         ctypes.POINTER(Options), V]
             lib.fsa_varlen_attention_fwd_ex.restype = I
+            lib.fsa_mx_pack.argtypes = [V, I64, I64, I64, I, V, V, V]
+            lib.fsa_mx_pack.restype = I
+            lib.fsa_mx_unpack.argtypes = [V, V, I64, I64, I, V, I64, V]
+            lib.fsa_mx_unpack.restype = I
+            lib.fsa_rms_norm_mx.argtypes = [V, I64, V, I64, V, F, I64, I64, I, V, I64, V, V, V]
+            lib.fsa_rms_norm_mx.restype = I
+            lib.fsa_mx_linear.argtypes = [V, V, I, V, V, I, I64, I64, I64, V, I64, ctypes.POINTER(Options), V]
+            lib.fsa_mx_linear.restype = I
             lib.fsa_get_device_error.argtypes = [V]
             lib.fsa_get_device_error.restype = I
             lib.fsa_status_string.argtypes = [I]
@@ -627,10 +636,177 @@ def varlen_attention_fwd(q, k, v, cu_seqlens_q, cu_seqlens_k=None, *, causal: bo
     if wait_timeout_ms or debug_flags:
         opt = Options(sm_scale=sm_scale, wait_timeout_ms=wait_timeout_ms, debug_flags=debug_flags)
         _check(load().fsa_varlen_attention_fwd_ex(*args, ctypes.byref(opt), _raw_stream(dev)),
-               "fsa_varlen_attention_fwd_ex")
+               "fsa_varlen_attention_fwd_ex", "fsa_mx_pack", "fsa_mx_unpack", "fsa_rms_norm_mx", "fsa_mx_linear")
     else:
         _check(load().fsa_varlen_attention_fwd(*args, sm_scale, _raw_stream(dev)), "fsa_varlen_attention_fwd")
     return (o, lse) if return_lse else o
+
+
+# ---- products of matrices in MX formats --------------------------------------
+
+
+class MxOperand(NamedTuple):
+    """A matrix [rows, cols] in an MX format as an operand of mx_linear (layout:
+    include/fsa.h): codes uint8 [rows, ceil(cols / 128) * 64 ("mxfp4") or * 128
+    ("mxfp8")], scales uint8 [ceil(rows / 128), ceil(cols / 128), 512]."""
+    codes: torch.Tensor
+    scales: torch.Tensor
+    cols: int
+    fmt: str
+
+
+_OPERANDS = {"mxfp4": (ELEM_E2M1, 64), "mxfp8": (ELEM_E4M3, 128)}
+
+
+def _operand_format(fmt: str):
+    try:
+        return _OPERANDS[fmt]
+    except KeyError:
+        raise ValueError(f"an operand's format is mxfp4 or mxfp8, not {fmt!r}") from None
+
+
+def mx_new_operand(rows: int, cols: int, fmt: str, device="cuda") -> MxOperand:
+    """An operand whose contents are arbitrary, for mx_pack and rms_norm_mx to fill."""
+    _, width = _operand_format(fmt)
+    if rows < 0 or cols < 1:
+        raise ValueError("an operand has at least one column")
+    atoms = -(-cols // 128)
+    return MxOperand(torch.empty((rows, atoms * width), dtype=_u8, device=device),
+                     torch.empty((-(-rows // 128), atoms, 512), dtype=_u8, device=device), cols, fmt)
+
+
+def _operand(op: MxOperand, name: str, dev: int):
+    """(rows, element) of an operand, whose tensors are checked against its shape."""
+    elem, width = _operand_format(op.fmt)
+    c, s = op.codes, op.scales
+    atoms = -(-op.cols // 128)
+    rows = c.shape[0]
+    if c.dtype is not _u8 or s.dtype is not _u8 or c.get_device() != dev or s.get_device() != dev:
+        raise ValueError(f"codes and scales of {name} must be uint8 tensors on cuda:{dev}")
+    if c.shape != (rows, atoms * width) or s.shape != (-(-rows // 128), atoms, 512) or op.cols < 1:
+        raise ValueError(f"{name}: codes {list(c.shape)} and scales {list(s.shape)} are not those of {op.cols} columns "
+                         f"in {op.fmt}")
+    if not c.is_contiguous() or not s.is_contiguous():
+        raise ValueError(f"codes and scales of {name} must be contiguous")
+    return rows, elem
+
+
+def _rows(t: torch.Tensor, name: str, shape, dev: int) -> int:
+    """A CUDA bf16 tensor [rows, cols] of the given shape whose rows are contiguous;
+    returns their distance."""
+    st = t.stride()
+    if t.dtype is not _bf16 or t.shape != shape or t.get_device() != dev:
+        raise ValueError(f"{name} must be a bf16 tensor {list(shape)} on cuda:{dev}")
+    if st[1] != 1 and shape[1] > 1:
+        raise ValueError(f"the rows of {name} must be contiguous")
+    return st[0] if shape[0] > 1 else shape[1]  # (a lone row's stride is arbitrary)
+
+
+def _filled(out, shape, fmt: str, dev: int, device) -> tuple:
+    """The operand that a call fills, new or given, and its element."""
+    if out is None:
+        out = mx_new_operand(*shape, fmt, device)
+        return out, _operand_format(fmt)[0]
+    rows, elem = _operand(out, "out", dev)
+    if (rows, out.cols) != tuple(shape) or out.fmt != fmt:
+        raise ValueError(f"out must be an operand of {list(shape)} in {fmt}")
+    return out, elem
+
+
+def mx_pack(x, fmt: str = "mxfp4", *, out=None, stream=None) -> MxOperand:
+    """fsa_mx_pack: x, CUDA bf16 [rows, cols] (contiguous rows at any distance),
+    quantized into an operand of mx_linear (`out`, or a new one)."""
+    dev = x.get_device()
+    if dev < 0 or x.dim() != 2:
+        raise ValueError("x must be a CUDA tensor [rows, cols]")
+    if stream is not None or dev != _device():
+        with _on(x, stream):
+            return mx_pack(x, fmt, out=out)
+    shape = x.shape
+    stride = _rows(x, "x", shape, dev)
+    op, elem = _filled(out, shape, fmt, dev, x.device)
+    _check(load().fsa_mx_pack(x.data_ptr(), stride, shape[0], shape[1], elem, op.codes.data_ptr(), op.scales.data_ptr(),
+                              _raw_stream(dev)), "fsa_mx_pack")
+    return op
+
+
+def mx_unpack(op: MxOperand, *, out=None, stream=None):
+    """fsa_mx_unpack: an operand's values as bf16 [rows, cols]."""
+    dev = op.codes.get_device()
+    if dev < 0:
+        raise ValueError("op must be an operand on a CUDA device")
+    if stream is not None or dev != _device():
+        with _on(op.codes, stream):
+            return mx_unpack(op, out=out)
+    rows, elem = _operand(op, "op", dev)
+    shape = (rows, op.cols)
+    if out is None:
+        out, stride = torch.empty(shape, dtype=_bf16, device=op.codes.device), op.cols
+    else:
+        stride = _rows(out, "out", shape, dev)
+    _check(load().fsa_mx_unpack(op.codes.data_ptr(), op.scales.data_ptr(), rows, op.cols, elem, out.data_ptr(), stride,
+                                _raw_stream(dev)), "fsa_mx_unpack")
+    return out
+
+
+def rms_norm_mx(x, gain, *, residual=None, eps: float = 1e-6, fmt: str = "mxfp8", out=None, out_sum=None, stream=None):
+    """fsa_rms_norm_mx: the root-mean-square norm of x, CUDA bf16 [rows, cols]
+    (contiguous rows at any distance), times gain, bf16 [cols], as an operand of
+    mx_linear.  With a residual, bf16 like x, the norm is that of h = x + residual
+    (rounded to bf16), and (operand, h) is returned; out_sum, written instead of a new
+    tensor, may be x or residual itself."""
+    dev = x.get_device()
+    if dev < 0 or x.dim() != 2:
+        raise ValueError("x must be a CUDA tensor [rows, cols]")
+    if stream is not None or dev != _device():
+        with _on(x, stream):
+            return rms_norm_mx(x, gain, residual=residual, eps=eps, fmt=fmt, out=out, out_sum=out_sum)
+    shape = x.shape
+    rows, cols = shape
+    xs, rs, ss, rp, sp = _rows(x, "x", shape, dev), 0, 0, None, None
+    _plain(gain, "gain", _bf16, (cols,), dev)
+    if residual is not None:
+        rs, rp = _rows(residual, "residual", shape, dev), residual.data_ptr()
+        if out_sum is None:
+            out_sum, ss = torch.empty(shape, dtype=_bf16, device=x.device), cols
+        else:
+            ss = _rows(out_sum, "out_sum", shape, dev)
+        sp = out_sum.data_ptr()
+    elif out_sum is not None:
+        raise ValueError("there is no sum without a residual")
+    op, elem = _filled(out, shape, fmt, dev, x.device)
+    _check(load().fsa_rms_norm_mx(x.data_ptr(), xs, rp, rs, gain.data_ptr(), eps, rows, cols, elem, sp, ss,
+                                  op.codes.data_ptr(), op.scales.data_ptr(), _raw_stream(dev)), "fsa_rms_norm_mx")
+    return op if residual is None else (op, out_sum)
+
+
+def mx_linear(x: MxOperand, w: MxOperand, *, out=None, wait_timeout_ms: int = 0, debug_flags: int = 0, stream=None):
+    """fsa_mx_linear: y = x w^T of two operands, activations [T, K] and a weight [N,
+    K], as bf16 [T, N].  Formats of x and w: mxfp4 and mxfp4, mxfp8 and mxfp4, mxfp8
+    and mxfp8.  out: written instead of a new tensor (contiguous rows at any distance
+    that keeps them apart).  wait_timeout_ms: limit of the kernel's bounded waits (0:
+    2000)."""
+    dev = x.codes.get_device()
+    if dev < 0:
+        raise ValueError("x must be an operand on a CUDA device")
+    if stream is not None or dev != _device():
+        with _on(x.codes, stream):
+            return mx_linear(x, w, out=out, wait_timeout_ms=wait_timeout_ms, debug_flags=debug_flags)
+    T, ex = _operand(x, "x", dev)
+    N, ew = _operand(w, "w", dev)
+    K = x.cols
+    if w.cols != K:
+        raise ValueError(f"x has {K} columns and w {w.cols}")
+    if out is None:
+        out, stride = torch.empty((T, N), dtype=_bf16, device=x.codes.device), N
+    else:
+        stride = _rows(out, "out", (T, N), dev)
+    opt = None
+    if wait_timeout_ms or debug_flags:
+        opt = ctypes.byref(Options(wait_timeout_ms=wait_timeout_ms, debug_flags=debug_flags))
+    _check(load().fsa_mx_linear(x.codes.data_ptr(), x.scales.data_ptr(), ex, w.codes.data_ptr(), w.scales.data_ptr(), ew, T,
+                                N, K, out.data_ptr(), stride, opt, _raw_stream(dev)), "fsa_mx_linear")
+    return out
 
 
 # kinds of fsa_mma_rate_probe

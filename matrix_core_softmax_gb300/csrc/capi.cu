@@ -6,6 +6,7 @@
 
 #include "fsa.h"
 #include "fsa_internal.h"
+#include "mx_operand.cuh"
 
 namespace fsa {
 
@@ -101,6 +102,21 @@ bool make_map_heads(CUtensorMap* m, const void* base, int D, int H, int T, int64
     return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, es,
               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Codes of an operand of the MX product in boxes of 128 bytes of shared memory x
+// `box` rows; E2M1 codes stay packed, or are spread 16 to 16 bytes.
+bool make_map_mx(CUtensorMap* m, const uint8_t* codes, int64_t rows, int64_t cols, int elem, bool spread, int box) {
+    EncodeTiledFn fn = encode_tiled();
+    if (!fn) return false;
+    const int64_t pitch = mx_pitch(cols, elem);
+    cuuint64_t dims[2] = {static_cast<cuuint64_t>(spread ? 2 * pitch : pitch), static_cast<cuuint64_t>(rows)};
+    cuuint64_t strides[1] = {static_cast<cuuint64_t>(pitch)};
+    cuuint32_t boxes[2] = {128, static_cast<cuuint32_t>(box)};
+    cuuint32_t es[2] = {1, 1};
+    return fn(m, spread ? CU_TENSOR_MAP_DATA_TYPE_16U4_ALIGN16B : CU_TENSOR_MAP_DATA_TYPE_UINT8, 2,
+              const_cast<uint8_t*>(codes), dims, strides, boxes, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 size_t align256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
@@ -653,6 +669,123 @@ fsa_status fsa_varlen_attention_fwd_ex(const void* q, const void* k, const void*
     a.debug_flags = op.debug_flags;
     a.err_word = ds->err;
     return launch_varlen_attention(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? FSA_OK : FSA_ERR_CUDA;
+}
+
+namespace {
+
+// Shape and addresses of an operand of the MX product.
+fsa_status check_operand(const uint8_t* codes, const uint8_t* scales, int64_t rows, int64_t cols, int elem) {
+    if (elem == FSA_ELEM_E2M3) return FSA_ERR_UNSUPPORTED;
+    if (elem != FSA_ELEM_E4M3 && elem != FSA_ELEM_E2M1) return FSA_ERR_INVALID_ARGUMENT;
+    if (rows < 0 || rows > (1 << 30) || cols < 1 || cols > (1 << 20)) return FSA_ERR_INVALID_ARGUMENT;
+    if (rows > 0 && (!codes || !scales || (reinterpret_cast<uintptr_t>(codes) & 31) || !aligned16(scales)))
+        return FSA_ERR_INVALID_ARGUMENT;
+    return FSA_OK;
+}
+
+// Rows of bf16, `least` elements apart or more.
+bool rows_ok(const void* x, int64_t stride, int64_t least) {
+    return x && (reinterpret_cast<uintptr_t>(x) & 1) == 0 && stride >= least && stride < (int64_t{1} << 36);
+}
+
+}  // namespace
+
+fsa_status fsa_mx_pack(const void* x, int64_t x_stride, int64_t rows, int64_t cols, int elem, uint8_t* codes,
+                       uint8_t* scales, void* stream) {
+    fsa_status s = check_operand(codes, scales, rows, cols, elem);
+    if (s != FSA_OK) return s;
+    if (rows == 0) return FSA_OK;
+    if (!rows_ok(x, x_stride, 0)) return FSA_ERR_INVALID_ARGUMENT;
+    int dev;
+    DeviceState* ds;
+    s = current_device(&dev, &ds);
+    if (s != FSA_OK) return s;
+    return launch_mx_pack(x, x_stride, rows, static_cast<int>(cols), elem, codes, scales,
+                          static_cast<cudaStream_t>(stream)) == cudaSuccess ? FSA_OK : FSA_ERR_CUDA;
+}
+
+fsa_status fsa_mx_unpack(const uint8_t* codes, const uint8_t* scales, int64_t rows, int64_t cols, int elem, void* out,
+                         int64_t out_stride, void* stream) {
+    fsa_status s = check_operand(codes, scales, rows, cols, elem);
+    if (s != FSA_OK) return s;
+    if (rows == 0) return FSA_OK;
+    if (!rows_ok(out, out_stride, rows > 1 ? cols : 0)) return FSA_ERR_INVALID_ARGUMENT;
+    int dev;
+    DeviceState* ds;
+    s = current_device(&dev, &ds);
+    if (s != FSA_OK) return s;
+    return launch_mx_unpack(codes, scales, rows, static_cast<int>(cols), elem, out, out_stride,
+                            static_cast<cudaStream_t>(stream)) == cudaSuccess ? FSA_OK : FSA_ERR_CUDA;
+}
+
+fsa_status fsa_rms_norm_mx(const void* x, int64_t x_stride, const void* residual, int64_t residual_stride,
+                           const void* gain, float eps, int64_t rows, int64_t cols, int elem, void* sum,
+                           int64_t sum_stride, uint8_t* codes, uint8_t* scales, void* stream) {
+    fsa_status s = check_operand(codes, scales, rows, cols, elem);
+    if (s != FSA_OK) return s;
+    if (cols > kNormMaxCols || !std::isfinite(eps) || !(eps > 0.0f)) return FSA_ERR_INVALID_ARGUMENT;
+    if (rows == 0) return FSA_OK;
+    if (!rows_ok(x, x_stride, 0) || !rows_ok(gain, 0, 0)) return FSA_ERR_INVALID_ARGUMENT;
+    if (residual && (!rows_ok(residual, residual_stride, 0) || !rows_ok(sum, sum_stride, rows > 1 ? cols : 0)))
+        return FSA_ERR_INVALID_ARGUMENT;
+    int dev;
+    DeviceState* ds;
+    s = current_device(&dev, &ds);
+    if (s != FSA_OK) return s;
+    RmsNormMx a{};
+    a.x = x;
+    a.residual = residual;
+    a.gain = gain;
+    a.sum = sum;
+    a.x_stride = x_stride;
+    a.residual_stride = residual_stride;
+    a.sum_stride = sum_stride;
+    a.rows = rows;
+    a.cols = static_cast<int>(cols);
+    a.eps = eps;
+    a.codes = codes;
+    a.scales = scales;
+    return launch_rms_norm_mx(a, elem, static_cast<cudaStream_t>(stream)) == cudaSuccess ? FSA_OK : FSA_ERR_CUDA;
+}
+
+fsa_status fsa_mx_linear(const uint8_t* x_codes, const uint8_t* x_scales, int x_elem, const uint8_t* w_codes,
+                         const uint8_t* w_scales, int w_elem, int64_t T, int64_t N, int64_t K, void* y, int64_t y_stride,
+                         const fsa_options* opt, void* stream) {
+    const fsa_options op = opt ? *opt : fsa_options{};
+    fsa_status s = check_operand(x_codes, x_scales, T, K, x_elem);
+    if (s != FSA_OK) return s;
+    s = check_operand(w_codes, w_scales, N, K, w_elem);
+    if (s != FSA_OK) return s;
+    if (x_elem == FSA_ELEM_E2M1 && w_elem == FSA_ELEM_E4M3) return FSA_ERR_UNSUPPORTED;
+    // (128 x 128 tiles, up to eight CTAs each, number the blocks of a grid)
+    if (mx_atoms(T) * mx_atoms(N) > (1 << 27)) return FSA_ERR_INVALID_ARGUMENT;
+    if (T == 0 || N == 0) return FSA_OK;
+    if (!rows_ok(y, y_stride, T > 1 ? N : 0)) return FSA_ERR_INVALID_ARGUMENT;
+    int dev;
+    DeviceState* ds;
+    s = current_device(&dev, &ds);
+    if (s != FSA_OK) return s;
+    const MxLinearPlan plan = mx_linear_plan(static_cast<int>(T), static_cast<int>(N), static_cast<int>(K), x_elem, w_elem);
+    CUtensorMap tx, tw;
+    if (!make_map_mx(&tx, x_codes, T, K, x_elem, false, plan.x_rows) ||
+        !make_map_mx(&tw, w_codes, N, K, w_elem, w_elem == FSA_ELEM_E2M1 && x_elem == FSA_ELEM_E4M3, plan.w_rows))
+        return FSA_ERR_CUDA;
+    MxLinearLaunch a{};
+    a.tm_x = &tx;
+    a.tm_w = &tw;
+    a.xs = x_scales;
+    a.ws = w_scales;
+    a.y = y;
+    a.y_stride = y_stride;
+    a.T = static_cast<int>(T);
+    a.N = static_cast<int>(N);
+    a.K = static_cast<int>(K);
+    a.x_elem = x_elem;
+    a.w_elem = w_elem;
+    a.timeout_ns = wait_limit_ns(op);
+    a.debug_flags = op.debug_flags;
+    a.err_word = ds->err;
+    return launch_mx_linear(a, plan, static_cast<cudaStream_t>(stream)) == cudaSuccess ? FSA_OK : FSA_ERR_CUDA;
 }
 
 uint64_t fsa_attention_workspace_size(int B, int H, int S, int D, int fmt) {

@@ -159,6 +159,41 @@ struct VarlenLaunch {
 };
 cudaError_t launch_varlen_attention(const VarlenLaunch& a, cudaStream_t st);
 
+// Operands of the MX product (mx_operand.cu): E4M3 or E2M1, layout in mx_operand.cuh.
+cudaError_t launch_mx_pack(const void* x, int64_t stride, int64_t rows, int cols, int elem, uint8_t* codes, uint8_t* scales,
+                           cudaStream_t st);
+cudaError_t launch_mx_unpack(const uint8_t* codes, const uint8_t* scales, int64_t rows, int cols, int elem, void* out,
+                             int64_t stride, cudaStream_t st);
+struct RmsNormMx {
+    const void *x, *residual, *gain;  // residual: or null
+    void* sum;                        // with a residual
+    int64_t x_stride, residual_stride, sum_stride, rows;
+    int cols;
+    float eps;
+    uint8_t *codes, *scales;
+    int vec;  // which of x, residual, sum, gain have rows on 16 bytes (set by the launcher)
+};
+constexpr int kNormMaxCols = 32768;
+cudaError_t launch_rms_norm_mx(const RmsNormMx& a, int elem, cudaStream_t st);
+
+// Product of two MX operands (mx_linear.cu).
+struct MxLinearLaunch {
+    const CUtensorMap *tm_x, *tm_w;  // boxes of 128 bytes x mx_linear_plan's rows
+    const uint8_t *xs, *ws;          // scale atoms
+    void* y;                         // [T][N], y_stride elements apart
+    int64_t y_stride;
+    int T, N, K, x_elem, w_elem;
+    uint64_t timeout_ns;
+    int debug_flags;
+    unsigned int* err_word;
+};
+struct MxLinearPlan {
+    int x_rows, w_rows;  // rows of a tile: box heights of the copies
+    int split;           // CTAs of a cluster that share a tile's K
+};
+MxLinearPlan mx_linear_plan(int T, int N, int K, int x_elem, int w_elem);
+cudaError_t launch_mx_linear(const MxLinearLaunch& a, const MxLinearPlan& plan, cudaStream_t st);
+
 // Tensor-core rate probe (mma_rate.cu).
 double mma_probe_flops(int kind, int ctas, int iters);
 cudaError_t launch_mma_probe(int kind, int ctas, int iters, uint64_t timeout_ns,

@@ -1,0 +1,308 @@
+// mx_linear.cu -- y[t][n] = sum over k of x^[t][k] w^[n][k]: the product of
+// activations and weights that are both in an MX format, on the block-scaled tensor
+// cores, with FP32 sums and one rounding to bf16.
+//
+//   x E2M1, w E2M1   kind::mxf4      64 elements an instruction, both packed
+//   x E4M3, w E2M1   kind::mxf8f6f4  32 elements; the copy spreads 16 four-bit codes
+//                                    over 16 bytes of shared memory
+//   x E4M3, w E4M3   kind::mxf8f6f4
+//
+// A stage of the copy ring is 128 bytes of shared memory a row in each of them: 256
+// elements of K (two scale atoms) in the first, 128 (one) in the others, and four
+// instructions.
+#include <cuda_bf16.h>
+
+#include "fsa_internal.h"
+#include "mx_operand.cuh"
+#include "sm100_ptx.cuh"
+
+namespace fsa {
+namespace {
+
+enum Mode : int { X4W4 = 0, X8W4 = 1, X8W8 = 2 };
+
+constexpr int kThreads = 192;       // warps 0-3 output, 4 copies, 5 products
+constexpr int kWarpLoad = 4, kWarpMma = 5;
+constexpr int kMaxStages = 6;
+constexpr int kSmem = 112 * 1024;   // of a CTA's ring: two CTAs an SM
+constexpr uint32_t kTmemCols = 256; // of two CTAs: all 512
+constexpr uint32_t kColSf = 128;    // accumulator at 0, scales of stage s at 128 + 16 s
+constexpr int kPartRow = 132;       // FP32 of a token's 128 outputs in shared memory, padded
+
+struct Params {
+    const uint8_t *xs, *ws;
+    __nv_bfloat16* y;
+    int64_t y_stride;
+    int T, N, n_atoms, n_tok, split, stages, t_tiles, vec;
+    uint64_t timeout_ns;
+    unsigned int* err_word;
+    int skip;  // test use: stage 1 never arrives
+};
+
+struct Bars {
+    uint64_t full[kMaxStages], empty[kMaxStages];
+    uint64_t done;
+    uint32_t tmem_base;
+    int abort;
+};
+
+constexpr int stage_atoms(int mode) { return mode == X4W4 ? 2 : 1; }
+constexpr int stage_bytes(int mode, int n_tok) { return 128 * 128 + n_tok * 128 + 2 * stage_atoms(mode) * kAtomBytes; }
+
+__device__ __forceinline__ void raise_abort(Bars& sm, const Params& p) {
+    sm.abort = 1;
+    atomicOr(p.err_word, kErrTimeout);
+}
+
+// The weights' rows are the accumulator's lanes and the tokens its columns, so that
+// one token costs 16 columns and not 128 rows.  A CTA: 128 outputs of n_tok tokens,
+// over its part of K; the `split` CTAs of a cluster add their sums up through
+// distributed shared memory, each for its share of the outputs, in the order of
+// their ranks.
+template <int kMode>
+__global__ void __launch_bounds__(kThreads, 2)
+    mx_linear_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_w, const Params p) {
+    extern __shared__ __align__(1024) uint8_t ring[];
+    __shared__ Bars sm;
+    constexpr int kAtoms = stage_atoms(kMode);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    // (dynamic shared memory begins behind `sm`; swizzled tiles want 1024 bytes)
+    const uint32_t pad = (1024u - (smem_u32(ring) & 1023u)) & 1023u;
+    uint8_t* w_tiles = ring + pad;
+    uint8_t* x_tiles = w_tiles + p.stages * 16384;
+    uint8_t* sf_tiles = x_tiles + p.stages * p.n_tok * 128;
+
+    const int tile = blockIdx.x / p.split, rank = blockIdx.x - tile * p.split;
+    const int n_tile = tile / p.t_tiles, t_tile = tile - n_tile * p.t_tiles;
+    const int n0 = n_tile * 128, t0 = t_tile * p.n_tok;
+    const int steps = (p.n_atoms + kAtoms - 1) / kAtoms;
+    const int first = static_cast<int>(static_cast<int64_t>(steps) * rank / p.split);
+    const int last = static_cast<int>(static_cast<int64_t>(steps) * (rank + 1) / p.split);
+
+    if (tid == 0) {
+        sm.abort = 0;
+        for (int i = 0; i < p.stages; ++i) {
+            mbar_init(&sm.full[i], i == 1 && p.skip ? 2 : 1);
+            mbar_init(&sm.empty[i], 1);
+        }
+        mbar_init(&sm.done, 1);
+        fence_mbar_init();
+    }
+    if (warp == kWarpMma) {
+        tmem_alloc(&sm.tmem_base, kTmemCols);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = sm.tmem_base;
+    bool ok = true;
+
+    if (warp == kWarpLoad) {
+        // (a spread copy counts the bytes that it reads, 64 a row)
+        const uint32_t bytes = 128 * (kMode == X8W4 ? 64 : 128) + p.n_tok * 128;
+        const uint8_t* ws = p.ws + static_cast<int64_t>(n_tile) * p.n_atoms * kAtomBytes;
+        const uint8_t* xs = p.xs + static_cast<int64_t>(t0 / 128) * p.n_atoms * kAtomBytes;
+        int st = 0, issued = 0;
+        uint32_t ph = 0;
+        for (int i = first; i < last; ++i, ++issued) {
+            if (issued >= p.stages) ok = __all_sync(0xFFFFFFFFu, mbar_wait(&sm.empty[st], ph ^ 1u, p.timeout_ns, &sm.abort)) != 0;
+            if (!ok) break;
+            if (lane == 0) {
+                const uint32_t sf = min(kAtoms, p.n_atoms - i * kAtoms) * kAtomBytes;  // (the last step may hold one atom)
+                uint8_t* sf_at = sf_tiles + st * 2 * kAtoms * kAtomBytes;
+                mbar_arrive_expect_tx(&sm.full[st], bytes + 2 * sf);
+                tma_load_2d(w_tiles + st * 16384, &tm_w, &sm.full[st], i * 128, n0);
+                tma_load_2d(x_tiles + st * p.n_tok * 128, &tm_x, &sm.full[st], i * 128, t0);
+                bulk_load(sf_at, ws + static_cast<int64_t>(i) * kAtoms * kAtomBytes, sf, &sm.full[st]);
+                bulk_load(sf_at + kAtoms * kAtomBytes, xs + static_cast<int64_t>(i) * kAtoms * kAtomBytes, sf, &sm.full[st]);
+            }
+            if (++st == p.stages) {
+                st = 0;
+                ph ^= 1u;
+            }
+        }
+        if (lane == 0) {
+            if (!ok) raise_abort(sm, p);
+            // every copy lands before the CTA goes on, whoever gives up and when (in a
+            // call that ends well they have landed)
+            int dummy = 0;
+            for (int i = max(0, issued - p.stages); i < issued; ++i)
+                mbar_wait(&sm.full[i % p.stages], (i / p.stages) & 1, p.timeout_ns, &dummy);
+        }
+    } else if (warp == kWarpMma) {
+        const uint32_t tm = __shfl_sync(0xFFFFFFFFu, tmem, 0);
+        const uint64_t dw = smem_desc(smem_u32(w_tiles), 16, 1024, SWZ_128B), dx = smem_desc(smem_u32(x_tiles), 16, 1024, SWZ_128B);
+        const uint64_t dsf = smem_desc(smem_u32(sf_tiles), 0, 128, SWZ_NONE);
+        const uint32_t id = kMode == X4W4 ? idesc_mxf8f6f4(128, p.n_tok, 1, 1, 0, 0)
+                                          : idesc_mxf8f6f4(128, p.n_tok, kMode == X8W4 ? 5 : 0, 0, 0, 0);
+        int st = 0;
+        uint32_t ph = 0;
+        for (int i = first; i < last; ++i) {
+            ok = __all_sync(0xFFFFFFFFu, mbar_wait(&sm.full[st], ph, p.timeout_ns, &sm.abort)) != 0;
+            if (!ok) break;
+            tc_fence_after();
+            const uint32_t sfw = tm + kColSf + 16 * st, sfx = sfw + 4 * kAtoms;
+            const uint64_t sf = dsf + st * (2 * kAtoms * kAtomBytes >> 4);
+            const bool half = kAtoms == 2 && p.n_atoms - i * kAtoms == 1;
+#pragma unroll
+            for (int a = 0; a < kAtoms; ++a) {
+                if (a && half) break;
+                tc_cp_32x128b_x4_one(sfw + 4 * a, sf + a * (kAtomBytes >> 4));
+                tc_cp_32x128b_x4_one(sfx + 4 * a, sf + (kAtoms + a) * (kAtomBytes >> 4));
+            }
+            const uint64_t aw = dw + st * (16384 >> 4), ax = dx + st * (p.n_tok * 128 >> 4);
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk) {
+                const uint32_t acc = (i > first || kk > 0) ? 1u : 0u;
+                if constexpr (kMode == X4W4) {
+                    if (kk >= 2 && half) break;
+                    const uint32_t s = (kk & 1) * 2;  // scale bytes 0-1 or 2-3 of the atom
+                    mma_mxf4_one(tm, aw + 2 * kk, ax + 2 * kk, id | s << 4 | s << 29, sfw + 4 * (kk >> 1), sfx + 4 * (kk >> 1), acc);
+                } else {
+                    mma_mxf8f6f4_one(tm, aw + 2 * kk, ax + 2 * kk, id | kk << 4 | static_cast<uint32_t>(kk) << 29, sfw, sfx, acc);
+                }
+            }
+            tc_commit_one(&sm.empty[st]);
+            if (++st == p.stages) {
+                st = 0;
+                ph ^= 1u;
+            }
+        }
+        if (!ok && lane == 0) raise_abort(sm, p);
+        tc_commit_one(&sm.done);  // every product issued retires before its sums are read or TMEM is freed
+        int dummy = 0;
+        if (!__all_sync(0xFFFFFFFFu, mbar_wait(&sm.done, 0, p.timeout_ns, &dummy)) && lane == 0) raise_abort(sm, p);
+    }
+    // (all copies have landed: the products that read them are done, or the loader waited)
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    float* part = reinterpret_cast<float*>(w_tiles);
+    if (warp < 4) {
+        const uint32_t col = tmem + (static_cast<uint32_t>(32 * warp) << 16);
+        for (int c = 0; c < p.n_tok; c += 16) {
+            uint32_t v[16];
+            tmem_ld16(col + c, v);
+            tmem_ld_wait();
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+                asm volatile("" : "+r"(v[j]));  // (not before the wait)
+                part[(c + j) * kPartRow + tid] = __uint_as_float(v[j]);
+            }
+        }
+    }
+    tc_fence_before();
+    __syncwarp();
+    if (p.split > 1)
+        cluster_sync();
+    else
+        __syncthreads();
+    if (warp == kWarpMma) {
+        tc_fence_after();
+        tmem_dealloc(tmem, kTmemCols);
+    }
+    if (!sm.abort) {
+        // this CTA's share: 128 / split outputs of each token, four a thread
+        const int quads = 32 / p.split;
+        const int rows = min(p.n_tok, p.T - t0);
+        const uint32_t base = smem_u32(part);
+        for (int e = tid; e < rows * quads; e += kThreads) {
+            const int t = e / quads, n = 4 * (e - t * quads + rank * quads);
+            if (n0 + n >= p.N) continue;
+            float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            const uint32_t at = base + 4 * (t * kPartRow + n);
+            for (int r = 0; r < p.split; ++r) {
+                const float4 v = p.split > 1 ? ld_cluster_f4(mapa(at, r)) : *reinterpret_cast<const float4*>(part + t * kPartRow + n);
+                s = make_float4(s.x + v.x, s.y + v.y, s.z + v.z, s.w + v.w);
+            }
+            __nv_bfloat16* dst = p.y + (t0 + t) * p.y_stride + n0 + n;
+            const __nv_bfloat162 lo = __floats2bfloat162_rn(s.x, s.y), hi = __floats2bfloat162_rn(s.z, s.w);
+            if (p.vec && n0 + n + 4 <= p.N) {
+                *reinterpret_cast<uint2*>(dst) =
+                    make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
+            } else {
+                const __nv_bfloat16 v[4] = {lo.x, lo.y, hi.x, hi.y};
+                for (int j = 0; j < 4 && n0 + n + j < p.N; ++j) dst[j] = v[j];
+            }
+        }
+    }
+    __syncwarp();
+    if (p.split > 1) cluster_sync();  // no CTA leaves while another reads its sums
+}
+
+int stages_for(int mode, int n_tok) {
+    const int n = (kSmem - 1024) / stage_bytes(mode, n_tok);
+    return n < kMaxStages ? n : kMaxStages;
+}
+
+int mode_of(int x_elem, int w_elem) { return w_elem == ELEM_E4M3 ? X8W8 : x_elem == ELEM_E4M3 ? X8W4 : X4W4; }
+
+template <int kMode>
+cudaError_t launch(const MxLinearLaunch& a, const Params& p, int tiles, cudaStream_t st) {
+    static KernelSetup setup;
+    cudaError_t e = setup(reinterpret_cast<const void*>(mx_linear_kernel<kMode>), kSmem, 0);
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(static_cast<unsigned>(tiles) * p.split);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = kSmem;
+    cfg.stream = st;
+    cudaLaunchAttribute at{};
+    at.id = cudaLaunchAttributeClusterDimension;
+    at.val.clusterDim.x = p.split;
+    at.val.clusterDim.y = at.val.clusterDim.z = 1;
+    cfg.attrs = &at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, mx_linear_kernel<kMode>, *a.tm_x, *a.tm_w, p);
+}
+
+}  // namespace
+
+MxLinearPlan mx_linear_plan(int T, int N, int K, int x_elem, int w_elem) {
+    MxLinearPlan plan{};
+    plan.w_rows = 128;
+    plan.x_rows = T >= 128 ? 128 : (T + 15) / 16 * 16;
+    const int kAtoms = stage_atoms(mode_of(x_elem, w_elem));
+    const int64_t steps = (mx_atoms(K) + kAtoms - 1) / kAtoms;
+    const int64_t tiles = mx_atoms(N) * ((T + plan.x_rows - 1) / plan.x_rows);
+    // the time goes with the rounds of CTAs (two an SM) times the steps of each
+    plan.split = 1;
+    int64_t best = 0;
+    for (int s = 1; s <= 8 && s <= steps; s *= 2) {
+        const int64_t cost = ((tiles * s + 303) / 304) * ((steps + s - 1) / s);
+        if (s == 1 || cost < best) {
+            best = cost;
+            plan.split = s;
+        }
+    }
+    return plan;
+}
+
+cudaError_t launch_mx_linear(const MxLinearLaunch& a, const MxLinearPlan& plan, cudaStream_t st) {
+    const int mode = mode_of(a.x_elem, a.w_elem);
+    Params p{};
+    p.xs = a.xs;
+    p.ws = a.ws;
+    p.y = static_cast<__nv_bfloat16*>(a.y);
+    p.y_stride = a.y_stride;
+    p.T = a.T;
+    p.N = a.N;
+    p.n_atoms = static_cast<int>(mx_atoms(a.K));
+    p.n_tok = plan.x_rows;
+    p.split = plan.split;
+    p.stages = stages_for(mode, p.n_tok);
+    p.t_tiles = (a.T + p.n_tok - 1) / p.n_tok;
+    p.vec = (reinterpret_cast<uintptr_t>(a.y) & 7) == 0 && a.y_stride % 4 == 0;
+    p.timeout_ns = a.timeout_ns;
+    p.err_word = a.err_word;
+    p.skip = a.debug_flags & 1;
+    const int tiles = static_cast<int>(mx_atoms(a.N)) * p.t_tiles;
+    switch (mode) {
+        case X4W4: return launch<X4W4>(a, p, tiles, st);
+        case X8W4: return launch<X8W4>(a, p, tiles, st);
+        default: return launch<X8W8>(a, p, tiles, st);
+    }
+}
+
+}  // namespace fsa

@@ -1,0 +1,313 @@
+// mx_operand.cu -- operands of the MX product: bf16 rows quantized into one, one
+// read back as bf16, and the root-mean-square norm (with the residual's addition)
+// that writes its output as one.
+//
+// All three move each byte once and are HBM-bound at length, launch-bound for a
+// token.  A lane holds pieces of 8 elements (16 bytes of bf16), a quad a 32-element
+// block, 16 lanes the four blocks whose scales are one word of an atom; a row
+// belongs to 1 to 32 warps, by how many rows there are.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "fsa_internal.h"
+#include "mx_operand.cuh"
+#include "sm100_ptx.cuh"
+
+namespace fsa {
+namespace {
+
+constexpr int kWarps = 8;   // warps of a block, unless a row has more
+constexpr int kUnroll = 4;  // pieces that a lane has under way
+
+// Elements 8 p .. 8 p + 7 of a row, zeros from column `cols` on.  vec: the row starts
+// on 16 bytes.  (Ordinary loads: the norm's sum may replace what it reads.)
+__device__ __forceinline__ uint4 load8(const uint16_t* row, int p, int cols, bool vec) {
+    if (vec && 8 * p + 8 <= cols) return *reinterpret_cast<const uint4*>(row + 8 * p);
+    uint32_t h[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) h[i] = 8 * p + i < cols ? row[8 * p + i] : 0u;
+    return make_uint4(h[0] | h[1] << 16, h[2] | h[3] << 16, h[4] | h[5] << 16, h[6] | h[7] << 16);
+}
+
+__device__ __forceinline__ void store8(uint16_t* row, int p, int cols, bool vec, uint4 u) {
+    if (vec && 8 * p + 8 <= cols) {
+        *reinterpret_cast<uint4*>(row + 8 * p) = u;
+        return;
+    }
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        if (8 * p + i < cols) row[8 * p + i] = static_cast<uint16_t>(w[i / 2] >> (16 * (i & 1)));
+}
+
+__device__ __forceinline__ void widen(uint4 u, float (&v)[8]) {
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        v[2 * i] = __uint_as_float(w[i] << 16);
+        v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+    }
+}
+
+__device__ __forceinline__ uint32_t pair_bf16(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+// 2^lg warps a row.
+template <int kElem>
+__global__ void __launch_bounds__(32 * kWarps) mx_pack_kernel(const uint16_t* x, int64_t stride, int64_t rows, int cols, int lg,
+                                                              int vec, uint8_t* codes, uint8_t* scales) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int64_t r = blockIdx.x * static_cast<int64_t>(kWarps >> lg) + (warp >> lg);
+    if (r >= rows) return;
+    const int n_atoms = static_cast<int>(mx_atoms(cols)), step = 32 << lg;
+    const uint16_t* row = x + r * stride;
+    // whole warps: every lane takes part in the shuffles
+    for (int p0 = (warp & ((1 << lg) - 1)) * 32; p0 < 16 * n_atoms; p0 += kUnroll * step) {
+        uint4 u[kUnroll];
+#pragma unroll
+        for (int i = 0; i < kUnroll; ++i) u[i] = load8(row, p0 + i * step + lane, cols, vec);
+#pragma unroll
+        for (int i = 0; i < kUnroll; ++i) {
+            if (p0 + i * step >= 16 * n_atoms) break;
+            float v[8];
+            widen(u[i], v);
+            mx_store8<kElem>(v, r, p0 + i * step + lane, cols, n_atoms, codes, scales);
+        }
+    }
+}
+
+// Values of a piece: E2M1 and E4M3 are exact in f16, and f16 times a power of two in
+// FP32; one rounding to bf16, which only a value below bf16's normal range needs.
+template <int kElem>
+__device__ __forceinline__ uint4 values8(uint2 c, uint32_t byte) {
+    // 2^X, and 2^-127 (byte 0) as a subnormal; byte 255 is NaN
+    const float f = byte == 0 ? __uint_as_float(0x00400000u) : byte == 255 ? __uint_as_float(0x7FC00000u) : __uint_as_float(byte << 23);
+    uint32_t h[4];
+    if constexpr (kElem == ELEM_E2M1) {
+        asm("{\n.reg .b8 a, b, c, d;\n"
+            "mov.b32 {a, b, c, d}, %4;\n"
+            "cvt.rn.f16x2.e2m1x2 %0, a;\n"
+            "cvt.rn.f16x2.e2m1x2 %1, b;\n"
+            "cvt.rn.f16x2.e2m1x2 %2, c;\n"
+            "cvt.rn.f16x2.e2m1x2 %3, d;\n}"
+            : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3]) : "r"(c.x));
+    } else {
+        asm("{\n.reg .b16 a, b, c, d;\n"
+            "mov.b32 {a, b}, %4;\n"
+            "mov.b32 {c, d}, %5;\n"
+            "cvt.rn.f16x2.e4m3x2 %0, a;\n"
+            "cvt.rn.f16x2.e4m3x2 %1, b;\n"
+            "cvt.rn.f16x2.e4m3x2 %2, c;\n"
+            "cvt.rn.f16x2.e4m3x2 %3, d;\n}"
+            : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3]) : "r"(c.x), "r"(c.y));
+    }
+    uint32_t o[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&h[i]));
+        o[i] = pair_bf16(v.x * f, v.y * f);
+    }
+    return make_uint4(o[0], o[1], o[2], o[3]);
+}
+
+template <int kElem>
+__global__ void __launch_bounds__(32 * kWarps) mx_unpack_kernel(const uint8_t* __restrict__ codes, const uint8_t* __restrict__ scales,
+                                                                int64_t rows, int cols, int lg, int vec, uint16_t* __restrict__ out,
+                                                                int64_t stride) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int64_t r = blockIdx.x * static_cast<int64_t>(kWarps >> lg) + (warp >> lg);
+    if (r >= rows) return;
+    const int n_atoms = static_cast<int>(mx_atoms(cols)), step = 32 << lg;
+    uint16_t* row = out + r * stride;
+    for (int p0 = (warp & ((1 << lg) - 1)) * 32 + lane; p0 < 16 * n_atoms; p0 += kUnroll * step) {
+        uint2 c[kUnroll];
+        uint32_t s[kUnroll];
+#pragma unroll
+        for (int i = 0; i < kUnroll; ++i) {
+            const int p = p0 + i * step;
+            c[i] = make_uint2(0u, 0u);
+            s[i] = 127u;
+            if (p < 16 * n_atoms) {
+                const uint8_t* src = codes + (r * n_atoms * 16 + p) * MxElem<kElem>::piece_bytes;
+                if constexpr (kElem == ELEM_E2M1)
+                    c[i].x = __ldg(reinterpret_cast<const uint32_t*>(src));
+                else
+                    c[i] = __ldg(reinterpret_cast<const uint2*>(src));
+                s[i] = __ldg(scales + mx_scale_word(r, p >> 4, n_atoms) + ((p >> 2) & 3));
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < kUnroll; ++i) {
+            const int p = p0 + i * step;
+            if (8 * p < cols) store8(row, p, cols, vec, values8<kElem>(c[i], s[i]));
+        }
+    }
+}
+
+// y = h / sqrt(mean(h^2) + eps) g of the sum h = bf16(x + residual), or of h = x,
+// quantized.  A row's h stays in registers (bf16, as it is stored) between the sum
+// of its squares and its output, so x and the residual are read once.  kV pieces a
+// lane, 2^lg warps a row; kWide: a block of 32 warps for one row.
+template <int kElem, int kV, bool kWide>
+__global__ void __launch_bounds__(kWide ? 1024 : 512) rms_norm_mx_kernel(const RmsNormMx a, int lg) {
+    __shared__ double part[32];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, n_warps = blockDim.x >> 5;
+    const int64_t r = blockIdx.x * static_cast<int64_t>(n_warps >> lg) + (warp >> lg);
+    const int first = (warp & ((1 << lg) - 1)) * 32 + lane, step = 32 << lg;
+    const int n_atoms = static_cast<int>(mx_atoms(a.cols));
+    const bool row = r < a.rows;  // (a warp without a row still meets the others at the barriers)
+    uint4 h[kV];
+    const uint16_t* x = static_cast<const uint16_t*>(a.x) + r * a.x_stride;
+#pragma unroll
+    for (int i = 0; i < kV; ++i) h[i] = row ? load8(x, first + i * step, a.cols, a.vec & 1) : make_uint4(0, 0, 0, 0);
+    if (a.residual) {
+        const uint16_t* res = static_cast<const uint16_t*>(a.residual) + r * a.residual_stride;
+        uint4 d[kV];
+#pragma unroll
+        for (int i = 0; i < kV; ++i) d[i] = row ? load8(res, first + i * step, a.cols, a.vec & 2) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+        for (int i = 0; i < kV; ++i) {
+            float u[8], v[8];
+            widen(h[i], u);
+            widen(d[i], v);
+            h[i] = make_uint4(pair_bf16(u[0] + v[0], u[1] + v[1]), pair_bf16(u[2] + v[2], u[3] + v[3]),
+                              pair_bf16(u[4] + v[4], u[5] + v[5]), pair_bf16(u[6] + v[6], u[7] + v[7]));
+        }
+        if (row) {
+            uint16_t* sum = static_cast<uint16_t*>(a.sum) + r * a.sum_stride;
+#pragma unroll
+            for (int i = 0; i < kV; ++i)
+                if (8 * (first + i * step) < a.cols) store8(sum, first + i * step, a.cols, a.vec & 4, h[i]);
+        }
+    }
+    // sum over the row's warps, the same in each of them
+    auto over_row = [&](auto s) {
+#pragma unroll
+        for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
+        if (lg > 0) {
+            __syncthreads();
+            if (lane == 0) part[warp] = static_cast<double>(s);
+            __syncthreads();
+            const int w0 = warp & ~((1 << lg) - 1);
+            s = 0;
+            for (int w = 0; w < 1 << lg; ++w) s += static_cast<decltype(s)>(part[w0 + w]);
+        }
+        return s;
+    };
+    float s = 0.0f;
+#pragma unroll
+    for (int i = 0; i < kV; ++i) {
+        float v[8];
+        widen(h[i], v);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) s = __fmaf_rn(v[j], v[j], s);
+    }
+    s = over_row(s);
+    const float inv = 1.0f / sqrtf(s / static_cast<float>(a.cols) + a.eps);
+    // squares beyond FP32, or lost below it where no larger eps covers them: rare, and
+    // in 64 bits (all warps of a block go the same way through the barriers)
+    const bool far = !(s <= 1e36f) || (s < 1e-25f && a.eps < 1e-12f);
+    double inv_far = 0.0;
+    if (__syncthreads_or(far)) {
+        double t = 0.0;
+#pragma unroll
+        for (int i = 0; i < kV; ++i) {
+            float v[8];
+            widen(h[i], v);
+#pragma unroll 1
+            for (int j = 0; j < 8; ++j) t += static_cast<double>(v[j]) * v[j];
+        }
+        t = over_row(t);
+        inv_far = 1.0 / sqrt(t / a.cols + static_cast<double>(a.eps));
+    }
+    if (!row) return;
+#pragma unroll
+    for (int i = 0; i < kV; ++i) {
+        const int p = first + i * step;
+        if (p - lane >= 16 * n_atoms) break;  // (the whole warp is behind the row's end)
+        float v[8], g[8];
+        widen(h[i], v);
+        widen(load8(static_cast<const uint16_t*>(a.gain), p, a.cols, a.vec & 8), g);
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            v[j] = (far ? static_cast<float>(v[j] * inv_far) : v[j] * inv) * g[j];
+        mx_store8<kElem>(v, r, p, a.cols, n_atoms, a.codes, a.scales);
+    }
+}
+
+// log2 of the warps for a row of `pieces` pieces, so that `rows` rows fill the GPU
+// (152 SMs x 32 warps) as far as the row has work for them.
+int warps_log2(int64_t rows, int64_t pieces, int most) {
+    int lg = 0;
+    while (lg < most && (rows << lg) < 152 * 32 && (int64_t{64} << lg) <= pieces) ++lg;
+    return lg;
+}
+
+bool starts_on_16(const void* p, int64_t stride) {
+    return (reinterpret_cast<uintptr_t>(p) & 15) == 0 && stride % 8 == 0;
+}
+
+template <int kElem, int kV>
+cudaError_t norm_launch(const RmsNormMx& a, int lg, cudaStream_t st) {
+    const int warps = 1 << lg > kWarps ? 1 << lg : kWarps;
+    const int64_t per = warps >> lg;
+    const unsigned grid = static_cast<unsigned>((a.rows + per - 1) / per);
+    if constexpr (kV <= 4)
+        if (lg == 5) {
+            rms_norm_mx_kernel<kElem, kV, true><<<grid, 32 * warps, 0, st>>>(a, lg);
+            return cudaGetLastError();
+        }
+    rms_norm_mx_kernel<kElem, kV, false><<<grid, 32 * warps, 0, st>>>(a, lg);
+    return cudaGetLastError();
+}
+
+template <int kElem>
+cudaError_t norm_pieces(const RmsNormMx& a, int lg, int v, cudaStream_t st) {
+    switch (v) {
+        case 1: return norm_launch<kElem, 1>(a, lg, st);
+        case 2: return norm_launch<kElem, 2>(a, lg, st);
+        case 3: return norm_launch<kElem, 3>(a, lg, st);
+        case 4: return norm_launch<kElem, 4>(a, lg, st);
+        default: return norm_launch<kElem, 5>(a, lg, st);
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_mx_pack(const void* x, int64_t stride, int64_t rows, int cols, int elem, uint8_t* codes, uint8_t* scales,
+                           cudaStream_t st) {
+    const int lg = warps_log2(rows, 16 * mx_atoms(cols), 3);
+    const unsigned grid = static_cast<unsigned>((rows + (kWarps >> lg) - 1) / (kWarps >> lg));
+    auto kernel = elem == ELEM_E2M1 ? mx_pack_kernel<ELEM_E2M1> : mx_pack_kernel<ELEM_E4M3>;
+    kernel<<<grid, 32 * kWarps, 0, st>>>(static_cast<const uint16_t*>(x), stride, rows, cols, lg, starts_on_16(x, stride), codes,
+                                         scales);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_mx_unpack(const uint8_t* codes, const uint8_t* scales, int64_t rows, int cols, int elem, void* out,
+                             int64_t stride, cudaStream_t st) {
+    const int lg = warps_log2(rows, 16 * mx_atoms(cols), 3);
+    const unsigned grid = static_cast<unsigned>((rows + (kWarps >> lg) - 1) / (kWarps >> lg));
+    auto kernel = elem == ELEM_E2M1 ? mx_unpack_kernel<ELEM_E2M1> : mx_unpack_kernel<ELEM_E4M3>;
+    kernel<<<grid, 32 * kWarps, 0, st>>>(codes, scales, rows, cols, lg, starts_on_16(out, stride), static_cast<uint16_t*>(out),
+                                         stride);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_rms_norm_mx(const RmsNormMx& args, int elem, cudaStream_t st) {
+    RmsNormMx a = args;
+    a.vec = starts_on_16(a.x, a.x_stride) | starts_on_16(a.residual, a.residual_stride) << 1 |
+            starts_on_16(a.sum, a.sum_stride) << 2 | starts_on_16(a.gain, 0) << 3;
+    // up to five pieces a lane where the rows alone fill the GPU, fewer where they do
+    // not; 32 warps take four, which is all of the 32768 columns a row may have
+    const int64_t pieces = 16 * mx_atoms(a.cols);
+    int lg = warps_log2(a.rows, pieces, 5);
+    while (lg < 5 && (int64_t{5} * 32 << lg) < pieces) ++lg;
+    const int v = static_cast<int>((pieces + (32 << lg) - 1) / (32 << lg));
+    return elem == ELEM_E2M1 ? norm_pieces<ELEM_E2M1>(a, lg, v, st) : norm_pieces<ELEM_E4M3>(a, lg, v, st);
+}
+
+}  // namespace fsa

@@ -171,7 +171,7 @@ struct RmsNormMx {
     int cols;
     float eps;
     uint8_t *codes, *scales;
-    int vec;  // which of x, residual, sum, gain have rows on 16 bytes (set by the launcher)
+    int x_align, residual_align, sum_align, gain_align;  // bytes that rows start on (set by the launcher)
 };
 constexpr int kNormMaxCols = 32768;
 cudaError_t launch_rms_norm_mx(const RmsNormMx& a, int elem, cudaStream_t st);

@@ -19,20 +19,44 @@ namespace {
 constexpr int kWarps = 8;   // warps of a block, unless a row has more
 constexpr int kUnroll = 4;  // pieces that a lane has under way
 
-// Elements 8 p .. 8 p + 7 of a row, zeros from column `cols` on.  vec: the row starts
-// on 16 bytes.  (Ordinary loads: the norm's sum may replace what it reads.)
-__device__ __forceinline__ uint4 load8(const uint16_t* row, int p, int cols, bool vec) {
-    if (vec && 8 * p + 8 <= cols) return *reinterpret_cast<const uint4*>(row + 8 * p);
+// Elements 8 p .. 8 p + 7 of a row that starts on `align` (16, 8, 4 or 2) bytes, zeros
+// from column `cols` on.  (Ordinary loads: the norm's sum may replace what it reads.)
+__device__ __forceinline__ uint4 load8(const uint16_t* row, int p, int cols, int align) {
+    if (8 * p + 8 <= cols) {
+        const uint16_t* src = row + 8 * p;
+        if (align == 16) return *reinterpret_cast<const uint4*>(src);
+        if (align == 8) {
+            const uint2 a = *reinterpret_cast<const uint2*>(src), b = *reinterpret_cast<const uint2*>(src + 4);
+            return make_uint4(a.x, a.y, b.x, b.y);
+        }
+        if (align == 4) {
+            const uint32_t* w = reinterpret_cast<const uint32_t*>(src);
+            return make_uint4(w[0], w[1], w[2], w[3]);
+        }
+    }
     uint32_t h[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) h[i] = 8 * p + i < cols ? row[8 * p + i] : 0u;
     return make_uint4(h[0] | h[1] << 16, h[2] | h[3] << 16, h[4] | h[5] << 16, h[6] | h[7] << 16);
 }
 
-__device__ __forceinline__ void store8(uint16_t* row, int p, int cols, bool vec, uint4 u) {
-    if (vec && 8 * p + 8 <= cols) {
-        *reinterpret_cast<uint4*>(row + 8 * p) = u;
-        return;
+__device__ __forceinline__ void store8(uint16_t* row, int p, int cols, int align, uint4 u) {
+    if (8 * p + 8 <= cols) {
+        uint16_t* dst = row + 8 * p;
+        if (align == 16) {
+            *reinterpret_cast<uint4*>(dst) = u;
+            return;
+        }
+        if (align == 8) {
+            reinterpret_cast<uint2*>(dst)[0] = make_uint2(u.x, u.y);
+            reinterpret_cast<uint2*>(dst)[1] = make_uint2(u.z, u.w);
+            return;
+        }
+        if (align == 4) {
+            uint32_t* w = reinterpret_cast<uint32_t*>(dst);
+            w[0] = u.x, w[1] = u.y, w[2] = u.z, w[3] = u.w;
+            return;
+        }
     }
     const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
@@ -58,7 +82,7 @@ __device__ __forceinline__ uint32_t pair_bf16(float lo, float hi) {
 // 2^lg warps a row.
 template <int kElem>
 __global__ void __launch_bounds__(32 * kWarps) mx_pack_kernel(const uint16_t* x, int64_t stride, int64_t rows, int cols, int lg,
-                                                              int vec, uint8_t* codes, uint8_t* scales) {
+                                                              int align, uint8_t* codes, uint8_t* scales) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int64_t r = blockIdx.x * static_cast<int64_t>(kWarps >> lg) + (warp >> lg);
     if (r >= rows) return;
@@ -68,7 +92,7 @@ __global__ void __launch_bounds__(32 * kWarps) mx_pack_kernel(const uint16_t* x,
     for (int p0 = (warp & ((1 << lg) - 1)) * 32; p0 < 16 * n_atoms; p0 += kUnroll * step) {
         uint4 u[kUnroll];
 #pragma unroll
-        for (int i = 0; i < kUnroll; ++i) u[i] = load8(row, p0 + i * step + lane, cols, vec);
+        for (int i = 0; i < kUnroll; ++i) u[i] = load8(row, p0 + i * step + lane, cols, align);
 #pragma unroll
         for (int i = 0; i < kUnroll; ++i) {
             if (p0 + i * step >= 16 * n_atoms) break;
@@ -115,7 +139,7 @@ __device__ __forceinline__ uint4 values8(uint2 c, uint32_t byte) {
 
 template <int kElem>
 __global__ void __launch_bounds__(32 * kWarps) mx_unpack_kernel(const uint8_t* __restrict__ codes, const uint8_t* __restrict__ scales,
-                                                                int64_t rows, int cols, int lg, int vec, uint16_t* __restrict__ out,
+                                                                int64_t rows, int cols, int lg, int align, uint16_t* __restrict__ out,
                                                                 int64_t stride) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int64_t r = blockIdx.x * static_cast<int64_t>(kWarps >> lg) + (warp >> lg);
@@ -142,7 +166,7 @@ __global__ void __launch_bounds__(32 * kWarps) mx_unpack_kernel(const uint8_t* _
 #pragma unroll
         for (int i = 0; i < kUnroll; ++i) {
             const int p = p0 + i * step;
-            if (8 * p < cols) store8(row, p, cols, vec, values8<kElem>(c[i], s[i]));
+            if (8 * p < cols) store8(row, p, cols, align, values8<kElem>(c[i], s[i]));
         }
     }
 }
@@ -153,7 +177,7 @@ __global__ void __launch_bounds__(32 * kWarps) mx_unpack_kernel(const uint8_t* _
 // lane, 2^lg warps a row; kWide: a block of 32 warps for one row.
 template <int kElem, int kV, bool kWide>
 __global__ void __launch_bounds__(kWide ? 1024 : 512) rms_norm_mx_kernel(const RmsNormMx a, int lg) {
-    __shared__ double part[32];
+    __shared__ float part[2][32];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, n_warps = blockDim.x >> 5;
     const int64_t r = blockIdx.x * static_cast<int64_t>(n_warps >> lg) + (warp >> lg);
     const int first = (warp & ((1 << lg) - 1)) * 32 + lane, step = 32 << lg;
@@ -162,12 +186,12 @@ __global__ void __launch_bounds__(kWide ? 1024 : 512) rms_norm_mx_kernel(const R
     uint4 h[kV];
     const uint16_t* x = static_cast<const uint16_t*>(a.x) + r * a.x_stride;
 #pragma unroll
-    for (int i = 0; i < kV; ++i) h[i] = row ? load8(x, first + i * step, a.cols, a.vec & 1) : make_uint4(0, 0, 0, 0);
+    for (int i = 0; i < kV; ++i) h[i] = row ? load8(x, first + i * step, a.cols, a.x_align) : make_uint4(0, 0, 0, 0);
     if (a.residual) {
         const uint16_t* res = static_cast<const uint16_t*>(a.residual) + r * a.residual_stride;
         uint4 d[kV];
 #pragma unroll
-        for (int i = 0; i < kV; ++i) d[i] = row ? load8(res, first + i * step, a.cols, a.vec & 2) : make_uint4(0, 0, 0, 0);
+        for (int i = 0; i < kV; ++i) d[i] = row ? load8(res, first + i * step, a.cols, a.residual_align) : make_uint4(0, 0, 0, 0);
 #pragma unroll
         for (int i = 0; i < kV; ++i) {
             float u[8], v[8];
@@ -180,60 +204,69 @@ __global__ void __launch_bounds__(kWide ? 1024 : 512) rms_norm_mx_kernel(const R
             uint16_t* sum = static_cast<uint16_t*>(a.sum) + r * a.sum_stride;
 #pragma unroll
             for (int i = 0; i < kV; ++i)
-                if (8 * (first + i * step) < a.cols) store8(sum, first + i * step, a.cols, a.vec & 4, h[i]);
+                if (8 * (first + i * step) < a.cols) store8(sum, first + i * step, a.cols, a.sum_align, h[i]);
         }
     }
-    // sum over the row's warps, the same in each of them
-    auto over_row = [&](auto s) {
+    uint4 g[kV];  // (asked for ahead of the row's sum)
 #pragma unroll
-        for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
+    for (int i = 0; i < kV; ++i) g[i] = load8(static_cast<const uint16_t*>(a.gain), first + i * step, a.cols, a.gain_align);
+    // sum (or maximum) over the row's warps, the same in each of them
+    auto over_row = [&](float s, bool most, float* part) {
+#pragma unroll
+        for (int o = 16; o; o >>= 1) {
+            const float other = __shfl_xor_sync(0xFFFFFFFFu, s, o);
+            s = most ? fmaxf(s, other) : s + other;
+        }
         if (lg > 0) {
-            __syncthreads();
-            if (lane == 0) part[warp] = static_cast<double>(s);
+            if (lane == 0) part[warp] = s;
             __syncthreads();
             const int w0 = warp & ~((1 << lg) - 1);
-            s = 0;
-            for (int w = 0; w < 1 << lg; ++w) s += static_cast<decltype(s)>(part[w0 + w]);
+            s = 0.0f;
+            for (int w = 0; w < 1 << lg; ++w) s = most ? fmaxf(s, part[w0 + w]) : s + part[w0 + w];
         }
         return s;
     };
-    float s = 0.0f;
-#pragma unroll
-    for (int i = 0; i < kV; ++i) {
-        float v[8];
-        widen(h[i], v);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) s = __fmaf_rn(v[j], v[j], s);
-    }
-    s = over_row(s);
-    const float inv = 1.0f / sqrtf(s / static_cast<float>(a.cols) + a.eps);
-    // squares beyond FP32, or lost below it where no larger eps covers them: rare, and
-    // in 64 bits (all warps of a block go the same way through the barriers)
-    const bool far = !(s <= 1e36f) || (s < 1e-25f && a.eps < 1e-12f);
-    double inv_far = 0.0;
-    if (__syncthreads_or(far)) {
-        double t = 0.0;
+    auto squares = [&](float f) {
+        float s = 0.0f;
 #pragma unroll
         for (int i = 0; i < kV; ++i) {
             float v[8];
             widen(h[i], v);
-#pragma unroll 1
-            for (int j = 0; j < 8; ++j) t += static_cast<double>(v[j]) * v[j];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) s = __fmaf_rn(v[j] * f, v[j] * f, s);
         }
-        t = over_row(t);
-        inv_far = 1.0 / sqrt(t / a.cols + static_cast<double>(a.eps));
+        return over_row(s, false, part[0]);
+    };
+    // y = (h f) inv g with f = 1, except where squares leave FP32 (or get lost below it and
+    // no larger eps covers them): there f is the power of two that brings the larger of
+    // the row's maximum and sqrt(eps) next to 1.  (Every warp of a block goes the same way
+    // through the barriers.)
+    float f = 1.0f, s = squares(1.0f);
+    const bool far = !(s <= 1e36f) || (s < 1e-25f && a.eps < 1e-12f);
+    if (__syncthreads_or(far)) {
+        float m = 0.0f;
+#pragma unroll
+        for (int i = 0; i < kV; ++i) {
+            float v[8];
+            widen(h[i], v);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) m = fmaxf(m, fabsf(v[j]));
+        }
+        m = fmaxf(over_row(m, true, part[1]), sqrtf(a.eps));
+        if (far) f = __uint_as_float((254u - min(__float_as_uint(m) >> 23, 253u)) << 23);
+        s = squares(f);
     }
+    const float inv = 1.0f / sqrtf(s / static_cast<float>(a.cols) + a.eps * f * f);
     if (!row) return;
 #pragma unroll
     for (int i = 0; i < kV; ++i) {
         const int p = first + i * step;
         if (p - lane >= 16 * n_atoms) break;  // (the whole warp is behind the row's end)
-        float v[8], g[8];
+        float v[8], w[8];
         widen(h[i], v);
-        widen(load8(static_cast<const uint16_t*>(a.gain), p, a.cols, a.vec & 8), g);
+        widen(g[i], w);
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-            v[j] = (far ? static_cast<float>(v[j] * inv_far) : v[j] * inv) * g[j];
+        for (int j = 0; j < 8; ++j) v[j] = v[j] * f * inv * w[j];
         mx_store8<kElem>(v, r, p, a.cols, n_atoms, a.codes, a.scales);
     }
 }
@@ -246,8 +279,10 @@ int warps_log2(int64_t rows, int64_t pieces, int most) {
     return lg;
 }
 
-bool starts_on_16(const void* p, int64_t stride) {
-    return (reinterpret_cast<uintptr_t>(p) & 15) == 0 && stride % 8 == 0;
+// The largest of 16, 8, 4 and 2 bytes on which all rows start.
+int row_align(const void* p, int64_t stride) {
+    const uintptr_t bits = reinterpret_cast<uintptr_t>(p) | static_cast<uintptr_t>(2 * stride) | 16;
+    return static_cast<int>(bits & -bits);
 }
 
 template <int kElem, int kV>
@@ -282,7 +317,7 @@ cudaError_t launch_mx_pack(const void* x, int64_t stride, int64_t rows, int cols
     const int lg = warps_log2(rows, 16 * mx_atoms(cols), 3);
     const unsigned grid = static_cast<unsigned>((rows + (kWarps >> lg) - 1) / (kWarps >> lg));
     auto kernel = elem == ELEM_E2M1 ? mx_pack_kernel<ELEM_E2M1> : mx_pack_kernel<ELEM_E4M3>;
-    kernel<<<grid, 32 * kWarps, 0, st>>>(static_cast<const uint16_t*>(x), stride, rows, cols, lg, starts_on_16(x, stride), codes,
+    kernel<<<grid, 32 * kWarps, 0, st>>>(static_cast<const uint16_t*>(x), stride, rows, cols, lg, row_align(x, stride), codes,
                                          scales);
     return cudaGetLastError();
 }
@@ -292,15 +327,17 @@ cudaError_t launch_mx_unpack(const uint8_t* codes, const uint8_t* scales, int64_
     const int lg = warps_log2(rows, 16 * mx_atoms(cols), 3);
     const unsigned grid = static_cast<unsigned>((rows + (kWarps >> lg) - 1) / (kWarps >> lg));
     auto kernel = elem == ELEM_E2M1 ? mx_unpack_kernel<ELEM_E2M1> : mx_unpack_kernel<ELEM_E4M3>;
-    kernel<<<grid, 32 * kWarps, 0, st>>>(codes, scales, rows, cols, lg, starts_on_16(out, stride), static_cast<uint16_t*>(out),
+    kernel<<<grid, 32 * kWarps, 0, st>>>(codes, scales, rows, cols, lg, row_align(out, stride), static_cast<uint16_t*>(out),
                                          stride);
     return cudaGetLastError();
 }
 
 cudaError_t launch_rms_norm_mx(const RmsNormMx& args, int elem, cudaStream_t st) {
     RmsNormMx a = args;
-    a.vec = starts_on_16(a.x, a.x_stride) | starts_on_16(a.residual, a.residual_stride) << 1 |
-            starts_on_16(a.sum, a.sum_stride) << 2 | starts_on_16(a.gain, 0) << 3;
+    a.x_align = row_align(a.x, a.x_stride);
+    a.residual_align = row_align(a.residual, a.residual_stride);
+    a.sum_align = row_align(a.sum, a.sum_stride);
+    a.gain_align = row_align(a.gain, 0);
     // up to five pieces a lane where the rows alone fill the GPU, fewer where they do
     // not; 32 warps take four, which is all of the 32768 columns a row may have
     const int64_t pieces = 16 * mx_atoms(a.cols);

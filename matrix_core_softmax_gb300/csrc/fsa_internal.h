@@ -189,7 +189,7 @@ struct MxLinearLaunch {
 };
 struct MxLinearPlan {
     int x_rows, w_rows;  // rows of a tile: box heights of the copies
-    int split;           // CTAs of a cluster that share a tile's K
+    int split;           // CTAs of a cluster that share a tile's K; 0: pairs of CTAs
 };
 MxLinearPlan mx_linear_plan(int T, int N, int K, int x_elem, int w_elem);
 cudaError_t launch_mx_linear(const MxLinearLaunch& a, const MxLinearPlan& plan, cudaStream_t st);

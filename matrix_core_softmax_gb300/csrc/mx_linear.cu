@@ -231,6 +231,301 @@ __global__ void __launch_bounds__(kThreads, 2)
     if (p.split > 1) cluster_sync();  // no CTA leaves while another reads its sums
 }
 
+// ---- many tokens: pairs of CTAs --------------------------------------------
+// Tokens are the accumulator's lanes here, so that a thread of the output holds
+// neighbouring outputs of one token.  A pair of CTAs works on 256 tokens x 256
+// outputs: each has 128 tokens' rows and half of the weights' in its shared memory
+// and its tokens' sums in its tensor memory, so a step brings an SM 32 KB of codes for
+// as many operations as a 128 x 128 tile's for half of them.
+// warps 0-7 output, 8 copies of codes, 10 of scales (one warp for both held the products
+// up: five copies a step take 560 clocks to issue, a step's products 640 to 730), 9 the
+// products (rank 0) or word of its copies (rank 1)
+constexpr int kPairThreads = 352;
+constexpr int kPairLoad = 8, kPairMma = 9, kPairLoadSf = 10;
+constexpr int kPairStages = 6;
+constexpr uint32_t kPairCols = 512;
+constexpr uint32_t kPairSf = 256;   // accumulator at 0, scales of stage s at 256 + 24 s
+constexpr int kPairGroup = 8;       // token tiles that are walked side by side
+
+struct PairBars {
+    uint64_t full[kPairStages], empty[kPairStages];
+    uint64_t peer[kPairStages];     // rank 0: the other CTA's copies of a stage have landed
+    uint64_t acc_full, acc_empty;   // (acc_empty: rank 0's, an arrival a warp of both CTAs' output)
+    uint64_t drain;
+    uint32_t tmem_base;
+    int abort;
+};
+
+constexpr int pair_stage_bytes(int mode) { return 2 * 128 * 128 + 3 * stage_atoms(mode) * kAtomBytes; }
+constexpr int kOutBytes = 8 * 32 * 64;  // per output warp: 32 rows x 32 outputs on their way
+constexpr int pair_smem(int mode) { return kPairStages * pair_stage_bytes(mode) + kOutBytes + static_cast<int>(sizeof(PairBars)); }
+static_assert(pair_smem(X4W4) <= 232448, "shared memory beyond the 227 KB a CTA may use");
+
+struct PairParams {
+    const uint8_t *xs, *ws;
+    __nv_bfloat16* y;
+    int64_t y_stride;
+    int T, N, n_atoms, t_tiles, n_tiles, vec;
+    uint64_t timeout_ns;
+    unsigned int* err_word;
+    int skip;
+};
+
+// Token and output tile of number i: groups of kPairGroup token tiles, in a group
+// token tiles first, so that the pairs at work share a square of the product.
+__device__ __forceinline__ void pair_tile(const PairParams& p, int i, int& t_tile, int& n_tile) {
+    const int per = kPairGroup * p.n_tiles, group = i / per, in = i - group * per;
+    const int width = min(kPairGroup, p.t_tiles - group * kPairGroup);
+    n_tile = in / width;
+    t_tile = group * kPairGroup + in - n_tile * width;
+}
+
+template <int kMode>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
+    mx_linear_pair_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_w, const PairParams p) {
+    extern __shared__ __align__(1024) uint8_t ring[];
+    // the 128-byte-swizzled tiles need a 1024-byte aligned base (the same in both CTAs)
+    if (smem_u32(ring) & 1023u) {
+        if (threadIdx.x == 0) atomicOr(p.err_word, kErrMisaligned);
+        return;
+    }
+    constexpr int kAtoms = stage_atoms(kMode), kSf = 3 * kAtoms * kAtomBytes;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const uint32_t rank = cluster_ctarank();
+    const int first_tile = blockIdx.x >> 1, tile_step = gridDim.x >> 1, tiles = p.t_tiles * p.n_tiles;
+    const int steps = (p.n_atoms + kAtoms - 1) / kAtoms;
+    uint8_t* x_tiles = ring;
+    uint8_t* w_tiles = x_tiles + kPairStages * 16384;
+    uint8_t* sf_tiles = w_tiles + kPairStages * 16384;
+    uint4* out = reinterpret_cast<uint4*>(sf_tiles + kPairStages * kSf);
+    PairBars& sm = *reinterpret_cast<PairBars*>(out + kOutBytes / 16);
+
+    if (tid == 0) {
+        sm.abort = 0;
+        for (int i = 0; i < kPairStages; ++i) {
+            mbar_init(&sm.full[i], i == 1 && p.skip ? 3 : 2);
+            mbar_init(&sm.empty[i], 1);
+            mbar_init(&sm.peer[i], 1);
+        }
+        mbar_init(&sm.acc_full, 1);
+        mbar_init(&sm.acc_empty, 16);
+        mbar_init(&sm.drain, 1);
+        fence_mbar_init();
+    }
+    if (warp == kPairMma) pair_tmem_alloc(&sm.tmem_base, kPairCols);
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync();  // both CTAs' barriers are there
+    tc_fence_after();
+    const uint32_t tmem = sm.tmem_base;
+    auto give_up = [&] {
+        sm.abort = 1;
+        atomicOr(p.err_word, kErrTimeout);
+    };
+    auto wait = [&](uint64_t* bar, uint32_t phase) {
+        return __all_sync(0xFFFFFFFFu, mbar_wait(bar, phase & 1u, p.timeout_ns, &sm.abort)) != 0;
+    };
+    auto wait_pair = [&](uint64_t* bar, uint32_t phase) {
+        return __all_sync(0xFFFFFFFFu, mbar_wait_cluster(bar, phase & 1u, p.timeout_ns, &sm.abort)) != 0;
+    };
+    bool ok = true;
+    int st = 0;       // stage and its phase, in step in all roles
+    uint32_t ph = 0;
+    auto advance = [&] {
+        if (++st == kPairStages) {
+            st = 0;
+            ph ^= 1u;
+        }
+    };
+
+    if (warp == kPairLoad || warp == kPairLoadSf) {
+        const int64_t x_groups = mx_atoms(p.T), w_groups = mx_atoms(p.N);
+        int issued = 0;
+        for (int i = first_tile; ok && i < tiles; i += tile_step) {
+            int t_tile, n_tile;
+            pair_tile(p, i, t_tile, n_tile);
+            const int t0 = 256 * t_tile + 128 * static_cast<int>(rank), n0 = 256 * n_tile + 128 * static_cast<int>(rank);
+            // scale rows that there are: this CTA's tokens, all of the tile's outputs
+            const int64_t xg = t0 / 128, wg = 2 * n_tile;
+            const bool have_x = xg < x_groups, have_w1 = wg + 1 < w_groups;
+            const uint8_t* xs = p.xs + xg * p.n_atoms * kAtomBytes;
+            const uint8_t* ws = p.ws + wg * p.n_atoms * kAtomBytes;
+            for (int k = 0; k < steps; ++k, ++issued) {
+                if (issued >= kPairStages) ok = wait_pair(&sm.empty[st], ph ^ 1u);
+                if (!ok) break;
+                if (lane == 0 && warp == kPairLoad) {
+                    mbar_arrive_expect_tx(&sm.full[st], 128 * 128 + 128 * (kMode == X8W4 ? 64 : 128));
+                    tma_load_2d(x_tiles + st * 16384, &tm_x, &sm.full[st], k * 128, t0);
+                    tma_load_2d(w_tiles + st * 16384, &tm_w, &sm.full[st], k * 128, n0);
+                } else if (lane == 0) {
+                    const uint32_t sf = min(kAtoms, p.n_atoms - k * kAtoms) * kAtomBytes;
+                    const int64_t at = static_cast<int64_t>(k) * kAtoms * kAtomBytes;
+                    uint8_t* dst = sf_tiles + st * kSf;
+                    mbar_arrive_expect_tx(&sm.full[st], sf * (1 + have_x + have_w1));
+                    if (have_x) bulk_load(dst, xs + at, sf, &sm.full[st]);
+                    bulk_load(dst + kAtoms * kAtomBytes, ws + at, sf, &sm.full[st]);
+                    if (have_w1)
+                        bulk_load(dst + 2 * kAtoms * kAtomBytes, ws + static_cast<int64_t>(p.n_atoms) * kAtomBytes + at, sf,
+                                  &sm.full[st]);
+                }
+                advance();
+            }
+        }
+        if (lane == 0) {
+            if (!ok) give_up();
+            // every copy lands before the CTA goes on, whoever gives up and when
+            int dummy = 0;
+            for (int i = max(0, issued - kPairStages); i < issued; ++i)
+                mbar_wait(&sm.full[i % kPairStages], (i / kPairStages) & 1, p.timeout_ns, &dummy);
+        }
+    } else if (warp == kPairMma && rank != 0) {
+        // says in rank 0 that a stage of this CTA has landed
+        for (int i = first_tile; ok && i < tiles; i += tile_step)
+            for (int k = 0; k < steps; ++k) {
+                ok = wait(&sm.full[st], ph);
+                if (!ok) break;
+                if (lane == 0) mbar_arrive_cluster(mapa(smem_u32(&sm.peer[st]), 0));
+                advance();
+            }
+        if (!ok && lane == 0) give_up();
+    } else if (warp == kPairMma) {
+        const uint32_t tm = __shfl_sync(0xFFFFFFFFu, tmem, 0);
+        const uint64_t dx = smem_desc(smem_u32(x_tiles), 16, 1024, SWZ_128B), dw = smem_desc(smem_u32(w_tiles), 16, 1024, SWZ_128B);
+        const uint64_t dsf = smem_desc(smem_u32(sf_tiles), 0, 128, SWZ_NONE);
+        constexpr uint32_t id = kMode == X4W4 ? idesc_mxf8f6f4(256, 256, 1, 1, 0, 0)
+                                              : idesc_mxf8f6f4(256, 256, 0, kMode == X8W4 ? 5 : 0, 0, 0);
+        uint32_t acc_ph = 1;  // (the first tile finds the accumulator empty)
+        for (int i = first_tile; ok && i < tiles; i += tile_step, acc_ph ^= 1u) {
+            if (i != first_tile) ok = wait_pair(&sm.acc_empty, acc_ph);
+            for (int k = 0; ok && k < steps; ++k) {
+                ok = wait(&sm.full[st], ph) && wait_pair(&sm.peer[st], ph);
+                if (!ok) break;
+                tc_fence_after();
+                // scale columns of a stage: x, then for each atom both halves of w
+                const uint32_t sfx = tm + kPairSf + 12 * kAtoms * st, sfw = sfx + 4 * kAtoms;
+                const uint64_t sf = dsf + st * (kSf >> 4);
+                const bool half = kAtoms == 2 && p.n_atoms - k * kAtoms == 1;
+#pragma unroll
+                for (int a = 0; a < kAtoms; ++a) {
+                    if (a && half) break;
+                    pair_cp_32x128b_x4_one(sfx + 4 * a, sf + a * (kAtomBytes >> 4));
+                    pair_cp_32x128b_x4_one(sfw + 8 * a, sf + (kAtoms + a) * (kAtomBytes >> 4));
+                    pair_cp_32x128b_x4_one(sfw + 8 * a + 4, sf + (2 * kAtoms + a) * (kAtomBytes >> 4));
+                }
+                const uint64_t ax = dx + st * (16384 >> 4), aw = dw + st * (16384 >> 4);
+#pragma unroll
+                for (int kk = 0; kk < 4; ++kk) {
+                    const uint32_t acc = (k > 0 || kk > 0) ? 1u : 0u;
+                    if constexpr (kMode == X4W4) {
+                        if (kk >= 2 && half) break;
+                        const uint32_t s = (kk & 1) * 2;
+                        pair_mma_mxf4_one(tm, ax + 2 * kk, aw + 2 * kk, id | s << 4 | s << 29, sfx + 4 * (kk >> 1), sfw + 8 * (kk >> 1),
+                                          acc);
+                    } else {
+                        pair_mma_mxf8f6f4_one(tm, ax + 2 * kk, aw + 2 * kk, id | kk << 4 | static_cast<uint32_t>(kk) << 29, sfx, sfw, acc);
+                    }
+                }
+                pair_commit_one(&sm.empty[st], 3);
+                advance();
+            }
+            if (ok) pair_commit_one(&sm.acc_full, 3);
+        }
+        if (!ok && lane == 0) give_up();
+        pair_commit_one(&sm.drain, 1);  // every product issued retires before anything is freed
+        int dummy = 0;
+        if (!__all_sync(0xFFFFFFFFu, mbar_wait(&sm.drain, 0, p.timeout_ns, &dummy)) && lane == 0) give_up();
+    } else {
+        const uint32_t col = tmem + (static_cast<uint32_t>(32 * (warp & 3)) << 16) + 128 * (warp >> 2);
+        const uint32_t acc_empty = mapa(smem_u32(&sm.acc_empty), 0);
+        uint4* mine = out + warp * 128;  // 32 rows x 4 pieces of 8 outputs
+        uint32_t acc_ph = 0;
+        for (int i = first_tile; i < tiles; i += tile_step, acc_ph ^= 1u) {
+            ok = wait_pair(&sm.acc_full, acc_ph);
+            if (!ok) break;
+            tc_fence_after();
+            // sums into registers first: the next tile's products wait for no store
+            uint32_t v[64];
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                uint32_t r[32];
+                tmem_ld32(col + 32 * c, r);
+                tmem_ld_wait();
+                tmem_reg_dep(r);
+#pragma unroll
+                for (int j = 0; j < 16; ++j) {
+                    const __nv_bfloat162 b = __floats2bfloat162_rn(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1]));
+                    v[16 * c + j] = *reinterpret_cast<const uint32_t*>(&b);
+                }
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_cluster(acc_empty);
+            int t_tile, n_tile;
+            pair_tile(p, i, t_tile, n_tile);
+            const int t0 = 256 * t_tile + 128 * static_cast<int>(rank) + 32 * (warp & 3), n0 = 256 * n_tile + 128 * (warp >> 2);
+            // through shared memory, so that a store covers eight rows' 64 bytes
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    mine[4 * lane + (j ^ ((lane >> 1) & 3))] = make_uint4(v[16 * c + 4 * j], v[16 * c + 4 * j + 1], v[16 * c + 4 * j + 2],
+                                                                         v[16 * c + 4 * j + 3]);
+                __syncwarp();
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const int wr = 8 * j + (lane >> 2), t = t0 + wr, n = n0 + 32 * c + 8 * (lane & 3);
+                    const uint4 u = mine[4 * wr + ((lane & 3) ^ ((wr >> 1) & 3))];
+                    if (t < p.T && n < p.N) {
+                        __nv_bfloat16* dst = p.y + t * p.y_stride + n;
+                        if (p.vec && n + 8 <= p.N) {
+                            *reinterpret_cast<uint4*>(dst) = u;
+                        } else {
+                            const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+                            for (int e = 0; e < 8; ++e)
+                                if (n + e < p.N)
+                                    reinterpret_cast<uint16_t*>(dst)[e] = static_cast<uint16_t>(w[e / 2] >> (16 * (e & 1)));
+                        }
+                    }
+                }
+                __syncwarp();
+            }
+        }
+        if (!ok && lane == 0) give_up();
+    }
+    tc_fence_before();
+    __syncwarp();
+    cluster_sync();  // no CTA leaves while the other reads its memory or arrives at its barriers
+    if (warp == kPairMma) {
+        tc_fence_after();
+        pair_tmem_dealloc(tmem, kPairCols);
+    }
+}
+
+template <int kMode>
+cudaError_t launch_pair(const MxLinearLaunch& a, cudaStream_t st) {
+    static KernelSetup setup;
+    cudaError_t e = setup(reinterpret_cast<const void*>(mx_linear_pair_kernel<kMode>), pair_smem(kMode), 0);
+    if (e != cudaSuccess) return e;
+    PairParams p{};
+    p.xs = a.xs;
+    p.ws = a.ws;
+    p.y = static_cast<__nv_bfloat16*>(a.y);
+    p.y_stride = a.y_stride;
+    p.T = a.T;
+    p.N = a.N;
+    p.n_atoms = static_cast<int>(mx_atoms(a.K));
+    p.t_tiles = (a.T + 255) / 256;
+    p.n_tiles = (a.N + 255) / 256;
+    p.vec = (reinterpret_cast<uintptr_t>(a.y) & 15) == 0 && a.y_stride % 8 == 0;
+    p.timeout_ns = a.timeout_ns;
+    p.err_word = a.err_word;
+    p.skip = a.debug_flags & 1;
+    const int tiles = p.t_tiles * p.n_tiles;
+    mx_linear_pair_kernel<kMode><<<2 * (tiles < 76 ? tiles : 76), kPairThreads, pair_smem(kMode), st>>>(*a.tm_x, *a.tm_w, p);
+    return cudaGetLastError();
+}
+
 int stages_for(int mode, int n_tok) {
     const int n = (kSmem - 1024) / stage_bytes(mode, n_tok);
     return n < kMaxStages ? n : kMaxStages;
@@ -262,6 +557,12 @@ cudaError_t launch(const MxLinearLaunch& a, const Params& p, int tiles, cudaStre
 MxLinearPlan mx_linear_plan(int T, int N, int K, int x_elem, int w_elem) {
     MxLinearPlan plan{};
     plan.w_rows = 128;
+    // pairs where their 256 x 256 tiles fill the GPU
+    if (static_cast<int64_t>((T + 255) / 256) * ((N + 255) / 256) >= 76) {
+        plan.x_rows = 128;
+        plan.split = 0;
+        return plan;
+    }
     plan.x_rows = T >= 128 ? 128 : (T + 15) / 16 * 16;
     const int kAtoms = stage_atoms(mode_of(x_elem, w_elem));
     const int64_t steps = (mx_atoms(K) + kAtoms - 1) / kAtoms;
@@ -281,6 +582,7 @@ MxLinearPlan mx_linear_plan(int T, int N, int K, int x_elem, int w_elem) {
 
 cudaError_t launch_mx_linear(const MxLinearLaunch& a, const MxLinearPlan& plan, cudaStream_t st) {
     const int mode = mode_of(a.x_elem, a.w_elem);
+    if (plan.split == 0) return mode == X4W4 ? launch_pair<X4W4>(a, st) : mode == X8W4 ? launch_pair<X8W4>(a, st) : launch_pair<X8W8>(a, st);
     Params p{};
     p.xs = a.xs;
     p.ws = a.ws;

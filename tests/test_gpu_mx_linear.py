@@ -38,6 +38,9 @@ SHAPES = [
     (1, 1, 1), (1, 16, 32), (2, 5, 33), (1, 128, 128), (3, 129, 127), (16, 256, 256), (17, 130, 129), (31, 100, 300),
     (1, 6144, 4096), (5, 1000, 5120), (64, 512, 1024), (65, 384, 640), (127, 200, 257), (128, 128, 128), (129, 128, 4128),
     (200, 777, 96), (300, 264, 8192), (513, 1111, 500), (1024, 1280, 256),
+    # many tiles of many tokens
+    (1300, 4000, 300), (2305, 2100, 257), (20000, 200, 128), (300, 10000, 640), (129, 20000, 96), (2048, 2560, 1024),
+    (5000, 1300, 33),
 ]
 
 
@@ -52,7 +55,7 @@ def test_matches_64_bits(fsa, T, N, K, fx, fw):
 
 
 @pytest.mark.parametrize("fx,fw", MODES)
-@pytest.mark.parametrize("T,N,K", [(1, 256, 512), (9, 200, 384), (130, 300, 640)])
+@pytest.mark.parametrize("T,N,K", [(1, 256, 512), (9, 200, 384), (130, 300, 640), (19500, 200, 384)])
 def test_whole_numbers_are_exact(fsa, T, N, K, fx, fw):
     """Elements 0 .. 6 of either sign under scales of 1 and 2: every sum is a whole
     number below 2^24, so y is its rounding to bf16 and nothing else."""
@@ -73,15 +76,16 @@ def test_whole_numbers_are_exact(fsa, T, N, K, fx, fw):
 
 
 @pytest.mark.parametrize("fx,fw", MODES)
-def test_one_element_at_a_time(fsa, fx, fw):
+@pytest.mark.parametrize("times", [1, 70])
+def test_one_element_at_a_time(fsa, fx, fw, times):
     """x holds one element 1 in each row, at every column in turn: y's rows are w's
     columns, so a wrong place of a code or a scale shows."""
     K, N = 288, 200
     w = fsa.mx_pack(_bf16((N, K), 3, 1.0, 1.0), fw)
     x = torch.zeros(K, K, dtype=torch.bfloat16, device="cuda")
     x.fill_diagonal_(1.0)
-    y = fsa.mx_linear(fsa.mx_pack(x, fx), w)
-    assert torch.equal(y, fsa.mx_unpack(w).T)
+    y = fsa.mx_linear(fsa.mx_pack(x.repeat(times, 1), fx), w)
+    assert torch.equal(y, fsa.mx_unpack(w).T.repeat(times, 1))
 
 
 @pytest.mark.parametrize("seed", range(10))
@@ -97,7 +101,7 @@ def test_random_shapes(fsa, seed):
 
 @pytest.mark.parametrize("fx,fw", MODES)
 @pytest.mark.parametrize("pad,first", [(8, 0), (4, 4), (1, 0), (3, 1)])
-@pytest.mark.parametrize("T", [3, 140])
+@pytest.mark.parametrize("T", [3, 140, 19800])
 def test_output_rows_at_a_distance(fsa, fx, fw, pad, first, T):
     N, K = 200, 160
     x, w = _operands(fsa, T, N, K, fx, fw)
@@ -109,9 +113,10 @@ def test_output_rows_at_a_distance(fsa, fx, fw, pad, first, T):
 
 
 @pytest.mark.parametrize("fx,fw", MODES)
-def test_scales_behind_the_last_row_and_neighbours(fsa, fx, fw):
+@pytest.mark.parametrize("T", [70, 10070])
+def test_scales_behind_the_last_row_and_neighbours(fsa, fx, fw, T):
     # NaN scales in rows behind the last one, and in a row of x and of w, stay there
-    T, N, K = 70, 300, 400
+    N, K = 300, 400
     x, w = _operands(fsa, T, N, K, fx, fw)
     good = fsa.mx_linear(x, w)
     for op, rows in ((x, T), (w, N)):
@@ -154,7 +159,7 @@ def test_nothing_to_do(fsa):
     assert fsa.mx_linear(x, fsa.mx_pack(e)).shape == (4, 0)
 
 
-@pytest.mark.parametrize("T,N", [(2, 512), (300, 600)])
+@pytest.mark.parametrize("T,N", [(2, 512), (300, 600), (2600, 2000)])
 def test_streams_and_graphs(fsa, T, N):
     K = 1024
     g = to_dev(fsa_inputs.to_bf16_bits(np.ones(K, np.float32)))
@@ -185,7 +190,7 @@ def test_streams_and_graphs(fsa, T, N):
     assert fsa.get_device_error() == 0
 
 
-@pytest.mark.parametrize("T", [1, 300])
+@pytest.mark.parametrize("T", [1, 300, 10000])
 def test_giving_up(fsa, T):
     # the second stage of every tile's ring never counts as arrived
     x, w = _operands(fsa, T, 600, 2048, "mxfp8", "mxfp4")

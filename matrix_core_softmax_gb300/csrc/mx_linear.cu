@@ -237,19 +237,21 @@ __global__ void __launch_bounds__(kThreads, 2)
 // outputs: each has 128 tokens' rows and half of the weights' in its shared memory
 // and its tokens' sums in its tensor memory, so a step brings an SM 32 KB of codes for
 // as many operations as a 128 x 128 tile's for half of them.
-// warps 0-7 output, 8 copies of codes, 10 of scales (one warp for both held the products
-// up: five copies a step take 560 clocks to issue, a step's products 640 to 730), 9 the
-// products (rank 0) or word of its copies (rank 1)
-constexpr int kPairThreads = 352;
-constexpr int kPairLoad = 8, kPairMma = 9, kPairLoadSf = 10;
+// warps 0-7 output; 8 copies of x and its scales, 9 of w and the scales of its first 128
+// rows, 10 the scales of the others; 11 the products (rank 0) or word that a stage has
+// landed (rank 1).  A copy takes some 150 clocks to issue and a wait 120, a step's
+// products 640 to 700: one warp for all five copies took 815 clocks a step, one for the
+// three of scales 720.
+constexpr int kPairThreads = 384;
+constexpr int kPairLoad = 8, kPairLoaders = 3, kPairMma = 11;
 constexpr int kPairStages = 6;
 constexpr uint32_t kPairCols = 512;
 constexpr uint32_t kPairSf = 256;   // accumulator at 0, scales of stage s at 256 + 24 s
 constexpr int kPairGroup = 8;       // token tiles that are walked side by side
 
 struct PairBars {
-    uint64_t full[kPairStages], empty[kPairStages];
-    uint64_t peer[kPairStages];     // rank 0: the other CTA's copies of a stage have landed
+    uint64_t full[kPairStages];     // rank 0's: the other CTA's copies, too
+    uint64_t empty[kPairStages];
     uint64_t acc_full, acc_empty;   // (acc_empty: rank 0's, an arrival a warp of both CTAs' output)
     uint64_t drain;
     uint32_t tmem_base;
@@ -303,9 +305,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     if (tid == 0) {
         sm.abort = 0;
         for (int i = 0; i < kPairStages; ++i) {
-            mbar_init(&sm.full[i], i == 1 && p.skip ? 3 : 2);
+            mbar_init(&sm.full[i], kPairLoaders + (rank == 0) + (i == 1 && p.skip));
             mbar_init(&sm.empty[i], 1);
-            mbar_init(&sm.peer[i], 1);
         }
         mbar_init(&sm.acc_full, 1);
         mbar_init(&sm.acc_empty, 16);
@@ -325,9 +326,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     auto wait = [&](uint64_t* bar, uint32_t phase) {
         return __all_sync(0xFFFFFFFFu, mbar_wait(bar, phase & 1u, p.timeout_ns, &sm.abort)) != 0;
     };
-    auto wait_pair = [&](uint64_t* bar, uint32_t phase) {
-        return __all_sync(0xFFFFFFFFu, mbar_wait_cluster(bar, phase & 1u, p.timeout_ns, &sm.abort)) != 0;
-    };
     bool ok = true;
     int st = 0;       // stage and its phase, in step in all roles
     uint32_t ph = 0;
@@ -338,40 +336,44 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
         }
     };
 
-    if (warp == kPairLoad || warp == kPairLoadSf) {
-        const int64_t x_groups = mx_atoms(p.T), w_groups = mx_atoms(p.N);
-        int issued = 0;
-        for (int i = first_tile; ok && i < tiles; i += tile_step) {
-            int t_tile, n_tile;
-            pair_tile(p, i, t_tile, n_tile);
-            const int t0 = 256 * t_tile + 128 * static_cast<int>(rank), n0 = 256 * n_tile + 128 * static_cast<int>(rank);
-            // scale rows that there are: this CTA's tokens, all of the tile's outputs
-            const int64_t xg = t0 / 128, wg = 2 * n_tile;
-            const bool have_x = xg < x_groups, have_w1 = wg + 1 < w_groups;
-            const uint8_t* xs = p.xs + xg * p.n_atoms * kAtomBytes;
-            const uint8_t* ws = p.ws + wg * p.n_atoms * kAtomBytes;
-            for (int k = 0; k < steps; ++k, ++issued) {
-                if (issued >= kPairStages) ok = wait_pair(&sm.empty[st], ph ^ 1u);
-                if (!ok) break;
-                if (lane == 0 && warp == kPairLoad) {
-                    mbar_arrive_expect_tx(&sm.full[st], 128 * 128 + 128 * (kMode == X8W4 ? 64 : 128));
-                    tma_load_2d(x_tiles + st * 16384, &tm_x, &sm.full[st], k * 128, t0);
-                    tma_load_2d(w_tiles + st * 16384, &tm_w, &sm.full[st], k * 128, n0);
-                } else if (lane == 0) {
+    if (warp >= kPairLoad && warp < kPairLoad + kPairLoaders) {
+        if (lane == 0) {
+            const int what = warp - kPairLoad;
+            const int64_t x_groups = mx_atoms(p.T), w_groups = mx_atoms(p.N);
+            int issued = 0;
+            for (int i = first_tile; ok && i < tiles; i += tile_step) {
+                int t_tile, n_tile;
+                pair_tile(p, i, t_tile, n_tile);
+                const int t0 = 256 * t_tile + 128 * static_cast<int>(rank), n0 = 256 * n_tile + 128 * static_cast<int>(rank);
+                // scale rows that there are: this CTA's tokens, all of the tile's outputs
+                const int64_t xg = t0 / 128, wg = 2 * n_tile;
+                const bool have_x = xg < x_groups, have_w1 = wg + 1 < w_groups;
+                const uint8_t* xs = p.xs + xg * p.n_atoms * kAtomBytes;
+                const uint8_t* ws = p.ws + wg * p.n_atoms * kAtomBytes;
+                for (int k = 0; k < steps; ++k, ++issued) {
+                    if (issued >= kPairStages) ok = mbar_wait(&sm.empty[st], ph ^ 1u, p.timeout_ns, &sm.abort);
+                    if (!ok) break;
+                    uint64_t* full = &sm.full[st];
                     const uint32_t sf = min(kAtoms, p.n_atoms - k * kAtoms) * kAtomBytes;
                     const int64_t at = static_cast<int64_t>(k) * kAtoms * kAtomBytes;
-                    uint8_t* dst = sf_tiles + st * kSf;
-                    mbar_arrive_expect_tx(&sm.full[st], sf * (1 + have_x + have_w1));
-                    if (have_x) bulk_load(dst, xs + at, sf, &sm.full[st]);
-                    bulk_load(dst + kAtoms * kAtomBytes, ws + at, sf, &sm.full[st]);
-                    if (have_w1)
-                        bulk_load(dst + 2 * kAtoms * kAtomBytes, ws + static_cast<int64_t>(p.n_atoms) * kAtomBytes + at, sf,
-                                  &sm.full[st]);
+                    uint8_t* dst = sf_tiles + st * kSf + what * kAtoms * kAtomBytes;
+                    if (what == 0) {
+                        mbar_arrive_expect_tx(full, 128 * 128 + (have_x ? sf : 0));
+                        tma_load_2d(x_tiles + st * 16384, &tm_x, full, k * 128, t0);
+                        if (have_x) bulk_load(dst, xs + at, sf, full);
+                    } else if (what == 1) {
+                        mbar_arrive_expect_tx(full, 128 * (kMode == X8W4 ? 64 : 128) + sf);
+                        tma_load_2d(w_tiles + st * 16384, &tm_w, full, k * 128, n0);
+                        bulk_load(dst, ws + at, sf, full);
+                    } else if (have_w1) {
+                        mbar_arrive_expect_tx(full, sf);
+                        bulk_load(dst, ws + static_cast<int64_t>(p.n_atoms) * kAtomBytes + at, sf, full);
+                    } else {
+                        mbar_arrive(full);
+                    }
+                    advance();
                 }
-                advance();
             }
-        }
-        if (lane == 0) {
             if (!ok) give_up();
             // every copy lands before the CTA goes on, whoever gives up and when
             int dummy = 0;
@@ -384,7 +386,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
             for (int k = 0; k < steps; ++k) {
                 ok = wait(&sm.full[st], ph);
                 if (!ok) break;
-                if (lane == 0) mbar_arrive_cluster(mapa(smem_u32(&sm.peer[st]), 0));
+                if (lane == 0) mbar_arrive_cluster(mapa(smem_u32(&sm.full[st]), 0));
                 advance();
             }
         if (!ok && lane == 0) give_up();
@@ -396,9 +398,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
                                               : idesc_mxf8f6f4(256, 256, 0, kMode == X8W4 ? 5 : 0, 0, 0);
         uint32_t acc_ph = 1;  // (the first tile finds the accumulator empty)
         for (int i = first_tile; ok && i < tiles; i += tile_step, acc_ph ^= 1u) {
-            if (i != first_tile) ok = wait_pair(&sm.acc_empty, acc_ph);
+            if (i != first_tile) ok = wait(&sm.acc_empty, acc_ph);
             for (int k = 0; ok && k < steps; ++k) {
-                ok = wait(&sm.full[st], ph) && wait_pair(&sm.peer[st], ph);
+                ok = wait(&sm.full[st], ph);
                 if (!ok) break;
                 tc_fence_after();
                 // scale columns of a stage: x, then for each atom both halves of w
@@ -440,7 +442,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
         uint4* mine = out + warp * 128;  // 32 rows x 4 pieces of 8 outputs
         uint32_t acc_ph = 0;
         for (int i = first_tile; i < tiles; i += tile_step, acc_ph ^= 1u) {
-            ok = wait_pair(&sm.acc_full, acc_ph);
+            ok = wait(&sm.acc_full, acc_ph);
             if (!ok) break;
             tc_fence_after();
             // sums into registers first: the next tile's products wait for no store

@@ -745,6 +745,8 @@ fsa_status fsa_rms_norm_mx(const void* x, int64_t x_stride, const void* residual
     a.eps = eps;
     a.codes = codes;
     a.scales = scales;
+    a.timeout_ns = wait_limit_ns(fsa_options{});
+    a.err_word = ds->err;
     return launch_rms_norm_mx(a, elem, static_cast<cudaStream_t>(stream)) == cudaSuccess ? FSA_OK : FSA_ERR_CUDA;
 }
 

@@ -171,7 +171,11 @@ struct RmsNormMx {
     int cols;
     float eps;
     uint8_t *codes, *scales;
-    int x_align, residual_align, sum_align, gain_align;  // bytes that rows start on (set by the launcher)
+    uint64_t timeout_ns;
+    unsigned int* err_word;
+    // set by the launcher: bytes that rows start on, 1 / cols
+    int x_align, residual_align, sum_align, gain_align;
+    float inv_cols;
 };
 constexpr int kNormMaxCols = 32768;
 cudaError_t launch_rms_norm_mx(const RmsNormMx& a, int elem, cudaStream_t st);

@@ -21,12 +21,23 @@ namespace {
 
 enum Mode : int { X4W4 = 0, X8W4 = 1, X8W8 = 2 };
 
-constexpr int kThreads = 192;       // warps 0-3 output, 4 copies, 5 products
-constexpr int kWarpLoad = 4, kWarpMma = 5;
-constexpr int kMaxStages = 6;
-constexpr int kSmem = 112 * 1024;   // of a CTA's ring: two CTAs an SM
+// ---- few tokens --------------------------------------------------------------
+// The weights' rows are the accumulator's lanes and the tokens its columns, so that
+// one token costs 16 columns and not 128 rows.  A CTA: 128 outputs of n_tok tokens,
+// over its part of K; the `split` CTAs of a cluster add their sums up through
+// distributed shared memory, each for its share of the outputs, in the order of
+// their ranks.
+constexpr int kSms = 152;
+constexpr int kFixed = 8;           // (see mx_linear_plan)
+constexpr int kThreads = 224;       // warps 0-3 output, 4 copies of codes, 5 products, 6 copies of scales
+constexpr int kWarpLoad = 4, kWarpMma = 5, kWarpScales = 6;
+constexpr int kMaxStages = 12;
+// Scales come for 512 elements of K at once, in a ring of their own: a copy holds the
+// SM's copy engine up for 110 clocks however small it is.
+constexpr int kSfAtoms = 4, kSfSlots = 2, kSfBytes = 2 * kSfAtoms * kAtomBytes;
+constexpr int kSmemTwo = 112 * 1024, kSmemOne = 224 * 1024;  // of a CTA, two or one an SM
 constexpr uint32_t kTmemCols = 256; // of two CTAs: all 512
-constexpr uint32_t kColSf = 128;    // accumulator at 0, scales of stage s at 128 + 16 s
+constexpr uint32_t kColSf = 128;    // accumulator at 0, scales of slot s at 128 + 32 s
 constexpr int kPartRow = 132;       // FP32 of a token's 128 outputs in shared memory, padded
 
 struct Params {
@@ -41,30 +52,26 @@ struct Params {
 
 struct Bars {
     uint64_t full[kMaxStages], empty[kMaxStages];
+    uint64_t sf_full[kSfSlots], sf_empty[kSfSlots];
     uint64_t done;
     uint32_t tmem_base;
     int abort;
 };
 
 constexpr int stage_atoms(int mode) { return mode == X4W4 ? 2 : 1; }
-constexpr int stage_bytes(int mode, int n_tok) { return 128 * 128 + n_tok * 128 + 2 * stage_atoms(mode) * kAtomBytes; }
+constexpr int stage_bytes(int n_tok) { return 128 * 128 + n_tok * 128; }
 
 __device__ __forceinline__ void raise_abort(Bars& sm, const Params& p) {
     sm.abort = 1;
     atomicOr(p.err_word, kErrTimeout);
 }
 
-// The weights' rows are the accumulator's lanes and the tokens its columns, so that
-// one token costs 16 columns and not 128 rows.  A CTA: 128 outputs of n_tok tokens,
-// over its part of K; the `split` CTAs of a cluster add their sums up through
-// distributed shared memory, each for its share of the outputs, in the order of
-// their ranks.
 template <int kMode>
 __global__ void __launch_bounds__(kThreads, 2)
     mx_linear_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_w, const Params p) {
     extern __shared__ __align__(1024) uint8_t ring[];
     __shared__ Bars sm;
-    constexpr int kAtoms = stage_atoms(kMode);
+    constexpr int kAtoms = stage_atoms(kMode), kSfSteps = kSfAtoms / kAtoms;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     // (dynamic shared memory begins behind `sm`; swizzled tiles want 1024 bytes)
     const uint32_t pad = (1024u - (smem_u32(ring) & 1023u)) & 1023u;
@@ -77,16 +84,29 @@ __global__ void __launch_bounds__(kThreads, 2)
     const int n0 = n_tile * 128, t0 = t_tile * p.n_tok;
     const int steps = (p.n_atoms + kAtoms - 1) / kAtoms;
     const int first = static_cast<int>(static_cast<int64_t>(steps) * rank / p.split);
-    const int last = static_cast<int>(static_cast<int64_t>(steps) * (rank + 1) / p.split);
+    const int mine = static_cast<int>(static_cast<int64_t>(steps) * (rank + 1) / p.split) - first;
 
-    if (tid == 0) {
+    // step i of this CTA's into stage st (one lane)
+    auto load = [&](int i, int st) {
+        // (a spread copy counts the bytes that it reads, 64 a row)
+        mbar_arrive_expect_tx(&sm.full[st], 128 * (kMode == X8W4 ? 64 : 128) + p.n_tok * 128);
+        tma_load_2d(w_tiles + st * 16384, &tm_w, &sm.full[st], (first + i) * 128, n0);
+        tma_load_2d(x_tiles + st * p.n_tok * 128, &tm_x, &sm.full[st], (first + i) * 128, t0);
+    };
+    const int ahead = min(mine, p.stages);
+    if (warp == kWarpLoad && lane == 0) {
         sm.abort = 0;
         for (int i = 0; i < p.stages; ++i) {
             mbar_init(&sm.full[i], i == 1 && p.skip ? 2 : 1);
             mbar_init(&sm.empty[i], 1);
         }
+        for (int i = 0; i < kSfSlots; ++i) {
+            mbar_init(&sm.sf_full[i], 1);
+            mbar_init(&sm.sf_empty[i], 1);
+        }
         mbar_init(&sm.done, 1);
         fence_mbar_init();
+        for (int i = 0; i < ahead; ++i) load(i, i);  // (the other warps need not be there yet)
     }
     if (warp == kWarpMma) {
         tmem_alloc(&sm.tmem_base, kTmemCols);
@@ -97,38 +117,47 @@ __global__ void __launch_bounds__(kThreads, 2)
     tc_fence_after();
     const uint32_t tmem = sm.tmem_base;
     bool ok = true;
+    // give-up and exit of a loader: every copy lands before the CTA goes on, whoever gives
+    // up and when (in a call that ends well they have landed)
+    auto settle = [&](uint64_t* full, int stages, int issued) {
+        if (!ok) raise_abort(sm, p);
+        int dummy = 0;
+        for (int i = max(0, issued - stages); i < issued; ++i) mbar_wait(full + i % stages, (i / stages) & 1, p.timeout_ns, &dummy);
+    };
 
     if (warp == kWarpLoad) {
-        // (a spread copy counts the bytes that it reads, 64 a row)
-        const uint32_t bytes = 128 * (kMode == X8W4 ? 64 : 128) + p.n_tok * 128;
-        const uint8_t* ws = p.ws + static_cast<int64_t>(n_tile) * p.n_atoms * kAtomBytes;
-        const uint8_t* xs = p.xs + static_cast<int64_t>(t0 / 128) * p.n_atoms * kAtomBytes;
-        int st = 0, issued = 0;
-        uint32_t ph = 0;
-        for (int i = first; i < last; ++i, ++issued) {
-            if (issued >= p.stages) ok = __all_sync(0xFFFFFFFFu, mbar_wait(&sm.empty[st], ph ^ 1u, p.timeout_ns, &sm.abort)) != 0;
-            if (!ok) break;
-            if (lane == 0) {
-                const uint32_t sf = min(kAtoms, p.n_atoms - i * kAtoms) * kAtomBytes;  // (the last step may hold one atom)
-                uint8_t* sf_at = sf_tiles + st * 2 * kAtoms * kAtomBytes;
-                mbar_arrive_expect_tx(&sm.full[st], bytes + 2 * sf);
-                tma_load_2d(w_tiles + st * 16384, &tm_w, &sm.full[st], i * 128, n0);
-                tma_load_2d(x_tiles + st * p.n_tok * 128, &tm_x, &sm.full[st], i * 128, t0);
-                bulk_load(sf_at, ws + static_cast<int64_t>(i) * kAtoms * kAtomBytes, sf, &sm.full[st]);
-                bulk_load(sf_at + kAtoms * kAtomBytes, xs + static_cast<int64_t>(i) * kAtoms * kAtomBytes, sf, &sm.full[st]);
-            }
-            if (++st == p.stages) {
-                st = 0;
-                ph ^= 1u;
-            }
-        }
         if (lane == 0) {
-            if (!ok) raise_abort(sm, p);
-            // every copy lands before the CTA goes on, whoever gives up and when (in a
-            // call that ends well they have landed)
-            int dummy = 0;
-            for (int i = max(0, issued - p.stages); i < issued; ++i)
-                mbar_wait(&sm.full[i % p.stages], (i / p.stages) & 1, p.timeout_ns, &dummy);
+            int st = ahead == p.stages ? 0 : ahead, issued = ahead;
+            uint32_t ph = 1;
+            for (; issued < mine; ++issued) {
+                ok = mbar_wait(&sm.empty[st], ph ^ 1u, p.timeout_ns, &sm.abort);
+                if (!ok) break;
+                load(issued, st);
+                if (++st == p.stages) {
+                    st = 0;
+                    ph ^= 1u;
+                }
+            }
+            settle(sm.full, p.stages, issued);
+        }
+    } else if (warp == kWarpScales) {
+        if (lane == 0) {
+            const int64_t at = static_cast<int64_t>(first) * kAtoms * kAtomBytes;
+            const uint8_t* ws = p.ws + static_cast<int64_t>(n_tile) * p.n_atoms * kAtomBytes + at;
+            const uint8_t* xs = p.xs + static_cast<int64_t>(t0 / 128) * p.n_atoms * kAtomBytes + at;
+            const int atoms = min(mine * kAtoms, p.n_atoms - first * kAtoms);  // (the last step may hold one atom)
+            int issued = 0;
+            for (int a = 0; a < atoms; a += kSfAtoms, ++issued) {
+                const int slot = issued % kSfSlots;
+                if (issued >= kSfSlots) ok = mbar_wait(&sm.sf_empty[slot], (issued / kSfSlots - 1) & 1, p.timeout_ns, &sm.abort);
+                if (!ok) break;
+                const uint32_t bytes = min(kSfAtoms, atoms - a) * kAtomBytes;
+                uint8_t* dst = sf_tiles + slot * kSfBytes;
+                mbar_arrive_expect_tx(&sm.sf_full[slot], 2 * bytes);
+                bulk_load(dst, ws + static_cast<int64_t>(a) * kAtomBytes, bytes, &sm.sf_full[slot]);
+                bulk_load(dst + kSfBytes / 2, xs + static_cast<int64_t>(a) * kAtomBytes, bytes, &sm.sf_full[slot]);
+            }
+            settle(sm.sf_full, kSfSlots, issued);
         }
     } else if (warp == kWarpMma) {
         const uint32_t tm = __shfl_sync(0xFFFFFFFFu, tmem, 0);
@@ -136,25 +165,30 @@ __global__ void __launch_bounds__(kThreads, 2)
         const uint64_t dsf = smem_desc(smem_u32(sf_tiles), 0, 128, SWZ_NONE);
         const uint32_t id = kMode == X4W4 ? idesc_mxf8f6f4(128, p.n_tok, 1, 1, 0, 0)
                                           : idesc_mxf8f6f4(128, p.n_tok, kMode == X8W4 ? 5 : 0, 0, 0, 0);
+        auto wait = [&](uint64_t* bar, uint32_t phase) {
+            return __all_sync(0xFFFFFFFFu, mbar_wait(bar, phase & 1u, p.timeout_ns, &sm.abort)) != 0;
+        };
         int st = 0;
         uint32_t ph = 0;
-        for (int i = first; i < last; ++i) {
-            ok = __all_sync(0xFFFFFFFFu, mbar_wait(&sm.full[st], ph, p.timeout_ns, &sm.abort)) != 0;
+        for (int i = 0; i < mine; ++i) {
+            const int chunk = i / kSfSteps, in = i - chunk * kSfSteps, slot = chunk % kSfSlots;
+            if (in == 0) ok = wait(&sm.sf_full[slot], chunk / kSfSlots);
+            ok = ok && wait(&sm.full[st], ph);
             if (!ok) break;
             tc_fence_after();
-            const uint32_t sfw = tm + kColSf + 16 * st, sfx = sfw + 4 * kAtoms;
-            const uint64_t sf = dsf + st * (2 * kAtoms * kAtomBytes >> 4);
-            const bool half = kAtoms == 2 && p.n_atoms - i * kAtoms == 1;
+            const uint32_t sfw = tm + kColSf + 8 * kSfAtoms * slot + 4 * kAtoms * in, sfx = sfw + 4 * kSfAtoms;
+            const uint64_t sf = dsf + slot * (kSfBytes >> 4) + in * (kAtoms * kAtomBytes >> 4);
+            const bool half = kAtoms == 2 && p.n_atoms - (first + i) * kAtoms == 1;
 #pragma unroll
             for (int a = 0; a < kAtoms; ++a) {
                 if (a && half) break;
                 tc_cp_32x128b_x4_one(sfw + 4 * a, sf + a * (kAtomBytes >> 4));
-                tc_cp_32x128b_x4_one(sfx + 4 * a, sf + (kAtoms + a) * (kAtomBytes >> 4));
+                tc_cp_32x128b_x4_one(sfx + 4 * a, sf + (kSfAtoms + a) * (kAtomBytes >> 4));
             }
             const uint64_t aw = dw + st * (16384 >> 4), ax = dx + st * (p.n_tok * 128 >> 4);
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk) {
-                const uint32_t acc = (i > first || kk > 0) ? 1u : 0u;
+                const uint32_t acc = (i > 0 || kk > 0) ? 1u : 0u;
                 if constexpr (kMode == X4W4) {
                     if (kk >= 2 && half) break;
                     const uint32_t s = (kk & 1) * 2;  // scale bytes 0-1 or 2-3 of the atom
@@ -164,6 +198,7 @@ __global__ void __launch_bounds__(kThreads, 2)
                 }
             }
             tc_commit_one(&sm.empty[st]);
+            if (in == kSfSteps - 1) tc_commit_one(&sm.sf_empty[slot]);
             if (++st == p.stages) {
                 st = 0;
                 ph ^= 1u;
@@ -528,22 +563,20 @@ cudaError_t launch_pair(const MxLinearLaunch& a, cudaStream_t st) {
     return cudaGetLastError();
 }
 
-int stages_for(int mode, int n_tok) {
-    const int n = (kSmem - 1024) / stage_bytes(mode, n_tok);
-    return n < kMaxStages ? n : kMaxStages;
-}
-
 int mode_of(int x_elem, int w_elem) { return w_elem == ELEM_E4M3 ? X8W8 : x_elem == ELEM_E4M3 ? X8W4 : X4W4; }
 
 template <int kMode>
-cudaError_t launch(const MxLinearLaunch& a, const Params& p, int tiles, cudaStream_t st) {
+cudaError_t launch(const MxLinearLaunch& a, Params p, int tiles, cudaStream_t st) {
     static KernelSetup setup;
-    cudaError_t e = setup(reinterpret_cast<const void*>(mx_linear_kernel<kMode>), kSmem, 0);
+    cudaError_t e = setup(reinterpret_cast<const void*>(mx_linear_kernel<kMode>), kSmemOne, 0);
     if (e != cudaSuccess) return e;
+    const int smem = tiles * p.split <= kSms ? kSmemOne : kSmemTwo;
+    p.stages = (smem - 1024 - kSfSlots * kSfBytes) / stage_bytes(p.n_tok);
+    if (p.stages > kMaxStages) p.stages = kMaxStages;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(static_cast<unsigned>(tiles) * p.split);
     cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = kSmem;
+    cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
     cudaLaunchAttribute at{};
     at.id = cudaLaunchAttributeClusterDimension;
@@ -559,21 +592,18 @@ cudaError_t launch(const MxLinearLaunch& a, const Params& p, int tiles, cudaStre
 MxLinearPlan mx_linear_plan(int T, int N, int K, int x_elem, int w_elem) {
     MxLinearPlan plan{};
     plan.w_rows = 128;
-    // pairs where their 256 x 256 tiles fill the GPU
-    if (static_cast<int64_t>((T + 255) / 256) * ((N + 255) / 256) >= 76) {
-        plan.x_rows = 128;
-        plan.split = 0;
-        return plan;
-    }
-    plan.x_rows = T >= 128 ? 128 : (T + 15) / 16 * 16;
+    plan.x_rows = 128;
+    if (T > 128) return plan;  // pairs of CTAs
+    plan.x_rows = (T + 15) / 16 * 16;
     const int kAtoms = stage_atoms(mode_of(x_elem, w_elem));
     const int64_t steps = (mx_atoms(K) + kAtoms - 1) / kAtoms;
-    const int64_t tiles = mx_atoms(N) * ((T + plan.x_rows - 1) / plan.x_rows);
-    // the time goes with the rounds of CTAs (two an SM) times the steps of each
+    const int64_t tiles = mx_atoms(N);
+    // the time goes with the rounds of CTAs (two an SM) times the steps of each and
+    // kFixed more for its start and end
     plan.split = 1;
     int64_t best = 0;
     for (int s = 1; s <= 8 && s <= steps; s *= 2) {
-        const int64_t cost = ((tiles * s + 303) / 304) * ((steps + s - 1) / s);
+        const int64_t cost = ((tiles * s + 2 * kSms - 1) / (2 * kSms)) * ((steps + s - 1) / s + kFixed);
         if (s == 1 || cost < best) {
             best = cost;
             plan.split = s;
@@ -595,7 +625,6 @@ cudaError_t launch_mx_linear(const MxLinearLaunch& a, const MxLinearPlan& plan, 
     p.n_atoms = static_cast<int>(mx_atoms(a.K));
     p.n_tok = plan.x_rows;
     p.split = plan.split;
-    p.stages = stages_for(mode, p.n_tok);
     p.t_tiles = (a.T + p.n_tok - 1) / p.n_tok;
     p.vec = (reinterpret_cast<uintptr_t>(a.y) & 7) == 0 && a.y_stride % 4 == 0;
     p.timeout_ns = a.timeout_ns;

@@ -16,6 +16,7 @@
 namespace fsa {
 namespace {
 
+constexpr int kSms = 152;
 constexpr int kWarps = 8;   // warps of a block, unless a row has more
 constexpr int kUnroll = 4;  // pieces that a lane has under way
 
@@ -73,6 +74,12 @@ __device__ __forceinline__ void widen(uint4 u, float (&v)[8]) {
     }
 }
 
+__device__ __forceinline__ void widen2(uint4 u, float2 (&v)[4]) {
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = make_float2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xFFFF0000u));
+}
+
 __device__ __forceinline__ uint32_t pair_bf16(float lo, float hi) {
     uint32_t r;
     asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
@@ -88,6 +95,7 @@ __global__ void __launch_bounds__(32 * kWarps) mx_pack_kernel(const uint16_t* x,
     if (r >= rows) return;
     const int n_atoms = static_cast<int>(mx_atoms(cols)), step = 32 << lg;
     const uint16_t* row = x + r * stride;
+    const MxRow out = mx_row<kElem>(codes, scales, r, n_atoms);
     // whole warps: every lane takes part in the shuffles
     for (int p0 = (warp & ((1 << lg) - 1)) * 32; p0 < 16 * n_atoms; p0 += kUnroll * step) {
         uint4 u[kUnroll];
@@ -96,9 +104,9 @@ __global__ void __launch_bounds__(32 * kWarps) mx_pack_kernel(const uint16_t* x,
 #pragma unroll
         for (int i = 0; i < kUnroll; ++i) {
             if (p0 + i * step >= 16 * n_atoms) break;
-            float v[8];
-            widen(u[i], v);
-            mx_store8<kElem>(v, r, p0 + i * step + lane, cols, n_atoms, codes, scales);
+            float2 v[4];
+            widen2(u[i], v);
+            mx_store8<kElem>(v, out, p0 + i * step + lane, cols, n_atoms);
         }
     }
 }
@@ -171,79 +179,70 @@ __global__ void __launch_bounds__(32 * kWarps) mx_unpack_kernel(const uint8_t* _
     }
 }
 
-// y = h / sqrt(mean(h^2) + eps) g of the sum h = bf16(x + residual), or of h = x,
-// quantized.  A row's h stays in registers (bf16, as it is stored) between the sum
-// of its squares and its output, so x and the residual are read once.  kV pieces a
-// lane, 2^lg warps a row; kWide: a block of 32 warps for one row.
-template <int kElem, int kV, bool kWide>
-__global__ void __launch_bounds__(kWide ? 1024 : 512) rms_norm_mx_kernel(const RmsNormMx a, int lg) {
-    __shared__ float part[2][32];
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, n_warps = blockDim.x >> 5;
-    const int64_t r = blockIdx.x * static_cast<int64_t>(n_warps >> lg) + (warp >> lg);
+// h = x + residual, rounded to bf16.
+__device__ __forceinline__ uint4 add8(uint4 x, uint4 d) {
+    float2 u[4], v[4];
+    widen2(x, u);
+    widen2(d, v);
+    uint32_t o[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float2 t = __fadd2_rn(u[i], v[i]);
+        o[i] = pair_bf16(t.x, t.y);
+    }
+    return make_uint4(o[0], o[1], o[2], o[3]);
+}
+
+// The 2^lg warps of a row wait for one another; rows of a block do not.
+__device__ __forceinline__ void row_sync(int lg) {
+    if (lg == 0)
+        __syncwarp();
+    else
+        asm volatile("bar.sync %0, %1;" ::"r"(1 + (static_cast<int>(threadIdx.x) >> (5 + lg))), "r"(32 << lg) : "memory");
+}
+
+// Sum (or maximum) of s over the row's warps, the same in each of them.  `part`: a word
+// a warp; it may be written again behind the row's next wait.
+__device__ __forceinline__ float over_row(float s, bool most, int lg, float* part) {
+    const int warp = threadIdx.x >> 5;
+#pragma unroll
+    for (int o = 16; o; o >>= 1) {
+        const float other = __shfl_xor_sync(0xFFFFFFFFu, s, o);
+        s = most ? fmaxf(s, other) : s + other;
+    }
+    if (lg > 0) {
+        if ((threadIdx.x & 31) == 0) part[warp] = s;
+        row_sync(lg);
+        const int w0 = warp & ~((1 << lg) - 1);
+        s = 0.0f;  // (of squares or magnitudes: none is below)
+        for (int w = 0; w < 1 << lg; ++w) s = most ? fmaxf(s, part[w0 + w]) : s + part[w0 + w];
+    }
+    return s;
+}
+
+// The norm of row r, whose h and gains this lane holds kV pieces of, into the operand;
+// 2^lg warps a row.  `turn` alternates from row to row; `read` is called once all of
+// the row's warps have h.
+template <int kElem, int kV, class Read>
+__device__ __forceinline__ void norm_row(const RmsNormMx& a, int64_t r, const uint4 (&h)[kV], const uint4 (&g)[kV], int lg,
+                                         float (&part)[4][32], int turn, Read read) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int first = (warp & ((1 << lg) - 1)) * 32 + lane, step = 32 << lg;
     const int n_atoms = static_cast<int>(mx_atoms(a.cols));
-    const bool row = r < a.rows;  // (a warp without a row still meets the others at the barriers)
-    uint4 h[kV];
-    const uint16_t* x = static_cast<const uint16_t*>(a.x) + r * a.x_stride;
+    float2 acc = make_float2(0.0f, 0.0f);
 #pragma unroll
-    for (int i = 0; i < kV; ++i) h[i] = row ? load8(x, first + i * step, a.cols, a.x_align) : make_uint4(0, 0, 0, 0);
-    if (a.residual) {
-        const uint16_t* res = static_cast<const uint16_t*>(a.residual) + r * a.residual_stride;
-        uint4 d[kV];
+    for (int i = 0; i < kV; ++i) {
+        float2 v[4];
+        widen2(h[i], v);
 #pragma unroll
-        for (int i = 0; i < kV; ++i) d[i] = row ? load8(res, first + i * step, a.cols, a.residual_align) : make_uint4(0, 0, 0, 0);
-#pragma unroll
-        for (int i = 0; i < kV; ++i) {
-            float u[8], v[8];
-            widen(h[i], u);
-            widen(d[i], v);
-            h[i] = make_uint4(pair_bf16(u[0] + v[0], u[1] + v[1]), pair_bf16(u[2] + v[2], u[3] + v[3]),
-                              pair_bf16(u[4] + v[4], u[5] + v[5]), pair_bf16(u[6] + v[6], u[7] + v[7]));
-        }
-        if (row) {
-            uint16_t* sum = static_cast<uint16_t*>(a.sum) + r * a.sum_stride;
-#pragma unroll
-            for (int i = 0; i < kV; ++i)
-                if (8 * (first + i * step) < a.cols) store8(sum, first + i * step, a.cols, a.sum_align, h[i]);
-        }
+        for (int j = 0; j < 4; ++j) acc = __ffma2_rn(v[j], v[j], acc);
     }
-    uint4 g[kV];  // (asked for ahead of the row's sum)
-#pragma unroll
-    for (int i = 0; i < kV; ++i) g[i] = load8(static_cast<const uint16_t*>(a.gain), first + i * step, a.cols, a.gain_align);
-    // sum (or maximum) over the row's warps, the same in each of them
-    auto over_row = [&](float s, bool most, float* part) {
-#pragma unroll
-        for (int o = 16; o; o >>= 1) {
-            const float other = __shfl_xor_sync(0xFFFFFFFFu, s, o);
-            s = most ? fmaxf(s, other) : s + other;
-        }
-        if (lg > 0) {
-            if (lane == 0) part[warp] = s;
-            __syncthreads();
-            const int w0 = warp & ~((1 << lg) - 1);
-            s = 0.0f;
-            for (int w = 0; w < 1 << lg; ++w) s = most ? fmaxf(s, part[w0 + w]) : s + part[w0 + w];
-        }
-        return s;
-    };
-    auto squares = [&](float f) {
-        float s = 0.0f;
-#pragma unroll
-        for (int i = 0; i < kV; ++i) {
-            float v[8];
-            widen(h[i], v);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) s = __fmaf_rn(v[j] * f, v[j] * f, s);
-        }
-        return over_row(s, false, part[0]);
-    };
-    // y = (h f) inv g with f = 1, except where squares leave FP32 (or get lost below it and
-    // no larger eps covers them): there f is the power of two that brings the larger of
-    // the row's maximum and sqrt(eps) next to 1.  (Every warp of a block goes the same way
-    // through the barriers.)
-    float f = 1.0f, s = squares(1.0f);
-    const bool far = !(s <= 1e36f) || (s < 1e-25f && a.eps < 1e-12f);
-    if (__syncthreads_or(far)) {
+    float f = 1.0f, s = over_row(acc.x + acc.y, false, lg, part[turn]);
+    read();
+    // y = h (f inv) g with f = 1, except where squares leave FP32 (or get lost below it and
+    // no larger eps covers them): there f is a power of two that brings the larger of the
+    // row's maximum and sqrt(eps) near 1
+    if (!(s <= 1e36f) || (s < 1e-25f && a.eps < 1e-12f)) {
         float m = 0.0f;
 #pragma unroll
         for (int i = 0; i < kV; ++i) {
@@ -252,22 +251,149 @@ __global__ void __launch_bounds__(kWide ? 1024 : 512) rms_norm_mx_kernel(const R
 #pragma unroll
             for (int j = 0; j < 8; ++j) m = fmaxf(m, fabsf(v[j]));
         }
-        m = fmaxf(over_row(m, true, part[1]), sqrtf(a.eps));
-        if (far) f = __uint_as_float((254u - min(__float_as_uint(m) >> 23, 253u)) << 23);
-        s = squares(f);
+        m = fmaxf(over_row(m, true, lg, part[2]), sqrtf(a.eps));
+        // (2^-100 at least, so that f inv keeps its bits)
+        f = __uint_as_float((254u - min(__float_as_uint(m) >> 23, 227u)) << 23);
+        float t = 0.0f;
+#pragma unroll
+        for (int i = 0; i < kV; ++i) {
+            float v[8];
+            widen(h[i], v);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) t = __fmaf_rn(v[j] * f, v[j] * f, t);
+        }
+        s = over_row(t, false, lg, part[3]);
     }
-    const float inv = 1.0f / sqrtf(s / static_cast<float>(a.cols) + a.eps * f * f);
-    if (!row) return;
+    const float inv = f * rsqrtf(s * a.inv_cols + a.eps * f * f);
+    const float2 inv2 = make_float2(inv, inv);
+    const MxRow out = mx_row<kElem>(a.codes, a.scales, r, n_atoms);
 #pragma unroll
     for (int i = 0; i < kV; ++i) {
         const int p = first + i * step;
         if (p - lane >= 16 * n_atoms) break;  // (the whole warp is behind the row's end)
-        float v[8], w[8];
-        widen(h[i], v);
-        widen(g[i], w);
+        float2 v[4], w[4];
+        widen2(h[i], v);
+        widen2(g[i], w);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = v[j] * f * inv * w[j];
-        mx_store8<kElem>(v, r, p, a.cols, n_atoms, a.codes, a.scales);
+        for (int j = 0; j < 4; ++j) v[j] = __fmul2_rn(__fmul2_rn(v[j], inv2), w[j]);
+        mx_store8<kElem>(v, out, p, a.cols, n_atoms);
+    }
+}
+
+// y = h / sqrt(mean(h^2) + eps) g of the sum h = bf16(x + residual), or of h = x,
+// quantized.  A row's h stays in registers (bf16, as it is stored) between the sum
+// of its squares and its output, so x and the residual are read once.  kV pieces a
+// lane, 2^lg warps a row; kWide: a block of 32 warps for one row.
+template <int kElem, int kV, bool kWide>
+__global__ void __launch_bounds__(kWide ? 1024 : 512) rms_norm_mx_kernel(const RmsNormMx a, int lg) {
+    __shared__ float part[4][32];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, n_warps = blockDim.x >> 5;
+    const int64_t r = blockIdx.x * static_cast<int64_t>(n_warps >> lg) + (warp >> lg);
+    const int first = (warp & ((1 << lg) - 1)) * 32 + lane, step = 32 << lg;
+    if (r >= a.rows) return;
+    uint4 h[kV], g[kV];
+    const uint16_t* x = static_cast<const uint16_t*>(a.x) + r * a.x_stride;
+#pragma unroll
+    for (int i = 0; i < kV; ++i) h[i] = load8(x, first + i * step, a.cols, a.x_align);
+    if (a.residual) {
+        const uint16_t* res = static_cast<const uint16_t*>(a.residual) + r * a.residual_stride;
+        uint4 d[kV];
+#pragma unroll
+        for (int i = 0; i < kV; ++i) d[i] = load8(res, first + i * step, a.cols, a.residual_align);
+        uint16_t* sum = static_cast<uint16_t*>(a.sum) + r * a.sum_stride;
+#pragma unroll
+        for (int i = 0; i < kV; ++i) {
+            h[i] = add8(h[i], d[i]);
+            if (8 * (first + i * step) < a.cols) store8(sum, first + i * step, a.cols, a.sum_align, h[i]);
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < kV; ++i) g[i] = load8(static_cast<const uint16_t*>(a.gain), first + i * step, a.cols, a.gain_align);
+    norm_row<kElem, kV>(a, r, h, g, lg, part, 0, [] {});
+}
+
+// The same for many rows that start on 16 bytes: the warps of a row stay and take every
+// gridDim'th group's row, which bulk copies bring into a ring of shared memory ahead of
+// them, so that the copies wait for no row's sum; the gains stay in registers.
+constexpr int kMaxRing = 4;
+
+template <int kElem, int kV, int kThreads>
+__global__ void __launch_bounds__(kThreads, kThreads == 256 ? 3 : 1) rms_norm_mx_ring_kernel(const RmsNormMx a, int lg, int stages) {
+    extern __shared__ __align__(16) uint8_t ring[];
+    __shared__ float part[4][32];
+    __shared__ uint64_t full[kMaxRing][kThreads / 32];
+    __shared__ int gone;  // some row's copy did not arrive
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int per = (kThreads / 32) >> lg, mine = warp >> lg;  // rows of a group, this warp's
+    const int first = (warp & ((1 << lg) - 1)) * 32 + lane, step = 32 << lg;
+    const uint32_t row_bytes = 2 * a.cols;                      // (a multiple of 16)
+    const uint32_t slot_bytes = row_bytes * (a.residual ? 2 : 1);
+    const bool leader = lane == 0 && (warp & ((1 << lg) - 1)) == 0;  // of a row
+    uint8_t* at = ring + mine * stages * slot_bytes;
+    if (threadIdx.x == 0) {
+        gone = 0;
+        for (int i = 0; i < stages; ++i)
+            for (int j = 0; j < per; ++j) mbar_init(&full[i][j], 1);
+        fence_mbar_init();
+    }
+    __syncthreads();
+    const int64_t hop = static_cast<int64_t>(per) * gridDim.x;
+    int64_t r = static_cast<int64_t>(blockIdx.x) * per + mine;
+    auto fetch = [&](int64_t r, int st) {
+        if (r >= a.rows) return;
+        uint8_t* dst = at + st * slot_bytes;
+        uint64_t* bar = &full[st][mine];
+        mbar_arrive_expect_tx(bar, slot_bytes);
+        bulk_load(dst, static_cast<const uint16_t*>(a.x) + r * a.x_stride, row_bytes, bar);
+        if (a.residual) bulk_load(dst + row_bytes, static_cast<const uint16_t*>(a.residual) + r * a.residual_stride, row_bytes, bar);
+    };
+    if (leader)
+        for (int i = 0; i < stages; ++i) fetch(r + i * hop, i);
+    uint4 g[kV];
+#pragma unroll
+    for (int i = 0; i < kV; ++i) g[i] = load8(static_cast<const uint16_t*>(a.gain), first + i * step, a.cols, a.gain_align);
+    int st = 0, turn = 0;
+    uint32_t ph = 0;
+    bool lost = false;
+    for (; r < a.rows; r += hop) {
+        // a copy that does not arrive is reported, and the outputs from its row on are
+        // undefined: nothing more is fetched, and what is in flight lands before anyone
+        // leaves (the row's warps still meet, so that none waits for another)
+        if (!lost && !mbar_wait(&full[st][mine], ph, a.timeout_ns, &gone)) {
+            lost = true;
+            gone = 1;
+            if (leader) {
+                atomicOr(a.err_word, kErrTimeout);
+                int dummy = 0;
+                for (int i = 0; i < stages; ++i)
+                    if (r + i * hop < a.rows)
+                        mbar_wait(&full[(st + i) % stages][mine], st + i < stages ? ph : ph ^ 1u, a.timeout_ns, &dummy);
+            }
+        }
+        const uint8_t* src = at + st * slot_bytes;
+        uint16_t* sum = static_cast<uint16_t*>(a.sum) + r * a.sum_stride;
+        uint4 h[kV];
+#pragma unroll
+        for (int i = 0; i < kV; ++i) {
+            const int p = first + i * step;
+            h[i] = make_uint4(0, 0, 0, 0);
+            if (8 * p < a.cols) {
+                h[i] = *reinterpret_cast<const uint4*>(src + 16 * p);
+                if (a.residual) {
+                    h[i] = add8(h[i], *reinterpret_cast<const uint4*>(src + row_bytes + 16 * p));
+                    store8(sum, p, a.cols, a.sum_align, h[i]);
+                }
+            }
+        }
+        norm_row<kElem, kV>(a, r, h, g, lg, part, turn, [&] {
+            if (lg == 0) __syncwarp();
+            if (leader && !lost) fetch(r + stages * hop, st);
+        });
+        turn ^= 1;
+        if (++st == stages) {
+            st = 0;
+            ph ^= 1u;
+        }
     }
 }
 
@@ -285,17 +411,40 @@ int row_align(const void* p, int64_t stride) {
     return static_cast<int>(bits & -bits);
 }
 
+// Blocks an SM and stages of the ring for a stage of that many bytes; none: no ring.
+struct NormRing {
+    int blocks, stages, smem;
+};
+NormRing norm_ring(int64_t stage) {
+    for (int blocks = 3; blocks >= 1; --blocks) {
+        const int64_t room = (blocks == 3 ? 72 : blocks == 2 ? 110 : 222) * 1024;
+        const int n = static_cast<int>(room / stage < kMaxRing ? room / stage : kMaxRing);
+        if (n >= (blocks == 3 ? 2 : 3)) return {blocks, n, static_cast<int>(n * stage)};
+    }
+    return {0, 0, 0};
+}
+
 template <int kElem, int kV>
 cudaError_t norm_launch(const RmsNormMx& a, int lg, cudaStream_t st) {
     const int warps = 1 << lg > kWarps ? 1 << lg : kWarps;
-    const int64_t per = warps >> lg;
-    const unsigned grid = static_cast<unsigned>((a.rows + per - 1) / per);
-    if constexpr (kV <= 4)
-        if (lg == 5) {
-            rms_norm_mx_kernel<kElem, kV, true><<<grid, 32 * warps, 0, st>>>(a, lg);
+    const int64_t per = warps >> lg, groups = (a.rows + per - 1) / per;
+    if (lg <= 4 && a.x_align == 16 && a.cols % 8 == 0 && (!a.residual || a.residual_align == 16)) {
+        const NormRing ring = norm_ring(per * 2 * a.cols * (a.residual ? 2 : 1));
+        const int blocks = warps == 8 ? ring.blocks : ring.blocks > 1 ? 1 : ring.blocks;
+        if (blocks && groups >= 2 * kSms * blocks) {
+            static KernelSetup small, large;
+            const auto kernel = warps == 8 ? rms_norm_mx_ring_kernel<kElem, kV, 256> : rms_norm_mx_ring_kernel<kElem, kV, 512>;
+            const cudaError_t e = (warps == 8 ? small : large)(reinterpret_cast<const void*>(kernel), 222 * 1024, 0);
+            if (e != cudaSuccess) return e;
+            kernel<<<kSms * blocks, 32 * warps, ring.smem, st>>>(a, lg, ring.stages);
             return cudaGetLastError();
         }
-    rms_norm_mx_kernel<kElem, kV, false><<<grid, 32 * warps, 0, st>>>(a, lg);
+    }
+    if (lg == 5) {
+        rms_norm_mx_kernel<kElem, kV, true><<<static_cast<unsigned>(groups), 32 * warps, 0, st>>>(a, lg);
+        return cudaGetLastError();
+    }
+    rms_norm_mx_kernel<kElem, kV, false><<<static_cast<unsigned>(groups), 32 * warps, 0, st>>>(a, lg);
     return cudaGetLastError();
 }
 
@@ -305,8 +454,7 @@ cudaError_t norm_pieces(const RmsNormMx& a, int lg, int v, cudaStream_t st) {
         case 1: return norm_launch<kElem, 1>(a, lg, st);
         case 2: return norm_launch<kElem, 2>(a, lg, st);
         case 3: return norm_launch<kElem, 3>(a, lg, st);
-        case 4: return norm_launch<kElem, 4>(a, lg, st);
-        default: return norm_launch<kElem, 5>(a, lg, st);
+        default: return norm_launch<kElem, 4>(a, lg, st);
     }
 }
 
@@ -338,11 +486,12 @@ cudaError_t launch_rms_norm_mx(const RmsNormMx& args, int elem, cudaStream_t st)
     a.residual_align = row_align(a.residual, a.residual_stride);
     a.sum_align = row_align(a.sum, a.sum_stride);
     a.gain_align = row_align(a.gain, 0);
-    // up to five pieces a lane where the rows alone fill the GPU, fewer where they do
-    // not; 32 warps take four, which is all of the 32768 columns a row may have
+    a.inv_cols = 1.0f / static_cast<float>(a.cols);
+    // up to four pieces a lane where the rows alone fill the GPU, fewer where they do
+    // not; 32 warps take all of the 32768 columns a row may have
     const int64_t pieces = 16 * mx_atoms(a.cols);
     int lg = warps_log2(a.rows, pieces, 5);
-    while (lg < 5 && (int64_t{5} * 32 << lg) < pieces) ++lg;
+    while (lg < 5 && (int64_t{4} * 32 << lg) < pieces) ++lg;
     const int v = static_cast<int>((pieces + (32 << lg) - 1) / (32 << lg));
     return elem == ELEM_E2M1 ? norm_pieces<ELEM_E2M1>(a, lg, v, st) : norm_pieces<ELEM_E4M3>(a, lg, v, st);
 }

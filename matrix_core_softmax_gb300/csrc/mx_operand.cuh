@@ -50,17 +50,17 @@ __device__ __forceinline__ int64_t mx_scale_word(int64_t r, int a, int n_atoms) 
 // 127; codes are v / 2^X (exact: a power of two, no product leaves FP32's range)
 // rounded to the nearest element, ties to even.
 template <int kElem>
-__device__ __forceinline__ uint32_t mx_quantize8(const float (&v)[8], uint2& codes) {
-    float m = fmaxf(fmaxf(fmaxf(fabsf(v[0]), fabsf(v[1])), fmaxf(fabsf(v[2]), fabsf(v[3]))),
-                    fmaxf(fmaxf(fabsf(v[4]), fabsf(v[5])), fmaxf(fabsf(v[6]), fabsf(v[7]))));
+__device__ __forceinline__ uint32_t mx_quantize8(const float2 (&v)[4], uint2& codes) {
+    float m = fmaxf(fmaxf(fmaxf(fabsf(v[0].x), fabsf(v[0].y)), fmaxf(fabsf(v[1].x), fabsf(v[1].y))),
+                    fmaxf(fmaxf(fabsf(v[2].x), fabsf(v[2].y)), fmaxf(fabsf(v[3].x), fabsf(v[3].y))));
     m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
     m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
     const int e = static_cast<int>((__float_as_uint(m) + MxElem<kElem>::carry) >> 23) - MxElem<kElem>::emax;
     const uint32_t byte = static_cast<uint32_t>(max(e, 0));
     const float f = __uint_as_float((254u - byte) << 23);
-    float w[8];
+    float2 w[4];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) w[i] = v[i] * f;
+    for (int i = 0; i < 4; ++i) w[i] = __fmul2_rn(v[i], make_float2(f, f));
     if constexpr (kElem == ELEM_E2M1) {
         asm("{\n.reg .b8 a, b, c, d;\n"
             "cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n"
@@ -69,34 +69,40 @@ __device__ __forceinline__ uint32_t mx_quantize8(const float (&v)[8], uint2& cod
             "cvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n"
             "mov.b32 %0, {a, b, c, d};\n}"
             : "=r"(codes.x)
-            : "f"(w[0]), "f"(w[1]), "f"(w[2]), "f"(w[3]), "f"(w[4]), "f"(w[5]), "f"(w[6]), "f"(w[7]));
+            : "f"(w[0].x), "f"(w[0].y), "f"(w[1].x), "f"(w[1].y), "f"(w[2].x), "f"(w[2].y), "f"(w[3].x), "f"(w[3].y));
         codes.y = 0;
     } else {
-        codes.x = cvt_e4m3x4(w[0], w[1], w[2], w[3]);
-        codes.y = cvt_e4m3x4(w[4], w[5], w[6], w[7]);
+        codes.x = cvt_e4m3x4(w[0].x, w[0].y, w[1].x, w[1].y);
+        codes.y = cvt_e4m3x4(w[2].x, w[2].y, w[3].x, w[3].y);
     }
     return byte;
 }
 
-// Quantizes and stores piece p (8 elements; 16 lanes in a row hold a 128-element
-// piece, all of the warp calls it) of row r.
+// Where a row of an operand is: its codes, and the four scale bytes of its first piece.
+struct MxRow {
+    uint8_t *codes, *scales;
+};
 template <int kElem>
-__device__ __forceinline__ void mx_store8(const float (&v)[8], int64_t r, int p, int cols, int n_atoms, uint8_t* codes,
-                                          uint8_t* scales) {
+__device__ __forceinline__ MxRow mx_row(uint8_t* codes, uint8_t* scales, int64_t r, int n_atoms) {
+    return {codes + r * (n_atoms * 16 * MxElem<kElem>::piece_bytes), scales + mx_scale_word(r, 0, n_atoms)};
+}
+
+// Quantizes and stores piece p (8 elements; 16 lanes in a row hold a 128-element
+// piece, all of the warp calls it) of a row.
+template <int kElem>
+__device__ __forceinline__ void mx_store8(const float2 (&v)[4], MxRow row, int p, int cols, int n_atoms) {
     uint2 c;
     uint32_t byte = mx_quantize8<kElem>(v, c);
-    const int b = (p >> 2) & 3;
     if (8 * (p & ~3) >= cols) byte = 127u;  // a block behind the row's end
-    uint32_t word = byte << (8 * b);
+    uint32_t word = byte << (8 * ((p >> 2) & 3));
     word |= __shfl_xor_sync(0xFFFFFFFFu, word, 4);
     word |= __shfl_xor_sync(0xFFFFFFFFu, word, 8);
     if (p >= 16 * n_atoms) return;
-    uint8_t* dst = codes + (r * n_atoms * 16 + p) * MxElem<kElem>::piece_bytes;
     if constexpr (kElem == ELEM_E2M1)
-        *reinterpret_cast<uint32_t*>(dst) = c.x;
+        *reinterpret_cast<uint32_t*>(row.codes + 4 * p) = c.x;
     else
-        *reinterpret_cast<uint2*>(dst) = c;
-    if ((p & 15) == 0) *reinterpret_cast<uint32_t*>(scales + mx_scale_word(r, p >> 4, n_atoms)) = word;
+        *reinterpret_cast<uint2*>(row.codes + 8 * p) = c;
+    if ((p & 15) == 0) *reinterpret_cast<uint32_t*>(row.scales + (p >> 4) * kAtomBytes) = word;
 }
 
 }  // namespace fsa

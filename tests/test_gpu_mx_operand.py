@@ -97,7 +97,9 @@ def test_rows_behind_and_given_operands(fsa):
 
 
 NORMS = [(1, 1), (1, 32), (2, 33), (5, 128), (9, 200), (300, 64), (130, 1024), (3, 4100), (1, 5120), (700, 5120), (2, 20480),
-         (3, 20500), (1, 32768), (40, 8192)]
+         (3, 20500), (1, 32768), (40, 8192),
+         # rows enough for the blocks to stay (on 16 bytes and off them)
+         (2001, 5120), (3000, 1001), (20005, 64), (700, 16384), (9000, 200)]
 
 
 @pytest.mark.parametrize("fmt", ["mxfp8", "mxfp4"])
@@ -115,16 +117,17 @@ def test_norm(fsa, R, K, residual, fmt):
     ref.check_norm_operand(got, ref.norm(h.double(), g.double(), 1e-5))
 
 
-@pytest.mark.parametrize("R,K", [(6, 96), (5, 4096), (300, 5000)])
-def test_norm_strides_and_sums_in_place(fsa, R, K):
+@pytest.mark.parametrize("R,K", [(6, 96), (5, 4096), (300, 5000), (2500, 2048)])
+@pytest.mark.parametrize("pad,off", [(7, 3), (16, 8)])
+def test_norm_strides_and_sums_in_place(fsa, R, K, pad, off):
     g = to_dev(_bits((K + 1,), 3))[1:] if K % 8 == 0 else to_dev(_bits((K,), 3))   # (gain off 16 bytes)
-    xw, rw = to_dev(_bits((R, K + 24), 4)), to_dev(_bits((R, K + 7), 5))
-    x, r = xw[:, 8:8 + K], rw[:, 3:3 + K]
+    xw, rw = to_dev(_bits((R, K + 24), 4)), to_dev(_bits((R, K + pad), 5))
+    x, r = xw[:, 8:8 + K], rw[:, off:off + K]
     h = (x.float() + r.float()).bfloat16()
     y = ref.norm(h.double(), g.double(), 1e-6)
-    left = rw[:, :3].clone(), rw[:, 3 + K:].clone()
+    left = rw[:, :off].clone(), rw[:, off + K:].clone()
     op, total = fsa.rms_norm_mx(x, g, residual=r, out_sum=r)
-    assert total is r and torch.equal(r, h) and torch.equal(rw[:, :3], left[0]) and torch.equal(rw[:, 3 + K:], left[1])
+    assert total is r and torch.equal(r, h) and torch.equal(rw[:, :off], left[0]) and torch.equal(rw[:, off + K:], left[1])
     ref.check_norm_operand(op, y)
     # the same with the sum in x's place, and one residual row for all
     one = to_dev(_bits((1, K), 6))

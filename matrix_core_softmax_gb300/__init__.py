@@ -11,7 +11,6 @@ import ctypes
 import functools
 import os
 import threading
-from typing import NamedTuple
 
 import torch
 
@@ -432,7 +431,7 @@ _device = torch._C._cuda_getDevice
 _bf16, _f32, _i32, _i64, _u8 = torch.bfloat16, torch.float32, torch.int32, torch.int64, torch.uint8
 
 
-def _on(t: torch.Tensor, stream):
+def _on(t, stream):
     """Makes `stream` (by default the current one of t's device) and its device
     current: what the call allocates then belongs to that stream."""
     s = torch.cuda.current_stream(t.device) if stream is None else stream
@@ -645,16 +644,7 @@ def varlen_attention_fwd(q, k, v, cu_seqlens_q, cu_seqlens_k=None, *, causal: bo
 # ---- products of matrices in MX formats --------------------------------------
 
 
-class MxOperand(NamedTuple):
-    """A matrix [rows, cols] in an MX format as an operand of mx_linear (layout:
-    include/fsa.h): codes uint8 [rows, ceil(cols / 128) * 64 ("mxfp4") or * 128
-    ("mxfp8")], scales uint8 [ceil(rows / 128), ceil(cols / 128), 512]."""
-    codes: torch.Tensor
-    scales: torch.Tensor
-    cols: int
-    fmt: str
-
-
+# element and bytes of 128 codes of a row
 _OPERANDS = {"mxfp4": (ELEM_E2M1, 64), "mxfp8": (ELEM_E4M3, 128)}
 
 
@@ -665,87 +655,122 @@ def _operand_format(fmt: str):
         raise ValueError(f"an operand's format is mxfp4 or mxfp8, not {fmt!r}") from None
 
 
+class MxOperand:
+    """A matrix [rows, cols] in an MX format as an operand of mx_linear (layout:
+    include/fsa.h): codes uint8 [rows, ceil(cols / 128) * 64 ("mxfp4") or * 128
+    ("mxfp8")], scales uint8 [ceil(rows / 128), ceil(cols / 128), 512].
+
+    MxOperand(codes, scales, cols, fmt) is one of given tensors; mx_new_operand, mx_pack
+    and rms_norm_mx make one in a single allocation, whose codes and scales are views."""
+    __slots__ = ("rows", "cols", "fmt", "elem", "_dev", "_bytes", "_codes", "_scales")
+
+    def __init__(self, codes: torch.Tensor, scales: torch.Tensor, cols: int, fmt: str):
+        elem, width = _operand_format(fmt)
+        atoms, shape = (cols + 127) >> 7, codes.shape
+        rows = shape[0] if shape else 0
+        if cols < 1 or shape != (rows, atoms * width) or scales.shape != ((rows + 127) >> 7, atoms, 512):
+            raise ValueError(f"codes {list(shape)} and scales {list(scales.shape)} are not those of {cols} columns in {fmt}")
+        if codes.dtype is not _u8 or scales.dtype is not _u8 or codes.get_device() != scales.get_device():
+            raise ValueError("codes and scales must be uint8 tensors on one device")
+        if not codes.is_contiguous() or not scales.is_contiguous():
+            raise ValueError("codes and scales must be contiguous")
+        self.rows, self.cols, self.fmt, self.elem = rows, cols, fmt, elem
+        self._dev, self._bytes, self._codes, self._scales = codes.get_device(), None, codes, scales
+
+    @classmethod
+    def _new(cls, rows: int, cols: int, fmt: str, device):
+        elem, width = _operand_format(fmt)
+        if rows < 0 or cols < 1:
+            raise ValueError("an operand has at least one column")
+        self = cls.__new__(cls)
+        atoms = (cols + 127) >> 7
+        data = torch.empty(atoms * (rows * width + ((rows + 127) >> 7) * 512), dtype=_u8, device=device)
+        self.rows, self.cols, self.fmt, self.elem = rows, cols, fmt, elem
+        self._dev, self._bytes, self._codes, self._scales = data.get_device(), data, None, None
+        return self
+
+    def _pointers(self):
+        if self._bytes is None:
+            return self._codes.data_ptr(), self._scales.data_ptr()
+        at = self._bytes.data_ptr()
+        return at, at + self.rows * ((self.cols + 127) >> 7) * _OPERANDS[self.fmt][1]
+
+    @property
+    def codes(self) -> torch.Tensor:
+        if self._codes is None:
+            pitch = ((self.cols + 127) >> 7) * _OPERANDS[self.fmt][1]
+            self._codes = self._bytes[:self.rows * pitch].view(self.rows, pitch)
+        return self._codes
+
+    @property
+    def scales(self) -> torch.Tensor:
+        if self._scales is None:
+            atoms = (self.cols + 127) >> 7
+            self._scales = self._bytes[self.rows * atoms * _OPERANDS[self.fmt][1]:].view((self.rows + 127) >> 7, atoms, 512)
+        return self._scales
+
+    @property
+    def device(self) -> torch.device:
+        return (self._codes if self._bytes is None else self._bytes).device
+
+    def __repr__(self):
+        return f"MxOperand(rows={self.rows}, cols={self.cols}, fmt={self.fmt!r}, device={str(self.device)!r})"
+
+
 def mx_new_operand(rows: int, cols: int, fmt: str, device="cuda") -> MxOperand:
     """An operand whose contents are arbitrary, for mx_pack and rms_norm_mx to fill."""
-    _, width = _operand_format(fmt)
-    if rows < 0 or cols < 1:
-        raise ValueError("an operand has at least one column")
-    atoms = -(-cols // 128)
-    return MxOperand(torch.empty((rows, atoms * width), dtype=_u8, device=device),
-                     torch.empty((-(-rows // 128), atoms, 512), dtype=_u8, device=device), cols, fmt)
-
-
-def _operand(op: MxOperand, name: str, dev: int):
-    """(rows, element) of an operand, whose tensors are checked against its shape."""
-    elem, width = _operand_format(op.fmt)
-    c, s = op.codes, op.scales
-    atoms = -(-op.cols // 128)
-    rows = c.shape[0]
-    if c.dtype is not _u8 or s.dtype is not _u8 or c.get_device() != dev or s.get_device() != dev:
-        raise ValueError(f"codes and scales of {name} must be uint8 tensors on cuda:{dev}")
-    if c.shape != (rows, atoms * width) or s.shape != (-(-rows // 128), atoms, 512) or op.cols < 1:
-        raise ValueError(f"{name}: codes {list(c.shape)} and scales {list(s.shape)} are not those of {op.cols} columns "
-                         f"in {op.fmt}")
-    if not c.is_contiguous() or not s.is_contiguous():
-        raise ValueError(f"codes and scales of {name} must be contiguous")
-    return rows, elem
+    return MxOperand._new(rows, cols, fmt, device)
 
 
 def _rows(t: torch.Tensor, name: str, shape, dev: int) -> int:
     """A CUDA bf16 tensor [rows, cols] of the given shape whose rows are contiguous;
     returns their distance."""
-    st = t.stride()
     if t.dtype is not _bf16 or t.shape != shape or t.get_device() != dev:
         raise ValueError(f"{name} must be a bf16 tensor {list(shape)} on cuda:{dev}")
-    if st[1] != 1 and shape[1] > 1:
+    step, one = t.stride()
+    if one != 1 and shape[1] > 1:
         raise ValueError(f"the rows of {name} must be contiguous")
-    return st[0] if shape[0] > 1 else shape[1]  # (a lone row's stride is arbitrary)
+    return step if shape[0] > 1 else shape[1]  # (a lone row's stride is arbitrary)
 
 
-def _filled(out, shape, fmt: str, dev: int, device) -> tuple:
-    """The operand that a call fills, new or given, and its element."""
+def _filled(out, shape, fmt: str, dev: int, device) -> MxOperand:
+    """The operand that a call fills, new or given."""
     if out is None:
-        out = mx_new_operand(*shape, fmt, device)
-        return out, _operand_format(fmt)[0]
-    rows, elem = _operand(out, "out", dev)
-    if (rows, out.cols) != tuple(shape) or out.fmt != fmt:
-        raise ValueError(f"out must be an operand of {list(shape)} in {fmt}")
-    return out, elem
+        return MxOperand._new(*shape, fmt, device)
+    if (out.rows, out.cols) != tuple(shape) or out.fmt != fmt or out._dev != dev:
+        raise ValueError(f"out must be an operand of {list(shape)} in {fmt} on cuda:{dev}")
+    return out
 
 
 def mx_pack(x, fmt: str = "mxfp4", *, out=None, stream=None) -> MxOperand:
     """fsa_mx_pack: x, CUDA bf16 [rows, cols] (contiguous rows at any distance),
     quantized into an operand of mx_linear (`out`, or a new one)."""
-    dev = x.get_device()
-    if dev < 0 or x.dim() != 2:
+    dev, shape = x.get_device(), x.shape
+    if dev < 0 or len(shape) != 2:
         raise ValueError("x must be a CUDA tensor [rows, cols]")
     if stream is not None or dev != _device():
         with _on(x, stream):
             return mx_pack(x, fmt, out=out)
-    shape = x.shape
-    stride = _rows(x, "x", shape, dev)
-    op, elem = _filled(out, shape, fmt, dev, x.device)
-    _check(load().fsa_mx_pack(x.data_ptr(), stride, shape[0], shape[1], elem, op.codes.data_ptr(), op.scales.data_ptr(),
-                              _raw_stream(dev)), "fsa_mx_pack")
+    step = _rows(x, "x", shape, dev)
+    op = _filled(out, shape, fmt, dev, x.device)
+    _check(load().fsa_mx_pack(x.data_ptr(), step, *shape, op.elem, *op._pointers(), _raw_stream(dev)), "fsa_mx_pack")
     return op
 
 
 def mx_unpack(op: MxOperand, *, out=None, stream=None):
     """fsa_mx_unpack: an operand's values as bf16 [rows, cols]."""
-    dev = op.codes.get_device()
+    dev = op._dev
     if dev < 0:
         raise ValueError("op must be an operand on a CUDA device")
     if stream is not None or dev != _device():
-        with _on(op.codes, stream):
+        with _on(op, stream):
             return mx_unpack(op, out=out)
-    rows, elem = _operand(op, "op", dev)
-    shape = (rows, op.cols)
+    rows, cols = op.rows, op.cols
     if out is None:
-        out, stride = torch.empty(shape, dtype=_bf16, device=op.codes.device), op.cols
+        out, step = torch.empty((rows, cols), dtype=_bf16, device=op.device), cols
     else:
-        stride = _rows(out, "out", shape, dev)
-    _check(load().fsa_mx_unpack(op.codes.data_ptr(), op.scales.data_ptr(), rows, op.cols, elem, out.data_ptr(), stride,
-                                _raw_stream(dev)), "fsa_mx_unpack")
+        step = _rows(out, "out", (rows, cols), dev)
+    _check(load().fsa_mx_unpack(*op._pointers(), rows, cols, op.elem, out.data_ptr(), step, _raw_stream(dev)), "fsa_mx_unpack")
     return out
 
 
@@ -755,28 +780,26 @@ def rms_norm_mx(x, gain, *, residual=None, eps: float = 1e-6, fmt: str = "mxfp8"
     mx_linear.  With a residual, bf16 like x, the norm is that of h = x + residual
     (rounded to bf16), and (operand, h) is returned; out_sum, written instead of a new
     tensor, may be x or residual itself."""
-    dev = x.get_device()
-    if dev < 0 or x.dim() != 2:
+    dev, shape = x.get_device(), x.shape
+    if dev < 0 or len(shape) != 2:
         raise ValueError("x must be a CUDA tensor [rows, cols]")
     if stream is not None or dev != _device():
         with _on(x, stream):
             return rms_norm_mx(x, gain, residual=residual, eps=eps, fmt=fmt, out=out, out_sum=out_sum)
-    shape = x.shape
-    rows, cols = shape
-    xs, rs, ss, rp, sp = _rows(x, "x", shape, dev), 0, 0, None, None
-    _plain(gain, "gain", _bf16, (cols,), dev)
+    step, res, res_step, total, total_step = _rows(x, "x", shape, dev), None, 0, None, 0
+    _plain(gain, "gain", _bf16, shape[1:], dev)
     if residual is not None:
-        rs, rp = _rows(residual, "residual", shape, dev), residual.data_ptr()
+        res_step, res = _rows(residual, "residual", shape, dev), residual.data_ptr()
         if out_sum is None:
-            out_sum, ss = torch.empty(shape, dtype=_bf16, device=x.device), cols
+            out_sum, total_step = torch.empty(shape, dtype=_bf16, device=x.device), shape[1]
         else:
-            ss = _rows(out_sum, "out_sum", shape, dev)
-        sp = out_sum.data_ptr()
+            total_step = _rows(out_sum, "out_sum", shape, dev)
+        total = out_sum.data_ptr()
     elif out_sum is not None:
         raise ValueError("there is no sum without a residual")
-    op, elem = _filled(out, shape, fmt, dev, x.device)
-    _check(load().fsa_rms_norm_mx(x.data_ptr(), xs, rp, rs, gain.data_ptr(), eps, rows, cols, elem, sp, ss,
-                                  op.codes.data_ptr(), op.scales.data_ptr(), _raw_stream(dev)), "fsa_rms_norm_mx")
+    op = _filled(out, shape, fmt, dev, x.device)
+    _check(load().fsa_rms_norm_mx(x.data_ptr(), step, res, res_step, gain.data_ptr(), eps, *shape, op.elem, total, total_step,
+                                  *op._pointers(), _raw_stream(dev)), "fsa_rms_norm_mx")
     return op if residual is None else (op, out_sum)
 
 
@@ -786,26 +809,24 @@ def mx_linear(x: MxOperand, w: MxOperand, *, out=None, wait_timeout_ms: int = 0,
     and mxfp8.  out: written instead of a new tensor (contiguous rows at any distance
     that keeps them apart).  wait_timeout_ms: limit of the kernel's bounded waits (0:
     2000)."""
-    dev = x.codes.get_device()
-    if dev < 0:
-        raise ValueError("x must be an operand on a CUDA device")
+    dev = x._dev
+    if dev < 0 or w._dev != dev:
+        raise ValueError("x and w must be operands on one CUDA device")
     if stream is not None or dev != _device():
-        with _on(x.codes, stream):
+        with _on(x, stream):
             return mx_linear(x, w, out=out, wait_timeout_ms=wait_timeout_ms, debug_flags=debug_flags)
-    T, ex = _operand(x, "x", dev)
-    N, ew = _operand(w, "w", dev)
-    K = x.cols
+    T, N, K = x.rows, w.rows, x.cols
     if w.cols != K:
         raise ValueError(f"x has {K} columns and w {w.cols}")
     if out is None:
-        out, stride = torch.empty((T, N), dtype=_bf16, device=x.codes.device), N
+        out, step = torch.empty((T, N), dtype=_bf16, device=x.device), N
     else:
-        stride = _rows(out, "out", (T, N), dev)
+        step = _rows(out, "out", (T, N), dev)
     opt = None
     if wait_timeout_ms or debug_flags:
         opt = ctypes.byref(Options(wait_timeout_ms=wait_timeout_ms, debug_flags=debug_flags))
-    _check(load().fsa_mx_linear(x.codes.data_ptr(), x.scales.data_ptr(), ex, w.codes.data_ptr(), w.scales.data_ptr(), ew, T,
-                                N, K, out.data_ptr(), stride, opt, _raw_stream(dev)), "fsa_mx_linear")
+    _check(load().fsa_mx_linear(*x._pointers(), x.elem, *w._pointers(), w.elem, T, N, K, out.data_ptr(), step, opt,
+                                _raw_stream(dev)), "fsa_mx_linear")
     return out
 
 

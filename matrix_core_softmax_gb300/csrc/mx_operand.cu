@@ -370,6 +370,7 @@ __global__ void __launch_bounds__(kThreads, kThreads == 256 ? 3 : 1) rms_norm_mx
                         mbar_wait(&full[(st + i) % stages][mine], st + i < stages ? ph : ph ^ 1u, a.timeout_ns, &dummy);
             }
         }
+        __syncwarp();
         const uint8_t* src = at + st * slot_bytes;
         uint16_t* sum = static_cast<uint16_t*>(a.sum) + r * a.sum_stride;
         uint4 h[kV];

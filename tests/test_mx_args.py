@@ -80,3 +80,28 @@ def test_binding_refuses_host_and_mismatched_tensors():
                  lambda: fsa.mx_new_operand(4, 64, "mxfp6", device="cpu")):
         with pytest.raises(ValueError):
             call()
+
+
+def test_operand_of_given_tensors():
+    codes, scales = torch.zeros(130, 128, dtype=torch.uint8), torch.zeros(2, 2, 512, dtype=torch.uint8)
+    op = fsa.MxOperand(codes, scales, 200, "mxfp4")
+    assert op.codes is codes and op.scales is scales and (op.rows, op.cols, op.fmt) == (130, 200, "mxfp4")
+    for bad in ((codes, scales, 128, "mxfp4"), (codes, scales, 300, "mxfp4"), (codes, scales, 200, "mxfp8"),
+                (codes, scales, 200, "mxfp6"), (codes, scales[:1], 200, "mxfp4"), (codes[:, :64], scales, 200, "mxfp4"),
+                (codes.int(), scales, 200, "mxfp4"), (codes, scales.float(), 200, "mxfp4"), (codes.T, scales, 200, "mxfp4"),
+                (torch.zeros(130, 256, dtype=torch.uint8)[:, ::2], scales, 200, "mxfp4"), (codes[0], scales, 200, "mxfp4"),
+                (codes, scales, 0, "mxfp4")):
+        with pytest.raises(ValueError):
+            fsa.MxOperand(*bad)
+
+
+@pytest.mark.parametrize("rows,cols,fmt", [(0, 5, "mxfp4"), (1, 1, "mxfp8"), (200, 300, "mxfp4"), (128, 128, "mxfp8")])
+def test_new_operand_holds_both_parts(rows, cols, fmt):
+    op = fsa.mx_new_operand(rows, cols, fmt, device="cpu")
+    atoms, groups = -(-cols // 128), -(-rows // 128)
+    assert op.codes.shape == (rows, atoms * (64 if fmt == "mxfp4" else 128)) and op.scales.shape == (groups, atoms, 512)
+    assert op.codes is op.codes and op.codes.is_contiguous() and op.scales.is_contiguous()
+    op.codes.fill_(1), op.scales.fill_(2)
+    assert (op.codes == 1).all() and (op.scales == 2).all()
+    if rows:
+        assert op._pointers() == (op.codes.data_ptr(), op.scales.data_ptr())

@@ -86,6 +86,28 @@ struct Bf16Launch {
 };
 cudaError_t launch_bf16_attention(const Bf16Launch& a, cudaStream_t st);
 
+// A launch that may begin while the kernel before it in the stream ends
+// (programmatic dependent launch): its threads read and write global memory only
+// behind grid_wait(), or in the order of a thread that has passed it.
+template <class... Params, class... Args>
+cudaError_t launch_early(void (*kernel)(Params...), unsigned grid, unsigned threads, size_t smem, cudaStream_t st, unsigned cluster,
+                         const Args&... args) {
+    cudaLaunchAttribute at[2]{};
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    at[1].id = cudaLaunchAttributeClusterDimension;
+    at[1].val.clusterDim.x = cluster;
+    at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cfg.attrs = at;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 // Once per device and kernel: the dynamic shared memory it may use, and, where a
 // register split is built on it, the registers of its launch (0: not checked).
 // The short calls save these two queries.

@@ -106,6 +106,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         }
         mbar_init(&sm.done, 1);
         fence_mbar_init();
+        grid_wait();
         for (int i = 0; i < ahead; ++i) load(i, i);  // (the other warps need not be there yet)
     }
     if (warp == kWarpMma) {
@@ -115,6 +116,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
+    grid_launch_next();  // (the next kernel's CTAs find this one's tensor memory taken)
     const uint32_t tmem = sm.tmem_base;
     bool ok = true;
     // give-up and exit of a loader: every copy lands before the CTA goes on, whoever gives
@@ -142,6 +144,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         }
     } else if (warp == kWarpScales) {
         if (lane == 0) {
+            grid_wait();
             const int64_t at = static_cast<int64_t>(first) * kAtoms * kAtomBytes;
             const uint8_t* ws = p.ws + static_cast<int64_t>(n_tile) * p.n_atoms * kAtomBytes + at;
             const uint8_t* xs = p.xs + static_cast<int64_t>(t0 / 128) * p.n_atoms * kAtomBytes + at;
@@ -318,7 +321,7 @@ __device__ __forceinline__ void pair_tile(const PairParams& p, int i, int& t_til
 }
 
 template <int kMode>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
+__global__ void __launch_bounds__(kPairThreads, 1)
     mx_linear_pair_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_w, const PairParams p) {
     extern __shared__ __align__(1024) uint8_t ring[];
     // the 128-byte-swizzled tiles need a 1024-byte aligned base (the same in both CTAs)
@@ -353,6 +356,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     __syncthreads();
     cluster_sync();  // both CTAs' barriers are there
     tc_fence_after();
+    grid_launch_next();  // (the next kernel's CTAs find this one's tensor memory taken)
     const uint32_t tmem = sm.tmem_base;
     auto give_up = [&] {
         sm.abort = 1;
@@ -373,6 +377,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
 
     if (warp >= kPairLoad && warp < kPairLoad + kPairLoaders) {
         if (lane == 0) {
+            grid_wait();
             const int what = warp - kPairLoad;
             const int64_t x_groups = mx_atoms(p.T), w_groups = mx_atoms(p.N);
             int issued = 0;
@@ -559,8 +564,8 @@ cudaError_t launch_pair(const MxLinearLaunch& a, cudaStream_t st) {
     p.err_word = a.err_word;
     p.skip = a.debug_flags & 1;
     const int tiles = p.t_tiles * p.n_tiles;
-    mx_linear_pair_kernel<kMode><<<2 * (tiles < 76 ? tiles : 76), kPairThreads, pair_smem(kMode), st>>>(*a.tm_x, *a.tm_w, p);
-    return cudaGetLastError();
+    return launch_early(mx_linear_pair_kernel<kMode>, 2 * (tiles < kSms / 2 ? tiles : kSms / 2), kPairThreads, pair_smem(kMode), st, 2,
+                        *a.tm_x, *a.tm_w, p);
 }
 
 int mode_of(int x_elem, int w_elem) { return w_elem == ELEM_E4M3 ? X8W8 : x_elem == ELEM_E4M3 ? X8W4 : X4W4; }
@@ -573,18 +578,8 @@ cudaError_t launch(const MxLinearLaunch& a, Params p, int tiles, cudaStream_t st
     const int smem = tiles * p.split <= kSms ? kSmemOne : kSmemTwo;
     p.stages = (smem - 1024 - kSfSlots * kSfBytes) / stage_bytes(p.n_tok);
     if (p.stages > kMaxStages) p.stages = kMaxStages;
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(static_cast<unsigned>(tiles) * p.split);
-    cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = st;
-    cudaLaunchAttribute at{};
-    at.id = cudaLaunchAttributeClusterDimension;
-    at.val.clusterDim.x = p.split;
-    at.val.clusterDim.y = at.val.clusterDim.z = 1;
-    cfg.attrs = &at;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, mx_linear_kernel<kMode>, *a.tm_x, *a.tm_w, p);
+    return launch_early(mx_linear_kernel<kMode>, static_cast<unsigned>(tiles) * p.split, kThreads, smem, st, p.split, *a.tm_x,
+                        *a.tm_w, p);
 }
 
 }  // namespace

@@ -92,6 +92,8 @@ __global__ void __launch_bounds__(32 * kWarps) mx_pack_kernel(const uint16_t* x,
                                                               int align, uint8_t* codes, uint8_t* scales) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int64_t r = blockIdx.x * static_cast<int64_t>(kWarps >> lg) + (warp >> lg);
+    grid_launch_next();
+    grid_wait();
     if (r >= rows) return;
     const int n_atoms = static_cast<int>(mx_atoms(cols)), step = 32 << lg;
     const uint16_t* row = x + r * stride;
@@ -151,6 +153,8 @@ __global__ void __launch_bounds__(32 * kWarps) mx_unpack_kernel(const uint8_t* _
                                                                 int64_t stride) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int64_t r = blockIdx.x * static_cast<int64_t>(kWarps >> lg) + (warp >> lg);
+    grid_launch_next();
+    grid_wait();
     if (r >= rows) return;
     const int n_atoms = static_cast<int>(mx_atoms(cols)), step = 32 << lg;
     uint16_t* row = out + r * stride;
@@ -290,6 +294,8 @@ __global__ void __launch_bounds__(kWide ? 1024 : 512) rms_norm_mx_kernel(const R
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, n_warps = blockDim.x >> 5;
     const int64_t r = blockIdx.x * static_cast<int64_t>(n_warps >> lg) + (warp >> lg);
     const int first = (warp & ((1 << lg) - 1)) * 32 + lane, step = 32 << lg;
+    grid_launch_next();
+    grid_wait();
     if (r >= a.rows) return;
     uint4 h[kV], g[kV];
     const uint16_t* x = static_cast<const uint16_t*>(a.x) + r * a.x_stride;
@@ -336,7 +342,9 @@ __global__ void __launch_bounds__(kThreads, kThreads == 256 ? 3 : 1) rms_norm_mx
             for (int j = 0; j < per; ++j) mbar_init(&full[i][j], 1);
         fence_mbar_init();
     }
+    grid_launch_next();
     __syncthreads();
+    grid_wait();
     const int64_t hop = static_cast<int64_t>(per) * gridDim.x;
     int64_t r = static_cast<int64_t>(blockIdx.x) * per + mine;
     auto fetch = [&](int64_t r, int st) {
@@ -437,16 +445,11 @@ cudaError_t norm_launch(const RmsNormMx& a, int lg, cudaStream_t st) {
             const auto kernel = warps == 8 ? rms_norm_mx_ring_kernel<kElem, kV, 256> : rms_norm_mx_ring_kernel<kElem, kV, 512>;
             const cudaError_t e = (warps == 8 ? small : large)(reinterpret_cast<const void*>(kernel), 222 * 1024, 0);
             if (e != cudaSuccess) return e;
-            kernel<<<kSms * blocks, 32 * warps, ring.smem, st>>>(a, lg, ring.stages);
-            return cudaGetLastError();
+            return launch_early(kernel, kSms * blocks, 32 * warps, ring.smem, st, 1, a, lg, ring.stages);
         }
     }
-    if (lg == 5) {
-        rms_norm_mx_kernel<kElem, kV, true><<<static_cast<unsigned>(groups), 32 * warps, 0, st>>>(a, lg);
-        return cudaGetLastError();
-    }
-    rms_norm_mx_kernel<kElem, kV, false><<<static_cast<unsigned>(groups), 32 * warps, 0, st>>>(a, lg);
-    return cudaGetLastError();
+    return launch_early(lg == 5 ? rms_norm_mx_kernel<kElem, kV, true> : rms_norm_mx_kernel<kElem, kV, false>,
+                        static_cast<unsigned>(groups), 32 * warps, 0, st, 1, a, lg);
 }
 
 template <int kElem>
@@ -466,9 +469,8 @@ cudaError_t launch_mx_pack(const void* x, int64_t stride, int64_t rows, int cols
     const int lg = warps_log2(rows, 16 * mx_atoms(cols), 3);
     const unsigned grid = static_cast<unsigned>((rows + (kWarps >> lg) - 1) / (kWarps >> lg));
     auto kernel = elem == ELEM_E2M1 ? mx_pack_kernel<ELEM_E2M1> : mx_pack_kernel<ELEM_E4M3>;
-    kernel<<<grid, 32 * kWarps, 0, st>>>(static_cast<const uint16_t*>(x), stride, rows, cols, lg, row_align(x, stride), codes,
-                                         scales);
-    return cudaGetLastError();
+    return launch_early(kernel, grid, 32 * kWarps, 0, st, 1, static_cast<const uint16_t*>(x), stride, rows, cols, lg,
+                        row_align(x, stride), codes, scales);
 }
 
 cudaError_t launch_mx_unpack(const uint8_t* codes, const uint8_t* scales, int64_t rows, int cols, int elem, void* out,
@@ -476,9 +478,8 @@ cudaError_t launch_mx_unpack(const uint8_t* codes, const uint8_t* scales, int64_
     const int lg = warps_log2(rows, 16 * mx_atoms(cols), 3);
     const unsigned grid = static_cast<unsigned>((rows + (kWarps >> lg) - 1) / (kWarps >> lg));
     auto kernel = elem == ELEM_E2M1 ? mx_unpack_kernel<ELEM_E2M1> : mx_unpack_kernel<ELEM_E4M3>;
-    kernel<<<grid, 32 * kWarps, 0, st>>>(codes, scales, rows, cols, lg, row_align(out, stride), static_cast<uint16_t*>(out),
-                                         stride);
-    return cudaGetLastError();
+    return launch_early(kernel, grid, 32 * kWarps, 0, st, 1, codes, scales, rows, cols, lg, row_align(out, stride),
+                        static_cast<uint16_t*>(out), stride);
 }
 
 cudaError_t launch_rms_norm_mx(const RmsNormMx& args, int elem, cudaStream_t st) {

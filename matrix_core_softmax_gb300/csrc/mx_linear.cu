@@ -29,8 +29,10 @@ enum Mode : int { X4W4 = 0, X8W4 = 1, X8W8 = 2 };
 // their ranks.
 constexpr int kSms = 152;
 constexpr int kFixed = 8;           // (see mx_linear_plan)
-constexpr int kThreads = 224;       // warps 0-3 output, 4 copies of codes, 5 products, 6 copies of scales
-constexpr int kWarpLoad = 4, kWarpMma = 5, kWarpScales = 6;
+// warps 0-3 output; 4, 5 copies of w and of x (one warp for both: 560 clocks a step); 6
+// products; 7 copies of scales
+constexpr int kThreads = 256;
+constexpr int kWarpLoad = 4, kWarpLoadX = 5, kWarpMma = 6, kWarpScales = 7;
 constexpr int kMaxStages = 12;
 // Scales come for 512 elements of K at once, in a ring of their own: a copy holds the
 // SM's copy engine up for 110 clocks however small it is.
@@ -86,18 +88,21 @@ __global__ void __launch_bounds__(kThreads, 2)
     const int first = static_cast<int>(static_cast<int64_t>(steps) * rank / p.split);
     const int mine = static_cast<int>(static_cast<int64_t>(steps) * (rank + 1) / p.split) - first;
 
-    // step i of this CTA's into stage st (one lane)
+    // w's, or x's, part of step i of this CTA's into stage st (one lane)
+    const bool is_x = warp == kWarpLoadX;
     auto load = [&](int i, int st) {
         // (a spread copy counts the bytes that it reads, 64 a row)
-        mbar_arrive_expect_tx(&sm.full[st], 128 * (kMode == X8W4 ? 64 : 128) + p.n_tok * 128);
-        tma_load_2d(w_tiles + st * 16384, &tm_w, &sm.full[st], (first + i) * 128, n0);
-        tma_load_2d(x_tiles + st * p.n_tok * 128, &tm_x, &sm.full[st], (first + i) * 128, t0);
+        mbar_arrive_expect_tx(&sm.full[st], is_x ? p.n_tok * 128 : 128 * (kMode == X8W4 ? 64 : 128));
+        if (is_x)
+            tma_load_2d(x_tiles + st * p.n_tok * 128, &tm_x, &sm.full[st], (first + i) * 128, t0);
+        else
+            tma_load_2d(w_tiles + st * 16384, &tm_w, &sm.full[st], (first + i) * 128, n0);
     };
     const int ahead = min(mine, p.stages);
     if (warp == kWarpLoad && lane == 0) {
         sm.abort = 0;
         for (int i = 0; i < p.stages; ++i) {
-            mbar_init(&sm.full[i], i == 1 && p.skip ? 2 : 1);
+            mbar_init(&sm.full[i], i == 1 && p.skip ? 3 : 2);
             mbar_init(&sm.empty[i], 1);
         }
         for (int i = 0; i < kSfSlots; ++i) {
@@ -127,9 +132,13 @@ __global__ void __launch_bounds__(kThreads, 2)
         for (int i = max(0, issued - stages); i < issued; ++i) mbar_wait(full + i % stages, (i / stages) & 1, p.timeout_ns, &dummy);
     };
 
-    if (warp == kWarpLoad) {
+    if (warp == kWarpLoad || is_x) {
         if (lane == 0) {
-            int st = ahead == p.stages ? 0 : ahead, issued = ahead;
+            int st = 0, issued = 0;
+            if (is_x) grid_wait();
+            for (; issued < ahead; ++issued)
+                if (is_x) load(issued, issued);  // (w's are under way)
+            if (ahead < p.stages) st = ahead;
             uint32_t ph = 1;
             for (; issued < mine; ++issued) {
                 ok = mbar_wait(&sm.empty[st], ph ^ 1u, p.timeout_ns, &sm.abort);

@@ -635,7 +635,7 @@ def varlen_attention_fwd(q, k, v, cu_seqlens_q, cu_seqlens_k=None, *, causal: bo
     if wait_timeout_ms or debug_flags:
         opt = Options(sm_scale=sm_scale, wait_timeout_ms=wait_timeout_ms, debug_flags=debug_flags)
         _check(load().fsa_varlen_attention_fwd_ex(*args, ctypes.byref(opt), _raw_stream(dev)),
-               "fsa_varlen_attention_fwd_ex", "fsa_mx_pack", "fsa_mx_unpack", "fsa_rms_norm_mx", "fsa_mx_linear")
+               "fsa_varlen_attention_fwd_ex")
     else:
         _check(load().fsa_varlen_attention_fwd(*args, sm_scale, _raw_stream(dev)), "fsa_varlen_attention_fwd")
     return (o, lse) if return_lse else o

@@ -41,6 +41,8 @@ SHAPES = [
     # many tiles of many tokens
     (1300, 4000, 300), (2305, 2100, 257), (20000, 200, 128), (300, 10000, 640), (129, 20000, 96), (2048, 2560, 1024),
     (5000, 1300, 33),
+    # long rows
+    (2, 130, 100000), (300, 200, 40001),
 ]
 
 
@@ -150,6 +152,18 @@ def test_extreme_scales(fsa, fx, fw):
         w[:, 32 * b:32 * b + 32] *= 2.0 ** -e
     x, w = fsa.mx_pack(x.bfloat16(), fx), fsa.mx_pack(w.bfloat16(), fw)
     ref.check_product(fsa.mx_linear(x, w), ref.values(x), ref.values(w))
+
+
+def test_outputs_beyond_32_bits(fsa):
+    # 2.6e9 outputs; a few rows and columns from everywhere, the last ones among them
+    T, N, K = 65700, 40000, 64
+    x, w = _operands(fsa, T, N, K, "mxfp8", "mxfp4")
+    y = fsa.mx_linear(x, w)
+    assert fsa.get_device_error() == 0
+    t = torch.tensor([0, 1, 33000, 53687, 53688, 65535, T - 1], device="cuda")
+    n = torch.tensor([0, 127, 128, 20001, N - 1], device="cuda")
+    ref.check_product(y[t], ref.values(x)[t.cpu()], ref.values(w))
+    ref.check_product(y[:, n].contiguous(), ref.values(x), ref.values(w)[n.cpu()])
 
 
 def test_nothing_to_do(fsa):

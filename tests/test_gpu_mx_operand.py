@@ -152,6 +152,27 @@ def test_norm_ranges(fsa, K, size, eps):
     ref.check_norm_operand(op, y)
 
 
+@pytest.mark.parametrize("fmt", ["mxfp8", "mxfp4"])
+def test_offsets_beyond_32_bits(fsa, fmt):
+    # 2.3e9 elements; the rows around 2^31 elements and 2^32 bytes and the last ones
+    R, K = 70000, 32768
+    at = [0, 1, 32767, 32768, 65535, 65536, 65537, R - 1]
+    bits, gain = _bits((len(at), K), 1), _bits((K,), 2)
+    x = torch.zeros(R, K, dtype=torch.bfloat16, device="cuda")
+    x[at] = to_dev(bits)
+    op = fsa.mx_pack(x, fmt)
+    back = fsa.mx_unpack(op)
+    small = fsa.mx_pack(to_dev(bits), fmt)
+    assert torch.equal(back[at], fsa.mx_unpack(small)) and torch.equal(op.codes[at], small.codes)
+    assert (back[2:30000] == 0).all() and (back[40000:60000] == 0).all()
+    del back
+    g = to_dev(gain)
+    want, total = fsa.rms_norm_mx(to_dev(bits), g, residual=to_dev(bits), fmt=fmt)
+    got, h = fsa.rms_norm_mx(x, g, residual=x, fmt=fmt, out=op)
+    assert got is op and torch.equal(got.codes[at], want.codes) and torch.equal(h[at], total)
+    assert fsa.get_device_error() == 0
+
+
 def test_norm_rows_stand_alone(fsa):
     # a row of NaN or infinity does not reach its neighbours
     for R, K in ((9, 64), (5, 5120)):

@@ -32,7 +32,7 @@ def _check_pack(op, bits):
 
 
 SHAPES = [(1, 1), (1, 32), (3, 31), (2, 33), (5, 127), (130, 128), (7, 129), (257, 96), (4, 4100), (1, 8192), (33, 640),
-          (1000, 300), (5000, 64)]
+          (1000, 300), (5000, 64), (5001, 100), (4870, 128), (100, 2100)]
 
 
 @pytest.mark.parametrize("fmt", ["mxfp4", "mxfp8"])

@@ -40,6 +40,7 @@ constexpr int kSfAtoms = 4, kSfSlots = 2, kSfBytes = 2 * kSfAtoms * kAtomBytes;
 constexpr int kSmemTwo = 112 * 1024, kSmemOne = 224 * 1024;  // of a CTA, two or one an SM
 constexpr uint32_t kTmemCols = 256; // of two CTAs: all 512
 constexpr uint32_t kColSf = 128;    // accumulator at 0, scales of slot s at 128 + 32 s
+constexpr int kMaxSplit = 8;       // portable cluster
 constexpr int kPartRow = 132;       // FP32 of a token's 128 outputs in shared memory, padded
 
 struct Params {
@@ -257,11 +258,19 @@ __global__ void __launch_bounds__(kThreads, 2)
         for (int e = tid; e < rows * quads; e += kThreads) {
             const int t = e / quads, n = 4 * (e - t * quads + rank * quads);
             if (n0 + n >= p.N) continue;
-            float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-            const uint32_t at = base + 4 * (t * kPartRow + n);
-            for (int r = 0; r < p.split; ++r) {
-                const float4 v = p.split > 1 ? ld_cluster_f4(mapa(at, r)) : *reinterpret_cast<const float4*>(part + t * kPartRow + n);
-                s = make_float4(s.x + v.x, s.y + v.y, s.z + v.z, s.w + v.w);
+            const int word = t * kPartRow + n;
+            float4 s = *reinterpret_cast<const float4*>(part + word);
+            if (p.split > 1) {
+                // all parts asked for before the first is added (a load from another SM
+                // takes some 600 clocks)
+                float4 v[kMaxSplit];
+#pragma unroll
+                for (int r = 0; r < kMaxSplit; ++r)
+                    if (r < p.split) v[r] = ld_cluster_f4(mapa(base + 4 * word, r));
+                s = v[0];
+#pragma unroll
+                for (int r = 1; r < kMaxSplit; ++r)
+                    if (r < p.split) s = make_float4(s.x + v[r].x, s.y + v[r].y, s.z + v[r].z, s.w + v[r].w);
             }
             __nv_bfloat16* dst = p.y + (t0 + t) * p.y_stride + n0 + n;
             const __nv_bfloat162 lo = __floats2bfloat162_rn(s.x, s.y), hi = __floats2bfloat162_rn(s.z, s.w);
@@ -602,12 +611,16 @@ MxLinearPlan mx_linear_plan(int T, int N, int K, int x_elem, int w_elem) {
     const int kAtoms = stage_atoms(mode_of(x_elem, w_elem));
     const int64_t steps = (mx_atoms(K) + kAtoms - 1) / kAtoms;
     const int64_t tiles = mx_atoms(N);
-    // the time goes with the rounds of CTAs (two an SM) times the steps of each and
-    // kFixed more for its start and end
+    // The time goes with the rounds of CTAs (two an SM), times the steps of each and kFixed
+    // more for its start and end; where two CTAs of an SM add up parts of K, the parts' way
+    // through the SMs counts as a step for eight tokens (4096 outputs of 6144 columns in
+    // eight by four bits, 1 / 64 / 128 tokens: split by 8, 256 CTAs, 6.4 / 10.2 / 13.9 us;
+    // by 4 7.4 / 8.2 / 9.5; by 1 12.8 / 14.0 / 15.9).
     plan.split = 1;
     int64_t best = 0;
-    for (int s = 1; s <= 8 && s <= steps; s *= 2) {
-        const int64_t cost = ((tiles * s + 2 * kSms - 1) / (2 * kSms)) * ((steps + s - 1) / s + kFixed);
+    for (int s = 1; s <= kMaxSplit && s <= steps; s *= 2) {
+        int64_t cost = ((tiles * s + 2 * kSms - 1) / (2 * kSms)) * ((steps + s - 1) / s + kFixed);
+        if (s > 1 && tiles * s > kSms) cost += plan.x_rows / 8;
         if (s == 1 || cost < best) {
             best = cost;
             plan.split = s;

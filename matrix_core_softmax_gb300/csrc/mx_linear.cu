@@ -36,7 +36,8 @@ constexpr int kWarpLoad = 4, kWarpLoadX = 5, kWarpMma = 6, kWarpScales = 7;
 constexpr int kMaxStages = 12;
 // Scales come for 512 elements of K at once, in a ring of their own: a copy holds the
 // SM's copy engine up for 110 clocks however small it is.
-constexpr int kSfAtoms = 4, kSfSlots = 2, kSfBytes = 2 * kSfAtoms * kAtomBytes;
+// (Two slots held one token over weights in four bits up by 700 clocks a step.)
+constexpr int kSfAtoms = 4, kSfSlots = 4, kSfBytes = 2 * kSfAtoms * kAtomBytes;
 constexpr int kSmemTwo = 112 * 1024, kSmemOne = 224 * 1024;  // of a CTA, two or one an SM
 constexpr uint32_t kTmemCols = 256; // of two CTAs: all 512
 constexpr uint32_t kColSf = 128;    // accumulator at 0, scales of slot s at 128 + 32 s
@@ -47,7 +48,7 @@ struct Params {
     const uint8_t *xs, *ws;
     __nv_bfloat16* y;
     int64_t y_stride;
-    int T, N, n_atoms, n_tok, split, stages, t_tiles, vec;
+    int T, N, n_atoms, n_tok, split, stages, slots, t_tiles, vec;
     uint64_t timeout_ns;
     unsigned int* err_word;
     int skip;  // test use: stage 1 never arrives
@@ -106,7 +107,7 @@ __global__ void __launch_bounds__(kThreads, 2)
             mbar_init(&sm.full[i], i == 1 && p.skip ? 3 : 2);
             mbar_init(&sm.empty[i], 1);
         }
-        for (int i = 0; i < kSfSlots; ++i) {
+        for (int i = 0; i < p.slots; ++i) {
             mbar_init(&sm.sf_full[i], 1);
             mbar_init(&sm.sf_empty[i], 1);
         }
@@ -159,18 +160,22 @@ __global__ void __launch_bounds__(kThreads, 2)
             const uint8_t* ws = p.ws + static_cast<int64_t>(n_tile) * p.n_atoms * kAtomBytes + at;
             const uint8_t* xs = p.xs + static_cast<int64_t>(t0 / 128) * p.n_atoms * kAtomBytes + at;
             const int atoms = min(mine * kAtoms, p.n_atoms - first * kAtoms);  // (the last step may hold one atom)
-            int issued = 0;
+            int issued = 0, slot = 0;
+            uint32_t ph = 1;
             for (int a = 0; a < atoms; a += kSfAtoms, ++issued) {
-                const int slot = issued % kSfSlots;
-                if (issued >= kSfSlots) ok = mbar_wait(&sm.sf_empty[slot], (issued / kSfSlots - 1) & 1, p.timeout_ns, &sm.abort);
+                if (issued >= p.slots) ok = mbar_wait(&sm.sf_empty[slot], ph, p.timeout_ns, &sm.abort);
                 if (!ok) break;
                 const uint32_t bytes = min(kSfAtoms, atoms - a) * kAtomBytes;
                 uint8_t* dst = sf_tiles + slot * kSfBytes;
                 mbar_arrive_expect_tx(&sm.sf_full[slot], 2 * bytes);
                 bulk_load(dst, ws + static_cast<int64_t>(a) * kAtomBytes, bytes, &sm.sf_full[slot]);
                 bulk_load(dst + kSfBytes / 2, xs + static_cast<int64_t>(a) * kAtomBytes, bytes, &sm.sf_full[slot]);
+                if (++slot == p.slots) {
+                    slot = 0;
+                    ph ^= 1u;
+                }
             }
-            settle(sm.sf_full, kSfSlots, issued);
+            settle(sm.sf_full, p.slots, issued);
         }
     } else if (warp == kWarpMma) {
         const uint32_t tm = __shfl_sync(0xFFFFFFFFu, tmem, 0);
@@ -181,11 +186,11 @@ __global__ void __launch_bounds__(kThreads, 2)
         auto wait = [&](uint64_t* bar, uint32_t phase) {
             return __all_sync(0xFFFFFFFFu, mbar_wait(bar, phase & 1u, p.timeout_ns, &sm.abort)) != 0;
         };
-        int st = 0;
-        uint32_t ph = 0;
+        int st = 0, slot = 0;
+        uint32_t ph = 0, sf_ph = 0;
         for (int i = 0; i < mine; ++i) {
-            const int chunk = i / kSfSteps, in = i - chunk * kSfSteps, slot = chunk % kSfSlots;
-            if (in == 0) ok = wait(&sm.sf_full[slot], chunk / kSfSlots);
+            const int in = i % kSfSteps;
+            if (in == 0) ok = wait(&sm.sf_full[slot], sf_ph);
             ok = ok && wait(&sm.full[st], ph);
             if (!ok) break;
             tc_fence_after();
@@ -211,7 +216,13 @@ __global__ void __launch_bounds__(kThreads, 2)
                 }
             }
             tc_commit_one(&sm.empty[st]);
-            if (in == kSfSteps - 1) tc_commit_one(&sm.sf_empty[slot]);
+            if (in == kSfSteps - 1) {
+                tc_commit_one(&sm.sf_empty[slot]);
+                if (++slot == p.slots) {
+                    slot = 0;
+                    sf_ph ^= 1u;
+                }
+            }
             if (++st == p.stages) {
                 st = 0;
                 ph ^= 1u;
@@ -227,16 +238,24 @@ __global__ void __launch_bounds__(kThreads, 2)
     __syncthreads();
     tc_fence_after();
     float* part = reinterpret_cast<float*>(w_tiles);
+    const int rows = min(p.n_tok, p.T - t0);
     if (warp < 4) {
         const uint32_t col = tmem + (static_cast<uint32_t>(32 * warp) << 16);
-        for (int c = 0; c < p.n_tok; c += 16) {
+        const bool put = p.split == 1 && n0 + tid < p.N && !sm.abort;
+        __nv_bfloat16* dst = p.y + t0 * p.y_stride + n0 + tid;
+        for (int c = 0; c < rows; c += 16) {
             uint32_t v[16];
             tmem_ld16(col + c, v);
             tmem_ld_wait();
 #pragma unroll
-            for (int j = 0; j < 16; ++j) {
-                asm volatile("" : "+r"(v[j]));  // (not before the wait)
-                part[(c + j) * kPartRow + tid] = __uint_as_float(v[j]);
+            for (int j = 0; j < 16; ++j) asm volatile("" : "+r"(v[j]));  // (not before the wait)
+            if (p.split > 1) {
+#pragma unroll
+                for (int j = 0; j < 16; ++j) part[(c + j) * kPartRow + tid] = __uint_as_float(v[j]);
+            } else if (put) {
+#pragma unroll
+                for (int j = 0; j < 16; ++j)
+                    if (c + j < rows) dst[(c + j) * p.y_stride] = __float2bfloat16_rn(__uint_as_float(v[j]));
             }
         }
     }
@@ -250,28 +269,23 @@ __global__ void __launch_bounds__(kThreads, 2)
         tc_fence_after();
         tmem_dealloc(tmem, kTmemCols);
     }
-    if (!sm.abort) {
+    if (p.split > 1 && !sm.abort) {
         // this CTA's share: 128 / split outputs of each token, four a thread
-        const int quads = 32 / p.split;
-        const int rows = min(p.n_tok, p.T - t0);
+        const int lg = __ffs(32 / p.split) - 1;
         const uint32_t base = smem_u32(part);
-        for (int e = tid; e < rows * quads; e += kThreads) {
-            const int t = e / quads, n = 4 * (e - t * quads + rank * quads);
+        for (int e = tid; e < rows << lg; e += kThreads) {
+            const int t = e >> lg, n = 4 * ((e & ((1 << lg) - 1)) + (rank << lg));
             if (n0 + n >= p.N) continue;
-            const int word = t * kPartRow + n;
-            float4 s = *reinterpret_cast<const float4*>(part + word);
-            if (p.split > 1) {
-                // all parts asked for before the first is added (a load from another SM
-                // takes some 600 clocks)
-                float4 v[kMaxSplit];
+            // all parts asked for before the first is added (a load from another SM takes
+            // some 600 clocks)
+            float4 v[kMaxSplit];
 #pragma unroll
-                for (int r = 0; r < kMaxSplit; ++r)
-                    if (r < p.split) v[r] = ld_cluster_f4(mapa(base + 4 * word, r));
-                s = v[0];
+            for (int r = 0; r < kMaxSplit; ++r)
+                if (r < p.split) v[r] = ld_cluster_f4(mapa(base + 4 * (t * kPartRow + n), r));
+            float4 s = v[0];
 #pragma unroll
-                for (int r = 1; r < kMaxSplit; ++r)
-                    if (r < p.split) s = make_float4(s.x + v[r].x, s.y + v[r].y, s.z + v[r].z, s.w + v[r].w);
-            }
+            for (int r = 1; r < kMaxSplit; ++r)
+                if (r < p.split) s = make_float4(s.x + v[r].x, s.y + v[r].y, s.z + v[r].z, s.w + v[r].w);
             __nv_bfloat16* dst = p.y + (t0 + t) * p.y_stride + n0 + n;
             const __nv_bfloat162 lo = __floats2bfloat162_rn(s.x, s.y), hi = __floats2bfloat162_rn(s.z, s.w);
             if (p.vec && n0 + n + 4 <= p.N) {
@@ -594,7 +608,11 @@ cudaError_t launch(const MxLinearLaunch& a, Params p, int tiles, cudaStream_t st
     cudaError_t e = setup(reinterpret_cast<const void*>(mx_linear_kernel<kMode>), kSmemOne, 0);
     if (e != cudaSuccess) return e;
     const int smem = tiles * p.split <= kSms ? kSmemOne : kSmemTwo;
-    p.stages = (smem - 1024 - kSfSlots * kSfBytes) / stage_bytes(p.n_tok);
+    // scales as far ahead as codes: a slot is two steps in four bits and four in eight
+    for (p.slots = kMode == X4W4 || smem == kSmemOne ? kSfSlots : 2; p.slots >= 2; p.slots /= 2) {
+        p.stages = (smem - 1024 - p.slots * kSfBytes) / stage_bytes(p.n_tok);
+        if (p.stages >= 3) break;
+    }
     if (p.stages > kMaxStages) p.stages = kMaxStages;
     return launch_early(mx_linear_kernel<kMode>, static_cast<unsigned>(tiles) * p.split, kThreads, smem, st, p.split, *a.tm_x,
                         *a.tm_w, p);
@@ -604,13 +622,16 @@ cudaError_t launch(const MxLinearLaunch& a, Params p, int tiles, cudaStream_t st
 
 MxLinearPlan mx_linear_plan(int T, int N, int K, int x_elem, int w_elem) {
     MxLinearPlan plan{};
-    plan.w_rows = 128;
-    plan.x_rows = 128;
-    if (T > 128) return plan;  // pairs of CTAs
-    plan.x_rows = (T + 15) / 16 * 16;
+    plan.w_rows = plan.x_rows = 128;
+    // 128 x 128 tiles of more than 128 tokens where they are so few that parts of K go to
+    // two CTAs and more, pairs of CTAs otherwise (256 x 4096 x 4096 in eight by four bits:
+    // 10.4 us against 13.6; 333 x 5000 x 4128, 120 tiles: 14.5 against 13.9; 2048 x 2048 x
+    // 2048: 13.3 against 9.8)
+    const int64_t tiles = mx_atoms(N) * mx_atoms(T);
+    if (T > 128 && tiles > kSms / 2) return plan;
+    if (T <= 128) plan.x_rows = (T + 15) / 16 * 16;
     const int kAtoms = stage_atoms(mode_of(x_elem, w_elem));
     const int64_t steps = (mx_atoms(K) + kAtoms - 1) / kAtoms;
-    const int64_t tiles = mx_atoms(N);
     // The time goes with the rounds of CTAs (two an SM), times the steps of each and kFixed
     // more for its start and end; where two CTAs of an SM add up parts of K, the parts' way
     // through the SMs counts as a step for eight tokens (4096 outputs of 6144 columns in

@@ -7,9 +7,14 @@
 //                                    over 16 bytes of shared memory
 //   x E4M3, w E4M3   kind::mxf8f6f4
 //
-// A stage of the copy ring is 128 bytes of shared memory a row in each of them: 256
-// elements of K (two scale atoms) in the first, 128 (one) in the others, and four
-// instructions.
+// A step is 128 bytes of shared memory a row in each of them: 256 elements of K (two
+// scale atoms) in the first, 128 (one) in the others, and four instructions.
+//
+// Few tokens are bound by the weights' way out of HBM (one token, 16384 x 16384: 25.0 us
+// in four bits, 5.7 TB/s; 43.4 in eight, 6.4), small products by their start and end
+// (3 us), many tokens by the tensor core and, when they keep on, by the power that it may
+// draw (8192 x 16384 x 8192: 303 us in four bits, 7.3 PFLOP/s, 88 % of what the tensor
+// cores do without any copies; 591 in eight, 3.7 PFLOP/s).
 #include <cuda_bf16.h>
 
 #include "fsa_internal.h"
@@ -34,9 +39,9 @@ constexpr int kFixed = 8;           // (see mx_linear_plan)
 constexpr int kThreads = 256;
 constexpr int kWarpLoad = 4, kWarpLoadX = 5, kWarpMma = 6, kWarpScales = 7;
 constexpr int kMaxStages = 12;
-// Scales come for 512 elements of K at once, in a ring of their own: a copy holds the
-// SM's copy engine up for 110 clocks however small it is.
-// (Two slots held one token over weights in four bits up by 700 clocks a step.)
+// Scales come for 512 elements of K at once, in a ring of their own, so that a step costs
+// a warp one copy (some 150 clocks to issue, and 120 for a wait that is over).  Two slots
+// held one token over weights in four bits up by 700 clocks a step.
 constexpr int kSfAtoms = 4, kSfSlots = 4, kSfBytes = 2 * kSfAtoms * kAtomBytes;
 constexpr int kSmemTwo = 112 * 1024, kSmemOne = 224 * 1024;  // of a CTA, two or one an SM
 constexpr uint32_t kTmemCols = 256; // of two CTAs: all 512
@@ -306,12 +311,17 @@ __global__ void __launch_bounds__(kThreads, 2)
 // neighbouring outputs of one token.  A pair of CTAs works on 256 tokens x 256
 // outputs: each has 128 tokens' rows and half of the weights' in its shared memory
 // and its tokens' sums in its tensor memory, so a step brings an SM 32 KB of codes for
-// as many operations as a 128 x 128 tile's for half of them.
+// twice the operations that a 128 x 128 tile's 32 KB serve (8192 x 16384 x 8192 in 128 x
+// 128 tiles, two CTAs an SM: 550 us in four bits, 941 in eight, 17 to 19 TB/s out of L2).
+// An output tile leaves through registers, so that the next tile's products begin 450
+// clocks after the last one's end.
+//
 // warps 0-7 output; 8 copies of x and its scales, 9 of w and the scales of its first 128
 // rows, 10 the scales of the others; 11 the products (rank 0) or word that a stage has
 // landed (rank 1).  A copy takes some 150 clocks to issue and a wait 120, a step's
-// products 640 to 700: one warp for all five copies took 815 clocks a step, one for the
-// three of scales 720.
+// products 540: one warp for all five copies took 815 clocks a step, one for the three
+// of scales 720, two copies a warp 560.  (Tried: five warps, 600; two steps a stage; a ring
+// of scales as above, which is no faster where the clock follows the power.)
 constexpr int kPairThreads = 384;
 constexpr int kPairLoad = 8, kPairLoaders = 3, kPairMma = 11;
 constexpr int kPairStages = 6;

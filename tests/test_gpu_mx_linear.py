@@ -41,6 +41,8 @@ SHAPES = [
     # many tiles of many tokens
     (1300, 4000, 300), (2305, 2100, 257), (20000, 200, 128), (300, 10000, 640), (129, 20000, 96), (2048, 2560, 1024),
     (5000, 1300, 33),
+    # one and two CTAs an SM, rings of all depths, tiles of more than 128 tokens in parts
+    (16, 20480, 1000), (128, 20000, 700), (100, 10000, 2100), (40, 4000, 6000), (256, 4096, 1100), (1000, 1000, 2900),
     # long rows
     (2, 130, 100000), (300, 200, 40001),
 ]

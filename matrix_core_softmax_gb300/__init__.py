@@ -661,7 +661,8 @@ class MxOperand:
     ("mxfp8")], scales uint8 [ceil(rows / 128), ceil(cols / 128), 512].
 
     MxOperand(codes, scales, cols, fmt) is one of given tensors; mx_new_operand, mx_pack
-    and rms_norm_mx make one in a single allocation, whose codes and scales are views."""
+    and rms_norm_mx make one in a single storage, of which codes and scales become
+    tensors when they are asked for (beside a launch a tensor costs 5 us, a storage 2)."""
     __slots__ = ("rows", "cols", "fmt", "elem", "_dev", "_bytes", "_codes", "_scales")
 
     def __init__(self, codes: torch.Tensor, scales: torch.Tensor, cols: int, fmt: str):
@@ -678,15 +679,18 @@ class MxOperand:
         self._dev, self._bytes, self._codes, self._scales = codes.get_device(), None, codes, scales
 
     @classmethod
-    def _new(cls, rows: int, cols: int, fmt: str, device):
+    def _new(cls, rows: int, cols: int, fmt: str, device, dev=None):
+        """An operand with arbitrary contents on `device`, whose index is dev."""
         elem, width = _operand_format(fmt)
         if rows < 0 or cols < 1:
             raise ValueError("an operand has at least one column")
         self = cls.__new__(cls)
         atoms = (cols + 127) >> 7
-        data = torch.empty(atoms * (rows * width + ((rows + 127) >> 7) * 512), dtype=_u8, device=device)
+        data = torch.UntypedStorage(atoms * (rows * width + ((rows + 127) >> 7) * 512), device=device)
+        if dev is None:
+            dev = data.device.index if data.device.type == "cuda" else -1
         self.rows, self.cols, self.fmt, self.elem = rows, cols, fmt, elem
-        self._dev, self._bytes, self._codes, self._scales = data.get_device(), data, None, None
+        self._dev, self._bytes, self._codes, self._scales = dev, data, None, None
         return self
 
     def _pointers(self):
@@ -695,23 +699,28 @@ class MxOperand:
         at = self._bytes.data_ptr()
         return at, at + self.rows * ((self.cols + 127) >> 7) * _OPERANDS[self.fmt][1]
 
+    def _tensor(self, at: int, shape):
+        return torch.empty(0, dtype=_u8, device=self._bytes.device).set_(self._bytes, at, shape)
+
     @property
     def codes(self) -> torch.Tensor:
         if self._codes is None:
-            pitch = ((self.cols + 127) >> 7) * _OPERANDS[self.fmt][1]
-            self._codes = self._bytes[:self.rows * pitch].view(self.rows, pitch)
+            self._codes = self._tensor(0, (self.rows, ((self.cols + 127) >> 7) * _OPERANDS[self.fmt][1]))
         return self._codes
 
     @property
     def scales(self) -> torch.Tensor:
         if self._scales is None:
             atoms = (self.cols + 127) >> 7
-            self._scales = self._bytes[self.rows * atoms * _OPERANDS[self.fmt][1]:].view((self.rows + 127) >> 7, atoms, 512)
+            self._scales = self._tensor(self.rows * atoms * _OPERANDS[self.fmt][1], ((self.rows + 127) >> 7, atoms, 512))
         return self._scales
 
     @property
     def device(self) -> torch.device:
         return (self._codes if self._bytes is None else self._bytes).device
+
+    def __reduce__(self):  # copies and files hold the two tensors
+        return MxOperand, (self.codes, self.scales, self.cols, self.fmt)
 
     def __repr__(self):
         return f"MxOperand(rows={self.rows}, cols={self.cols}, fmt={self.fmt!r}, device={str(self.device)!r})"
@@ -736,7 +745,7 @@ def _rows(t: torch.Tensor, name: str, shape, dev: int) -> int:
 def _filled(out, shape, fmt: str, dev: int, device) -> MxOperand:
     """The operand that a call fills, new or given."""
     if out is None:
-        return MxOperand._new(*shape, fmt, device)
+        return MxOperand._new(*shape, fmt, device, dev)
     if (out.rows, out.cols) != tuple(shape) or out.fmt != fmt or out._dev != dev:
         raise ValueError(f"out must be an operand of {list(shape)} in {fmt} on cuda:{dev}")
     return out

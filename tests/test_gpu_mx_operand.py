@@ -196,3 +196,21 @@ def test_operands_on_other_streams(fsa):
     torch.cuda.current_stream().wait_stream(side)
     for a, b in zip(got, want):
         assert torch.equal(a, b)
+
+
+def test_operands_live_as_long_as_their_tensors(fsa):
+    x = to_dev(_bits((1000, 512), 1))
+    op = fsa.mx_pack(x, "mxfp8")
+    codes, scales = op.codes, op.scales
+    want = codes.clone(), scales.clone()
+    assert op.codes is codes and op.device == x.device
+    del op
+    others = [fsa.mx_pack(torch.zeros_like(x), "mxfp8") for _ in range(8)]
+    assert torch.equal(codes, want[0]) and torch.equal(scales, want[1])
+    again = fsa.MxOperand(codes, scales, 512, "mxfp8")
+    assert torch.equal(fsa.mx_unpack(again), fsa.mx_unpack(fsa.mx_pack(x, "mxfp8")))
+    del others
+    before = torch.cuda.memory_allocated()
+    for _ in range(50):
+        fsa.mx_pack(x, "mxfp8")
+    assert torch.cuda.memory_allocated() == before

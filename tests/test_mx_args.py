@@ -105,3 +105,15 @@ def test_new_operand_holds_both_parts(rows, cols, fmt):
     assert (op.codes == 1).all() and (op.scales == 2).all()
     if rows:
         assert op._pointers() == (op.codes.data_ptr(), op.scales.data_ptr())
+
+
+def test_operands_are_copied_and_stored(tmp_path):
+    import copy
+    op = fsa.mx_new_operand(5, 200, "mxfp8", device="cpu")
+    op.codes.copy_(torch.arange(5 * 256).view(5, 256) % 251), op.scales.fill_(120)
+    torch.save(op, tmp_path / "op")
+    for other in (copy.deepcopy(op), torch.load(tmp_path / "op", weights_only=False)):
+        assert (other.rows, other.cols, other.fmt, other.elem) == (op.rows, op.cols, op.fmt, op.elem)
+        assert torch.equal(other.codes, op.codes) and torch.equal(other.scales, op.scales)
+        assert other._pointers() == (other.codes.data_ptr(), other.scales.data_ptr())
+        assert other.codes.data_ptr() != op.codes.data_ptr() and repr(other) == repr(op)

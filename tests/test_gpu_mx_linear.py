@@ -254,3 +254,37 @@ def test_a_layer_as_it_is_served(fsa, T, fmt):
     nxt, h2 = fsa.rms_norm_mx(y, g, residual=h1, fmt=fmt, out_sum=h1)
     ref.check_norm_operand(nxt, ref.norm(h2.double(), g.double(), 1e-6))
     assert fsa.get_device_error() == 0
+
+
+@pytest.mark.parametrize("T", [1, 40, 300, 2600])
+def test_buffers_that_every_call_reuses(fsa, T):
+    """Product, packing and norm in turn over the same buffers: what one call reads the
+    next but one writes, called one after another and replayed."""
+    n = 512
+    w = [fsa.mx_pack(_bf16((n, n), 80 + i, n ** -0.5), f) for i, f in enumerate(("mxfp4", "mxfp8", "mxfp4"))]
+    g = to_dev(fsa_inputs.to_bf16_bits(np.ones(n, np.float32)))
+    x0 = _bf16((T, n), 90)
+
+    def chain(keep):
+        h, op = x0.clone(), None
+        y = torch.empty_like(x0) if keep else None
+        op8, op4 = (fsa.mx_new_operand(T, n, f) if keep else None for f in ("mxfp8", "mxfp4"))
+        for i in range(12):
+            kw = dict(out=op8, out_sum=h) if keep else {}
+            op, h = fsa.rms_norm_mx(h if i == 0 else y, g, residual=h, **kw)
+            y = fsa.mx_linear(op, w[i % 3], out=y if keep else None)
+            op = fsa.mx_pack(y, "mxfp4", out=op4)
+            y = fsa.mx_linear(op, w[0], out=y if keep else None)
+        return h, y
+
+    want = chain(False)
+    for _ in range(5):
+        got = chain(True)
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = chain(True)
+    for _ in range(10):
+        graph.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want)) and fsa.get_device_error() == 0

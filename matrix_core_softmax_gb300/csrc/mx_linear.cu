@@ -316,38 +316,56 @@ __global__ void __launch_bounds__(kThreads, 2)
 // An output tile leaves through registers, so that the next tile's products begin 450
 // clocks after the last one's end.
 //
-// warps 0-7 output; 8 copies of x and its scales, 9 of w and the scales of its first 128
-// rows, 10 the scales of the others; 11 the products (rank 0) or word that a stage has
-// landed (rank 1).  A copy takes some 150 clocks to issue and a wait 120, a step's
-// products 540: one warp for all five copies took 815 clocks a step, one for the three
-// of scales 720, two copies a warp 560.  (Tried: five warps, 600; two steps a stage; a ring
-// of scales as above, which is no faster where the clock follows the power.)
+// warps 0-7 output; 8, 9, 10 copies; 11 the products (rank 0) or word that a stage has
+// landed (rank 1).  An SM begins a copy every 110 clocks, whatever its size, where a
+// step's products take 540, and a warp takes 150 to issue one and 120 for a wait that is
+// over (clocks a step of 256 outputs: one warp for its five copies 815, three of them in
+// one 720, the five over three warps 545, a warp each 600).  Narrower tiles' products take
+// less, so their scales come for 512 elements of K at once, in a ring of their own (kRing;
+// 512 x 5120 x 5120 in eight by four bits 16.5 -> 13.7 us); tiles of 256 outputs keep them
+// in the stages, because the second wait holds the products up (in four bits 24.0 us for
+// 1024 x 8192 x 8192, with the ring 25.5; 8192 x 16384 x 4096 in eight by four 282, 288).
 constexpr int kPairThreads = 384;
-constexpr int kPairLoad = 8, kPairLoaders = 3, kPairMma = 11;
-constexpr int kPairStages = 6;
+constexpr int kPairLoadX = 8, kPairLoadW = 9, kPairLoadSf = 10, kPairMma = 11;
+constexpr int kPairStages = 6, kPairSlots = 3;
+constexpr int kPairSf = 3 * kPairSlots * kSfAtoms * kAtomBytes;  // scales: x, w's rows in two groups of 128
 constexpr uint32_t kPairCols = 512;
-constexpr uint32_t kPairSf = 256;   // accumulator at 0, scales of stage s at 256 + 24 s
-constexpr int kPairGroup = 8;       // token tiles that are walked side by side
+constexpr uint32_t kPairColSf = 256;  // accumulator at 0, scales of slot s at 256 + 12 s times a slot's atoms
+constexpr int kPairGroup = 8;         // token tiles that are walked side by side
+static_assert(kPairSlots * kSfAtoms >= kPairStages * 2, "scales in the stages take the ring's room");
 
 struct PairBars {
-    uint64_t full[kPairStages];     // rank 0's: the other CTA's copies, too
+    uint64_t full[kPairStages];       // rank 0's: the other CTA's copies, too
     uint64_t empty[kPairStages];
-    uint64_t acc_full, acc_empty;   // (acc_empty: rank 0's, an arrival a warp of both CTAs' output)
+    uint64_t sf_full[kPairSlots], sf_empty[kPairSlots];  // the same of scales (kRing)
+    uint64_t acc_full, acc_empty;     // (acc_empty: rank 0's, an arrival a warp of both CTAs' output)
     uint64_t drain;
     uint32_t tmem_base;
     int abort;
 };
 
-constexpr int pair_stage_bytes(int mode) { return 2 * 128 * 128 + 3 * stage_atoms(mode) * kAtomBytes; }
 constexpr int kOutBytes = 8 * 32 * 64;  // per output warp: 32 rows x 32 outputs on their way
-constexpr int pair_smem(int mode) { return kPairStages * pair_stage_bytes(mode) + kOutBytes + static_cast<int>(sizeof(PairBars)); }
-static_assert(pair_smem(X4W4) <= 232448, "shared memory beyond the 227 KB a CTA may use");
+constexpr int kPairSmem = kPairStages * 2 * 16384 + kPairSf + kOutBytes + static_cast<int>(sizeof(PairBars));
+static_assert(kPairSmem <= 232448, "shared memory beyond the 227 KB a CTA may use");
+
+// A place in a ring of n.
+template <int n>
+struct Turn {
+    int at = 0;
+    uint32_t ph = 0;
+    __device__ __forceinline__ void next() {
+        if (++at == n) {
+            at = 0;
+            ph ^= 1u;
+        }
+    }
+};
 
 struct PairParams {
     const uint8_t *xs, *ws;
     __nv_bfloat16* y;
     int64_t y_stride;
-    int T, N, n_atoms, t_tiles, n_tiles, vec;
+    int T, N, n_atoms, t_tiles, n_tiles, bn, vec;  // bn: outputs of a tile, 256, 192 or 128
     uint64_t timeout_ns;
     unsigned int* err_word;
     int skip;
@@ -362,7 +380,7 @@ __device__ __forceinline__ void pair_tile(const PairParams& p, int i, int& t_til
     t_tile = group * kPairGroup + in - n_tile * width;
 }
 
-template <int kMode>
+template <int kMode, bool kRing>
 __global__ void __launch_bounds__(kPairThreads, 1)
     mx_linear_pair_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_w, const PairParams p) {
     extern __shared__ __align__(1024) uint8_t ring[];
@@ -371,7 +389,10 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         if (threadIdx.x == 0) atomicOr(p.err_word, kErrMisaligned);
         return;
     }
-    constexpr int kAtoms = stage_atoms(kMode), kSf = 3 * kAtoms * kAtomBytes;
+    constexpr int kAtoms = stage_atoms(kMode);                           // of a step
+    constexpr int kSlot = kRing ? kSfAtoms : kAtoms;                     // of a slot of scales
+    constexpr int kSfSteps = kSlot / kAtoms, kSfGroup = kSlot * kAtomBytes;
+    const int bn = kRing ? p.bn : 256;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint32_t rank = cluster_ctarank();
     const int first_tile = blockIdx.x >> 1, tile_step = gridDim.x >> 1, tiles = p.t_tiles * p.n_tiles;
@@ -379,14 +400,18 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     uint8_t* x_tiles = ring;
     uint8_t* w_tiles = x_tiles + kPairStages * 16384;
     uint8_t* sf_tiles = w_tiles + kPairStages * 16384;
-    uint4* out = reinterpret_cast<uint4*>(sf_tiles + kPairStages * kSf);
+    uint4* out = reinterpret_cast<uint4*>(sf_tiles + kPairSf);
     PairBars& sm = *reinterpret_cast<PairBars*>(out + kOutBytes / 16);
 
     if (tid == 0) {
         sm.abort = 0;
         for (int i = 0; i < kPairStages; ++i) {
-            mbar_init(&sm.full[i], kPairLoaders + (rank == 0) + (i == 1 && p.skip));
+            mbar_init(&sm.full[i], (kRing ? 2 : 3) + (rank == 0) + (i == 1 && p.skip));
             mbar_init(&sm.empty[i], 1);
+        }
+        for (int i = 0; i < kPairSlots; ++i) {
+            mbar_init(&sm.sf_full[i], 1 + (rank == 0));
+            mbar_init(&sm.sf_empty[i], 1);
         }
         mbar_init(&sm.acc_full, 1);
         mbar_init(&sm.acc_empty, 16);
@@ -396,7 +421,10 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     if (warp == kPairMma) pair_tmem_alloc(&sm.tmem_base, kPairCols);
     tc_fence_before();
     __syncthreads();
-    cluster_sync();  // both CTAs' barriers are there
+    // both CTAs' barriers are there behind the wait; the loaders only use their own CTA's
+    cluster_arrive();
+    const bool loader = warp >= kPairLoadX && warp <= kPairLoadSf;
+    if (!loader) cluster_wait();
     tc_fence_after();
     grid_launch_next();  // (the next kernel's CTAs find this one's tensor memory taken)
     const uint32_t tmem = sm.tmem_base;
@@ -408,109 +436,135 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         return __all_sync(0xFFFFFFFFu, mbar_wait(bar, phase & 1u, p.timeout_ns, &sm.abort)) != 0;
     };
     bool ok = true;
-    int st = 0;       // stage and its phase, in step in all roles
-    uint32_t ph = 0;
-    auto advance = [&] {
-        if (++st == kPairStages) {
-            st = 0;
-            ph ^= 1u;
-        }
-    };
+    Turn<kPairStages> st;   // in step in all roles
+    Turn<kPairSlots> slot;
 
-    if (warp >= kPairLoad && warp < kPairLoad + kPairLoaders) {
+    if (loader) {
         if (lane == 0) {
             grid_wait();
-            const int what = warp - kPairLoad;
             const int64_t x_groups = mx_atoms(p.T), w_groups = mx_atoms(p.N);
             int issued = 0;
             for (int i = first_tile; ok && i < tiles; i += tile_step) {
                 int t_tile, n_tile;
                 pair_tile(p, i, t_tile, n_tile);
-                const int t0 = 256 * t_tile + 128 * static_cast<int>(rank), n0 = 256 * n_tile + 128 * static_cast<int>(rank);
+                const int t0 = 256 * t_tile + 128 * static_cast<int>(rank), n0 = bn * n_tile;
                 // scale rows that there are: this CTA's tokens, all of the tile's outputs
-                const int64_t xg = t0 / 128, wg = 2 * n_tile;
-                const bool have_x = xg < x_groups, have_w1 = wg + 1 < w_groups;
+                const int64_t xg = t0 / 128, wg = n0 / 128;
+                const bool have_x = xg < x_groups, have_w1 = bn > 128 && wg + 1 < w_groups;
                 const uint8_t* xs = p.xs + xg * p.n_atoms * kAtomBytes;
                 const uint8_t* ws = p.ws + wg * p.n_atoms * kAtomBytes;
-                for (int k = 0; k < steps; ++k, ++issued) {
-                    if (issued >= kPairStages) ok = mbar_wait(&sm.empty[st], ph ^ 1u, p.timeout_ns, &sm.abort);
-                    if (!ok) break;
-                    uint64_t* full = &sm.full[st];
-                    const uint32_t sf = min(kAtoms, p.n_atoms - k * kAtoms) * kAtomBytes;
-                    const int64_t at = static_cast<int64_t>(k) * kAtoms * kAtomBytes;
-                    uint8_t* dst = sf_tiles + st * kSf + what * kAtoms * kAtomBytes;
-                    if (what == 0) {
-                        mbar_arrive_expect_tx(full, 128 * 128 + (have_x ? sf : 0));
-                        tma_load_2d(x_tiles + st * 16384, &tm_x, full, k * 128, t0);
-                        if (have_x) bulk_load(dst, xs + at, sf, full);
-                    } else if (what == 1) {
-                        mbar_arrive_expect_tx(full, 128 * (kMode == X8W4 ? 64 : 128) + sf);
-                        tma_load_2d(w_tiles + st * 16384, &tm_w, full, k * 128, n0);
-                        bulk_load(dst, ws + at, sf, full);
-                    } else if (have_w1) {
-                        mbar_arrive_expect_tx(full, sf);
-                        bulk_load(dst, ws + static_cast<int64_t>(p.n_atoms) * kAtomBytes + at, sf, full);
-                    } else {
-                        mbar_arrive(full);
+                const uint8_t* ws1 = ws + static_cast<int64_t>(p.n_atoms) * kAtomBytes;
+                if (kRing && warp == kPairLoadSf) {
+                    for (int a = 0; a < p.n_atoms; a += kSlot, ++issued) {
+                        if (issued >= kPairSlots) ok = mbar_wait(&sm.sf_empty[slot.at], slot.ph ^ 1u, p.timeout_ns, &sm.abort);
+                        if (!ok) break;
+                        uint64_t* full = &sm.sf_full[slot.at];
+                        const uint32_t bytes = min(kSlot, p.n_atoms - a) * kAtomBytes;
+                        const int64_t at = static_cast<int64_t>(a) * kAtomBytes;
+                        uint8_t* dst = sf_tiles + slot.at * 3 * kSfGroup;
+                        mbar_arrive_expect_tx(full, bytes * (1 + have_x + have_w1));
+                        if (have_x) bulk_load(dst, xs + at, bytes, full);
+                        bulk_load(dst + kSfGroup, ws + at, bytes, full);
+                        if (have_w1) bulk_load(dst + 2 * kSfGroup, ws1 + at, bytes, full);
+                        slot.next();
                     }
-                    advance();
+                    continue;
+                }
+                // codes of x (and its scales), of w (and its first group's), or the second group's scales
+                const bool codes = warp != kPairLoadSf, is_x = warp == kPairLoadX, is_w = warp == kPairLoadW;
+                const CUtensorMap* map = is_x ? &tm_x : &tm_w;
+                uint8_t* tiles_at = is_x ? x_tiles : w_tiles;
+                const int row = is_x ? t0 : n0 + bn / 2 * static_cast<int>(rank);
+                // (a spread copy counts the bytes that it reads, 64 a row)
+                const uint32_t code_bytes = is_x ? 128 * 128 : is_w ? bn / 2 * (kMode == X8W4 ? 64 : 128) : 0;
+                const bool scales = !kRing && (is_x ? have_x : is_w || have_w1);
+                const uint8_t* src = is_x ? xs : is_w ? ws : ws1;
+                for (int k = 0; k < steps; ++k, ++issued) {
+                    if (issued >= kPairStages) ok = mbar_wait(&sm.empty[st.at], st.ph ^ 1u, p.timeout_ns, &sm.abort);
+                    if (!ok) break;
+                    uint64_t* full = &sm.full[st.at];
+                    const uint32_t bytes = scales ? min(kAtoms, p.n_atoms - k * kAtoms) * kAtomBytes : 0;
+                    mbar_arrive_expect_tx(full, code_bytes + bytes);
+                    if (codes) tma_load_2d(tiles_at + st.at * 16384, map, full, k * 128, row);
+                    if (scales)
+                        bulk_load(sf_tiles + (3 * st.at + warp - kPairLoadX) * kSfGroup, src + static_cast<int64_t>(k) * kSfGroup, bytes, full);
+                    st.next();
                 }
             }
             if (!ok) give_up();
             // every copy lands before the CTA goes on, whoever gives up and when
             int dummy = 0;
-            for (int i = max(0, issued - kPairStages); i < issued; ++i)
-                mbar_wait(&sm.full[i % kPairStages], (i / kPairStages) & 1, p.timeout_ns, &dummy);
+            const int n = kRing && warp == kPairLoadSf ? kPairSlots : kPairStages;
+            uint64_t* full = kRing && warp == kPairLoadSf ? sm.sf_full : sm.full;
+            for (int i = max(0, issued - n); i < issued; ++i) mbar_wait(full + i % n, (i / n) & 1, p.timeout_ns, &dummy);
         }
     } else if (warp == kPairMma && rank != 0) {
-        // says in rank 0 that a stage of this CTA has landed
+        // says in rank 0 that scales or a stage of this CTA have landed
         for (int i = first_tile; ok && i < tiles; i += tile_step)
             for (int k = 0; k < steps; ++k) {
-                ok = wait(&sm.full[st], ph);
+                if (kRing && k % kSfSteps == 0) {
+                    ok = wait(&sm.sf_full[slot.at], slot.ph);
+                    if (!ok) break;
+                    if (lane == 0) mbar_arrive_cluster(mapa(smem_u32(&sm.sf_full[slot.at]), 0));
+                    slot.next();
+                }
+                ok = wait(&sm.full[st.at], st.ph);
                 if (!ok) break;
-                if (lane == 0) mbar_arrive_cluster(mapa(smem_u32(&sm.full[st]), 0));
-                advance();
+                if (lane == 0) mbar_arrive_cluster(mapa(smem_u32(&sm.full[st.at]), 0));
+                st.next();
             }
         if (!ok && lane == 0) give_up();
     } else if (warp == kPairMma) {
         const uint32_t tm = __shfl_sync(0xFFFFFFFFu, tmem, 0);
         const uint64_t dx = smem_desc(smem_u32(x_tiles), 16, 1024, SWZ_128B), dw = smem_desc(smem_u32(w_tiles), 16, 1024, SWZ_128B);
         const uint64_t dsf = smem_desc(smem_u32(sf_tiles), 0, 128, SWZ_NONE);
-        constexpr uint32_t id = kMode == X4W4 ? idesc_mxf8f6f4(256, 256, 1, 1, 0, 0)
-                                              : idesc_mxf8f6f4(256, 256, 0, kMode == X8W4 ? 5 : 0, 0, 0);
+        const uint32_t id = kMode == X4W4 ? idesc_mxf8f6f4(256, bn, 1, 1, 0, 0)
+                                          : idesc_mxf8f6f4(256, bn, 0, kMode == X8W4 ? 5 : 0, 0, 0);
         uint32_t acc_ph = 1;  // (the first tile finds the accumulator empty)
         for (int i = first_tile; ok && i < tiles; i += tile_step, acc_ph ^= 1u) {
             if (i != first_tile) ok = wait(&sm.acc_empty, acc_ph);
+            int t_tile, n_tile;
+            pair_tile(p, i, t_tile, n_tile);
+            const uint32_t skew = bn * n_tile % 128 / 32;  // a tile that begins inside a group (32 rows a column)
             for (int k = 0; ok && k < steps; ++k) {
-                ok = wait(&sm.full[st], ph);
+                const int in = k % kSfSteps;
+                if (kRing && in == 0) ok = wait(&sm.sf_full[slot.at], slot.ph);
+                ok = ok && wait(&sm.full[st.at], st.ph);
                 if (!ok) break;
                 tc_fence_after();
-                // scale columns of a stage: x, then for each atom both halves of w
-                const uint32_t sfx = tm + kPairSf + 12 * kAtoms * st, sfw = sfx + 4 * kAtoms;
-                const uint64_t sf = dsf + st * (kSf >> 4);
+                // scale columns of a slot: x's atoms, then for each atom both groups of w
+                const int at = kRing ? slot.at : st.at;
+                const uint32_t sfx = tm + kPairColSf + 12 * kSlot * at + 4 * kAtoms * in;
+                const uint32_t sfw = tm + kPairColSf + 12 * kSlot * at + 4 * kSlot + 8 * kAtoms * in;
+                const uint64_t sf = dsf + at * (3 * kSfGroup >> 4) + in * (kAtoms * kAtomBytes >> 4);
                 const bool half = kAtoms == 2 && p.n_atoms - k * kAtoms == 1;
 #pragma unroll
                 for (int a = 0; a < kAtoms; ++a) {
                     if (a && half) break;
                     pair_cp_32x128b_x4_one(sfx + 4 * a, sf + a * (kAtomBytes >> 4));
-                    pair_cp_32x128b_x4_one(sfw + 8 * a, sf + (kAtoms + a) * (kAtomBytes >> 4));
-                    pair_cp_32x128b_x4_one(sfw + 8 * a + 4, sf + (2 * kAtoms + a) * (kAtomBytes >> 4));
+                    pair_cp_32x128b_x4_one(sfw + 8 * a, sf + (kSlot + a) * (kAtomBytes >> 4));
+                    if (bn > 128) pair_cp_32x128b_x4_one(sfw + 8 * a + 4, sf + (2 * kSlot + a) * (kAtomBytes >> 4));
                 }
-                const uint64_t ax = dx + st * (16384 >> 4), aw = dw + st * (16384 >> 4);
+                const uint64_t ax = dx + st.at * (16384 >> 4), aw = dw + st.at * (16384 >> 4);
 #pragma unroll
                 for (int kk = 0; kk < 4; ++kk) {
                     const uint32_t acc = (k > 0 || kk > 0) ? 1u : 0u;
                     if constexpr (kMode == X4W4) {
                         if (kk >= 2 && half) break;
                         const uint32_t s = (kk & 1) * 2;
-                        pair_mma_mxf4_one(tm, ax + 2 * kk, aw + 2 * kk, id | s << 4 | s << 29, sfx + 4 * (kk >> 1), sfw + 8 * (kk >> 1),
-                                          acc);
+                        pair_mma_mxf4_one(tm, ax + 2 * kk, aw + 2 * kk, id | s << 4 | s << 29, sfx + 4 * (kk >> 1),
+                                          sfw + 8 * (kk >> 1) + skew, acc);
                     } else {
-                        pair_mma_mxf8f6f4_one(tm, ax + 2 * kk, aw + 2 * kk, id | kk << 4 | static_cast<uint32_t>(kk) << 29, sfx, sfw, acc);
+                        pair_mma_mxf8f6f4_one(tm, ax + 2 * kk, aw + 2 * kk, id | kk << 4 | static_cast<uint32_t>(kk) << 29, sfx, sfw + skew,
+                                              acc);
                     }
                 }
-                pair_commit_one(&sm.empty[st], 3);
-                advance();
+                pair_commit_one(&sm.empty[st.at], 3);
+                st.next();
+                if (kRing && (in == kSfSteps - 1 || k + 1 == steps)) {
+                    pair_commit_one(&sm.sf_empty[slot.at], 3);
+                    slot.next();
+                }
             }
             if (ok) pair_commit_one(&sm.acc_full, 3);
         }
@@ -519,7 +573,9 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         int dummy = 0;
         if (!__all_sync(0xFFFFFFFFu, mbar_wait(&sm.drain, 0, p.timeout_ns, &dummy)) && lane == 0) give_up();
     } else {
-        const uint32_t col = tmem + (static_cast<uint32_t>(32 * (warp & 3)) << 16) + 128 * (warp >> 2);
+        // four warps for each half of the tile's outputs, 32 at a time
+        const int half = bn / 2 * (warp >> 2), pieces = bn / 64;
+        const uint32_t col = tmem + (static_cast<uint32_t>(32 * (warp & 3)) << 16) + half;
         const uint32_t acc_empty = mapa(smem_u32(&sm.acc_empty), 0);
         uint4* mine = out + warp * 128;  // 32 rows x 4 pieces of 8 outputs
         uint32_t acc_ph = 0;
@@ -531,6 +587,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
             uint32_t v[64];
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
+                if (c >= pieces) break;
                 uint32_t r[32];
                 tmem_ld32(col + 32 * c, r);
                 tmem_ld_wait();
@@ -546,10 +603,11 @@ __global__ void __launch_bounds__(kPairThreads, 1)
             if (lane == 0) mbar_arrive_cluster(acc_empty);
             int t_tile, n_tile;
             pair_tile(p, i, t_tile, n_tile);
-            const int t0 = 256 * t_tile + 128 * static_cast<int>(rank) + 32 * (warp & 3), n0 = 256 * n_tile + 128 * (warp >> 2);
+            const int t0 = 256 * t_tile + 128 * static_cast<int>(rank) + 32 * (warp & 3), n0 = bn * n_tile + half;
             // through shared memory, so that a store covers eight rows' 64 bytes
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
+                if (c >= pieces) break;
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
                     mine[4 * lane + (j ^ ((lane >> 1) & 3))] = make_uint4(v[16 * c + 4 * j], v[16 * c + 4 * j + 1], v[16 * c + 4 * j + 2],
@@ -579,6 +637,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     }
     tc_fence_before();
     __syncwarp();
+    if (loader) cluster_wait();
     cluster_sync();  // no CTA leaves while the other reads its memory or arrives at its barriers
     if (warp == kPairMma) {
         tc_fence_after();
@@ -586,10 +645,10 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     }
 }
 
-template <int kMode>
-cudaError_t launch_pair(const MxLinearLaunch& a, cudaStream_t st) {
+template <int kMode, bool kRing>
+cudaError_t launch_pair(const MxLinearLaunch& a, int bn, cudaStream_t st) {
     static KernelSetup setup;
-    cudaError_t e = setup(reinterpret_cast<const void*>(mx_linear_pair_kernel<kMode>), pair_smem(kMode), 0);
+    cudaError_t e = setup(reinterpret_cast<const void*>(mx_linear_pair_kernel<kMode, kRing>), kPairSmem, 0);
     if (e != cudaSuccess) return e;
     PairParams p{};
     p.xs = a.xs;
@@ -600,13 +659,14 @@ cudaError_t launch_pair(const MxLinearLaunch& a, cudaStream_t st) {
     p.N = a.N;
     p.n_atoms = static_cast<int>(mx_atoms(a.K));
     p.t_tiles = (a.T + 255) / 256;
-    p.n_tiles = (a.N + 255) / 256;
+    p.bn = bn;
+    p.n_tiles = (a.N + bn - 1) / bn;
     p.vec = (reinterpret_cast<uintptr_t>(a.y) & 15) == 0 && a.y_stride % 8 == 0;
     p.timeout_ns = a.timeout_ns;
     p.err_word = a.err_word;
     p.skip = a.debug_flags & 1;
     const int tiles = p.t_tiles * p.n_tiles;
-    return launch_early(mx_linear_pair_kernel<kMode>, 2 * (tiles < kSms / 2 ? tiles : kSms / 2), kPairThreads, pair_smem(kMode), st, 2,
+    return launch_early(mx_linear_pair_kernel<kMode, kRing>, 2 * (tiles < kSms / 2 ? tiles : kSms / 2), kPairThreads, kPairSmem, st, 2,
                         *a.tm_x, *a.tm_w, p);
 }
 
@@ -638,10 +698,24 @@ MxLinearPlan mx_linear_plan(int T, int N, int K, int x_elem, int w_elem) {
     // 10.4 us against 13.6; 333 x 5000 x 4128, 120 tiles: 14.5 against 13.9; 2048 x 2048 x
     // 2048: 13.3 against 9.8)
     const int64_t tiles = mx_atoms(N) * mx_atoms(T);
-    if (T > 128 && tiles > kSms / 2) return plan;
-    if (T <= 128) plan.x_rows = (T + 15) / 16 * 16;
     const int kAtoms = stage_atoms(mode_of(x_elem, w_elem));
     const int64_t steps = (mx_atoms(K) + kAtoms - 1) / kAtoms;
+    if (T > 128 && tiles > kSms / 2) {
+        // Tiles of 256, 192 or 128 outputs, whichever take the fewest rounds of pairs' time
+        // together (a step of fewer than 144 outputs is held up by its copies, a tile costs
+        // two steps more).
+        int64_t best = 0;
+        for (int bn = 256; bn >= 128; bn -= 64) {
+            const int64_t n = static_cast<int64_t>((T + 255) / 256) * ((N + bn - 1) / bn);
+            const int64_t cost = (n + kSms / 2 - 1) / (kSms / 2) * (steps * (bn > 144 ? bn : 144) + 2 * 256);
+            if (bn == 256 || cost < best) {
+                best = cost;
+                plan.w_rows = bn / 2;
+            }
+        }
+        return plan;
+    }
+    if (T <= 128) plan.x_rows = (T + 15) / 16 * 16;
     // The time goes with the rounds of CTAs (two an SM), times the steps of each and kFixed
     // more for its start and end; where two CTAs of an SM add up parts of K, the parts' way
     // through the SMs counts as a step for eight tokens (4096 outputs of 6144 columns in
@@ -662,7 +736,12 @@ MxLinearPlan mx_linear_plan(int T, int N, int K, int x_elem, int w_elem) {
 
 cudaError_t launch_mx_linear(const MxLinearLaunch& a, const MxLinearPlan& plan, cudaStream_t st) {
     const int mode = mode_of(a.x_elem, a.w_elem);
-    if (plan.split == 0) return mode == X4W4 ? launch_pair<X4W4>(a, st) : mode == X8W4 ? launch_pair<X8W4>(a, st) : launch_pair<X8W8>(a, st);
+    if (plan.split == 0) {
+        const int bn = 2 * plan.w_rows;
+        if (bn == 256)
+            return mode == X4W4 ? launch_pair<X4W4, false>(a, bn, st) : mode == X8W4 ? launch_pair<X8W4, false>(a, bn, st) : launch_pair<X8W8, false>(a, bn, st);
+        return mode == X4W4 ? launch_pair<X4W4, true>(a, bn, st) : mode == X8W4 ? launch_pair<X8W4, true>(a, bn, st) : launch_pair<X8W8, true>(a, bn, st);
+    }
     Params p{};
     p.xs = a.xs;
     p.ws = a.ws;

@@ -40,7 +40,7 @@ SHAPES = [
     (200, 777, 96), (300, 264, 8192), (513, 1111, 500), (1024, 1280, 256),
     # many tiles of many tokens
     (1300, 4000, 300), (2305, 2100, 257), (20000, 200, 128), (300, 10000, 640), (129, 20000, 96), (2048, 2560, 1024),
-    (5000, 1300, 33),
+    (5000, 1300, 33), (512, 4096, 500), (1440, 2000, 1100), (400, 5000, 900), (2050, 5120, 640),
     # one and two CTAs an SM, rings of all depths, tiles of more than 128 tokens in parts
     (16, 20480, 1000), (128, 20000, 700), (100, 10000, 2100), (40, 4000, 6000), (256, 4096, 1100), (1000, 1000, 2900),
     # long rows
@@ -80,11 +80,11 @@ def test_whole_numbers_are_exact(fsa, T, N, K, fx, fw):
 
 
 @pytest.mark.parametrize("fx,fw", MODES)
-@pytest.mark.parametrize("times", [1, 70])
-def test_one_element_at_a_time(fsa, fx, fw, times):
+@pytest.mark.parametrize("times,N", [(1, 200), (70, 200), (5, 2000), (16, 2000)])
+def test_one_element_at_a_time(fsa, fx, fw, times, N):
     """x holds one element 1 in each row, at every column in turn: y's rows are w's
     columns, so a wrong place of a code or a scale shows."""
-    K, N = 288, 200
+    K = 288
     w = fsa.mx_pack(_bf16((N, K), 3, 1.0, 1.0), fw)
     x = torch.zeros(K, K, dtype=torch.bfloat16, device="cuda")
     x.fill_diagonal_(1.0)

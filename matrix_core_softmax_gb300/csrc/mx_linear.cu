@@ -670,6 +670,18 @@ cudaError_t launch_pair(const MxLinearLaunch& a, int bn, cudaStream_t st) {
                         *a.tm_x, *a.tm_w, p);
 }
 
+// Tiles that run at once, each split between `split` CTAs of a cluster, one CTA or two an SM.
+// A cluster stays within a group of SMs that are not all as many, so clusters of eight leave
+// some SMs out (a token by 4096 columns in eight by four bits with one CTA an SM: 15 tiles
+// split by 8 4.9 us, 16 tiles 8.1; 36 tiles split by 4 5.6, 37 tiles 8.4; 74 tiles split by 2
+// 7.9, 75 tiles 12.0. With two an SM: 36 and 37 tiles 5.5 and 8.1; 74 and 75 7.6 and 12.2;
+// 152 and 153 10.6 and 11.8).
+int64_t tiles_at_once(int split, int per_sm) {
+    const int64_t one = split == 1 ? kSms : split == 2 ? 74 : split == 4 ? 36 : 15;
+    const int64_t two = split == 1 ? 2 * kSms : split == 2 ? 152 : split == 4 ? 74 : 36;
+    return per_sm == 1 ? one : two;
+}
+
 int mode_of(int x_elem, int w_elem) { return w_elem == ELEM_E4M3 ? X8W8 : x_elem == ELEM_E4M3 ? X8W4 : X4W4; }
 
 template <int kMode>
@@ -677,7 +689,7 @@ cudaError_t launch(const MxLinearLaunch& a, Params p, int tiles, cudaStream_t st
     static KernelSetup setup;
     cudaError_t e = setup(reinterpret_cast<const void*>(mx_linear_kernel<kMode>), kSmemOne, 0);
     if (e != cudaSuccess) return e;
-    const int smem = tiles * p.split <= kSms ? kSmemOne : kSmemTwo;
+    const int smem = tiles <= tiles_at_once(p.split, 1) ? kSmemOne : kSmemTwo;
     // scales as far ahead as codes: a slot is two steps in four bits and four in eight
     for (p.slots = kMode == X4W4 || smem == kSmemOne ? kSfSlots : 2; p.slots >= 2; p.slots /= 2) {
         p.stages = (smem - 1024 - p.slots * kSfBytes) / stage_bytes(p.n_tok);
@@ -693,14 +705,13 @@ cudaError_t launch(const MxLinearLaunch& a, Params p, int tiles, cudaStream_t st
 MxLinearPlan mx_linear_plan(int T, int N, int K, int x_elem, int w_elem) {
     MxLinearPlan plan{};
     plan.w_rows = plan.x_rows = 128;
-    // 128 x 128 tiles of more than 128 tokens where they are so few that parts of K go to
-    // two CTAs and more, pairs of CTAs otherwise (256 x 4096 x 4096 in eight by four bits:
-    // 10.4 us against 13.6; 333 x 5000 x 4128, 120 tiles: 14.5 against 13.9; 2048 x 2048 x
-    // 2048: 13.3 against 9.8)
+    // More than 128 tokens: 128 x 128 tiles where four CTAs to a tile run at once, one an SM,
+    // pairs of CTAs otherwise (256 x 2048 x 4096, 32 tiles: 8.6 us against 9.9 in eight by four
+    // bits; 256 x 4096 x 4096, 64 tiles: 10.4 against 10.1, and 8.9 against 7.7 in four bits).
     const int64_t tiles = mx_atoms(N) * mx_atoms(T);
     const int kAtoms = stage_atoms(mode_of(x_elem, w_elem));
     const int64_t steps = (mx_atoms(K) + kAtoms - 1) / kAtoms;
-    if (T > 128 && tiles > kSms / 2) {
+    if (T > 128 && tiles > tiles_at_once(4, 1)) {
         // Tiles of 256, 192 or 128 outputs, whichever take the fewest rounds of pairs' time
         // together (a step of fewer than 144 outputs is held up by its copies, a tile costs
         // two steps more).
@@ -716,7 +727,7 @@ MxLinearPlan mx_linear_plan(int T, int N, int K, int x_elem, int w_elem) {
         return plan;
     }
     if (T <= 128) plan.x_rows = (T + 15) / 16 * 16;
-    // The time goes with the rounds of CTAs (two an SM), times the steps of each and kFixed
+    // The time goes with the rounds of tiles (two CTAs an SM), times the steps of each and kFixed
     // more for its start and end; where two CTAs of an SM add up parts of K, the parts' way
     // through the SMs counts as a step for eight tokens (4096 outputs of 6144 columns in
     // eight by four bits, 1 / 64 / 128 tokens: split by 8, 256 CTAs, 6.4 / 10.2 / 13.9 us;
@@ -724,8 +735,8 @@ MxLinearPlan mx_linear_plan(int T, int N, int K, int x_elem, int w_elem) {
     plan.split = 1;
     int64_t best = 0;
     for (int s = 1; s <= kMaxSplit && s <= steps; s *= 2) {
-        int64_t cost = ((tiles * s + 2 * kSms - 1) / (2 * kSms)) * ((steps + s - 1) / s + kFixed);
-        if (s > 1 && tiles * s > kSms) cost += plan.x_rows / 8;
+        int64_t cost = ((tiles - 1) / tiles_at_once(s, 2) + 1) * ((steps + s - 1) / s + kFixed);
+        if (s > 1 && tiles > tiles_at_once(s, 1)) cost += plan.x_rows / 8;
         if (s == 1 || cost < best) {
             best = cost;
             plan.split = s;

@@ -288,3 +288,77 @@ def test_buffers_that_every_call_reuses(fsa, T):
         graph.replay()
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(got, want)) and fsa.get_device_error() == 0
+
+
+@pytest.mark.parametrize("fx,fw", MODES)
+@pytest.mark.parametrize("T,N,K", [(1, 1920, 4200), (3, 2048, 4096), (20, 4600, 4100), (7, 4736, 4096), (50, 9500, 3000), (12, 9600, 4096),
+                                   (100, 19456, 1300), (200, 1024, 5120), (256, 2300, 2500), (257, 1500, 2500), (140, 4700, 1100)])
+def test_as_many_clusters_as_run_at_once(fsa, T, N, K, fx, fw):
+    """Tiles around the numbers that parts of K in two, four and eight leave at work."""
+    x, w = _operands(fsa, T, N, K, fx, fw, T + N + K)
+    y = fsa.mx_linear(x, w)
+    assert fsa.get_device_error() == 0
+    ref.check_product(y, ref.values(x), ref.values(w))
+
+
+def test_all_kinds_at_once(fsa):
+    """Products in tiles of every kind, norms and the packed attention, each on a stream of
+    its own, give what they give alone."""
+    shapes = [(1, 2048, 2048), (30, 9000, 1024), (100, 20000, 512), (200, 1500, 2048), (512, 4096, 1024), (3000, 3000, 512)]
+    ops = [_operands(fsa, T, N, K, *MODES[i % 3], seed=i) for i, (T, N, K) in enumerate(shapes)]
+    jobs = [lambda x=x, w=w: fsa.mx_linear(x, w) for x, w in ops]
+    h, g = _bf16((6000, 1024), 40), _bf16((1, 1024), 41).view(-1)
+    jobs.append(lambda: fsa.mx_unpack(fsa.rms_norm_mx(h, g)))
+    q, kv = _bf16((2000, 8 * 64), 42).view(2000, 8, 64), _bf16((2000, 4 * 64), 43).view(2000, 4, 64)
+    ends = torch.tensor([0, 700, 2000], dtype=torch.int32, device="cuda")
+    jobs.append(lambda: fsa.varlen_attention_fwd(q, kv[:, :2], kv[:, 2:], ends))
+    want = [job() for job in jobs]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in jobs]
+    for _ in range(15):
+        got = []
+        for job, st in zip(jobs, streams):
+            with torch.cuda.stream(st):
+                got.append(job())
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+    assert fsa.get_device_error() == 0
+
+
+@pytest.mark.parametrize("T", [1, 400])
+def test_captured_beside_copies_and_forks(fsa, T):
+    """Calls captured right behind a fill, a copy, and a join with another stream."""
+    K, N = 1024, 768
+    w = fsa.mx_pack(_bf16((N, K), 1, K ** -0.5), "mxfp4")
+    src = [_bf16((T, K), 2 + i) for i in range(2)]
+    x, z, op = torch.empty_like(src[0]), torch.empty(T, N, dtype=torch.bfloat16, device="cuda"), fsa.mx_new_operand(T, K, "mxfp8")
+    side = torch.cuda.Stream()
+
+    def step():
+        z.zero_()
+        x.copy_(src[0])
+        fsa.mx_pack(x, "mxfp8", out=op)
+        here = torch.cuda.current_stream()
+        side.wait_stream(here)
+        with torch.cuda.stream(side):
+            a = fsa.mx_linear(op, w)
+        fsa.mx_linear(op, w, out=z)
+        here.wait_stream(side)
+        back = fsa.mx_unpack(op)
+        op2 = fsa.mx_pack(back, "mxfp4")
+        x.fill_(0)
+        return fsa.mx_linear(op2, w), a, z
+
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = step()
+    for s in (src[1], src[0]):
+        src[0].copy_(s.clone())
+        for _ in range(3):
+            graph.replay()
+        torch.cuda.synchronize()
+        first = fsa.mx_pack(src[0], "mxfp8")
+        want = fsa.mx_linear(first, w)
+        assert torch.equal(got[1], want) and torch.equal(got[2], want)
+        assert torch.equal(got[0], fsa.mx_linear(fsa.mx_pack(fsa.mx_unpack(first), "mxfp4"), w))
+    assert fsa.get_device_error() == 0

@@ -172,21 +172,21 @@ __device__ __forceinline__ uint4 values8(uint2 c, uint32_t byte) {
     return make_uint4(o[0], o[1], o[2], o[3]);
 }
 
-// The codes and the scale byte of piece p of a row.
+// The codes and the scale byte of piece p of a row.  (Ordinary loads: the kernel before
+// may still write them when this one begins.)
 template <int kElem>
 __device__ __forceinline__ uint32_t read8(const uint8_t* codes, const uint8_t* scales, int64_t r, int p, int n_atoms, uint2& c) {
     const uint8_t* src = codes + (r * n_atoms * 16 + p) * MxElem<kElem>::piece_bytes;
     if constexpr (kElem == ELEM_E2M1)
-        c = make_uint2(__ldg(reinterpret_cast<const uint32_t*>(src)), 0u);
+        c = make_uint2(*reinterpret_cast<const uint32_t*>(src), 0u);
     else
-        c = __ldg(reinterpret_cast<const uint2*>(src));
-    return __ldg(scales + mx_scale_word(r, p >> 4, n_atoms) + ((p >> 2) & 3));
+        c = *reinterpret_cast<const uint2*>(src);
+    return scales[mx_scale_word(r, p >> 4, n_atoms) + ((p >> 2) & 3)];
 }
 
 template <int kElem>
-__global__ void __launch_bounds__(32 * kWarps) mx_unpack_kernel(const uint8_t* __restrict__ codes, const uint8_t* __restrict__ scales,
-                                                                int64_t rows, int cols, int lg, int align, uint16_t* __restrict__ out,
-                                                                int64_t stride) {
+__global__ void __launch_bounds__(32 * kWarps) mx_unpack_kernel(const uint8_t* codes, const uint8_t* scales, int64_t rows,
+                                                                int cols, int lg, int align, uint16_t* out, int64_t stride) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int64_t r = blockIdx.x * static_cast<int64_t>(kWarps >> lg) + (warp >> lg);
     grid_launch_next();
@@ -208,9 +208,8 @@ __global__ void __launch_bounds__(32 * kWarps) mx_unpack_kernel(const uint8_t* _
 
 // As mx_pack_short_kernel.
 template <int kElem>
-__global__ void __launch_bounds__(32 * kWarps) mx_unpack_short_kernel(const uint8_t* __restrict__ codes,
-                                                                      const uint8_t* __restrict__ scales, int64_t rows, int cols,
-                                                                      int align, uint16_t* __restrict__ out, int64_t stride) {
+__global__ void __launch_bounds__(32 * kWarps) mx_unpack_short_kernel(const uint8_t* codes, const uint8_t* scales, int64_t rows,
+                                                                      int cols, int align, uint16_t* out, int64_t stride) {
     const int64_t r0 = (blockIdx.x * static_cast<int64_t>(2 * kWarps) + (threadIdx.x >> 4)) * kUnroll;
     const int p = threadIdx.x & 15;
     grid_launch_next();

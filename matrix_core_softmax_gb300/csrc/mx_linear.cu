@@ -525,7 +525,9 @@ __global__ void __launch_bounds__(kPairThreads, 1)
             if (i != first_tile) ok = wait(&sm.acc_empty, acc_ph);
             int t_tile, n_tile;
             pair_tile(p, i, t_tile, n_tile);
-            const uint32_t skew = bn * n_tile % 128 / 32;  // a tile that begins inside a group (32 rows a column)
+            // scales of a tile that begins inside a group, 32 rows a column (an odd column would
+            // be a misaligned address: tiles begin at multiples of 64)
+            const uint32_t skew = bn * n_tile % 128 / 32;
             for (int k = 0; ok && k < steps; ++k) {
                 const int in = k % kSfSteps;
                 if (kRing && in == 0) ok = wait(&sm.sf_full[slot.at], slot.ph);
@@ -749,9 +751,11 @@ cudaError_t launch_mx_linear(const MxLinearLaunch& a, const MxLinearPlan& plan, 
     const int mode = mode_of(a.x_elem, a.w_elem);
     if (plan.split == 0) {
         const int bn = 2 * plan.w_rows;
-        if (bn == 256)
-            return mode == X4W4 ? launch_pair<X4W4, false>(a, bn, st) : mode == X8W4 ? launch_pair<X8W4, false>(a, bn, st) : launch_pair<X8W8, false>(a, bn, st);
-        return mode == X4W4 ? launch_pair<X4W4, true>(a, bn, st) : mode == X8W4 ? launch_pair<X8W4, true>(a, bn, st) : launch_pair<X8W8, true>(a, bn, st);
+        switch (mode) {
+            case X4W4: return bn == 256 ? launch_pair<X4W4, false>(a, bn, st) : launch_pair<X4W4, true>(a, bn, st);
+            case X8W4: return bn == 256 ? launch_pair<X8W4, false>(a, bn, st) : launch_pair<X8W4, true>(a, bn, st);
+            default: return bn == 256 ? launch_pair<X8W8, false>(a, bn, st) : launch_pair<X8W8, true>(a, bn, st);
+        }
     }
     Params p{};
     p.xs = a.xs;

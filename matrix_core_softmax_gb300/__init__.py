@@ -644,6 +644,10 @@ def varlen_attention_fwd(q, k, v, cu_seqlens_q, cu_seqlens_k=None, *, causal: bo
 # ---- products of matrices in MX formats --------------------------------------
 
 
+# New tensors on the current device (of two calls that pack a token and read it back,
+# 11.8 us of host time with it, 19.6 with torch.empty and a storage for the operand).
+_empty_cuda = torch._C._dynamo.guards._empty_strided_cuda
+
 # element and bytes of 128 codes of a row
 _OPERANDS = {"mxfp4": (ELEM_E2M1, 64), "mxfp8": (ELEM_E4M3, 128)}
 
@@ -661,8 +665,8 @@ class MxOperand:
     ("mxfp8")], scales uint8 [ceil(rows / 128), ceil(cols / 128), 512].
 
     MxOperand(codes, scales, cols, fmt) is one of given tensors; mx_new_operand, mx_pack
-    and rms_norm_mx make one in a single storage, of which codes and scales become
-    tensors when they are asked for (beside a launch a tensor costs 5 us, a storage 2)."""
+    and rms_norm_mx make one of a single tensor of bytes, of which codes and scales are
+    views that are made when they are asked for."""
     __slots__ = ("rows", "cols", "fmt", "elem", "_dev", "_bytes", "_codes", "_scales")
 
     def __init__(self, codes: torch.Tensor, scales: torch.Tensor, cols: int, fmt: str):
@@ -679,16 +683,19 @@ class MxOperand:
         self._dev, self._bytes, self._codes, self._scales = codes.get_device(), None, codes, scales
 
     @classmethod
-    def _new(cls, rows: int, cols: int, fmt: str, device, dev=None):
-        """An operand with arbitrary contents on `device`, whose index is dev."""
+    def _new(cls, rows: int, cols: int, fmt: str, dev: int, device=None):
+        """An operand with arbitrary contents on the current CUDA device dev, or on `device`."""
         elem, width = _operand_format(fmt)
         if rows < 0 or cols < 1:
             raise ValueError("an operand has at least one column")
         self = cls.__new__(cls)
         atoms = (cols + 127) >> 7
-        data = torch.UntypedStorage(atoms * (rows * width + ((rows + 127) >> 7) * 512), device=device)
-        if dev is None:
-            dev = data.device.index if data.device.type == "cuda" else -1
+        size = atoms * (rows * width + ((rows + 127) >> 7) * 512)
+        if device is None:
+            data = _empty_cuda((size,), (1,), _u8)
+        else:
+            data = torch.empty(size, dtype=_u8, device=device)
+            dev = data.get_device()
         self.rows, self.cols, self.fmt, self.elem = rows, cols, fmt, elem
         self._dev, self._bytes, self._codes, self._scales = dev, data, None, None
         return self
@@ -699,20 +706,22 @@ class MxOperand:
         at = self._bytes.data_ptr()
         return at, at + self.rows * ((self.cols + 127) >> 7) * _OPERANDS[self.fmt][1]
 
-    def _tensor(self, at: int, shape):
-        return torch.empty(0, dtype=_u8, device=self._bytes.device).set_(self._bytes, at, shape)
+    def _split(self):
+        atoms, width = (self.cols + 127) >> 7, _OPERANDS[self.fmt][1]
+        size = self.rows * atoms * width
+        self._codes = self._bytes[:size].view(self.rows, atoms * width)
+        self._scales = self._bytes[size:].view((self.rows + 127) >> 7, atoms, 512)
 
     @property
     def codes(self) -> torch.Tensor:
         if self._codes is None:
-            self._codes = self._tensor(0, (self.rows, ((self.cols + 127) >> 7) * _OPERANDS[self.fmt][1]))
+            self._split()
         return self._codes
 
     @property
     def scales(self) -> torch.Tensor:
         if self._scales is None:
-            atoms = (self.cols + 127) >> 7
-            self._scales = self._tensor(self.rows * atoms * _OPERANDS[self.fmt][1], ((self.rows + 127) >> 7, atoms, 512))
+            self._split()
         return self._scales
 
     @property
@@ -728,7 +737,7 @@ class MxOperand:
 
 def mx_new_operand(rows: int, cols: int, fmt: str, device="cuda") -> MxOperand:
     """An operand whose contents are arbitrary, for mx_pack and rms_norm_mx to fill."""
-    return MxOperand._new(rows, cols, fmt, device)
+    return MxOperand._new(rows, cols, fmt, -1, device)
 
 
 def _rows(t: torch.Tensor, name: str, shape, dev: int) -> int:
@@ -742,10 +751,15 @@ def _rows(t: torch.Tensor, name: str, shape, dev: int) -> int:
     return step if shape[0] > 1 else shape[1]  # (a lone row's stride is arbitrary)
 
 
-def _filled(out, shape, fmt: str, dev: int, device) -> MxOperand:
+def _new_rows(rows: int, cols: int) -> torch.Tensor:
+    """bf16 [rows, cols] with arbitrary contents on the current device."""
+    return _empty_cuda((rows, cols), (cols, 1), _bf16)
+
+
+def _filled(out, shape, fmt: str, dev: int) -> MxOperand:
     """The operand that a call fills, new or given."""
     if out is None:
-        return MxOperand._new(*shape, fmt, device, dev)
+        return MxOperand._new(*shape, fmt, dev)
     if (out.rows, out.cols) != tuple(shape) or out.fmt != fmt or out._dev != dev:
         raise ValueError(f"out must be an operand of {list(shape)} in {fmt} on cuda:{dev}")
     return out
@@ -761,7 +775,7 @@ def mx_pack(x, fmt: str = "mxfp4", *, out=None, stream=None) -> MxOperand:
         with _on(x, stream):
             return mx_pack(x, fmt, out=out)
     step = _rows(x, "x", shape, dev)
-    op = _filled(out, shape, fmt, dev, x.device)
+    op = _filled(out, shape, fmt, dev)
     _check(load().fsa_mx_pack(x.data_ptr(), step, *shape, op.elem, *op._pointers(), _raw_stream(dev)), "fsa_mx_pack")
     return op
 
@@ -776,7 +790,7 @@ def mx_unpack(op: MxOperand, *, out=None, stream=None):
             return mx_unpack(op, out=out)
     rows, cols = op.rows, op.cols
     if out is None:
-        out, step = torch.empty((rows, cols), dtype=_bf16, device=op.device), cols
+        out, step = _new_rows(rows, cols), cols
     else:
         step = _rows(out, "out", (rows, cols), dev)
     _check(load().fsa_mx_unpack(*op._pointers(), rows, cols, op.elem, out.data_ptr(), step, _raw_stream(dev)), "fsa_mx_unpack")
@@ -800,13 +814,13 @@ def rms_norm_mx(x, gain, *, residual=None, eps: float = 1e-6, fmt: str = "mxfp8"
     if residual is not None:
         res_step, res = _rows(residual, "residual", shape, dev), residual.data_ptr()
         if out_sum is None:
-            out_sum, total_step = torch.empty(shape, dtype=_bf16, device=x.device), shape[1]
+            out_sum, total_step = _new_rows(*shape), shape[1]
         else:
             total_step = _rows(out_sum, "out_sum", shape, dev)
         total = out_sum.data_ptr()
     elif out_sum is not None:
         raise ValueError("there is no sum without a residual")
-    op = _filled(out, shape, fmt, dev, x.device)
+    op = _filled(out, shape, fmt, dev)
     _check(load().fsa_rms_norm_mx(x.data_ptr(), step, res, res_step, gain.data_ptr(), eps, *shape, op.elem, total, total_step,
                                   *op._pointers(), _raw_stream(dev)), "fsa_rms_norm_mx")
     return op if residual is None else (op, out_sum)
@@ -828,7 +842,7 @@ def mx_linear(x: MxOperand, w: MxOperand, *, out=None, wait_timeout_ms: int = 0,
     if w.cols != K:
         raise ValueError(f"x has {K} columns and w {w.cols}")
     if out is None:
-        out, step = torch.empty((T, N), dtype=_bf16, device=x.device), N
+        out, step = _new_rows(T, N), N
     else:
         step = _rows(out, "out", (T, N), dev)
     opt = None

@@ -266,6 +266,17 @@ __device__ __forceinline__ float over_row(float s, bool most, int lg, float* par
     return s;
 }
 
+// 1 / sqrt(m) within 2^-24 (1 + 2^-18) of itself, m far from either end of FP32: rsqrtf's r
+// (within 2 units) and a step of Newton, r + r / 2 (1 - m r^2), m r in two parts.  The
+// error of a root is a whole row's: rsqrtf alone put values on the wrong side of a border
+// between two codes that a rounded root gets right (777 x 4096 in eight bits: 5.1e-5 off 64
+// bits in the 2-norm, with this 4.8e-5).  16384 x 8192 takes 154 us with either, 156 with
+// __frsqrt_rn.
+__device__ __forceinline__ float root_inverse(float m) {
+    const float r = rsqrtf(m), q = m * r, low = __fmaf_rn(m, r, -q);
+    return __fmaf_rn(0.5f * r, __fmaf_rn(-low, r, __fmaf_rn(-q, r, 1.0f)), r);
+}
+
 // The norm of row r, whose h and gains this lane holds kV pieces of, into the operand;
 // 2^lg warps a row.  `turn` alternates from row to row; `read` is called once all of
 // the row's warps have h.
@@ -310,7 +321,7 @@ __device__ __forceinline__ void norm_row(const RmsNormMx& a, int64_t r, const ui
         }
         s = over_row(t, false, lg, part[3]);
     }
-    const float inv = f * rsqrtf(s * a.inv_cols + a.eps * f * f);
+    const float inv = f * root_inverse(s * a.inv_cols + a.eps * f * f);
     const float2 inv2 = make_float2(inv, inv);
     const MxRow out = mx_row<kElem>(a.codes, a.scales, r, n_atoms);
 #pragma unroll

@@ -427,6 +427,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     if (!loader) cluster_wait();
     tc_fence_after();
     grid_launch_next();  // (the next kernel's CTAs find this one's tensor memory taken)
+    grid_wait();         // in all warps: the time of the kernel before is not their waits'
     const uint32_t tmem = sm.tmem_base;
     auto give_up = [&] {
         sm.abort = 1;
@@ -441,7 +442,6 @@ __global__ void __launch_bounds__(kPairThreads, 1)
 
     if (loader) {
         if (lane == 0) {
-            grid_wait();
             const int64_t x_groups = mx_atoms(p.T), w_groups = mx_atoms(p.N);
             int issued = 0;
             for (int i = first_tile; ok && i < tiles; i += tile_step) {

@@ -82,6 +82,10 @@ typedef enum {
                                         word reads FSA_ERR_TIMEOUT (attention
                                         over the four-bit cache: no warp sees
                                         its second group of keys) */
+#define FSA_DEBUG_LOSE_ONE_WAIT 0x2  /* fsa_rms_norm_mx_ex: one lane of a row's
+                                        last warp takes the copy that it has
+                                        waited for in the ring's second place
+                                        for one whose wait ran out */
 
 typedef struct {
     /* Score scale; <= 0 selects 1/sqrt(D). */
@@ -549,11 +553,22 @@ FSA_API fsa_status fsa_mx_unpack(const uint8_t *codes, const uint8_t *scales, in
  *  x or residual itself (same address and stride), and overlap nothing else.
  * h and y must be finite; the squares' sum may pass FP32's range.  eps > 0.
  * cols in 1 .. 32768.
+ * Many rows go through a ring of copies, whose bounded waits are reported by
+ * fsa_get_device_error when one runs out; operand and sum are then undefined, what
+ * the sum replaces included.
  */
 FSA_API fsa_status fsa_rms_norm_mx(const void *x, int64_t x_stride, const void *residual,
                                    int64_t residual_stride, const void *gain, float eps, int64_t rows,
                                    int64_t cols, int elem, void *sum, int64_t sum_stride,
                                    uint8_t *codes, uint8_t *scales, void *stream);
+
+/* As fsa_rms_norm_mx; of *opt (NULL: all zero) wait_timeout_ms and debug_flags
+ * (FSA_DEBUG_SKIP_KV_ARRIVE: the ring's second place never arrives) are used. */
+FSA_API fsa_status fsa_rms_norm_mx_ex(const void *x, int64_t x_stride, const void *residual,
+                                      int64_t residual_stride, const void *gain, float eps, int64_t rows,
+                                      int64_t cols, int elem, void *sum, int64_t sum_stride,
+                                      uint8_t *codes, uint8_t *scales, const fsa_options *opt,
+                                      void *stream);
 
 /*
  * fsa_mx_linear -- y[t][n] = sum over k of x[t][k] w[n][k] of two operands: T tokens'

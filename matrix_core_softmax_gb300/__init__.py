@@ -20,7 +20,7 @@ LIB_PATH = os.path.join(_HERE, "_build", "libfsa.so")
 FSA_MXFP8, FSA_MXFP6, FSA_MXFP4, FSA_MXFP4_EFQ = 0, 1, 2, 3
 FORMATS = {"mxfp8": FSA_MXFP8, "mxfp6": FSA_MXFP6, "mxfp4": FSA_MXFP4, "mxfp4_efq": FSA_MXFP4_EFQ}
 ELEM_E4M3, ELEM_E2M3, ELEM_E2M1 = 0, 1, 2
-DEBUG_SKIP_KV_ARRIVE = 0x1
+DEBUG_SKIP_KV_ARRIVE, DEBUG_LOSE_ONE_WAIT = 0x1, 0x2
 
 STATUS = {0: "FSA_OK", 1: "FSA_ERR_INVALID_ARGUMENT", 2: "FSA_ERR_UNSUPPORTED",
           3: "FSA_ERR_CUDA", 4: "FSA_ERR_OUT_OF_MEMORY", 5: "FSA_ERR_TIMEOUT"}
@@ -34,7 +34,8 @@ EXPORTS = ("fsa_quantize_mx", "fsa_attention_fwd", "fsa_attention_fwd_ex",
            "fsa_attention_fwd_host", "fsa_cross_attention_fwd_host", "fsa_mma_rate_probe",
            "fsa_kv4_page_bytes", "fsa_kv4_append", "fsa_kv4_read", "fsa_kv4_attention_fwd",
            "fsa_kv4_attention_workspace_size", "fsa_varlen_attention_fwd", "fsa_kv4_attention_fwd_ex",
-           "fsa_varlen_attention_fwd_ex", "fsa_mx_pack", "fsa_mx_unpack", "fsa_rms_norm_mx", "fsa_mx_linear")
+           "fsa_varlen_attention_fwd_ex", "fsa_mx_pack", "fsa_mx_unpack", "fsa_rms_norm_mx", "fsa_mx_linear",
+           "fsa_rms_norm_mx_ex")
 
 
 class FsaError(RuntimeError):
@@ -139,6 +140,8 @@ def load(path: str | None = None):
             lib.fsa_mx_unpack.restype = I
             lib.fsa_rms_norm_mx.argtypes = [V, I64, V, I64, V, F, I64, I64, I, V, I64, V, V, V]
             lib.fsa_rms_norm_mx.restype = I
+            lib.fsa_rms_norm_mx_ex.argtypes = [V, I64, V, I64, V, F, I64, I64, I, V, I64, V, V, ctypes.POINTER(Options), V]
+            lib.fsa_rms_norm_mx_ex.restype = I
             lib.fsa_mx_linear.argtypes = [V, V, I, V, V, I, I64, I64, I64, V, I64, ctypes.POINTER(Options), V]
             lib.fsa_mx_linear.restype = I
             lib.fsa_get_device_error.argtypes = [V]
@@ -797,18 +800,21 @@ def mx_unpack(op: MxOperand, *, out=None, stream=None):
     return out
 
 
-def rms_norm_mx(x, gain, *, residual=None, eps: float = 1e-6, fmt: str = "mxfp8", out=None, out_sum=None, stream=None):
+def rms_norm_mx(x, gain, *, residual=None, eps: float = 1e-6, fmt: str = "mxfp8", out=None, out_sum=None,
+                wait_timeout_ms: int = 0, debug_flags: int = 0, stream=None):
     """fsa_rms_norm_mx: the root-mean-square norm of x, CUDA bf16 [rows, cols]
     (contiguous rows at any distance), times gain, bf16 [cols], as an operand of
     mx_linear.  With a residual, bf16 like x, the norm is that of h = x + residual
     (rounded to bf16), and (operand, h) is returned; out_sum, written instead of a new
-    tensor, may be x or residual itself."""
+    tensor, may be x or residual itself.  wait_timeout_ms: limit of the kernel's bounded
+    waits (0: 2000)."""
     dev, shape = x.get_device(), x.shape
     if dev < 0 or len(shape) != 2:
         raise ValueError("x must be a CUDA tensor [rows, cols]")
     if stream is not None or dev != _device():
         with _on(x, stream):
-            return rms_norm_mx(x, gain, residual=residual, eps=eps, fmt=fmt, out=out, out_sum=out_sum)
+            return rms_norm_mx(x, gain, residual=residual, eps=eps, fmt=fmt, out=out, out_sum=out_sum,
+                               wait_timeout_ms=wait_timeout_ms, debug_flags=debug_flags)
     step, res, res_step, total, total_step = _rows(x, "x", shape, dev), None, 0, None, 0
     _plain(gain, "gain", _bf16, shape[1:], dev)
     if residual is not None:
@@ -821,8 +827,11 @@ def rms_norm_mx(x, gain, *, residual=None, eps: float = 1e-6, fmt: str = "mxfp8"
     elif out_sum is not None:
         raise ValueError("there is no sum without a residual")
     op = _filled(out, shape, fmt, dev)
-    _check(load().fsa_rms_norm_mx(x.data_ptr(), step, res, res_step, gain.data_ptr(), eps, *shape, op.elem, total, total_step,
-                                  *op._pointers(), _raw_stream(dev)), "fsa_rms_norm_mx")
+    opt = None
+    if wait_timeout_ms or debug_flags:
+        opt = ctypes.byref(Options(wait_timeout_ms=wait_timeout_ms, debug_flags=debug_flags))
+    _check(load().fsa_rms_norm_mx_ex(x.data_ptr(), step, res, res_step, gain.data_ptr(), eps, *shape, op.elem, total, total_step,
+                                     *op._pointers(), opt, _raw_stream(dev)), "fsa_rms_norm_mx")
     return op if residual is None else (op, out_sum)
 
 

@@ -721,6 +721,14 @@ fsa_status fsa_mx_unpack(const uint8_t* codes, const uint8_t* scales, int64_t ro
 fsa_status fsa_rms_norm_mx(const void* x, int64_t x_stride, const void* residual, int64_t residual_stride,
                            const void* gain, float eps, int64_t rows, int64_t cols, int elem, void* sum,
                            int64_t sum_stride, uint8_t* codes, uint8_t* scales, void* stream) {
+    return fsa_rms_norm_mx_ex(x, x_stride, residual, residual_stride, gain, eps, rows, cols, elem, sum, sum_stride, codes,
+                              scales, nullptr, stream);
+}
+
+fsa_status fsa_rms_norm_mx_ex(const void* x, int64_t x_stride, const void* residual, int64_t residual_stride,
+                              const void* gain, float eps, int64_t rows, int64_t cols, int elem, void* sum,
+                              int64_t sum_stride, uint8_t* codes, uint8_t* scales, const fsa_options* opt, void* stream) {
+    const fsa_options op = opt ? *opt : fsa_options{};
     fsa_status s = check_operand(codes, scales, rows, cols, elem);
     if (s != FSA_OK) return s;
     if (cols > kNormMaxCols || !std::isfinite(eps) || !(eps > 0.0f)) return FSA_ERR_INVALID_ARGUMENT;
@@ -732,7 +740,7 @@ fsa_status fsa_rms_norm_mx(const void* x, int64_t x_stride, const void* residual
     DeviceState* ds;
     s = current_device(&dev, &ds);
     if (s != FSA_OK) return s;
-    RmsNormMx a{};
+    RmsNormMxLaunch a{};
     a.x = x;
     a.residual = residual;
     a.gain = gain;
@@ -745,7 +753,8 @@ fsa_status fsa_rms_norm_mx(const void* x, int64_t x_stride, const void* residual
     a.eps = eps;
     a.codes = codes;
     a.scales = scales;
-    a.timeout_ns = wait_limit_ns(fsa_options{});
+    a.timeout_ns = wait_limit_ns(op);
+    a.debug_flags = op.debug_flags;
     a.err_word = ds->err;
     return launch_rms_norm_mx(a, elem, static_cast<cudaStream_t>(stream)) == cudaSuccess ? FSA_OK : FSA_ERR_CUDA;
 }

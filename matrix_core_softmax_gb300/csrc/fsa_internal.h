@@ -199,8 +199,11 @@ struct RmsNormMx {
     int x_align, residual_align, sum_align, gain_align;
     float inv_cols;
 };
+struct RmsNormMxLaunch : RmsNormMx {
+    int debug_flags;
+};
 constexpr int kNormMaxCols = 32768;
-cudaError_t launch_rms_norm_mx(const RmsNormMx& a, int elem, cudaStream_t st);
+cudaError_t launch_rms_norm_mx(const RmsNormMxLaunch& a, int elem, cudaStream_t st);
 
 // Product of two MX operands (mx_linear.cu).
 struct MxLinearLaunch {

@@ -9,6 +9,7 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include "fsa.h"
 #include "fsa_internal.h"
 #include "mx_operand.cuh"
 #include "sm100_ptx.cuh"
@@ -373,11 +374,13 @@ __global__ void __launch_bounds__(kWide ? 1024 : 512) rms_norm_mx_kernel(const R
 
 // The same for many rows that start on 16 bytes: the warps of a row stay and take every
 // gridDim'th group's row, which bulk copies bring into a ring of shared memory ahead of
-// them, so that the copies wait for no row's sum; the gains stay in registers.
+// them, so that the copies wait for no row's sum; the gains stay in registers.  (Its
+// arguments are one word more than the other kernel's; as many, and it took 2 to 6 % longer:
+// 65536 x 1024 55.5 us, with the word 51.6.)
 constexpr int kMaxRing = 4;
 
 template <int kElem, int kV, int kThreads>
-__global__ void __launch_bounds__(kThreads, kThreads == 256 ? 3 : 1) rms_norm_mx_ring_kernel(const RmsNormMx a, int lg, int stages) {
+__global__ void __launch_bounds__(kThreads, kThreads == 256 ? 3 : 1) rms_norm_mx_ring_kernel(const RmsNormMxLaunch a, int lg, int stages) {
     extern __shared__ __align__(16) uint8_t ring[];
     __shared__ float part[4][32];
     __shared__ uint64_t full[kMaxRing][kThreads / 32];
@@ -392,7 +395,7 @@ __global__ void __launch_bounds__(kThreads, kThreads == 256 ? 3 : 1) rms_norm_mx
     if (threadIdx.x == 0) {
         gone = 0;
         for (int i = 0; i < stages; ++i)
-            for (int j = 0; j < per; ++j) mbar_init(&full[i][j], 1);
+            for (int j = 0; j < per; ++j) mbar_init(&full[i][j], i == 1 && (a.debug_flags & FSA_DEBUG_SKIP_KV_ARRIVE) ? 2 : 1);
         fence_mbar_init();
     }
     grid_launch_next();
@@ -416,20 +419,21 @@ __global__ void __launch_bounds__(kThreads, kThreads == 256 ? 3 : 1) rms_norm_mx
     int st = 0, turn = 0;
     uint32_t ph = 0;
     bool lost = false;
+    // test use: the place of the ring at which this lane gives up
+    const int lose_at = (a.debug_flags & FSA_DEBUG_LOSE_ONE_WAIT) && lane == 31 && ((warp + 1) & ((1 << lg) - 1)) == 0 ? 1 : -1;
     for (; r < a.rows; r += hop) {
-        // a copy that does not arrive is reported, and the outputs from its row on are
-        // undefined: nothing more is fetched, and what is in flight lands before anyone
-        // leaves (the row's warps still meet, so that none waits for another)
-        if (!lost && !mbar_wait(&full[st][mine], ph, a.timeout_ns, &gone)) {
+        // a copy that any lane gave up waiting for is reported, and the outputs from its row
+        // on are undefined.  A leader that gives up fetches nothing more and waits for what
+        // is in flight; one that does not goes on fetching, and waiting for, the rows of
+        // lanes that did.  (The row's warps still meet, so that none waits for another.)
+        if (!lost && (!mbar_wait(&full[st][mine], ph, a.timeout_ns, &gone) || st == lose_at)) {
             lost = true;
             gone = 1;
-            if (leader) {
-                atomicOr(a.err_word, kErrTimeout);
-                int dummy = 0;
-                for (int i = 0; i < stages; ++i)
-                    if (r + i * hop < a.rows)
-                        mbar_wait(&full[(st + i) % stages][mine], st + i < stages ? ph : ph ^ 1u, a.timeout_ns, &dummy);
-            }
+            atomicOr(a.err_word, kErrTimeout);
+            int dummy = 0;
+            for (int i = 0; leader && i < stages; ++i)
+                if (r + i * hop < a.rows)
+                    mbar_wait(&full[(st + i) % stages][mine], st + i < stages ? ph : ph ^ 1u, a.timeout_ns, &dummy);
         }
         __syncwarp();
         const uint8_t* src = at + st * slot_bytes;
@@ -496,7 +500,7 @@ NormRing norm_ring(int64_t stage) {
 }
 
 template <int kElem, int kV>
-cudaError_t norm_launch(const RmsNormMx& a, int lg, cudaStream_t st) {
+cudaError_t norm_launch(const RmsNormMxLaunch& a, int lg, cudaStream_t st) {
     const int warps = 1 << lg > kWarps ? 1 << lg : kWarps;
     const int64_t per = warps >> lg, groups = (a.rows + per - 1) / per;
     if (lg <= 4 && a.x_align == 16 && a.cols % 8 == 0 && (!a.residual || a.residual_align == 16)) {
@@ -511,11 +515,11 @@ cudaError_t norm_launch(const RmsNormMx& a, int lg, cudaStream_t st) {
         }
     }
     return launch_early(lg == 5 ? rms_norm_mx_kernel<kElem, kV, true> : rms_norm_mx_kernel<kElem, kV, false>,
-                        static_cast<unsigned>(groups), 32 * warps, 0, st, 1, a, lg);
+                        static_cast<unsigned>(groups), 32 * warps, 0, st, 1, static_cast<const RmsNormMx&>(a), lg);
 }
 
 template <int kElem>
-cudaError_t norm_pieces(const RmsNormMx& a, int lg, int v, cudaStream_t st) {
+cudaError_t norm_pieces(const RmsNormMxLaunch& a, int lg, int v, cudaStream_t st) {
     switch (v) {
         case 1: return norm_launch<kElem, 1>(a, lg, st);
         case 2: return norm_launch<kElem, 2>(a, lg, st);
@@ -558,8 +562,8 @@ cudaError_t launch_mx_unpack(const uint8_t* codes, const uint8_t* scales, int64_
                         cols, lg, align, dst, stride);
 }
 
-cudaError_t launch_rms_norm_mx(const RmsNormMx& args, int elem, cudaStream_t st) {
-    RmsNormMx a = args;
+cudaError_t launch_rms_norm_mx(const RmsNormMxLaunch& args, int elem, cudaStream_t st) {
+    RmsNormMxLaunch a = args;
     a.x_align = row_align(a.x, a.x_stride);
     a.residual_align = row_align(a.residual, a.residual_stride);
     a.sum_align = row_align(a.sum, a.sum_stride);

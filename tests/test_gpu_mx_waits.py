@@ -52,3 +52,35 @@ def test_time_of_the_kernel_before_does_not_count(fsa, T, N):
         fsa.mx_linear(x, w, out=out, wait_timeout_ms=limit)
         assert fsa.get_device_error() == 0
         assert torch.equal(out, want) and (y0 == 0).all()
+
+
+# rows enough for the blocks to stay: one warp a row, eight, sixteen
+RINGS = [(20000, 1024), (3000, 8192), (700, 16384)]
+
+
+@pytest.mark.parametrize("flags", ["SKIP_KV_ARRIVE", "LOSE_ONE_WAIT"])
+@pytest.mark.parametrize("residual", [True, False])
+@pytest.mark.parametrize("R,K", RINGS)
+def test_a_norm_that_gives_up_says_so(fsa, R, K, residual, flags):
+    """A place of the ring that never arrives, and a wait that runs out in one lane while
+    the lane that fetches goes on."""
+    x, g = _bf16((R, K), 3), _bf16((K,), 4)
+    kw = dict(residual=x if residual else None)
+    good = fsa.rms_norm_mx(x, g, **kw)
+    assert fsa.get_device_error() == 0
+    fsa.rms_norm_mx(x, g, wait_timeout_ms=5, debug_flags=getattr(fsa, "DEBUG_" + flags), **kw)
+    assert fsa.get_device_error() == 5 and fsa.get_device_error() == 0
+    again = fsa.rms_norm_mx(x, g, wait_timeout_ms=500, **kw)
+    assert fsa.get_device_error() == 0
+    if residual:
+        assert torch.equal(again[1], good[1])
+        good, again = good[0], again[0]
+    assert torch.equal(again.codes, good.codes)
+    assert torch.equal(fsa.mx_unpack(again), fsa.mx_unpack(good))
+
+
+def test_few_rows_wait_for_nothing(fsa):
+    x, g = _bf16((5, 512), 5), _bf16((512,), 6)
+    good = fsa.rms_norm_mx(x, g)
+    got = fsa.rms_norm_mx(x, g, wait_timeout_ms=1, debug_flags=fsa.DEBUG_SKIP_KV_ARRIVE | fsa.DEBUG_LOSE_ONE_WAIT)
+    assert fsa.get_device_error() == 0 and torch.equal(got.codes, good.codes)

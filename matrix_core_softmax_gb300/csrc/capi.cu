@@ -119,6 +119,20 @@ bool make_map_mx(CUtensorMap* m, const uint8_t* codes, int64_t rows, int64_t col
               CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Its scales in boxes of `atoms` atoms (8-byte elements) of `groups` groups of 128 rows.
+bool make_map_mx_scales(CUtensorMap* m, const uint8_t* scales, int64_t rows, int64_t cols, int atoms, int groups) {
+    EncodeTiledFn fn = encode_tiled();
+    if (!fn) return false;
+    constexpr int kWords = kAtomBytes / 8;
+    cuuint64_t dims[2] = {static_cast<cuuint64_t>(mx_atoms(cols) * kWords), static_cast<cuuint64_t>(mx_atoms(rows))};
+    cuuint64_t strides[1] = {static_cast<cuuint64_t>(mx_atoms(cols) * kAtomBytes)};
+    cuuint32_t boxes[2] = {static_cast<cuuint32_t>(atoms * kWords), static_cast<cuuint32_t>(groups)};
+    cuuint32_t es[2] = {1, 1};
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT64, 2, const_cast<uint8_t*>(scales), dims, strides, boxes, es,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 size_t align256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
@@ -777,13 +791,18 @@ fsa_status fsa_mx_linear(const uint8_t* x_codes, const uint8_t* x_scales, int x_
     s = current_device(&dev, &ds);
     if (s != FSA_OK) return s;
     const MxLinearPlan plan = mx_linear_plan(static_cast<int>(T), static_cast<int>(N), static_cast<int>(K), x_elem, w_elem);
-    CUtensorMap tx, tw;
+    CUtensorMap tx, tw, txs, tws;
     if (!make_map_mx(&tx, x_codes, T, K, x_elem, false, plan.x_rows) ||
         !make_map_mx(&tw, w_codes, N, K, w_elem, w_elem == FSA_ELEM_E2M1 && x_elem == FSA_ELEM_E4M3, plan.w_rows))
+        return FSA_ERR_CUDA;
+    if (plan.split == 0 && (!make_map_mx_scales(&txs, x_scales, T, K, plan.sf_atoms, 1) ||
+                            !make_map_mx_scales(&tws, w_scales, N, K, plan.sf_atoms, plan.sf_rows)))
         return FSA_ERR_CUDA;
     MxLinearLaunch a{};
     a.tm_x = &tx;
     a.tm_w = &tw;
+    a.tm_xs = &txs;
+    a.tm_ws = &tws;
     a.xs = x_scales;
     a.ws = w_scales;
     a.y = y;

@@ -207,8 +207,9 @@ cudaError_t launch_rms_norm_mx(const RmsNormMxLaunch& a, int elem, cudaStream_t 
 
 // Product of two MX operands (mx_linear.cu).
 struct MxLinearLaunch {
-    const CUtensorMap *tm_x, *tm_w;  // boxes of 128 bytes x mx_linear_plan's rows
-    const uint8_t *xs, *ws;          // scale atoms
+    const CUtensorMap *tm_x, *tm_w;    // boxes of 128 bytes x mx_linear_plan's rows
+    const CUtensorMap *tm_xs, *tm_ws;  // scale atoms, of one row group and of sf_rows (pairs of CTAs)
+    const uint8_t *xs, *ws;            // scale atoms
     void* y;                         // [T][N], y_stride elements apart
     int64_t y_stride;
     int T, N, K, x_elem, w_elem;
@@ -219,6 +220,7 @@ struct MxLinearLaunch {
 struct MxLinearPlan {
     int x_rows, w_rows;  // rows of a tile: box heights of the copies
     int split;           // CTAs of a cluster that share a tile's K; 0: pairs of CTAs
+    int sf_atoms, sf_rows;  // pairs: scale atoms of a copy, row groups of w's
 };
 MxLinearPlan mx_linear_plan(int T, int N, int K, int x_elem, int w_elem);
 cudaError_t launch_mx_linear(const MxLinearLaunch& a, const MxLinearPlan& plan, cudaStream_t st);

@@ -316,15 +316,21 @@ __global__ void __launch_bounds__(kThreads, 2)
 // An output tile leaves through registers, so that the next tile's products begin 450
 // clocks after the last one's end.
 //
-// warps 0-7 output; 8, 9, 10 copies; 11 the products (rank 0) or word that a stage has
-// landed (rank 1).  An SM begins a copy every 110 clocks, whatever its size, where a
-// step's products take 540, and a warp takes 150 to issue one and 120 for a wait that is
-// over (clocks a step of 256 outputs: one warp for its five copies 815, three of them in
-// one 720, the five over three warps 545, a warp each 600).  Narrower tiles' products take
-// less, so their scales come for 512 elements of K at once, in a ring of their own (kRing;
-// 512 x 5120 x 5120 in eight by four bits 16.5 -> 13.7 us); tiles of 256 outputs keep them
-// in the stages, because the second wait holds the products up (in four bits 24.0 us for
-// 1024 x 8192 x 8192, with the ring 25.5; 8192 x 16384 x 4096 in eight by four 282, 288).
+// warps 0-7 output; 8, 9, 10 copies; 11 the products (rank 0).  The copies into either CTA's
+// memory count on rank 0's barriers, so that the products' wait is for the copies themselves:
+// a warp of rank 1 that waited and then told rank 0 would have to release to the cluster's
+// scope, 1450 clocks a step.  (The barriers expect fixed bytes: scales come by tensor copies,
+// too, which fill what is behind the matrix.  4096 x 5120 x 5120 in four bits 38.9 us, with
+// word from rank 1 39.2.)
+// An SM begins a copy every 110 clocks, whatever its size, where a step's products take 540,
+// and a warp takes 150 to issue one and 120 for a wait that is over, so three warps share a
+// step's copies (one for all 815 clocks a step of 256 outputs, three warps 545), each in a
+// loop of its own (one loop that asks what to copy: 2048 x 5120 x 5120 in eight by four bits
+// 32.2 -> 35.9 us).  Narrower tiles' products take less, so their scales come for 512
+// elements of K at once, in a ring of their own (kRing; 512 x 5120 x 5120 in eight by four
+// bits 16.5 -> 13.7 us); tiles of 256 outputs keep them in the stages, because the second wait
+// holds the products up (in four bits 24.0 us for 1024 x 8192 x 8192, with the ring 25.5;
+// 8192 x 16384 x 4096 in eight by four 282, 288).
 constexpr int kPairThreads = 384;
 constexpr int kPairLoadX = 8, kPairLoadW = 9, kPairLoadSf = 10, kPairMma = 11;
 constexpr int kPairStages = 6, kPairSlots = 3;
@@ -335,8 +341,8 @@ constexpr int kPairGroup = 8;         // token tiles that are walked side by sid
 static_assert(kPairSlots * kSfAtoms >= kPairStages * 2, "scales in the stages take the ring's room");
 
 struct PairBars {
-    uint64_t full[kPairStages];       // rank 0's: the other CTA's copies, too
-    uint64_t empty[kPairStages];
+    uint64_t full[kPairStages];       // rank 0's: both CTAs' copies
+    uint64_t empty[kPairStages];      // a commit of rank 0's products arrives in both
     uint64_t sf_full[kPairSlots], sf_empty[kPairSlots];  // the same of scales (kRing)
     uint64_t acc_full, acc_empty;     // (acc_empty: rank 0's, an arrival a warp of both CTAs' output)
     uint64_t drain;
@@ -362,7 +368,6 @@ struct Turn {
 };
 
 struct PairParams {
-    const uint8_t *xs, *ws;
     __nv_bfloat16* y;
     int64_t y_stride;
     int T, N, n_atoms, t_tiles, n_tiles, bn, vec;  // bn: outputs of a tile, 256, 192 or 128
@@ -382,7 +387,8 @@ __device__ __forceinline__ void pair_tile(const PairParams& p, int i, int& t_til
 
 template <int kMode, bool kRing>
 __global__ void __launch_bounds__(kPairThreads, 1)
-    mx_linear_pair_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_w, const PairParams p) {
+    mx_linear_pair_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_w,
+                          const __grid_constant__ CUtensorMap tm_xs, const __grid_constant__ CUtensorMap tm_ws, const PairParams p) {
     extern __shared__ __align__(1024) uint8_t ring[];
     // the 128-byte-swizzled tiles need a 1024-byte aligned base (the same in both CTAs)
     if (smem_u32(ring) & 1023u) {
@@ -406,11 +412,11 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     if (tid == 0) {
         sm.abort = 0;
         for (int i = 0; i < kPairStages; ++i) {
-            mbar_init(&sm.full[i], (kRing ? 2 : 3) + (rank == 0) + (i == 1 && p.skip));
+            mbar_init(&sm.full[i], (kRing ? 2 : 3) + (i == 1 && p.skip));
             mbar_init(&sm.empty[i], 1);
         }
         for (int i = 0; i < kPairSlots; ++i) {
-            mbar_init(&sm.sf_full[i], 1 + (rank == 0));
+            mbar_init(&sm.sf_full[i], 1);
             mbar_init(&sm.sf_empty[i], 1);
         }
         mbar_init(&sm.acc_full, 1);
@@ -421,10 +427,10 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     if (warp == kPairMma) pair_tmem_alloc(&sm.tmem_base, kPairCols);
     tc_fence_before();
     __syncthreads();
-    // both CTAs' barriers are there behind the wait; the loaders only use their own CTA's
+    // both CTAs' barriers are there behind the wait; rank 0's loaders only use their own CTA's
     cluster_arrive();
-    const bool loader = warp >= kPairLoadX && warp <= kPairLoadSf;
-    if (!loader) cluster_wait();
+    const bool loader = warp >= kPairLoadX && warp <= kPairLoadSf, early = loader && rank == 0;
+    if (!early) cluster_wait();
     tc_fence_after();
     grid_launch_next();  // (the next kernel's CTAs find this one's tensor memory taken)
     grid_wait();         // in all warps: the time of the kernel before is not their waits'
@@ -434,87 +440,69 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         atomicOr(p.err_word, kErrTimeout);
     };
     auto wait = [&](uint64_t* bar, uint32_t phase) {
-        return __all_sync(0xFFFFFFFFu, mbar_wait(bar, phase & 1u, p.timeout_ns, &sm.abort)) != 0;
+        return __all_sync(0xFFFFFFFFu, mbar_wait_cluster(bar, phase & 1u, p.timeout_ns, &sm.abort)) != 0;
     };
     bool ok = true;
-    Turn<kPairStages> st;   // in step in all roles
+    Turn<kPairStages> st;
     Turn<kPairSlots> slot;
 
     if (loader) {
         if (lane == 0) {
-            const int64_t x_groups = mx_atoms(p.T), w_groups = mx_atoms(p.N);
-            int issued = 0;
-            for (int i = first_tile; ok && i < tiles; i += tile_step) {
-                int t_tile, n_tile;
-                pair_tile(p, i, t_tile, n_tile);
-                const int t0 = 256 * t_tile + 128 * static_cast<int>(rank), n0 = bn * n_tile;
-                // scale rows that there are: this CTA's tokens, all of the tile's outputs
-                const int64_t xg = t0 / 128, wg = n0 / 128;
-                const bool have_x = xg < x_groups, have_w1 = bn > 128 && wg + 1 < w_groups;
-                const uint8_t* xs = p.xs + xg * p.n_atoms * kAtomBytes;
-                const uint8_t* ws = p.ws + wg * p.n_atoms * kAtomBytes;
-                const uint8_t* ws1 = ws + static_cast<int64_t>(p.n_atoms) * kAtomBytes;
-                if (kRing && warp == kPairLoadSf) {
-                    for (int a = 0; a < p.n_atoms; a += kSlot, ++issued) {
-                        if (issued >= kPairSlots) ok = mbar_wait(&sm.sf_empty[slot.at], slot.ph ^ 1u, p.timeout_ns, &sm.abort);
+            // copies of `per` scale atoms' part of K at once into n places, tile by tile; `bytes`:
+            // those that they bring one CTA (a spread copy counts the 64 a row that it reads;
+            // rows and scales behind the matrix come as zeros and count)
+            auto fill = [&](uint64_t* full, uint64_t* empty, int n, int per, uint32_t bytes, auto copy) {
+                const uint32_t full0 = mapa(smem_u32(full), 0);
+                int issued = 0, at = 0;
+                uint32_t ph = 1;
+                for (int i = first_tile; ok && i < tiles; i += tile_step) {
+                    int t_tile, n_tile;
+                    pair_tile(p, i, t_tile, n_tile);
+                    const int xg = 2 * t_tile + static_cast<int>(rank), n0 = bn * n_tile;
+                    for (int a = 0; a < p.n_atoms; a += per, ++issued) {
+                        if (issued >= n) ok = mbar_wait_cluster(&empty[at], ph, p.timeout_ns, &sm.abort);
                         if (!ok) break;
-                        uint64_t* full = &sm.sf_full[slot.at];
-                        const uint32_t bytes = min(kSlot, p.n_atoms - a) * kAtomBytes;
-                        const int64_t at = static_cast<int64_t>(a) * kAtomBytes;
-                        uint8_t* dst = sf_tiles + slot.at * 3 * kSfGroup;
-                        mbar_arrive_expect_tx(full, bytes * (1 + have_x + have_w1));
-                        if (have_x) bulk_load(dst, xs + at, bytes, full);
-                        bulk_load(dst + kSfGroup, ws + at, bytes, full);
-                        if (have_w1) bulk_load(dst + 2 * kSfGroup, ws1 + at, bytes, full);
-                        slot.next();
+                        if (rank == 0) mbar_arrive_expect_tx(&full[at], 2 * bytes);
+                        copy(at, full0 + 8 * at, a, xg, n0);
+                        if (++at == n) {
+                            at = 0;
+                            ph ^= 1u;
+                        }
                     }
-                    continue;
                 }
-                // codes of x (and its scales), of w (and its first group's), or the second group's scales
-                const bool codes = warp != kPairLoadSf, is_x = warp == kPairLoadX, is_w = warp == kPairLoadW;
-                const CUtensorMap* map = is_x ? &tm_x : &tm_w;
-                uint8_t* tiles_at = is_x ? x_tiles : w_tiles;
-                const int row = is_x ? t0 : n0 + bn / 2 * static_cast<int>(rank);
-                // (a spread copy counts the bytes that it reads, 64 a row)
-                const uint32_t code_bytes = is_x ? 128 * 128 : is_w ? bn / 2 * (kMode == X8W4 ? 64 : 128) : 0;
-                const bool scales = !kRing && (is_x ? have_x : is_w || have_w1);
-                const uint8_t* src = is_x ? xs : is_w ? ws : ws1;
-                for (int k = 0; k < steps; ++k, ++issued) {
-                    if (issued >= kPairStages) ok = mbar_wait(&sm.empty[st.at], st.ph ^ 1u, p.timeout_ns, &sm.abort);
-                    if (!ok) break;
-                    uint64_t* full = &sm.full[st.at];
-                    const uint32_t bytes = scales ? min(kAtoms, p.n_atoms - k * kAtoms) * kAtomBytes : 0;
-                    mbar_arrive_expect_tx(full, code_bytes + bytes);
-                    if (codes) tma_load_2d(tiles_at + st.at * 16384, map, full, k * 128, row);
-                    if (scales)
-                        bulk_load(sf_tiles + (3 * st.at + warp - kPairLoadX) * kSfGroup, src + static_cast<int64_t>(k) * kSfGroup, bytes, full);
-                    st.next();
-                }
-            }
-            if (!ok) give_up();
-            // every copy lands before the CTA goes on, whoever gives up and when
-            int dummy = 0;
-            const int n = kRing && warp == kPairLoadSf ? kPairSlots : kPairStages;
-            uint64_t* full = kRing && warp == kPairLoadSf ? sm.sf_full : sm.full;
-            for (int i = max(0, issued - n); i < issued; ++i) mbar_wait(full + i % n, (i / n) & 1, p.timeout_ns, &dummy);
+                if (!ok) give_up();
+                // the products that read them are done before the CTA goes on; where they are
+                // not because someone gave up, the copies have the waits' limit to land
+                int dummy = 0;
+                for (int i = max(0, issued - n); i < issued; ++i)
+                    if (!mbar_wait_cluster(&empty[i % n], (i / n) & 1, p.timeout_ns, &dummy)) break;
+            };
+            constexpr int kSfWords = kAtomBytes / 8;
+            auto x_scales = [&](int at, uint32_t bar, int a, int xg) {
+                pair_tma_load_2d(sf_tiles + at * 3 * kSfGroup, &tm_xs, bar, a * kSfWords, xg);
+            };
+            auto w_scales = [&](int at, uint32_t bar, int a, int n0) {
+                pair_tma_load_2d(sf_tiles + (at * 3 + 1) * kSfGroup, &tm_ws, bar, a * kSfWords, n0 / 128);
+            };
+            const int w_groups = bn > 128 ? 2 : 1;
+            if (warp == kPairLoadX)
+                fill(sm.full, sm.empty, kPairStages, kAtoms, 128 * 128 + (kRing ? 0 : kSfGroup), [&](int at, uint32_t bar, int a, int xg, int) {
+                    pair_tma_load_2d(x_tiles + at * 16384, &tm_x, bar, a / kAtoms * 128, 128 * xg);
+                    if (!kRing) x_scales(at, bar, a, xg);
+                });
+            else if (warp == kPairLoadW)
+                fill(sm.full, sm.empty, kPairStages, kAtoms, bn / 2 * (kMode == X8W4 ? 64 : 128), [&](int at, uint32_t bar, int a, int, int n0) {
+                    pair_tma_load_2d(w_tiles + at * 16384, &tm_w, bar, a / kAtoms * 128, n0 + bn / 2 * static_cast<int>(rank));
+                });
+            else if (kRing)
+                fill(sm.sf_full, sm.sf_empty, kPairSlots, kSlot, (1 + w_groups) * kSfGroup, [&](int at, uint32_t bar, int a, int xg, int n0) {
+                    x_scales(at, bar, a, xg);
+                    w_scales(at, bar, a, n0);
+                });
+            else
+                fill(sm.full, sm.empty, kPairStages, kAtoms, 2 * kSfGroup, [&](int at, uint32_t bar, int a, int, int n0) { w_scales(at, bar, a, n0); });
         }
-    } else if (warp == kPairMma && rank != 0) {
-        // says in rank 0 that scales or a stage of this CTA have landed
-        for (int i = first_tile; ok && i < tiles; i += tile_step)
-            for (int k = 0; k < steps; ++k) {
-                if (kRing && k % kSfSteps == 0) {
-                    ok = wait(&sm.sf_full[slot.at], slot.ph);
-                    if (!ok) break;
-                    if (lane == 0) mbar_arrive_cluster(mapa(smem_u32(&sm.sf_full[slot.at]), 0));
-                    slot.next();
-                }
-                ok = wait(&sm.full[st.at], st.ph);
-                if (!ok) break;
-                if (lane == 0) mbar_arrive_cluster(mapa(smem_u32(&sm.full[st.at]), 0));
-                st.next();
-            }
-        if (!ok && lane == 0) give_up();
-    } else if (warp == kPairMma) {
+    } else if (warp == kPairMma && rank == 0) {
         const uint32_t tm = __shfl_sync(0xFFFFFFFFu, tmem, 0);
         const uint64_t dx = smem_desc(smem_u32(x_tiles), 16, 1024, SWZ_128B), dw = smem_desc(smem_u32(w_tiles), 16, 1024, SWZ_128B);
         const uint64_t dsf = smem_desc(smem_u32(sf_tiles), 0, 128, SWZ_NONE);
@@ -574,7 +562,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         pair_commit_one(&sm.drain, 1);  // every product issued retires before anything is freed
         int dummy = 0;
         if (!__all_sync(0xFFFFFFFFu, mbar_wait(&sm.drain, 0, p.timeout_ns, &dummy)) && lane == 0) give_up();
-    } else {
+    } else if (warp < kPairLoadX) {
         // four warps for each half of the tile's outputs, 32 at a time
         const int half = bn / 2 * (warp >> 2), pieces = bn / 64;
         const uint32_t col = tmem + (static_cast<uint32_t>(32 * (warp & 3)) << 16) + half;
@@ -639,7 +627,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     }
     tc_fence_before();
     __syncwarp();
-    if (loader) cluster_wait();
+    if (early) cluster_wait();
     cluster_sync();  // no CTA leaves while the other reads its memory or arrives at its barriers
     if (warp == kPairMma) {
         tc_fence_after();
@@ -653,8 +641,6 @@ cudaError_t launch_pair(const MxLinearLaunch& a, int bn, cudaStream_t st) {
     cudaError_t e = setup(reinterpret_cast<const void*>(mx_linear_pair_kernel<kMode, kRing>), kPairSmem, 0);
     if (e != cudaSuccess) return e;
     PairParams p{};
-    p.xs = a.xs;
-    p.ws = a.ws;
     p.y = static_cast<__nv_bfloat16*>(a.y);
     p.y_stride = a.y_stride;
     p.T = a.T;
@@ -669,7 +655,7 @@ cudaError_t launch_pair(const MxLinearLaunch& a, int bn, cudaStream_t st) {
     p.skip = a.debug_flags & 1;
     const int tiles = p.t_tiles * p.n_tiles;
     return launch_early(mx_linear_pair_kernel<kMode, kRing>, 2 * (tiles < kSms / 2 ? tiles : kSms / 2), kPairThreads, kPairSmem, st, 2,
-                        *a.tm_x, *a.tm_w, p);
+                        *a.tm_x, *a.tm_w, *a.tm_xs, *a.tm_ws, p);
 }
 
 // Tiles that run at once, each split between `split` CTAs of a cluster, one CTA or two an SM.
@@ -726,6 +712,8 @@ MxLinearPlan mx_linear_plan(int T, int N, int K, int x_elem, int w_elem) {
                 plan.w_rows = bn / 2;
             }
         }
+        plan.sf_atoms = plan.w_rows == 128 ? kAtoms : kSfAtoms;
+        plan.sf_rows = plan.w_rows == 64 ? 1 : 2;
         return plan;
     }
     if (T <= 128) plan.x_rows = (T + 15) / 16 * 16;

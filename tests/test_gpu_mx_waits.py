@@ -84,3 +84,42 @@ def test_few_rows_wait_for_nothing(fsa):
     good = fsa.rms_norm_mx(x, g)
     got = fsa.rms_norm_mx(x, g, wait_timeout_ms=1, debug_flags=fsa.DEBUG_SKIP_KV_ARRIVE | fsa.DEBUG_LOSE_ONE_WAIT)
     assert fsa.get_device_error() == 0 and torch.equal(got.codes, good.codes)
+
+
+MODES = [("mxfp4", "mxfp4"), ("mxfp8", "mxfp4"), ("mxfp8", "mxfp8")]
+# pairs of CTAs on tiles of 256, 192 and 128 outputs, rows and outputs that end inside one
+PAIRS = [(1024, 8192, 1024), (2500, 2500, 1100), (300, 5000, 2500), (300, 2048, 600)]
+
+
+@pytest.mark.parametrize("fx,fw", MODES)
+@pytest.mark.parametrize("T,N,K", PAIRS)
+def test_pairs_that_give_up_leave_nothing_behind(fsa, T, N, K, fx, fw):
+    """The second stage never counts as arrived while both CTAs' copies are on their way;
+    what runs next on the same SMs is not disturbed by them."""
+    x, w = fsa.mx_pack(_bf16((T, K), 7), fx), fsa.mx_pack(_bf16((N, K), 8, K ** -0.5), fw)
+    good = fsa.mx_linear(x, w)
+    ref.check_product(good, ref.values(x), ref.values(w))
+    for _ in range(3):
+        fsa.mx_linear(x, w, wait_timeout_ms=3, debug_flags=fsa.DEBUG_SKIP_KV_ARRIVE)
+        y = fsa.mx_linear(x, w)
+        assert fsa.get_device_error() == 5 and fsa.get_device_error() == 0
+        assert torch.equal(y, good)
+
+
+@pytest.mark.parametrize("fx,fw", MODES)
+def test_pairs_repeat_beside_one_another(fsa, fx, fw):
+    """Products of every tile width on streams of their own: each stage's copies of both
+    CTAs are there when its products run, however late they land."""
+    ops = [(fsa.mx_pack(_bf16((T, K), 9 + i), fx), fsa.mx_pack(_bf16((N, K), 19 + i, K ** -0.5), fw))
+           for i, (T, N, K) in enumerate(PAIRS)]
+    want = [fsa.mx_linear(x, w) for x, w in ops]
+    streams = [torch.cuda.Stream() for _ in ops]
+    torch.cuda.synchronize()
+    for _ in range(25):
+        got = []
+        for (x, w), st in zip(ops, streams):
+            with torch.cuda.stream(st):
+                got.append(fsa.mx_linear(x, w))
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+    assert fsa.get_device_error() == 0

@@ -647,9 +647,17 @@ def varlen_attention_fwd(q, k, v, cu_seqlens_q, cu_seqlens_k=None, *, causal: bo
 # ---- products of matrices in MX formats --------------------------------------
 
 
-# New tensors on the current device (of two calls that pack a token and read it back,
-# 11.8 us of host time with it, 19.6 with torch.empty and a storage for the operand).
-_empty_cuda = torch._C._dynamo.guards._empty_strided_cuda
+def _empty_dispatched(size, stride, dtype) -> torch.Tensor:
+    return torch.empty_strided(size, stride, dtype=dtype, device="cuda")
+
+
+# New tensors on the current device, past torch's dispatcher where this torch has such a
+# function (of two calls that pack a token and read it back, 11.8 us of host time with it,
+# 19.6 with torch.empty and a storage for the operand).
+try:
+    _empty_cuda = torch._C._dynamo.guards._empty_strided_cuda
+except AttributeError:
+    _empty_cuda = _empty_dispatched
 
 # element and bytes of 128 codes of a row
 _OPERANDS = {"mxfp4": (ELEM_E2M1, 64), "mxfp8": (ELEM_E4M3, 128)}
@@ -669,7 +677,11 @@ class MxOperand:
 
     MxOperand(codes, scales, cols, fmt) is one of given tensors; mx_new_operand, mx_pack
     and rms_norm_mx make one of a single tensor of bytes, of which codes and scales are
-    views that are made when they are asked for."""
+    views that are made when they are asked for.
+
+    The tensors that mx_pack, mx_unpack, rms_norm_mx and mx_linear make do not pass
+    torch's dispatcher: dispatch modes and the deterministic fill of empty tensors do not
+    see them (what a call does not write of them are scale bytes of rows behind the last)."""
     __slots__ = ("rows", "cols", "fmt", "elem", "_dev", "_bytes", "_codes", "_scales")
 
     def __init__(self, codes: torch.Tensor, scales: torch.Tensor, cols: int, fmt: str):

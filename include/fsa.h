@@ -525,9 +525,9 @@ FSA_API fsa_status fsa_varlen_attention_fwd_ex(const void *q, const void *k, con
 
 /*
  * fsa_mx_pack -- quantizes bf16 rows x[rows][cols], x_stride elements apart (0
- * repeats a row), into an operand, by fsa_quantize_mx's rule.  Rows on 16 bytes
- * (pointer, and a stride that is a multiple of 8) are read in whole vectors,
- * others element by element.
+ * repeats a row), into an operand, by fsa_quantize_mx's rule.  Rows on 16, 8 or 4
+ * bytes (pointer and stride) are read in words of that many, others element by
+ * element.
  */
 FSA_API fsa_status fsa_mx_pack(const void *x, int64_t x_stride, int64_t rows, int64_t cols, int elem,
                                uint8_t *codes, uint8_t *scales, void *stream);
@@ -580,8 +580,8 @@ FSA_API fsa_status fsa_rms_norm_mx_ex(const void *x, int64_t x_stride, const voi
  *  counts down to 2^-22 of the largest of its 32 or 64 products and the sum so far at
  *  least), in an order that depends on T, N, K and the types only, and rounded once;
  *  products and sums must lie in FP32's range.
- *  opt: NULL, or wait_timeout_ms and debug_flags (stage 1 of a tile's ring never
- *  arrives) are used.
+ *  opt: NULL, or wait_timeout_ms (of each wait; that for the kernels before the call
+ *  does not count) and debug_flags (stage 1 of a tile's ring never arrives) are used.
  * ceil(T / 128) * ceil(N / 128) <= 2^27.  A bounded wait that ran out is reported by
  * fsa_get_device_error.
  */

@@ -663,7 +663,10 @@ cudaError_t launch_pair(const MxLinearLaunch& a, int bn, cudaStream_t st) {
 // some SMs out (a token by 4096 columns in eight by four bits with one CTA an SM: 15 tiles
 // split by 8 4.9 us, 16 tiles 8.1; 36 tiles split by 4 5.6, 37 tiles 8.4; 74 tiles split by 2
 // 7.9, 75 tiles 12.0. With two an SM: 36 and 37 tiles 5.5 and 8.1; 74 and 75 7.6 and 12.2;
-// 152 and 153 10.6 and 11.8).
+// 152 and 153 10.6 and 11.8).  GB300's numbers as constants: the split decides the order of a
+// sum, which is not to depend on the chip at hand.  (cudaOccupancyMaxActiveClusters says the
+// same there, but for 76 with two CTAs on SMs of their own, where 75 and 76 tiles take 8.4 us
+// against 8.1 with two CTAs an SM.)
 int64_t tiles_at_once(int split, int per_sm) {
     const int64_t one = split == 1 ? kSms : split == 2 ? 74 : split == 4 ? 36 : 15;
     const int64_t two = split == 1 ? 2 * kSms : split == 2 ? 152 : split == 4 ? 74 : 36;
@@ -694,8 +697,9 @@ MxLinearPlan mx_linear_plan(int T, int N, int K, int x_elem, int w_elem) {
     MxLinearPlan plan{};
     plan.w_rows = plan.x_rows = 128;
     // More than 128 tokens: 128 x 128 tiles where four CTAs to a tile run at once, one an SM,
-    // pairs of CTAs otherwise (256 x 2048 x 4096, 32 tiles: 8.6 us against 9.9 in eight by four
-    // bits; 256 x 4096 x 4096, 64 tiles: 10.4 against 10.1, and 8.9 against 7.7 in four bits).
+    // pairs of CTAs otherwise (256 tokens by 4096 columns, 16 / 32 / 36 / 38 / 64 tiles: 7.7 /
+    // 8.6 / 8.9 / 9.7 / 10.4 us against 9.7 / 9.8 / 9.8 / 9.8 / 10.0 in pairs in eight by four
+    // bits, 6.8 / 7.6 / 7.9 / 8.2 / 8.9 against 7.5 / 7.6 / 7.5 / 7.5 / 7.8 in four bits).
     const int64_t tiles = mx_atoms(N) * mx_atoms(T);
     const int kAtoms = stage_atoms(mode_of(x_elem, w_elem));
     const int64_t steps = (mx_atoms(K) + kAtoms - 1) / kAtoms;

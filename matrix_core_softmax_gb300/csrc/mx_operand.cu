@@ -464,10 +464,10 @@ __global__ void __launch_bounds__(kThreads, kThreads == 256 ? 3 : 1) rms_norm_mx
 }
 
 // log2 of the warps for a row of `pieces` pieces, so that `rows` rows fill the GPU
-// (152 SMs x 32 warps) as far as the row has work for them.
+// (kSms x 32 warps) as far as the row has work for them.
 int warps_log2(int64_t rows, int64_t pieces, int most) {
     int lg = 0;
-    while (lg < most && (rows << lg) < 152 * 32 && (int64_t{64} << lg) <= pieces) ++lg;
+    while (lg < most && (rows << lg) < kSms * 32 && (int64_t{64} << lg) <= pieces) ++lg;
     return lg;
 }
 
